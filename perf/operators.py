@@ -194,50 +194,56 @@ def _plain_top(z, M, s):
     return {"logprobs": logp, "ids": ids, "lse": lse[..., 0]}
 
 
-def _stats(y, logp, ids, weight, s, tail):
-    """What the loss and the gradient share: the loss and a row's (max, 1/sum, list factor, tail factor)."""
-    y = y.float()
+def _list(logp, ids, tail):
+    """Listed places, their probabilities, their sum, and the unlisted mass, in 64 bits."""
     here = ids >= 0
-    at = ids.clamp(min=0).long()
     p = torch.where(here, torch.exp(logp.double()), 0.0)
     P = p.sum(-1)
-    live = (weight != 0) & here.any(-1)
     if tail:
-        pt, logp_n = (1.0 - P).clamp(min=0.0), logp.double()
-    else:
-        pt, logp_n = torch.zeros_like(P), logp.double() - torch.log(P)[..., None]
-        p = p / P[..., None]
+        return here, p, P, (1.0 - P).clamp(min=0.0)
+    return here, p / P[..., None].clamp(min=1e-300), P, torch.zeros_like(P)
+
+
+def _unlisted(y, ids, here):
+    mark = torch.zeros(y.shape, dtype=torch.int32, device=y.device)
+    return mark.scatter_add_(-1, ids.clamp(min=0).long(), here.int()) == 0
+
+
+def _stats(y, logp, ids, weight, s, tail):
+    """The loss and what its gradient needs of a row: (maximum, 1/sum, the unlisted tokens' maximum and factor)."""
+    y = y.float()
+    here, p, P, pt = _list(logp, ids, tail)
+    live = (weight != 0) & here.any(-1)
+    at = ids.clamp(min=0).long()
     mx = y.amax(-1)
-    e = torch.exp(s * (y - mx[..., None]))
-    total = e.sum(-1)
-    mark = torch.zeros(y.shape, dtype=torch.int32, device=y.device).scatter_add_(-1, at, here.int())
-    qt = torch.where(mark > 0, 0.0, e).sum(-1) / total
-    del e, mark
-    logq = s * (torch.gather(y, -1, at) - mx[..., None]).double() - torch.log(total.double())[..., None]
-    kl = torch.where(here & (p > 0), p * (logp_n - logq), 0.0).sum(-1)
-    bucket = (pt > 0) & (qt > 0)
-    kl = kl + torch.where(bucket, pt * (torch.log(pt) - torch.log(qt.double())), 0.0)
-    a = P if tail else torch.ones_like(P)
-    a = torch.where(qt > 0, 1.0, a)
-    c = torch.where(bucket, 1.0 - pt / qt.double(), 1.0)
-    stats = torch.stack([mx.double(), 1.0 / total.double(), a, c], -1)
-    return {"loss": torch.where(live, weight * kl, 0.0).float(),
-            "stats": torch.where(live[..., None], stats, 0.0).float(), "p": torch.where(live[..., None], p, 0.0)}
+    total = torch.exp(s * (y - mx[..., None])).sum(-1).double()
+    out = torch.where(_unlisted(y, ids, here), y, -INF)
+    mo = out.amax(-1)
+    some = mo > -INF
+    so = torch.exp(s * (out - torch.where(some, mo, 0.0)[..., None])).sum(-1).double()
+    del out
+    lq_t = torch.where(some, s * (mo - mx).double() + torch.log(so) - torch.log(total), -INF)
+    logq = s * (torch.gather(y, -1, at) - mx[..., None]).double() - torch.log(total)[..., None]
+    logp = logp.double() if tail else logp.double() - torch.log(P)[..., None]
+    kl = torch.where(here & (p > 0), p * (logp - logq), 0.0).sum(-1)
+    kl = kl + torch.where(some & (pt > 0), pt * (torch.log(pt) - lq_t), 0.0)
+    factor = torch.where(some, (torch.exp(lq_t) - pt) / so, 0.0)
+    stats = torch.stack([mx.double(), 1.0 / total, mo.double(), factor], -1)
+    return {"loss": torch.where(live, weight * kl, 0.0).float(), "stats": torch.where(live[..., None], stats, 0.0).float()}
 
 
 def _plain_grad(y, logp, ids, stats, scale, s, tail):
-    here = ids >= 0
-    at = ids.clamp(min=0).long()
-    p = torch.where(here, torch.exp(logp.double()), 0.0)
-    if not tail:
-        p = p / p.sum(-1, keepdim=True).clamp(min=1e-300)
+    here, p, P, _ = _list(logp, ids, tail)
     live = (stats[..., 1] != 0) & (scale != 0)
-    mx, inv, a, c = (stats[..., i, None] for i in range(4))
-    q = torch.exp(s * (y.float() - mx)) * inv
-    mark = torch.zeros(y.shape, dtype=torch.int32, device=y.device).scatter_add_(-1, at, here.int())
-    g = q * torch.where(mark > 0, a, c)
-    del q, mark
-    g = g.scatter_add_(-1, at, -p.float()) * (scale * s)[..., None]
+    mx, inv, mo, factor = (stats[..., i, None] for i in range(4))
+    if tail:
+        inv = torch.where(mo == -INF, P[..., None].float(), 1.0) * inv
+    mo = torch.where(mo == -INF, 0.0, mo)
+    y32 = y.float()
+    free = _unlisted(y, ids, here)
+    g = torch.where(free, torch.exp(s * (y32 - mo)) * factor, torch.exp(s * (y32 - mx)) * inv)
+    del y32, free
+    g = g.scatter_add_(-1, ids.clamp(min=0).long(), -p.float()) * (scale * s)[..., None]
     return torch.where(live[..., None], g, 0.0).to(y.dtype)
 
 
@@ -382,26 +388,23 @@ def _exact_distill(st, op):
             lq = torch.log_softmax(row, 0)
             listed_ = torch.zeros(V, dtype=torch.bool, device=DEV)
             listed_[where] = True
+            free = row.masked_fill(listed_, -INF)
+            peak = free.max()
+            some = peak > -INF
             rest = torch.logsumexp(lq.masked_fill(listed_, -INF), 0)
+            share = torch.where(some, torch.softmax(free, 0), 0.0)  # of the unlisted mass
             mass = lp.exp().sum()
-            some = rest > -INF
-            if tail:
-                left = (1 - mass).clamp(min=0)
-                bucket = some & (left > 0)
-                d = (lp.exp() * (lp - lq[where])).sum() + torch.where(bucket, left * (left.log() - rest), 0.0)
-                a, c = torch.where(some, 1.0, mass), torch.where(bucket, 1 - left / rest.exp(), 1.0)
-                target = lp.exp()
-            else:
+            left = (1 - mass).clamp(min=0) if tail else torch.zeros_like(mass)
+            if not tail:
                 lp = lp - mass.log()
-                target = lp.exp()
-                d = (target * (lp - lq[where])).sum()
-                a = c = torch.ones((), dtype=torch.float64, device=DEV)
+            target = lp.exp()
+            d = (target * (lp - lq[where])).sum() + torch.where(some & (left > 0), left * (left.log() - rest), 0.0)
             loss[b, k] = w[b, k] * d
-            top = row.max() / s
-            stats[b, k] = torch.stack([top, lq.max().exp(), a, c])
+            excess = torch.where(some, rest.exp() - left, 0.0)
+            stats[b, k] = torch.stack([row.max() / s, lq.max().exp(), peak / s, excess * share.max()])
             if grads is not None:
-                q = lq.exp()
-                x = torch.where(listed_, a * q, c * q).index_add(0, where, -target)
+                q = lq.exp() * torch.where(some, 1.0, target.sum())
+                x = torch.where(listed_, q, excess * share).index_add(0, where, -target)
                 grads[b, k] = s * up[b, k] * x
     if op == "loss":
         return {"loss": loss, "stats": stats}
