@@ -71,6 +71,7 @@ extern "C" {
 #define SPEC_ERR_BAD_TOKEN 6     /* device status: a draft token was outside [0,V) */
 #define SPEC_ERR_BAD_TEMPERATURE 7 /* device status: an inverse temperature was out of range */
 #define SPEC_ERR_INDEX 8         /* device status, checked builds only: an index check failed */
+#define SPEC_ERR_BAD_PARENT 9    /* device status: a parent beam was outside [-1, W) */
 
 /* limits */
 #define SPEC_MAX_B (1 << 24)     /* sequences per call                      */
@@ -79,6 +80,10 @@ extern "C" {
 #define SPEC_STATIC_SCRATCH_BYTES (16u << 20) /* scratch of spec_verify_static */
 #define SPEC_MIN_INV_TEMPERATURE 1.0e-4f  /* inverse temperature range of   */
 #define SPEC_MAX_INV_TEMPERATURE 1.0e4f   /* spec_verify_temperature        */
+
+#define SPEC_MAX_TOP 128         /* entries of a top list (M)               */
+#define SPEC_MAX_BEAMS 32        /* beams per sequence (W)                  */
+#define SPEC_MAX_BEAM_OUT 64     /* continuations kept per sequence (N)     */
 
 typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
 
@@ -395,6 +400,150 @@ int spec_irls_accumulate(int32_t B, int32_t K, const float *feature, const int32
                          const float *est_params, void *state, void *stream);
 int spec_irls_refit(int32_t K, void *state, float *est_params, double damping, double *step_out,
                     void *stream);
+
+/*
+ * Operators on rows of vocabulary logits next to the verification pass: the
+ * draft model's distillation from the target's top log-probabilities, and
+ * beam search with the draft model. The pages have no counterpart to them:
+ * they serve the draft model that the verification pass judges ([SD]: the
+ * speed-up hangs on how often the target accepts the draft's tokens; its
+ * target rows are the teacher's rows).
+ *
+ * Rows: row (b, i), b < B, i < K, starts at element b * batch_stride +
+ * i * row_stride. Strides are in elements and may be 0 (a repeated row) for
+ * inputs; a stride smaller than V otherwise overlaps rows, which inputs may
+ * and outputs may not. Any alignment to the element works; no stride or
+ * length needs to be a multiple of anything. A logit of -inf or below -1e29
+ * is masked (the token has probability 0). NaN or +inf logits spoil their own
+ * row's outputs only (its floats are NaN or infinite) and raise
+ * SPEC_ERR_BAD_ROW.
+ *
+ * `status` is a device int32 or NULL: the largest code met is left there
+ * (atomic maximum). These calls never clear it: the caller zeroes it. They
+ * use no workspace except spec_beam_step. Asynchronous on `stream`, outputs
+ * bit-reproducible, B = 0 or K = 0 enqueues nothing.
+ */
+typedef struct {
+    int32_t B;            /* sequences, 0 .. SPEC_MAX_B                       */
+    int32_t K;            /* rows per sequence, 0 .. 4096                     */
+    int32_t V;            /* vocabulary size, 1 .. SPEC_MAX_V                 */
+    int32_t dtype;        /* spec_dtype of the logits (and of their gradient) */
+    int32_t M;            /* entries of a top list, 1 .. SPEC_MAX_TOP         */
+    int32_t tail;         /* distillation: 1 keeps the unlisted mass (below)  */
+    float inv_temperature;/* s in [SPEC_MIN_INV_TEMPERATURE, SPEC_MAX_...]    */
+    int32_t reserved;     /* must be 0                                        */
+    int64_t batch_stride; /* of the logits                                    */
+    int64_t row_stride;   /* of the logits                                    */
+} spec_rows_params;
+
+/*
+ * spec_top_logprobs -- the M largest log-probabilities of every row.
+ * Row z: lse = ln sum_v exp(s z_v); entry m is the m-th largest logit (equal
+ * logits in ascending token order), as logprobs[m] = s z - lse and its token
+ * ids[m]. Masked tokens are never listed: with fewer than M unmasked tokens
+ * the remaining entries are -inf and -1. A row without unmasked tokens has
+ * lse = -inf and an empty list (no error: rows past a sequence's end).
+ * logprobs [B][K][M] f32 and ids [B][K][M] int32 out; lse [B][K] f32 out or
+ * NULL. One read of the logits.
+ */
+int spec_top_logprobs(const spec_rows_params *params, const void *logits, float *logprobs, int32_t *ids, float *lse,
+                      int32_t *status, void *stream);
+
+/*
+ * Distillation of a student row y from a teacher's top list (l_m, id_m),
+ * m < M (spec_top_logprobs of the teacher's row; entries with id -1 are
+ * absent). q = softmax(s y) over the whole vocabulary, p_m = exp(l_m),
+ * P = sum_m p_m.
+ *   tail = 1: the unlisted tokens are one more outcome, of teacher mass
+ *     p_T = max(0, 1 - P) and student mass q_T = sum of q over unlisted tokens:
+ *       KL = sum_m p_m (l_m - ln q(id_m)) + p_T (ln p_T - ln q_T).
+ *     The last term is left out where p_T = 0 or no unlisted token is unmasked.
+ *   tail = 0: the list renormalised, p_m / P and l_m - ln P for p_m and l_m,
+ *     without the last term.
+ * loss = weight * KL, and the gradient of grad_loss * loss by y_v is
+ *   grad_loss * weight * s * (q_v - sum_m p_m [id_m = v])     at listed v,
+ *   grad_loss * weight * s * (q_T - p_T) q_v / q_T            at unlisted v
+ * (with tail = 0 p_T = 0; with tail = 1 and no unlisted token P q_v for q_v).
+ * A token listed twice carries both probabilities and counts once in q_T.
+ * A row of weight 0 or with an empty list (no id, or with tail = 0 no
+ * probability above 0) has loss 0 and gradient 0 whatever its logits. A listed token that the student masks makes the loss
+ * +inf, the gradient stays finite. A student row without unmasked tokens:
+ * loss +inf, gradient 0, SPEC_ERR_BAD_ROW. An id outside [-1, V) is taken as
+ * absent and raises SPEC_ERR_BAD_TOKEN.
+ *
+ * spec_distill_loss: loss [B][K] f32 out, stats [B][K][4] f32 out (16-byte
+ *   aligned): the row's maximum m, 1 / sum_v exp(s (y_v - m)), the unlisted
+ *   tokens' maximum m_o and (q_T - p_T) / sum over them of exp(s (y_v - m_o)).
+ *   Without unlisted tokens the last two are -inf and 0; a row of weight 0 or
+ *   with an empty list, or without unmasked tokens, has zeros.
+ * spec_distill_grad: the gradient from stats, dlogits [B][K][V] in the
+ *   logits' dtype with strides of its own; grad_loss [B][K] f32 or NULL (1).
+ * spec_distill_step: loss and gradient (grad_loss = 1) in one call.
+ * weight [B][K] f32 or NULL (1). dlogits may be the logits themselves
+ * (in place, equal strides), and must not overlap them otherwise.
+ * Precision: q and its sums in fp32, the list's terms in fp64.
+ */
+int spec_distill_loss(const spec_rows_params *params, const void *logits, const float *logprobs, const int32_t *ids,
+                      const float *weight, float *loss, float *stats, int32_t *status, void *stream);
+int spec_distill_grad(const spec_rows_params *params, const void *logits, const float *logprobs, const int32_t *ids,
+                      const float *weight, const float *stats, const float *grad_loss, void *dlogits,
+                      int64_t d_batch_stride, int64_t d_row_stride, int32_t *status, void *stream);
+int spec_distill_step(const spec_rows_params *params, const void *logits, const float *logprobs, const int32_t *ids,
+                      const float *weight, float *loss, void *dlogits, int64_t d_batch_stride, int64_t d_row_stride,
+                      int32_t *status, void *stream);
+
+/*
+ * spec_beam_step -- one step of beam search. Beam w of sequence b has the
+ * cumulative score scores[b][w] and the logits row (b, w) (params: K = W
+ * beams, 1 .. SPEC_MAX_BEAMS; M = N continuations kept, 1 ..
+ * SPEC_MAX_BEAM_OUT; inv_temperature must be 1, tail 0). Its continuations
+ * are all unmasked tokens v, of score scores[b][w] + ln softmax(z)_v. A
+ * finished beam (finished[b][w] != 0; finished may be NULL) has one
+ * continuation, the token eos at its own score; its logits are not read. A
+ * beam of score -inf has none; a score of NaN or +inf counts as -inf and
+ * raises SPEC_ERR_BAD_ROW.
+ * The N best of a sequence, best first, equal scores by w * V + v:
+ * out_scores, out_parent (w), out_token (v), out_finished (1 if the token is
+ * eos), each [B][N]; where there are fewer: -inf, -1, -1, 0. out_scores
+ * may be scores and out_finished finished (N = W).
+ * The order is that of exact arithmetic on the logits and scores, down to
+ * differences of 1e-9: where fp32 sums leave the order of two selected
+ * scores open, the kernel sums the beams' rows again in more bits.
+ * eos in [0, V) or -1 (none; finished must then be NULL).
+ * Workspace: spec_beam_workspace_size(params) bytes, 16-byte aligned, its
+ * content ignored on entry, not to be shared by calls that can overlap.
+ */
+size_t spec_beam_workspace_size(const spec_rows_params *params);
+int spec_beam_step(const spec_rows_params *params, const void *logits, const float *scores, const int32_t *finished,
+                   int32_t eos, float *out_scores, int32_t *out_parent, int32_t *out_token, int32_t *out_finished,
+                   int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * spec_beam_reorder -- states in the order of the surviving beams:
+ * dst row (o, b, n) = src row (o, b, parent[b][n]) for n < N. A row is H
+ * segments (heads) of T units (tokens) of unit_bytes each; with lengths only
+ * the first lengths[b] units (clamped to [0, T]) of each segment are moved,
+ * what lies behind them stays as it was. parent -1 leaves the row as it
+ * was; a parent outside [-1, W) does too and raises SPEC_ERR_BAD_PARENT.
+ * dst may be src (in place, any map including repeated parents; N <= W and
+ * equal strides; rows that keep their place are not touched), and must not
+ * overlap it otherwise. Strides in bytes, multiples of 1; rows and segments
+ * of dst must not overlap. All of base, strides and unit_bytes multiples of
+ * 16 is the fastest case.
+ */
+typedef struct {
+    int32_t O;            /* outer count (layers), 0 .. 65535                 */
+    int32_t B;            /* sequences, 0 .. SPEC_MAX_B                       */
+    int32_t W;            /* beams in src, 1 .. SPEC_MAX_BEAMS                */
+    int32_t N;            /* beams in dst, 1 .. SPEC_MAX_BEAMS                */
+    int32_t H;            /* segments per row, 0 .. 65535                     */
+    int32_t T;            /* units per segment, 0 .. 2^31 - 1                 */
+    int64_t unit_bytes;   /* bytes per unit, >= 1; units are contiguous       */
+    int64_t src_stride[4];/* of o, b, beam, segment                           */
+    int64_t dst_stride[4];
+} spec_reorder_params;
+int spec_beam_reorder(const spec_reorder_params *params, const void *src, void *dst, const int32_t *parent,
+                      const int32_t *lengths, int32_t *status, void *stream);
 
 /*
  * Synchronously read the device status word of a workspace last used by

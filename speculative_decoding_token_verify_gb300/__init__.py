@@ -11,3 +11,7 @@ from .api import (  # noqa: F401
     confidence, device_status, estimator_update, irls_accumulate, irls_refit, make_params, ngram_draft, verify,
     workspace_size,
 )
+from .rows import (  # noqa: F401
+    MAX_BEAM_OUT, MAX_BEAMS, MAX_TOP, beam_reorder, beam_step, beam_workspace_size, distill_grad, distill_loss,
+    distill_step, top_logprobs,
+)

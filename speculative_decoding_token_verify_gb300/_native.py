@@ -21,7 +21,8 @@ LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 # the same library with the kernels' index checks compiled in (SPEC_CHECKED);
 # for tests
 CHECKED_LIB_PATH = os.path.join(_PKG, "libspecverify_checked.so")
-SOURCES = ("spec_verify.cu", "spec_nucleus.cu", "spec_estimator.cu", "spec_irls.cu", "spec_av.cu", "spec_ngram.cu")
+SOURCES = ("spec_verify.cu", "spec_nucleus.cu", "spec_estimator.cu", "spec_irls.cu", "spec_av.cu", "spec_ngram.cu",
+           "spec_top.cu", "spec_distill.cu", "spec_beam.cu", "spec_reorder.cu")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
@@ -42,6 +43,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     path."""
     srcs = [os.path.join(_CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(_CSRC, "spec_device.cuh"), os.path.join(_CSRC, "spec_nucleus.cuh"),
+            os.path.join(_CSRC, "spec_rows.cuh"), os.path.join(_CSRC, "spec_top.cuh"),
             os.path.join(_INCLUDE, "spec_verify.h")]
     targets = [(LIB_PATH, [])] + ([(CHECKED_LIB_PATH, ["-DSPEC_CHECKED"])] if checked else [])
     newest = max(os.path.getmtime(d) for d in deps)
@@ -104,6 +106,37 @@ class VerifyParams(ctypes.Structure):
     ]
 
 
+class RowsParams(ctypes.Structure):
+    """Mirror of ``spec_rows_params``."""
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("K", ctypes.c_int32),
+        ("V", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("M", ctypes.c_int32),
+        ("tail", ctypes.c_int32),
+        ("inv_temperature", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("batch_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
+    ]
+
+
+class ReorderParams(ctypes.Structure):
+    """Mirror of ``spec_reorder_params``."""
+    _fields_ = [
+        ("O", ctypes.c_int32),
+        ("B", ctypes.c_int32),
+        ("W", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("T", ctypes.c_int32),
+        ("unit_bytes", ctypes.c_int64),
+        ("src_stride", ctypes.c_int64 * 4),
+        ("dst_stride", ctypes.c_int64 * 4),
+    ]
+
+
 # (name, restype, argtypes) of every symbol include/spec_verify.h declares
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -131,6 +164,16 @@ SIGNATURES = {
     "spec_irls_reset": (ctypes.c_int, [_I32, _P, _P]),
     "spec_irls_accumulate": (ctypes.c_int, [_I32, _I32, _P, _P, _P, _P, _P]),
     "spec_irls_refit": (ctypes.c_int, [_I32, _P, _P, ctypes.c_double, _P, _P]),
+    "spec_top_logprobs": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _P, _P, _P]),
+    "spec_distill_loss": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _P, _P, _P, _P, _P]),
+    "spec_distill_grad": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64,
+                                         ctypes.c_int64, _P, _P]),
+    "spec_distill_step": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _P, _P, _P, ctypes.c_int64,
+                                         ctypes.c_int64, _P, _P]),
+    "spec_beam_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(RowsParams)]),
+    "spec_beam_step": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
+    "spec_beam_reorder": (ctypes.c_int, [ctypes.POINTER(ReorderParams), _P, _P, _P, _P, _P, _P]),
     "spec_get_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_I32)]),
     "spec_static_device_status": (ctypes.c_int, [ctypes.POINTER(_I32)]),
     "spec_debug_set_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),

@@ -27,6 +27,7 @@ SPEC_ERR_BAD_ROW = 5
 SPEC_ERR_BAD_TOKEN = 6
 SPEC_ERR_BAD_TEMPERATURE = 7
 SPEC_ERR_INDEX = 8
+SPEC_ERR_BAD_PARENT = 9
 MAX_K = 31
 MAX_V = 1 << 20
 

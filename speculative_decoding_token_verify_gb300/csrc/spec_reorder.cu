@@ -1,0 +1,156 @@
+// spec_reorder.cu -- the beams' states in the order of the surviving beams.
+//
+// In place without a second buffer: a column (one vector's place in a row) is
+// one thread's alone, which loads that place from every parent before it
+// stores any. Rows that keep their place are neither read nor written.
+#include "spec_rows.cuh"
+
+namespace sr {
+
+constexpr int NTR = 256;
+
+struct ReorderArgs {
+    const char *src;
+    char *dst;
+    const int32_t *parent, *lengths;
+    int32_t *status;
+    int B, W, N, H, T;
+    long long unit, ss[4], ds[4];
+    long long seg_tiles;   // tiles of NTR vectors per segment
+    int in_place;
+};
+
+template <typename Vec, int WB>
+__global__ void __launch_bounds__(NTR) reorder_kernel(ReorderArgs a) {
+    __shared__ int s_par[SPEC_MAX_BEAMS];
+    const int o = blockIdx.z;
+    const int h = (int)(blockIdx.x / a.seg_tiles);
+    const long long tile = blockIdx.x - (long long)h * a.seg_tiles;
+    for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+        __syncthreads();
+        if (threadIdx.x < a.N) {
+            int p = a.parent[(size_t)b * a.N + threadIdx.x];
+            if (p < -1 || p >= a.W) {
+                if (blockIdx.x == 0 && o == 0) raise_status(a.status, SPEC_ERR_BAD_PARENT);
+                p = -1;
+            }
+            if (a.in_place && p == (int)threadIdx.x) p = -1;   // stays where it is
+            s_par[threadIdx.x] = p;
+        }
+        __syncthreads();
+        const long long units = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
+        const long long bytes = units * a.unit;
+        const long long at = (tile * NTR + threadIdx.x) * (long long)sizeof(Vec);
+        if (at >= bytes) continue;
+        const char *src = a.src + o * a.ss[0] + b * a.ss[1] + h * a.ss[3] + at;
+        char *dst = a.dst + o * a.ds[0] + b * a.ds[1] + h * a.ds[3] + at;
+        Vec v[WB];
+#pragma unroll
+        for (int n = 0; n < WB; ++n)
+            if (n < a.N && s_par[n] >= 0) v[n] = *reinterpret_cast<const Vec *>(src + s_par[n] * a.ss[2]);
+#pragma unroll
+        for (int n = 0; n < WB; ++n)
+            if (n < a.N && s_par[n] >= 0) *reinterpret_cast<Vec *>(dst + n * a.ds[2]) = v[n];
+    }
+}
+
+template <typename Vec>
+static cudaError_t launch_vec(ReorderArgs &a, int O, cudaStream_t stream) {
+    const long long seg = (long long)a.T * a.unit / (long long)sizeof(Vec);
+    a.seg_tiles = (seg + NTR - 1) / NTR;
+    const long long gx = a.seg_tiles * a.H;
+    if (gx > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)gx, (unsigned)(a.B < 65535 ? a.B : 65535), (unsigned)O);
+    if (a.N <= 4) reorder_kernel<Vec, 4><<<grid, NTR, 0, stream>>>(a);
+    else if (a.N <= 8) reorder_kernel<Vec, 8><<<grid, NTR, 0, stream>>>(a);
+    else if (a.N <= 16) reorder_kernel<Vec, 16><<<grid, NTR, 0, stream>>>(a);
+    else reorder_kernel<Vec, 32><<<grid, NTR, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
+// rows (o, b, beam, segment) of `bytes` bytes that do not overlap: with the
+// axes ordered by stride, each steps over the whole extent of the smaller ones
+static bool disjoint(const int64_t *stride, const int64_t *count, int64_t bytes) {
+    int order[4] = {0, 1, 2, 3};
+    for (int i = 0; i < 4; ++i)
+        for (int j = i + 1; j < 4; ++j)
+            if (stride[order[j]] < stride[order[i]]) {
+                const int t = order[i];
+                order[i] = order[j];
+                order[j] = t;
+            }
+    int64_t extent = bytes;
+    for (int i = 0; i < 4; ++i) {
+        const int k = order[i];
+        if (count[k] <= 1) continue;
+        if (stride[k] < extent) return false;
+        extent += (count[k] - 1) * stride[k];
+    }
+    return true;
+}
+
+}  // namespace sr
+
+extern "C" int spec_beam_reorder(const spec_reorder_params *p, const void *src, void *dst, const int32_t *parent,
+                                 const int32_t *lengths, int32_t *status, void *stream) {
+    using namespace sr;
+    if (!p) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "params is NULL");
+    if (p->O < 0 || p->B < 0 || p->H < 0 || p->T < 0)
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "O, B, H and T must be >= 0");
+    if (p->W < 1 || p->W > SPEC_MAX_BEAMS || p->N < 1 || p->N > SPEC_MAX_BEAMS || p->O > 65535 || p->H > 65535 ||
+        p->B > SPEC_MAX_B)
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "beam_reorder: O, B, W, N or H out of range");
+    if (p->unit_bytes < 1 || p->unit_bytes > (1 << 30))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: unit_bytes must be in [1, 2^30]");
+    const int64_t sc[4] = {p->O, p->B, p->W, p->H}, dc[4] = {p->O, p->B, p->N, p->H};
+    for (int i = 0; i < 4; ++i) {
+        if (p->src_stride[i] < 0 || p->dst_stride[i] < 0)
+            return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: strides must be >= 0");
+        if ((sc[i] > 1 && p->src_stride[i] > (INT64_MAX >> 4) / sc[i]) ||
+            (dc[i] > 1 && p->dst_stride[i] > (INT64_MAX >> 4) / dc[i]))
+            return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: strides are too large");
+    }
+    if (p->O == 0 || p->B == 0 || p->H == 0 || p->T == 0) return spec_internal_set_error(SPEC_OK, "");
+    if (!src || !dst || !parent) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "src / dst / parent is NULL");
+    const int64_t bytes = (int64_t)p->T * p->unit_bytes;
+    if (!disjoint(p->dst_stride, dc, bytes))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: rows of dst overlap");
+    ReorderArgs a{};
+    a.in_place = src == dst;
+    if (a.in_place) {
+        if (p->N > p->W) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: in place needs N <= W");
+        for (int i = 0; i < 4; ++i)
+            if (sc[i] > 1 && p->src_stride[i] != p->dst_stride[i])
+                return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: in place needs equal strides");
+        // beams past N are rows of the state too
+        if (!disjoint(p->src_stride, sc, bytes))
+            return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "beam_reorder: rows of src overlap");
+    }
+    a.src = static_cast<const char *>(src);
+    a.dst = static_cast<char *>(dst);
+    a.parent = parent;
+    a.lengths = lengths;
+    a.status = status;
+    a.B = p->B;
+    a.W = p->W;
+    a.N = p->N;
+    a.H = p->H;
+    a.T = p->T;
+    a.unit = p->unit_bytes;
+    uint64_t bits = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | (uint64_t)p->unit_bytes;
+    for (int i = 0; i < 4; ++i) {
+        a.ss[i] = sc[i] > 1 ? p->src_stride[i] : 0;
+        a.ds[i] = dc[i] > 1 ? p->dst_stride[i] : 0;
+        bits |= (uint64_t)(a.ss[i] | a.ds[i]);
+    }
+    spec_internal_set_error(SPEC_OK, "");
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (bits % 16 == 0) e = launch_vec<uint4>(a, p->O, st);
+    else if (bits % 4 == 0) e = launch_vec<uint32_t>(a, p->O, st);
+    else if (bits % 2 == 0) e = launch_vec<uint16_t>(a, p->O, st);
+    else e = launch_vec<uint8_t>(a, p->O, st);
+    if (e == cudaErrorInvalidConfiguration)
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "beam_reorder: segments too long");
+    return e == cudaSuccess ? SPEC_OK : spec_internal_set_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
+}

@@ -1,0 +1,217 @@
+// spec_rows.cuh -- building blocks of the row operators (top log-probabilities,
+// distillation, beam step): a row's layout in 16-byte vectors, the running sum
+// of a softmax, ordered keys, block reductions. Internal to the library.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "spec_device.cuh"
+#include "spec_verify.h"
+
+namespace sr {
+
+using sv::Elem;
+using sv::ex2;
+using sv::kLog2e;
+using sv::neg_inf;
+
+constexpr unsigned kFull = 0xffffffffu;
+
+__device__ __forceinline__ void raise_status(int32_t *status, int code) {
+    if (status) atomicMax(status, code);
+}
+
+// ---- a row as scalars, 16-byte vectors, scalars ----------------------------
+//
+// `head` elements up to the first 16-byte boundary, nvec vectors, `tail`
+// elements: any row base that is aligned to its element streams in whole
+// vectors, so odd vocabularies and strides cost two partial vectors a row.
+template <typename T>
+struct Row {
+    static constexpr int E = Elem<T>::kPerVec;
+    const T *p;
+    const uint4 *body;
+    int head, nvec, tail;
+
+    __device__ __forceinline__ Row(const T *row, int V) {
+        p = row;
+        const int mis = (int)(reinterpret_cast<uintptr_t>(row) & 15u);
+        head = mis ? min(V, (16 - mis) / (int)sizeof(T)) : 0;
+        nvec = (V - head) / E;
+        tail = V - head - nvec * E;
+        body = reinterpret_cast<const uint4 *>(row + head);
+    }
+    __device__ __forceinline__ int vec_index(int k) const { return head + k * E; }
+    // the element of the head or the tail that slot t (0 .. 2E-1) stands for, or -1
+    __device__ __forceinline__ int edge_index(int t) const {
+        if (t < head) return t;
+        if (t >= E && t - E < tail) return head + nvec * E + t - E;
+        return -1;
+    }
+};
+
+template <typename T>
+__device__ __forceinline__ float load1(const T *p) {
+    return Elem<T>::load(p);
+}
+
+// Loads of logits that the same kernel may overwrite (gradients in place):
+// ordered before later stores, and not through the read-only path.
+template <typename T>
+__device__ __forceinline__ float load1_rw(const T *p) {
+    if constexpr (sizeof(T) == 2) {
+        unsigned short h;
+        asm volatile("ld.global.u16 %0, [%1];" : "=h"(h) : "l"(p) : "memory");
+        return __uint_as_float((uint32_t)h << 16);
+    } else {
+        float f;
+        asm volatile("ld.global.f32 %0, [%1];" : "=f"(f) : "l"(p) : "memory");
+        return f;
+    }
+}
+
+// ---- running sum of 2^{(z - mr) sL} ------------------------------------------
+//
+// One thread's softmax sum against a lazy reference mr that moves only when a
+// chunk exceeds it by rs (8 processed nats), so that terms stay below e^8.
+// The exponent is one FMA, z sL - fl(mr sL); the rounding of mr sL is the
+// same factor on every term and is taken out with its exact value eps when
+// the reference moves and at the end.
+struct Sum {
+    float mr, mrL, eps, mrh;
+    float mx;   // largest logit seen
+    float S;
+};
+
+__device__ __forceinline__ Sum sum_init(float sL, float rs) {
+    Sum a;
+    a.mr = sv::kMaskFloor;
+    a.mrL = a.mr * sL;
+    a.eps = fmaf(a.mr, sL, -a.mrL);
+    a.mrh = a.mr + rs;
+    a.mx = neg_inf();
+    a.S = 0.f;
+    return a;
+}
+
+__device__ __forceinline__ void sum_move(Sum &a, float c, float sL, float rs) {
+    const float cL = c * sL, ce = fmaf(c, sL, -cL);
+    a.S *= ex2(fmaf(a.mr - c, sL, ce - a.eps));
+    a.mr = c;
+    a.mrL = cL;
+    a.eps = ce;
+    a.mrh = c + rs;
+}
+
+// E logits whose largest is c; entries of -inf add nothing
+template <int E>
+__device__ __forceinline__ void sum_add(Sum &a, const float (&z)[E], float c, float sL, float rs) {
+    if (c > a.mrh) sum_move(a, c, sL, rs);
+    a.mx = fmaxf(a.mx, c);
+    const float2 L2 = make_float2(sL, sL), ml = make_float2(-a.mrL, -a.mrL);
+    float2 e[E / 2];
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+        const float2 y = sv::pfma(make_float2(z[2 * j], z[2 * j + 1]), L2, ml);
+        e[j] = make_float2(ex2(y.x), ex2(y.y));
+    }
+#pragma unroll
+    for (int w = E / 4; w > 0; w >>= 1)
+#pragma unroll
+        for (int j = 0; j < w; ++j) e[j] = sv::padd(e[j], e[j + w]);
+    a.S += e[0].x + e[0].y;
+}
+
+__device__ __forceinline__ void sum_add1(Sum &a, float z, float sL, float rs) {
+    if (z > a.mrh) sum_move(a, z, sL, rs);
+    a.mx = fmaxf(a.mx, z);
+    a.S += ex2(fmaf(z, sL, -a.mrL));
+}
+
+// the sum against the row's maximum M
+__device__ __forceinline__ float sum_at(const Sum &a, float M, float sL) {
+    return a.mx > sv::kMaskFloor || a.S != 0.f ? a.S * ex2(fmaf(a.mr - M, sL, -a.eps)) : 0.f;
+}
+
+template <typename T>
+__device__ __forceinline__ float vec_max(const uint4 &w, const float (&z)[Elem<T>::kPerVec]) {
+    if constexpr (sizeof(T) == 2) {
+        const uint32_t m = sv::bmax2(sv::bmax2(w.x, w.y), sv::bmax2(w.z, w.w));
+        return fmaxf(sv::bf16_lo(m), sv::bf16_hi(m));
+    } else {
+        return fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    }
+}
+
+// ---- ordered keys --------------------------------------------------------------
+//
+// Larger logit, larger key; both zeros alike; masked logits (-inf, or below
+// -1e29: masks of a type's lowest value) and NaN are key 0.
+__device__ __forceinline__ uint32_t order_key(float z) {
+    if (!(z > sv::kMaskFloor)) return 0u;
+    const int i = __float_as_int(z + 0.f);
+    return i < 0 ? ~(uint32_t)i : (uint32_t)i | 0x80000000u;
+}
+
+__device__ __forceinline__ float key_value(uint32_t k) {
+    if (k == 0u) return neg_inf();
+    return __int_as_float(k & 0x80000000u ? (int)(k & 0x7fffffffu) : ~(int)k);
+}
+
+// a candidate: the logit's key over the complement of its index, so that the
+// larger word ranks first and equal logits rank by ascending index
+__device__ __forceinline__ unsigned long long cand(uint32_t key, int index) {
+    return ((unsigned long long)key << 32) | (uint32_t)~(uint32_t)index;
+}
+__device__ __forceinline__ int cand_index(unsigned long long c) { return (int)~(uint32_t)c; }
+__device__ __forceinline__ uint32_t cand_key(unsigned long long c) { return (uint32_t)(c >> 32); }
+
+// ---- block reductions (fixed order) ---------------------------------------------
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    return v;
+}
+
+// every thread gets the block's maximum; `buf`: NT / 32 floats, free to reuse
+// after the next barrier
+template <int NT>
+__device__ __forceinline__ float block_max(float v, float *buf) {
+    v = warp_max(v);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = buf[0];
+#pragma unroll
+    for (int i = 1; i < NT / 32; ++i) r = fmaxf(r, buf[i]);
+    return r;
+}
+template <int NT>
+__device__ __forceinline__ float block_sum(float v, float *buf) {
+    v = warp_sum(v);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+    __syncthreads();
+    float r = buf[0];
+#pragma unroll
+    for (int i = 1; i < NT / 32; ++i) r += buf[i];
+    return r;
+}
+
+// ---- host-side checks shared by the row operators --------------------------------
+
+int check_rows(const spec_rows_params *p, int max_m, int max_k);
+int check_strided(const char *name, const void *base, int64_t batch_stride, int64_t row_stride, int es, bool out, int B,
+                  int K, int V);
+
+}  // namespace sr
+
+// defined in spec_verify.cu: sets the thread-local message read by spec_last_error
+extern "C" int spec_internal_set_error(int code, const char *msg);

@@ -1,0 +1,344 @@
+"""Binding of the row operators of the C ABI (``include/spec_verify.h``): top
+log-probabilities, distillation of the draft, beam search.
+
+Argument marshalling only, like :mod:`.api`: tensors are checked for device,
+dtype, shape and strides, and every computation runs in the library's CUDA
+kernels on the current stream of the tensors' device (or ``stream``).
+
+Logits are ``[B, K, V]`` or ``[R, V]`` (K = 1), bfloat16 or float32, with a
+contiguous vocabulary axis and any other strides (0 repeats a row). ``status``
+is an int32 CUDA tensor of one element or None; the calls leave the largest
+device-side code there and never clear it.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional
+
+import torch
+
+from . import _native
+from .api import BF16, F32, SPEC_ERR_INVALID_ARG, SPEC_OK, SpecError
+
+MAX_TOP = 128
+MAX_BEAMS = 32
+MAX_BEAM_OUT = 64
+
+_DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+
+
+class _On:
+    """The device of ``t`` current, and ``stream`` too where one is given (so
+    that outputs are allocated on the stream that writes them)."""
+
+    __slots__ = ("ctx", "ptr")
+
+    def __init__(self, t: torch.Tensor, stream):
+        self.ctx = []
+        if t.device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(t.device))
+        if stream is not None:
+            if stream.device != t.device:
+                raise ValueError("stream must be a stream of the tensors' device")
+            self.ctx.append(torch.cuda.stream(stream))
+            self.ptr = stream.cuda_stream
+        else:
+            self.ptr = torch.cuda.current_stream(t.device).cuda_stream
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return self.ptr
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _check(rc: int):
+    if rc != SPEC_OK:
+        raise SpecError(rc, _native.last_error())
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _logits(z: torch.Tensor, name: str):
+    """(B, K, V, dtype code, batch stride, row stride) of a logits tensor."""
+    if not z.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dt = _DTYPES.get(z.dtype)
+    if dt is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {z.dtype}")
+    shape = z.shape
+    if len(shape) == 3:
+        B, K, V = shape
+        bs, rs, vs = z.stride()
+    elif len(shape) == 2:
+        (B, V), K = shape, 1
+        (bs, vs), rs = z.stride(), 0
+    else:
+        raise ValueError(f"{name} must be [B, K, V] or [R, V]")
+    if vs != 1 and V > 1:
+        raise ValueError(f"{name}: the vocabulary axis must be contiguous")
+    return B, K, V, dt, bs, rs
+
+
+def _tensor(t, name, dtype, shape, device, optional=True):
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is missing")
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on the logits' device")
+
+
+def _status(status, device):
+    if status is not None and (status.dtype != torch.int32 or status.numel() != 1 or status.device != device):
+        raise ValueError("status must be an int32 tensor of one element on the logits' device")
+
+
+def _out(out, name, dtype, shape, device):
+    t = None if out is None else out.get(name)
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _tensor(t, f"out['{name}']", dtype, torch.Size(shape), device)
+    return t
+
+
+def top_logprobs(logits: torch.Tensor, M: int, inv_temperature: float = 1.0, out: Optional[dict] = None,
+                 status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """The M (1..128) largest log-probabilities of every row
+    (spec_top_logprobs): a dict with ``logprobs`` [B,K,M] float32, descending,
+    ``ids`` [B,K,M] int32 and ``lse`` [B,K] float32 ([R,M] and [R] for [R,V]
+    logits). Unfilled places (masked tokens) are -inf and -1. ``out`` may hold
+    tensors to write into, under the same keys."""
+    B, K, V, dt, bs, rs = _logits(logits, "logits")
+    dev, lead = logits.device, tuple(logits.shape[:-1])
+    _status(status, dev)
+    p = _native.RowsParams(B, K, V, dt, M, 0, inv_temperature, 0, bs, rs)
+    if not 1 <= M <= MAX_TOP:
+        raise SpecError(2, f"top_logprobs: M must be in [1, {MAX_TOP}]")
+    with _On(logits, stream) as s:
+        lp = _out(out, "logprobs", torch.float32, lead + (M,), dev)
+        ids = _out(out, "ids", torch.int32, lead + (M,), dev)
+        lse = _out(out, "lse", torch.float32, lead, dev)
+        _check(_native.lib().spec_top_logprobs(ctypes.byref(p), logits.data_ptr(), lp.data_ptr(), ids.data_ptr(),
+                                               lse.data_ptr(), _addr(status), s))
+    return {"logprobs": lp, "ids": ids, "lse": lse}
+
+
+def _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status):
+    B, K, V, dt, bs, rs = _logits(logits, "logits")
+    dev, lead = logits.device, logits.shape[:-1]
+    M = logprobs.shape[-1] if logprobs.dim() else 0
+    _tensor(logprobs, "logprobs", torch.float32, lead + (M,), dev, optional=False)
+    _tensor(ids, "ids", torch.int32, lead + (M,), dev, optional=False)
+    _tensor(weight, "weight", torch.float32, lead, dev)
+    _status(status, dev)
+    return _native.RowsParams(B, K, V, dt, M, 1 if tail else 0, inv_temperature, 0, bs, rs), dev, lead
+
+
+def distill_loss(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor,
+                 weight: Optional[torch.Tensor] = None, inv_temperature: float = 1.0, tail: bool = True,
+                 out: Optional[dict] = None, status: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Distillation loss of the student's ``logits`` [B,K,V] from a teacher's
+    top list (spec_distill_loss): ``logprobs`` and ``ids`` [B,K,M] as
+    top_logprobs returns them, ``weight`` [B,K] or None (1). Returns ``loss``
+    [B,K] float32 and ``stats`` [B,K,4] float32, which distill_grad takes."""
+    p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
+    with _On(logits, stream) as s:
+        loss = _out(out, "loss", torch.float32, tuple(lead), dev)
+        stats = _out(out, "stats", torch.float32, tuple(lead) + (4,), dev)
+        _check(_native.lib().spec_distill_loss(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
+                                               _addr(weight), loss.data_ptr(), stats.data_ptr(), _addr(status), s))
+    return {"loss": loss, "stats": stats}
+
+
+def _dlogits(out, logits):
+    """The gradient's tensor and its two strides."""
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+    elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
+        raise ValueError("dlogits must have the logits' dtype, shape and device")
+    _, _, _, _, bs, rs = _logits(out, "dlogits")
+    return out, bs, rs
+
+
+def distill_grad(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor, stats: torch.Tensor,
+                 grad_loss: Optional[torch.Tensor] = None, weight: Optional[torch.Tensor] = None,
+                 inv_temperature: float = 1.0, tail: bool = True, out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Gradient of sum(grad_loss * loss) by the logits (spec_distill_grad),
+    from distill_loss's ``stats`` and the same other arguments; ``grad_loss``
+    [B,K] or None (1). ``out`` may be any tensor of the logits' shape and
+    dtype, the logits themselves too. Returns the gradient, which
+    ``logits.backward(gradient)`` takes on through the draft model."""
+    p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
+    _tensor(stats, "stats", torch.float32, lead + (4,), dev, optional=False)
+    _tensor(grad_loss, "grad_loss", torch.float32, lead, dev)
+    with _On(logits, stream) as s:
+        g, bs, rs = _dlogits(out, logits)
+        _check(_native.lib().spec_distill_grad(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
+                                               _addr(weight), stats.data_ptr(), _addr(grad_loss), g.data_ptr(), bs, rs,
+                                               _addr(status), s))
+    return g
+
+
+def distill_step(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor,
+                 weight: Optional[torch.Tensor] = None, inv_temperature: float = 1.0, tail: bool = True,
+                 out: Optional[dict] = None, status: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """Loss and gradient in one call (spec_distill_step): ``loss`` [B,K]
+    float32 and ``dlogits`` [B,K,V], the gradient of loss.sum(); scale it by
+    ``weight`` (a mean's 1/n, a loss scale). ``out['dlogits']`` may be the
+    logits themselves."""
+    p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
+    with _On(logits, stream) as s:
+        loss = _out(out, "loss", torch.float32, tuple(lead), dev)
+        g, bs, rs = _dlogits(None if out is None else out.get("dlogits"), logits)
+        _check(_native.lib().spec_distill_step(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
+                                               _addr(weight), loss.data_ptr(), g.data_ptr(), bs, rs, _addr(status), s))
+    return {"loss": loss, "dlogits": g}
+
+
+def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Optional[torch.Tensor] = None,
+              eos: int = -1, out: Optional[dict] = None, status: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+    """One step of beam search (spec_beam_step): the N best continuations of
+    the W beams of every sequence, from ``logits`` [B,W,V], cumulative
+    ``scores`` [B,W] float32 (-inf: no beam; at the first step all but one) and
+    ``finished`` [B,W] int32 or None. Returns ``scores`` [B,N] float32,
+    ``parent``, ``token`` and ``finished`` [B,N] int32. ``workspace`` is a
+    uint8 CUDA tensor of beam_workspace_size bytes or None (allocated for the
+    call on its stream)."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, W, V]")
+    B, W, V, dt, bs, rs = _logits(logits, "logits")
+    dev = logits.device
+    _tensor(scores, "scores", torch.float32, torch.Size((B, W)), dev, optional=False)
+    _tensor(finished, "finished", torch.int32, torch.Size((B, W)), dev)
+    _status(status, dev)
+    p = _native.RowsParams(B, W, V, dt, N, 0, 1.0, 0, bs, rs)
+    L = _native.lib()
+    nbytes = L.spec_beam_workspace_size(ctypes.byref(p))
+    if nbytes == 0:
+        raise SpecError(SPEC_ERR_INVALID_ARG, _native.last_error())
+    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
+    with _On(logits, stream) as s:
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        sc = _out(out, "scores", torch.float32, (B, N), dev)
+        par = _out(out, "parent", torch.int32, (B, N), dev)
+        tok = _out(out, "token", torch.int32, (B, N), dev)
+        fin = _out(out, "finished", torch.int32, (B, N), dev)
+        _check(L.spec_beam_step(ctypes.byref(p), logits.data_ptr(), scores.data_ptr(), _addr(finished), eos,
+                                sc.data_ptr(), par.data_ptr(), tok.data_ptr(), fin.data_ptr(), _addr(status),
+                                workspace.data_ptr(), workspace.numel(), s))
+    return {"scores": sc, "parent": par, "token": tok, "finished": fin}
+
+
+def beam_workspace_size(B: int, W: int, V: int, N: int) -> int:
+    """Bytes of workspace beam_step needs."""
+    p = _native.RowsParams(B, W, V, F32, N, 0, 1.0, 0, 0, 0)
+    n = _native.lib().spec_beam_workspace_size(ctypes.byref(p))
+    if n == 0:
+        raise SpecError(SPEC_ERR_INVALID_ARG, _native.last_error())
+    return int(n)
+
+
+def _merged(shape, stride):
+    """One (count, stride) for several axes, or None where they do not merge."""
+    n, st = 1, 0
+    for c, k in zip(reversed(shape), reversed(stride)):
+        if c == 1:
+            continue
+        if n > 1 and k != n * st:
+            return None
+        if n == 1:
+            st = k
+        n *= c
+    return n, st
+
+
+def _layout(t, batch_dim, length_dim, name):
+    shape, stride, es = t.shape, t.stride(), t.element_size()
+    outer = _merged(shape[:batch_dim], stride[:batch_dim])
+    seg = _merged(shape[batch_dim + 2:length_dim], stride[batch_dim + 2:length_dim])
+    unit = 1
+    for c, k in zip(reversed(shape[length_dim + 1:]), reversed(stride[length_dim + 1:])):
+        if c != 1 and k != unit:
+            raise ValueError(f"{name}: the axes after the length axis must be contiguous")
+        unit *= c
+    if shape[length_dim] > 1 and unit and stride[length_dim] != unit:
+        raise ValueError(f"{name}: the length axis must be contiguous with the axes after it")
+    if outer is None or seg is None:
+        raise ValueError(f"{name}: the axes before the batch, and those between beam and length, must each be "
+                         "evenly spaced")
+    st = [outer[1] * es, stride[batch_dim] * es, stride[batch_dim + 1] * es, seg[1] * es]
+    return outer[0], shape[batch_dim], shape[batch_dim + 1], seg[0], shape[length_dim], unit * es, st
+
+
+def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[torch.Tensor] = None,
+                 batch_dim: int = 0, length_dim: int = -2, out: Optional[torch.Tensor] = None,
+                 status: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """States in the order of the surviving beams (spec_beam_reorder): row
+    (..., b, n, ...) becomes row (..., b, parent[b, n], ...), ``parent`` [B,N]
+    int32, -1 leaves the row. Axis ``batch_dim`` is the sequence, the next one
+    the beam. With ``lengths`` [B] int32 only the first lengths[b] entries of
+    axis ``length_dim`` move. In place (``out`` None or ``state``), else into
+    ``out``, whose beam axis has N rows. Any dtype."""
+    if not state.is_cuda:
+        raise ValueError("state must be a CUDA tensor")
+    dst = state if out is None else out
+    nd, dev = state.dim(), state.device
+    if dst.dim() != nd or dst.dtype != state.dtype or dst.device != dev:
+        raise ValueError("out must have the state's dtype, device and number of axes")
+    bd = batch_dim + nd if batch_dim < 0 else batch_dim
+    if not 0 <= bd < nd - 1:
+        raise ValueError("state must have a batch and a beam axis")
+    if lengths is None:
+        ld = bd + 2
+        if ld == nd:   # [.., B, W]: one unit per row
+            state_v, dst_v = state.unsqueeze(-1), dst.unsqueeze(-1)
+        else:
+            state_v, dst_v = state, dst
+        if _try_layout(state_v, bd, ld) is None or _try_layout(dst_v, bd, ld) is None:
+            ld = state_v.dim() - 1   # rows of evenly spaced segments
+    else:
+        ld = length_dim + nd if length_dim < 0 else length_dim
+        if not bd + 2 <= ld < nd:
+            raise ValueError("length_dim must lie behind the beam axis")
+        state_v, dst_v = state, dst
+    O, B, W, H, T, unit, ss = _layout(state_v, bd, ld, "state")
+    O2, B2, N, H2, T2, unit2, ds = _layout(dst_v, bd, ld, "out")
+    want = list(state.shape)
+    want[bd + 1] = N
+    if list(dst.shape) != want:
+        raise ValueError("out must have the state's shape, but for the beam axis")
+    if parent.dim() != 2 or parent.shape[0] != B or (dst is not state and parent.shape[1] != N):
+        raise ValueError("parent must be int32 [B, N]")
+    N = parent.shape[1]
+    _tensor(parent, "parent", torch.int32, torch.Size((B, N)), dev, optional=False)
+    _tensor(lengths, "lengths", torch.int32, torch.Size((B,)), dev)
+    _status(status, dev)
+    if unit == 0:
+        return dst
+    p = _native.ReorderParams(O, B, W, N, H, T, unit)
+    p.src_stride[:] = ss
+    p.dst_stride[:] = ds
+    with _On(state, stream) as s:
+        _check(_native.lib().spec_beam_reorder(ctypes.byref(p), state.data_ptr(), dst.data_ptr(), parent.data_ptr(),
+                                               _addr(lengths), _addr(status), s))
+    return dst
+
+
+def _try_layout(t, bd, ld):
+    try:
+        return _layout(t, bd, ld, "")
+    except ValueError:
+        return None

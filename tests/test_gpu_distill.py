@@ -1,0 +1,265 @@
+"""Distillation loss and gradient on the GPU against the fp64 reference and
+against differences of it."""
+import numpy as np
+import pytest
+
+import rows_reference as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+INF = float("inf")
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _sv():
+    import speculative_decoding_token_verify_gb300 as sv
+    sv.build()
+    return sv
+
+
+def _case(B, K, V, M, dtype, seed, s=1.0, noise=1.0, sigma=3.0):
+    """A teacher's lists and a student some way off."""
+    g = torch.Generator().manual_seed(seed)
+    t = sigma * torch.randn((B, K, V), generator=g)
+    y = (t + noise * torch.randn((B, K, V), generator=g)).to(DT[dtype])
+    m = min(M, V)
+    lp, ids = torch.full((B, K, M), -INF), torch.full((B, K, M), -1, dtype=torch.int32)
+    val, at = torch.topk(t, m, dim=-1)
+    lp[..., :m] = s * val - torch.logsumexp(s * t, -1, keepdim=True)
+    ids[..., :m] = at.to(torch.int32)
+    w = torch.rand((B, K), generator=g) + 0.1
+    return y.to(DEV), lp.to(DEV), ids.to(DEV), w.to(DEV)
+
+
+def _check(y, lp, ids, w=None, s=1.0, tail=True, grad_loss=None, status_want=0):
+    """loss, stats, grad (from stats) and step against the reference."""
+    sv = _sv()
+    B, K, V = y.shape
+    bf16 = y.dtype == torch.bfloat16
+    kw = dict(weight=w, inv_temperature=s, tail=tail)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = {"loss": torch.full((B, K), 3.3e38, device=DEV), "stats": torch.full((B, K, 4), 3.3e38, device=DEV)}
+    a = sv.distill_loss(y, lp, ids, out=out, status=status, **kw)
+    g = sv.distill_grad(y, lp, ids, a["stats"], grad_loss, out=torch.full_like(y, 3e38), status=status, **kw)
+    step = sv.distill_step(y, lp, ids, out={"dlogits": torch.full_like(y, 3e38)}, status=status, **kw)
+    torch.cuda.synchronize()
+    assert int(status) == status_want
+    yn, lpn, idn = y.float().cpu().numpy(), lp.cpu().numpy(), ids.cpu().numpy()
+    wn = np.ones((B, K)) if w is None else w.cpu().numpy().astype(np.float64)
+    un = np.ones((B, K)) if grad_loss is None else grad_loss.cpu().numpy().astype(np.float64)
+    an = {k: v.cpu().numpy().astype(np.float64) for k, v in a.items()}
+    gn, sn = g.float().cpu().numpy().astype(np.float64), step["dlogits"].float().cpu().numpy().astype(np.float64)
+    sl = step["loss"].cpu().numpy()
+    for b in range(B):
+        for k in range(K):
+            r = ref.distill(yn[b, k], lpn[b, k], idn[b, k], wn[b, k], s, tail)
+            for got in (an["loss"][b, k], sl[b, k]):
+                if np.isfinite(r["loss"]):
+                    assert abs(got - r["loss"]) <= r["loss_tol"], (b, k, got, r["loss"])
+                else:
+                    assert got == r["loss"]
+            np.testing.assert_array_equal(np.isinf(an["stats"][b, k]), np.isinf(r["stats"]))
+            fin = np.isfinite(r["stats"])
+            off = np.abs(an["stats"][b, k][fin] - r["stats"][fin])
+            assert np.all(off <= r["stats_tol"][fin]), (an["stats"][b, k], r["stats"])
+            h = ref.half(bf16)
+            for got, up in ((gn[b, k], un[b, k]), (sn[b, k], 1.0)):
+                want, tol = r["grad"] * up, r["grad_tol"] * abs(up)
+                tol = tol + h * (np.abs(want) + tol)
+                bad = ~(np.abs(got - want) <= tol)
+                assert not bad.any(), (b, k, np.nonzero(bad)[0][:5], got[bad][:5], want[bad][:5], tol[bad][:5])
+    return a, g, step
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,K,V,M", [(2, 3, 1, 1), (2, 3, 2, 1), (1, 2, 7, 7), (3, 1, 9, 4), (2, 2, 33, 40),
+                                     (2, 3, 1000, 16), (1, 1, 4097, 128), (2, 2, 32001, 100), (40, 1, 5003, 50)])
+def test_against_reference(B, K, V, M, dtype, tail):
+    y, lp, ids, w = _case(B, K, V, M, dtype, B * 1000 + V + M)
+    _check(y, lp, ids, w, tail=tail, grad_loss=torch.rand((B, K), device=DEV) * 3)
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 128256), ("f32", 152064), ("bf16", 262147), ("f32", 300001)])
+@pytest.mark.parametrize("tail", [True, False])
+def test_long_rows(dtype, V, tail):
+    y, lp, ids, w = _case(1, 3, V, 64, dtype, V)
+    _check(y, lp, ids, w, tail=tail)
+
+
+def test_longest_row():
+    y, lp, ids, w = _case(1, 1, 1 << 20, 128, "f32", 1)
+    _check(y, lp, ids, w)
+    _check(y.to(torch.bfloat16), lp, ids, w)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows(dtype):
+    y, lp, ids, w = _case(300, 2, 2053, 20, dtype, 12)
+    w[::3] = 0
+    _check(y, lp, ids, w)
+
+
+@pytest.mark.parametrize("s", [0.1, 0.5, 2.0, 20.0])
+@pytest.mark.parametrize("tail", [True, False])
+def test_temperatures(s, tail):
+    for dtype in ("bf16", "f32"):
+        y, lp, ids, w = _case(2, 2, 3000, 30, dtype, 7, s=s)
+        _check(y, lp, ids, w, s=s, tail=tail)
+
+
+@pytest.mark.parametrize("tail", [True, False])
+def test_peaked_rows(tail):
+    """The list holds nearly all of the student's and the teacher's mass."""
+    y, lp, ids, w = _case(2, 3, 6000, 32, "f32", 8)
+    at = ids[..., 3:4].long()
+    y.scatter_(-1, at, 40.0)
+    lp[..., 0] = -1e-6
+    lp[..., 1:] -= 20.0
+    _check(y, lp, ids, w, tail=tail)
+
+
+@pytest.mark.parametrize("tail", [True, False])
+def test_lists_with_gaps_repeats_and_masks(tail):
+    for dtype in ("bf16", "f32"):
+        y, lp, ids, w = _case(3, 3, 2001, 24, dtype, 9)
+        ids[0, 0, ::2] = -1                       # gaps
+        ids[0, 1] = -1                            # an empty list
+        ids[0, 2, 5] = ids[0, 2, 2]               # a token twice
+        ids[1, 0, 1:] = ids[1, 0, 0]              # one token throughout
+        lp[1, 0] = -4.0
+        y[1, 1, ids[1, 1, 4].long()] = -INF       # a listed token the student masks
+        y[1, 2, ::3] = -INF                       # masked vocabulary
+        y[1, 2, ids[1, 2].long()] = 1.0
+        w[2, 0] = 0
+        y[2, 0] = float("nan")                    # not read
+        y[2, 1, 1::2] = -3.38e38
+        y[2, 1, ids[2, 1].long()] = 0.5
+        lp[2, 2, 20:] = -INF                      # probability zero
+        _check(y, lp, ids, w, tail=tail)
+
+
+def test_only_listed_tokens_have_mass():
+    y, lp, ids, w = _case(1, 2, 700, 10, "f32", 10)
+    keep = torch.zeros_like(y).scatter_(-1, ids.long(), 1.0)
+    y[keep == 0] = -INF
+    _check(y, lp, ids, w, tail=True)
+    _check(y, lp, ids, w, tail=False)
+
+
+def test_rows_and_ids_that_are_wrong():
+    sv = _sv()
+    y, lp, ids, w = _case(2, 2, 900, 10, "f32", 11)
+    ids2 = ids.clone()
+    ids2[0, 1, 3] = 900
+    ids2[1, 0, 0] = -7
+    _check(y, lp, ids2, w, status_want=sv.api.SPEC_ERR_BAD_TOKEN)
+    y2 = y.clone()
+    y2[1, 1] = -INF
+    _check(y2, lp, ids, w, status_want=sv.api.SPEC_ERR_BAD_ROW)
+    clean = sv.distill_step(y, lp, ids, w)
+    y2 = y.clone()
+    y2[0, 1, 5] = float("nan")
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = sv.distill_step(y2, lp, ids, w, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == sv.api.SPEC_ERR_BAD_ROW and not torch.isfinite(got["loss"][0, 1])
+    for b, k in ((0, 0), (1, 0), (1, 1)):
+        assert torch.equal(got["loss"][b, k], clean["loss"][b, k])
+        assert torch.equal(got["dlogits"][b, k], clean["dlogits"][b, k])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [1037, 40003])
+def test_strides_alignments_and_in_place(dtype, V):
+    """Every start of the rows and of the gradient's rows; a row's sum is added
+    in an order that its alignment sets, so bits are compared for one view."""
+    sv = _sv()
+    y, lp, ids, w = _case(3, 2, V, 20, dtype, 13)
+    for off in range(5):
+        wide = torch.full((3, 3, V + 9), 7.0, dtype=DT[dtype], device=DEV)
+        view = wide[:, 1:, off:off + V]
+        view.copy_(y)
+        a, gwant, want = _check(view, lp, ids, w)
+        stats = a["stats"]
+        for goff in (off, (off + 1) % 5):
+            gw = torch.full((3, 4, V + 11), 7.0, dtype=DT[dtype], device=DEV)
+            gv = gw[:, :2, goff:goff + V]
+            got = sv.distill_step(view, lp, ids, w, out={"dlogits": gv})
+            assert torch.equal(got["dlogits"], want["dlogits"]) and torch.equal(got["loss"], want["loss"])
+            gv.fill_(5.0)
+            sv.distill_grad(view, lp, ids, stats, weight=w, out=gv)
+            assert torch.equal(gv, gwant)
+            gv.fill_(7.0)
+            assert bool((gw == 7.0).all())          # nothing written beside the rows
+        sv.distill_step(view, lp, ids, w, out={"dlogits": view})
+        assert torch.equal(view, want["dlogits"])
+        view.copy_(y)
+        sv.distill_grad(view, lp, ids, stats, weight=w, out=view)
+        assert torch.equal(view, gwant)
+        view.fill_(7.0)
+        assert bool((wide == 7.0).all())
+    _check(y.transpose(0, 1).contiguous().transpose(0, 1), lp, ids, w)
+    _check(y[:1, :1].expand(3, 2, V), lp, ids, w)   # a repeated student row
+
+
+def test_gradient_against_differences():
+    """Central differences of the reference's loss, in fp64: the step h = 1e-5
+    leaves h^2 |f'''| / 6 < 1e-10 and 1e-16 * loss / h < 1e-10 per entry."""
+    sv = _sv()
+    for tail in (True, False):
+        y, lp, ids, w = _case(1, 1, 40, 6, "f32", 14)
+        got = sv.distill_step(y, lp, ids, w, inv_temperature=0.7, tail=tail)["dlogits"].cpu().numpy()[0, 0]
+        yn, l, i = y.cpu().double().numpy()[0, 0], lp.cpu().numpy()[0, 0], ids.cpu().numpy()[0, 0]
+        wt = float(w[0, 0])
+        r = ref.distill(yn, l, i, wt, 0.7, tail)
+        h = 1e-5
+        for v in range(40):
+            d = np.zeros(40)
+            d[v] = h
+            fd = (ref.distill(yn + d, l, i, wt, 0.7, tail)["loss"] - ref.distill(yn - d, l, i, wt, 0.7, tail)["loss"]) / (2 * h)
+            assert abs(fd - got[v]) <= 1e-8 + r["grad_tol"][v] + ref.U * abs(fd)
+
+
+def test_through_autograd():
+    """The gradient goes on through the draft model as logits.backward()."""
+    sv = _sv()
+    y, lp, ids, w = _case(2, 3, 500, 12, "f32", 15)
+    x = torch.randn((2, 3, 16), device=DEV)
+    head = torch.randn((500, 16), device=DEV, requires_grad=True)
+    logits = x @ head.t()
+    r = sv.distill_step(logits.detach(), lp, ids, w)
+    logits.backward(r["dlogits"])
+    want = torch.einsum("bkv,bkd->vd", r["dlogits"].double(), x.double())
+    err = (head.grad.double() - want).abs().max()
+    # at most 6 products per entry, summed in fp32 or tf32-free fp32
+    assert float(err) <= 8 * ref.U * float(torch.einsum("bkv,bkd->vd", r["dlogits"].double().abs(), x.double().abs()).max())
+
+
+def test_streams_graphs_and_repeats():
+    sv = _sv()
+    y, lp, ids, w = _case(4, 2, 20011, 30, "bf16", 16)
+    want = sv.distill_step(y, lp, ids, w)
+    again = sv.distill_step(y, lp, ids, w)
+    assert all(torch.equal(want[k], again[k]) for k in want)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = sv.distill_step(y, lp, ids, w, stream=s)
+    s.synchronize()
+    assert all(torch.equal(want[k], got[k]) for k in want)
+    yy = y.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        st = sv.distill_loss(yy, lp, ids, w)
+        gr = sv.distill_grad(yy, lp, ids, st["stats"], weight=w)
+        both = sv.distill_step(yy, lp, ids, w)
+    yy.zero_()
+    g.replay()
+    yy.copy_(y)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(both["dlogits"], want["dlogits"]) and torch.equal(st["loss"], want["loss"])
+    assert torch.equal(gr, sv.distill_grad(y, lp, ids, st["stats"], weight=w))
+    empty = sv.distill_step(y[:0], lp[:0], ids[:0], w[:0])
+    assert empty["dlogits"].shape == (0, 2, 20011)
