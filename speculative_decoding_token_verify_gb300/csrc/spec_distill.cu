@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a) {
             const uint4 v = __ldg(r.body + i);
             float z[E];
             Elem<T>::unpack(v, z);
-            float c = vec_max<T>(v, z);
+            float c = vec_max<T>(v);
             const uint32_t bits = s_map[(E * (i + 1)) >> 5] >> ((E * (i + 1)) & 31) & ((1u << E) - 1u);
             if (bits) {
 #pragma unroll
@@ -155,7 +155,8 @@ __global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a) {
 #pragma unroll
                 for (int j = 1; j < E; ++j) c = fmaxf(c, z[j]);
             }
-            sum_add<E>(acc, z, c, a.sL, a.resc);
+            sum_see(acc, c, a.sL, a.resc);
+            sum_put(acc, sum_terms<E>(acc, z, a.sL));
         }
         const float mo = block_max<NT>(acc.mx, fbuf[0]);
         const float So = block_sum<NT>(sum_at(acc, mo, a.sL), fbuf[1]);

@@ -76,14 +76,16 @@ __device__ __forceinline__ float load1_rw(const T *p) {
 // ---- running sum of 2^{(z - mr) sL} ------------------------------------------
 //
 // One thread's softmax sum against a lazy reference mr that moves only when a
-// chunk exceeds it by rs (8 processed nats), so that terms stay below e^8.
+// logit exceeds it by rs (8 processed nats), so that terms stay below e^8.
 // The exponent is one FMA, z sL - fl(mr sL); the rounding of mr sL is the
 // same factor on every term and is taken out with its exact value eps when
-// the reference moves and at the end.
+// the reference moves and at the end. Chunks of a few vectors are summed
+// apart and added with a compensation, so that a term meets at most about
+// twenty roundings on its way into the sum, however long the row.
 struct Sum {
     float mr, mrL, eps, mrh;
-    float mx;   // largest logit seen
-    float S;
+    float mx;      // largest logit seen
+    float S, lo;   // the sum is S - lo
 };
 
 __device__ __forceinline__ Sum sum_init(float sL, float rs) {
@@ -93,24 +95,28 @@ __device__ __forceinline__ Sum sum_init(float sL, float rs) {
     a.eps = fmaf(a.mr, sL, -a.mrL);
     a.mrh = a.mr + rs;
     a.mx = neg_inf();
-    a.S = 0.f;
+    a.S = a.lo = 0.f;
     return a;
 }
 
-__device__ __forceinline__ void sum_move(Sum &a, float c, float sL, float rs) {
-    const float cL = c * sL, ce = fmaf(c, sL, -cL);
-    a.S *= ex2(fmaf(a.mr - c, sL, ce - a.eps));
-    a.mr = c;
-    a.mrL = cL;
-    a.eps = ce;
-    a.mrh = c + rs;
+// before terms are added: c is the largest of their logits
+__device__ __forceinline__ void sum_see(Sum &a, float c, float sL, float rs) {
+    a.mx = fmaxf(a.mx, c);
+    if (c > a.mrh) {
+        const float cL = c * sL, ce = fmaf(c, sL, -cL);
+        const float al = ex2(fmaf(a.mr - c, sL, ce - a.eps));
+        a.S *= al;
+        a.lo *= al;
+        a.mr = c;
+        a.mrL = cL;
+        a.eps = ce;
+        a.mrh = c + rs;
+    }
 }
 
-// E logits whose largest is c; entries of -inf add nothing
+// E logits' terms; masked logits add nothing
 template <int E>
-__device__ __forceinline__ void sum_add(Sum &a, const float (&z)[E], float c, float sL, float rs) {
-    if (c > a.mrh) sum_move(a, c, sL, rs);
-    a.mx = fmaxf(a.mx, c);
+__device__ __forceinline__ float sum_terms(const Sum &a, const float (&z)[E], float sL) {
     const float2 L2 = make_float2(sL, sL), ml = make_float2(-a.mrL, -a.mrL);
     float2 e[E / 2];
 #pragma unroll
@@ -122,28 +128,43 @@ __device__ __forceinline__ void sum_add(Sum &a, const float (&z)[E], float c, fl
     for (int w = E / 4; w > 0; w >>= 1)
 #pragma unroll
         for (int j = 0; j < w; ++j) e[j] = sv::padd(e[j], e[j + w]);
-    a.S += e[0].x + e[0].y;
+    return e[0].x + e[0].y;
+}
+
+// a chunk's sum into the running one (Kahan)
+__device__ __forceinline__ void sum_put(Sum &a, float v) {
+    const float y = __fsub_rn(v, a.lo);
+    const float t = __fadd_rn(a.S, y);
+    a.lo = __fsub_rn(__fsub_rn(t, a.S), y);
+    a.S = t;
 }
 
 __device__ __forceinline__ void sum_add1(Sum &a, float z, float sL, float rs) {
-    if (z > a.mrh) sum_move(a, z, sL, rs);
-    a.mx = fmaxf(a.mx, z);
-    a.S += ex2(fmaf(z, sL, -a.mrL));
+    sum_see(a, z, sL, rs);
+    sum_put(a, ex2(fmaf(z, sL, -a.mrL)));
 }
 
-// the sum against the row's maximum M
+// the sum against the maximum M
 __device__ __forceinline__ float sum_at(const Sum &a, float M, float sL) {
-    return a.mx > sv::kMaskFloor || a.S != 0.f ? a.S * ex2(fmaf(a.mr - M, sL, -a.eps)) : 0.f;
+    const float S = a.S - a.lo;
+    return a.mx > sv::kMaskFloor || S != 0.f ? S * ex2(fmaf(a.mr - M, sL, -a.eps)) : 0.f;
 }
 
 template <typename T>
-__device__ __forceinline__ float vec_max(const uint4 &w, const float (&z)[Elem<T>::kPerVec]) {
+__device__ __forceinline__ float vec_max(const uint4 &w) {
     if constexpr (sizeof(T) == 2) {
         const uint32_t m = sv::bmax2(sv::bmax2(w.x, w.y), sv::bmax2(w.z, w.w));
         return fmaxf(sv::bf16_lo(m), sv::bf16_hi(m));
     } else {
-        return fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+        return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
     }
+}
+
+// a vector of masked logits
+template <typename T>
+__device__ __forceinline__ uint4 masked_vec() {
+    const uint32_t w = sizeof(T) == 2 ? 0xff80ff80u : 0xff800000u;
+    return make_uint4(w, w, w, w);
 }
 
 // ---- ordered keys --------------------------------------------------------------
@@ -203,6 +224,46 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 #pragma unroll
     for (int i = 1; i < NT / 32; ++i) r += buf[i];
     return r;
+}
+
+// ---- thread-block clusters ----------------------------------------------------------
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// the address of a shared variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t peer(const void *p, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store(uint32_t a, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ int peer_add(uint32_t a, int v) {
+    int r;
+    asm volatile("atom.relaxed.cluster.shared::cluster.add.s32 %0, [%1], %2;" : "=r"(r) : "r"(a), "r"(v) : "memory");
+    return r;
+}
+
+// Launch with clusters of `cluster` CTAs along x (1: none).
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, unsigned nt, unsigned cluster, size_t smem,
+                           cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(nt);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // ---- host-side checks shared by the row operators --------------------------------
