@@ -15,13 +15,22 @@
 // list's tokens are marked in a bit map of the row in shared memory, looked up
 // once per 16-byte vector. p_T = 1 - P is formed in fp64, as are the list's
 // terms of the loss: fp64 costs M exponentials per row beside V fp32 ones.
+//
+// Loss and step: a cluster of S CTAs per row, each a stretch of it; a CTA owns
+// the list's tokens in its stretch, and what the CTAs know (maxima, sums, P,
+// the loss's terms) meets in one exchange through distributed shared memory.
+// The step keeps the stretch in registers (U vectors a thread) across that
+// exchange, so the row is read once and its gradient written once; longer
+// rows keep their last U vectors a thread and read the others again, from L2.
+// The gradient alone needs no exchange: a CTA per NT U vectors.
 #include <mutex>
 
 #include "spec_rows.cuh"
 
 namespace sr {
 
-constexpr int NT = 512;
+constexpr int U = 8;   // vectors per thread
+constexpr int kMaxCluster = 8;
 
 struct DistillArgs {
     const void *y;
@@ -39,194 +48,464 @@ struct DistillArgs {
     int32_t *status;
 };
 
+// one rounding to nearest, the gradient's only one below fp32
 template <typename T>
-__device__ __forceinline__ T to_elem(float v);
-template <>
-__device__ __forceinline__ float to_elem<float>(float v) {
+__device__ __forceinline__ T to_elem(float v) {
+    if constexpr (sizeof(T) == 2) return __float2bfloat16_rn(v);
+    else return v;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t w;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
+    return w;
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_vec(const float (&z)[Elem<T>::kPerVec]) {
+    if constexpr (sizeof(T) == 2) return make_uint4(pack2(z[0], z[1]), pack2(z[2], z[3]), pack2(z[4], z[5]), pack2(z[6], z[7]));
+    else return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
+}
+
+// a CTA's part of a row: vectors [k0, k0 + n), the row's head in the first
+// part and its tail in the last, elements [e0, e1) in all
+template <typename T>
+struct Part {
+    static constexpr int E = Row<T>::E;
+    Row<T> r;
+    int k0, n, e0, e1;
+    bool first, last;
+    __device__ __forceinline__ Part(const T *row, int V, int rank, int parts)
+        : r(row, V), first(rank == 0), last(rank == parts - 1) {
+        k0 = (int)((long long)r.nvec * rank / parts);
+        n = (int)((long long)r.nvec * (rank + 1) / parts) - k0;
+        e0 = first ? 0 : r.vec_index(k0);
+        e1 = last ? V : r.vec_index(k0 + n);
+    }
+    // the head's or tail's element of slot t, or -1
+    __device__ __forceinline__ int edge(int t) const {
+        if (t >= 2 * E) return -1;
+        const int i = r.edge_index(t);
+        return i >= 0 && (t < E ? first : last) ? i : -1;
+    }
+    __device__ __forceinline__ const uint4 *body() const { return r.body + k0; }
+};
+
+// the part's map of listed tokens: bit 16 + 8 i or 16 + 4 i starts vector i,
+// the head lies before it and the tail behind the last vector
+template <typename T>
+__device__ __forceinline__ int map_bit(const Part<T> &p, int v) {
+    return v - p.r.vec_index(p.k0) + 16;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t map_vec(const uint8_t *map, int i) {
+    if constexpr (sizeof(T) == 2) return map[i + 2];
+    else return (uint32_t)map[(i + 4) >> 1] >> ((i & 1) * 4) & 15u;
+}
+
+// the gradient's part: vectors where both rows are aligned alike, else elements
+template <typename T>
+struct Out {
+    T *g;          // the row
+    uint4 *body;   // the part's first vector, or null
+    __device__ __forceinline__ Out(T *row, const Part<T> &p)
+        : g(row),
+          body(((reinterpret_cast<uintptr_t>(row) ^ reinterpret_cast<uintptr_t>(p.r.p)) & 15u) == 0
+                   ? reinterpret_cast<uint4 *>(row + p.r.vec_index(p.k0))
+                   : nullptr) {}
+    __device__ __forceinline__ void put(const Part<T> &p, int i, const float (&z)[Elem<T>::kPerVec]) const {
+        if (body) {
+            __stcs(body + i, pack_vec<T>(z));
+        } else {
+#pragma unroll
+            for (int j = 0; j < Elem<T>::kPerVec; ++j) g[p.r.vec_index(p.k0 + i) + j] = to_elem<T>(z[j]);
+        }
+    }
+};
+
+template <typename T, int NT>
+__device__ __forceinline__ void zero_part(const Part<T> &p, const Out<T> &o) {
+    float z[Part<T>::E];
+#pragma unroll
+    for (int j = 0; j < Part<T>::E; ++j) z[j] = 0.f;
+    for (int i = threadIdx.x; i < p.n; i += NT) o.put(p, i, z);
+    const int i = p.edge(threadIdx.x);
+    if (i >= 0) o.g[i] = to_elem<T>(0.f);
+}
+
+// ku e^{s (y - mo)} for the part's vector i; masked logits give 0
+template <typename T>
+__device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int i, const uint4 &w, float ku, float mo,
+                                         float sL) {
+    constexpr int E = Part<T>::E;
+    float z[E];
+    Elem<T>::unpack(w, z);
+#pragma unroll
+    for (int j = 0; j < E; ++j) z[j] = ku * ex2((fmaxf(z[j], sv::kMaskFloor) - mo) * sL);
+    o.put(p, i, z);
+}
+
+__device__ __forceinline__ uint4 ld_rw(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
     return v;
 }
-// one rounding to nearest, the gradient's only one below fp32
-template <>
-__device__ __forceinline__ __nv_bfloat16 to_elem<__nv_bfloat16>(float v) {
-    return __float2bfloat16_rn(v);
-}
 
-// bit of element v in the row's map: head and body keep a vector's bits in one word
-template <typename T>
-__device__ __forceinline__ int map_bit(const Row<T> &r, int v) {
-    return v - r.head + Row<T>::E;
-}
+// what a CTA knows of its part
+struct __align__(16) Known {
+    float mo, So;    // unlisted tokens: maximum, sum of 2^{(y - mo) sL}
+    float ml, Sl;    // listed tokens: the same, each once
+    double P, B;     // sum of p, and of p (l - s y)
+};
 
-template <typename T, bool kLoss, bool kGrad>
-__global__ void __launch_bounds__(NT) distill_kernel(DistillArgs a) {
-    constexpr int E = Row<T>::E;
-    extern __shared__ uint32_t s_map[];
-    __shared__ float fbuf[4][NT / 32];
-    __shared__ double dbuf[2][SPEC_MAX_TOP / 32];
-    __shared__ int s_ids[SPEC_MAX_TOP];
+template <typename T, bool kGrad, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S) {
+    constexpr int E = Row<T>::E, NW = NT / 32;
+    extern __shared__ __align__(16) uint8_t s_map[];
+    __shared__ float s_mx[2][NW], s_sm[2][NW];
+    __shared__ double s_d[2][NW];
+    __shared__ int s_ids[SPEC_MAX_TOP], s_dup;
     __shared__ float s_p[SPEC_MAX_TOP];
-    __shared__ float4 s_stats;
-    const int row = blockIdx.x, tid = threadIdx.x;
-    const int b = row / a.K, k = row - b * a.K;
-    const T *py = static_cast<const T *>(a.y) + b * a.bs + k * a.rs;
-    T *pg = kGrad ? static_cast<T *>(a.g) + b * a.gbs + k * a.grs : nullptr;
-    const Row<T> r(py, a.V);
+    __shared__ Known s_known[kMaxCluster];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = blockIdx.x / S, rank = blockIdx.x - row * S;
+    const int b = row / a.K, kr = row - b * a.K;
+    const T *py = static_cast<const T *>(a.y) + b * a.bs + kr * a.rs;
+    const Part<T> part(py, a.V, rank, S);
+    const int n = part.n, its = (n + U * NT - 1) / (U * NT);
+    const uint4 *body = part.body();
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {   // on their way during the list's work
+        const int i = u * NT + tid;
+        w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
+    }
 
-    float w = a.weight ? a.weight[row] : 1.f;
+    const float wt = a.weight ? a.weight[row] : 1.f;
     int id = -1;
     float lp = neg_inf();
     if (tid < a.M) {
         id = a.ids[(size_t)row * a.M + tid];
+        lp = a.logp[(size_t)row * a.M + tid];
         if (id >= a.V || id < -1) {
-            raise_status(a.status, SPEC_ERR_BAD_TOKEN);
+            if (rank == 0) raise_status(a.status, SPEC_ERR_BAD_TOKEN);
             id = -1;
         }
-        if (id >= 0) lp = a.logp[(size_t)row * a.M + tid];
     }
-    float4 st = make_float4(0.f, 0.f, 0.f, 0.f);
-    bool live = __syncthreads_or(id >= 0) && w != 0.f;
-    float up = w;   // the gradient's factor
-    if (kGrad && !kLoss) {
-        if (a.grad_loss) up *= a.grad_loss[row];
-        st = a.stats_in[row];
-        live = live && up != 0.f && st.y != 0.f;
-    }
-    auto dead_row = [&] {
-        if (kLoss && tid == 0) {
+    const uint32_t map_words = (16u + (uint32_t)E * n + 8u + 31u) / 32u;
+    for (uint32_t i = tid; i < (map_words + 3u) / 4u; i += NT) reinterpret_cast<uint4 *>(s_map)[i] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) s_dup = 0;
+    const bool live = __syncthreads_or(id >= 0) && wt != 0.f;
+    T *pg = kGrad ? static_cast<T *>(a.g) + b * a.gbs + kr * a.grs : nullptr;
+    const Out<T> out(kGrad ? pg : const_cast<T *>(py), part);
+    auto dead = [&] {
+        if (rank == 0 && tid == 0) {
             a.loss[row] = 0.f;
             if (a.stats_out) a.stats_out[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        if (kGrad)
-            for (int v = tid; v < a.V; v += NT) pg[v] = to_elem<T>(0.f);
+        if (kGrad) zero_part<T, NT>(part, out);
     };
-    if (!live) {
-        dead_row();
+    if (!live) {   // the whole cluster alike
+        dead();
         return;
     }
 
-    // the list: probabilities, their sum, the student's logits there
-    const double p64 = id >= 0 ? exp((double)lp) : 0.0;
-    double P = p64;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) P += __shfl_xor_sync(kFull, P, o);
-    if (tid < SPEC_MAX_TOP && (tid & 31) == 0) dbuf[0][tid >> 5] = P;
+    if (S > 1) cluster_arrive();   // waited for before the exchange: by then every CTA of the cluster runs
+
+    // the part's own entries of the list
+    const bool own = id >= part.e0 && id < part.e1;
+    if (!own) id = -1;
     if (tid < SPEC_MAX_TOP) s_ids[tid] = id;
-    if (kLoss)
-        for (int i = tid; i < (a.V + 2 * E + 31) / 32; i += NT) s_map[i] = 0u;
-    __syncthreads();
-    P = 0.0;
-    for (int i = 0; i < SPEC_MAX_TOP / 32; ++i) P += dbuf[0][i];
-    if (!a.tail && P == 0.0) {   // nothing to renormalise: an empty list
-        dead_row();
-        return;
+    float yl = neg_inf();
+    if (own) {
+        const int bit = map_bit(part, id);
+        const uint32_t m = 1u << (bit & 31);
+        if (atomicOr(reinterpret_cast<uint32_t *>(s_map) + (bit >> 5), m) & m) s_dup = 1;
+        yl = load1_rw(py + id);
     }
-    const double pn = a.tail ? p64 : p64 / P;
-    if (tid < SPEC_MAX_TOP) s_p[tid] = (float)pn;
-    const float yl = id >= 0 ? load1_rw(py + id) : neg_inf();
-    bool first = id >= 0;   // of the entries with this token
-    for (int i = 0; i < tid && i < a.M && first; ++i) first = s_ids[i] != id;
+    __syncthreads();
+    bool once = own;   // the first entry of its token
+    if (s_dup)
+        for (int i = 0; i < tid && i < a.M && once; ++i) once = s_ids[i] != id;
 
-    if (kLoss) {
-        if (id >= 0) {
-            const int bit = map_bit(r, id);
-            atomicOr(&s_map[bit >> 5], 1u << (bit & 31));
-        }
-        __syncthreads();
-        // unlisted tokens' sum, all tokens' maximum
-        Sum acc = sum_init(a.sL, a.resc);
-        if (tid < 2 * E) {
-            const int i = r.edge_index(tid);
-            if (i >= 0) {
-                const int bit = map_bit(r, i);
-                const float z = load1(py + i);
-                if (!(s_map[bit >> 5] >> (bit & 31) & 1u)) sum_add1(acc, z, a.sL, a.resc);
+    // the unlisted tokens' sum
+    Sum acc = sum_init(a.sL, a.resc);
+    for (int it = 0; it < its; ++it) {
+        if (it > 0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = (it * U + u) * NT + tid;
+                w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
             }
         }
-        for (int i = tid; i < r.nvec; i += NT) {
-            const uint4 v = __ldg(r.body + i);
+        uint32_t bits[U];
+        float cm = neg_inf();
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = (it * U + u) * NT + tid;
+            bits[u] = i < n ? map_vec<T>(s_map, i) : 0u;
+            float c = vec_max<T>(w[u]);
+            if (bits[u]) {
+                float z[E];
+                Elem<T>::unpack(w[u], z);
+                c = neg_inf();
+#pragma unroll
+                for (int j = 0; j < E; ++j) c = bits[u] >> j & 1u ? c : fmaxf(c, z[j]);
+            }
+            cm = fmaxf(cm, c);
+        }
+        sum_see(acc, cm, a.sL, a.resc);
+        float v = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
             float z[E];
-            Elem<T>::unpack(v, z);
-            float c = vec_max<T>(v);
-            const uint32_t bits = s_map[(E * (i + 1)) >> 5] >> ((E * (i + 1)) & 31) & ((1u << E) - 1u);
-            if (bits) {
+            Elem<T>::unpack(w[u], z);
+            if (bits[u]) {
 #pragma unroll
-                for (int j = 0; j < E; ++j) z[j] = bits >> j & 1u ? neg_inf() : z[j];
-                c = z[0];
+                for (int j = 0; j < E; ++j) z[j] = bits[u] >> j & 1u ? neg_inf() : z[j];
+            }
+            v += sum_terms<E>(acc, z, a.sL);
+        }
+        sum_put(acc, v);
+    }
+    const int ei = part.edge(tid);
+    const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
+    if (ei >= 0) {
+        const int bit = map_bit(part, ei);
+        if (!(s_map[bit >> 3] >> (bit & 7) & 1)) sum_add1(acc, ey, a.sL, a.resc);
+    }
+
+    // the part's maxima, then its sums
+    Known me;
+    {
+        const float x = warp_max(acc.mx), y = warp_max(yl);
+        if (lane == 0) {
+            s_mx[0][warp] = x;
+            s_mx[1][warp] = y;
+        }
+    }
+    const double p64 = own ? exp((double)lp) : 0.0;
+    double P = p64, B = p64 > 0.0 ? p64 * (yl > sv::kMaskFloor ? (double)lp - (double)a.s * (double)yl : INFINITY) : p64;
+    if (tid < SPEC_MAX_TOP) s_p[tid] = (float)p64;
+    if (warp < SPEC_MAX_TOP / 32) {
 #pragma unroll
-                for (int j = 1; j < E; ++j) c = fmaxf(c, z[j]);
-            }
-            sum_see(acc, c, a.sL, a.resc);
-            sum_put(acc, sum_terms<E>(acc, z, a.sL));
+        for (int o = 16; o > 0; o >>= 1) {
+            P += __shfl_xor_sync(kFull, P, o);
+            B += __shfl_xor_sync(kFull, B, o);
         }
-        const float mo = block_max<NT>(acc.mx, fbuf[0]);
-        const float So = block_sum<NT>(sum_at(acc, mo, a.sL), fbuf[1]);
-        const float mx = fmaxf(mo, block_max<NT>(yl, fbuf[2]));
-        const bool rest = mo > sv::kMaskFloor, some = mx > sv::kMaskFloor;
-        const float e = first && some ? ex2((yl - mx) * a.sL) : 0.f;
-        // a NaN among the unlisted stays in the sum
-        const float S = block_sum<NT>(e, fbuf[3]) + (rest ? So * ex2((mo - mx) * a.sL) : So);
-        // the list's terms
-        const double lnS = log((double)S);
-        double t = 0.0;
-        if (id >= 0 && pn > 0.0) {
-            const double lq = yl > sv::kMaskFloor ? (double)a.s * ((double)yl - (double)mx) - lnS : -INFINITY;
-            t = pn * ((a.tail ? (double)lp : (double)lp - log(P)) - lq);
+        if (lane == 0) {
+            s_d[0][warp] = P;
+            s_d[1][warp] = B;
         }
+    }
+    __syncthreads();
+    me.mo = s_mx[0][0];
+    me.ml = s_mx[1][0];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(kFull, t, o);
-        if (tid < SPEC_MAX_TOP && (tid & 31) == 0) dbuf[1][tid >> 5] = t;
-        __syncthreads();
-        if (tid == 0) {
-            double kl = 0.0;
-            for (int i = 0; i < SPEC_MAX_TOP / 32; ++i) kl += dbuf[1][i];
-            const double pT = a.tail ? fmax(0.0, 1.0 - P) : 0.0;
-            st = make_float4(mx, 1.f / S, neg_inf(), 0.f);
-            if (rest || So != 0.f) {
-                const double lqT = (double)a.s * ((double)mo - (double)mx) + log((double)So) - lnS;
-                if (pT > 0.0) kl += pT * (log(pT) - lqT);
-                st.z = mo;
-                st.w = (float)((exp(lqT) - pT) / (double)So);
-            }
-            if (!some || !(S > 0.f) || mx == -neg_inf()) raise_status(a.status, SPEC_ERR_BAD_ROW);
-            if (!some && S == 0.f) {   // no unmasked token
-                kl = INFINITY;
-                st = make_float4(0.f, 0.f, 0.f, 0.f);
-            }
-            a.loss[row] = w * (float)kl;
-            if (a.stats_out) a.stats_out[row] = st;
-            s_stats = st;
+    for (int i = 1; i < NW; ++i) {
+        me.mo = fmaxf(me.mo, s_mx[0][i]);
+        me.ml = fmaxf(me.ml, s_mx[1][i]);
+    }
+    {
+        const float x = warp_sum(sum_at(acc, me.mo, a.sL));
+        const float y = warp_sum(once && yl > sv::kMaskFloor ? ex2((yl - me.ml) * a.sL) : yl == yl ? 0.f : yl);
+        if (lane == 0) {
+            s_sm[0][warp] = x;
+            s_sm[1][warp] = y;
         }
-        __syncthreads();
-        st = s_stats;
+    }
+    __syncthreads();
+    if (warp == 0) {   // each lane one destination
+        me.So = me.Sl = 0.f;
+        for (int i = 0; i < NW; ++i) {
+            me.So += s_sm[0][i];
+            me.Sl += s_sm[1][i];
+        }
+        me.P = me.B = 0.0;
+        for (int i = 0; i < SPEC_MAX_TOP / 32; ++i) {
+            me.P += s_d[0][i];
+            me.B += s_d[1][i];
+        }
+        if (S > 1) {
+            cluster_wait();
+            if (lane < S) {
+                const uint32_t at = peer(&s_known[rank], lane);
+                const unsigned long long *v = reinterpret_cast<const unsigned long long *>(&me);
+#pragma unroll
+                for (int i = 0; i < (int)(sizeof(Known) / 8); ++i) peer_store(at + 8 * i, v[i]);
+            }
+        } else if (lane == 0) {
+            s_known[0] = me;
+        }
+    }
+    if (S > 1) {
+        if (warp != 0) cluster_wait();
+        cluster_arrive();
+        cluster_wait();
     } else {
         __syncthreads();
     }
 
+    // the row
+    float mo = neg_inf(), ml = neg_inf(), So = 0.f, Sl = 0.f;
+    P = 0.0;
+    for (int i = 0; i < S; ++i) {
+        mo = fmaxf(mo, s_known[i].mo);
+        ml = fmaxf(ml, s_known[i].ml);
+        P += s_known[i].P;
+    }
+    const float mx = fmaxf(mo, ml);
+    auto scaled = [&](float m, float sum, float to) { return sum != 0.f && m != to ? sum * ex2((m - to) * a.sL) : sum; };
+    for (int i = 0; i < S; ++i) {
+        So += scaled(s_known[i].mo, s_known[i].So, mo);
+        Sl += scaled(s_known[i].ml, s_known[i].Sl, mx);
+    }
+    if (!a.tail && P == 0.0) {   // nothing to renormalise: an empty list
+        dead();
+        return;
+    }
+    const bool some = mx > sv::kMaskFloor, rest = mo > sv::kMaskFloor || So != 0.f;
+    const float qo = scaled(mo, So, mx), Z = qo + Sl;
+    const double pT = a.tail ? fmax(0.0, 1.0 - P) : 0.0;
+    float4 st = make_float4(mx, 1.f / Z, mo, 0.f);
+    if (rest) st.w = (float)((double)qo / (double)Z - pT) / So;
+    else st.z = neg_inf();
+    const bool none = !some && Z == 0.f;   // no unmasked token
+    if (none) st = make_float4(0.f, 0.f, 0.f, 0.f);
+
     if (kGrad) {
-        const float us = up * a.s;
-        // listed: us (kl e^{s (y - m)} - p); unlisted: ku e^{s (y - m_o)}
-        const float kl = us * st.y * (a.tail && st.z == neg_inf() ? (float)P : 1.f), ku = us * st.w;
-        if (st.y == 0.f) {
-            for (int v = tid; v < a.V; v += NT) pg[v] = to_elem<T>(0.f);
-            return;
+        const float us = wt * a.s, ku = us * st.w, zo = rest ? mo : 0.f;
+        if (none) {
+            zero_part<T, NT>(part, out);
+        } else {
+            for (int it = its - 1; it >= 0; --it) {
+                if (it < its - 1) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        const int i = (it * U + u) * NT + tid;
+                        if (i < n) w[u] = ld_rw(body + i);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int i = (it * U + u) * NT + tid;
+                    if (i < n) grad_vec(part, out, i, w[u], ku, zo, a.sL);
+                }
+            }
+            if (ei >= 0) pg[ei] = to_elem<T>(ku * ex2((fmaxf(ey, sv::kMaskFloor) - zo) * a.sL));
+            __syncthreads();   // the listed tokens' values go over what was just written
+            if (once) {
+                const float norm = a.tail ? 1.f : (float)(1.0 / P);
+                float p = s_p[tid];
+                if (s_dup)
+                    for (int i = tid + 1; i < a.M; ++i) p += s_ids[i] == id ? s_p[i] : 0.f;
+                const float kl = us * st.y * (a.tail && !rest ? (float)P : 1.f);
+                const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - st.x) * a.sL) : 0.f;
+                pg[id] = to_elem<T>(fmaf(kl, q, -us * (p * norm)));
+            }
         }
-        for (int v = tid; v < a.V; v += NT) {
-            const float y = load1_rw(py + v);
-            pg[v] = to_elem<T>(ku * (y > sv::kMaskFloor ? ex2((y - st.z) * a.sL) : 0.f));
+    }
+    if (rank == 0 && tid == 0) {
+        double Bt = 0.0;
+        for (int i = 0; i < S; ++i) Bt += s_known[i].B;
+        const double lse = (double)a.s * (double)mx + log((double)Z);
+        double kl = a.tail ? Bt + P * lse : Bt / P - log(P) + lse;
+        if (rest && pT > 0.0) kl += pT * (log(pT) - ((double)a.s * (double)mo + log((double)So) - lse));
+        if (!some || !(Z > 0.f) || mx == -neg_inf()) raise_status(a.status, SPEC_ERR_BAD_ROW);
+        if (none) kl = INFINITY;
+        a.loss[row] = wt * (float)kl;
+        if (a.stats_out) a.stats_out[row] = st;
+    }
+}
+
+// the gradient from a row's statistics: a CTA per part of a row
+template <typename T, int NT>
+__global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
+    __shared__ int s_ids[SPEC_MAX_TOP];
+    __shared__ float s_p[SPEC_MAX_TOP];
+    __shared__ double s_d[SPEC_MAX_TOP / 32];
+    const int tid = threadIdx.x;
+    const int row = blockIdx.x / parts, rank = blockIdx.x - row * parts;
+    const int b = row / a.K, kr = row - b * a.K;
+    const T *py = static_cast<const T *>(a.y) + b * a.bs + kr * a.rs;
+    T *pg = static_cast<T *>(a.g) + b * a.gbs + kr * a.grs;
+    const Part<T> part(py, a.V, rank, parts);
+    const Out<T> out(pg, part);
+    const int n = part.n;
+    const uint4 *body = part.body();
+    const float4 st = a.stats_in[row];
+    const float us = (a.weight ? a.weight[row] : 1.f) * (a.grad_loss ? a.grad_loss[row] : 1.f) * a.s;
+    if (us == 0.f || st.y == 0.f) {
+        zero_part<T, NT>(part, out);
+        return;
+    }
+    uint4 w[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = u * NT + tid;
+        if (i < n) w[u] = ld_rw(body + i);
+    }
+    int id = -1;
+    float lp = neg_inf();
+    if (tid < a.M) {
+        id = a.ids[(size_t)row * a.M + tid];
+        lp = a.logp[(size_t)row * a.M + tid];
+        if (id >= a.V || id < -1) {
+            if (rank == 0) raise_status(a.status, SPEC_ERR_BAD_TOKEN);
+            id = -1;
         }
-        __syncthreads();   // the listed tokens' values go over what was just written
-        if (first) {
-            float p = 0.f;
-            for (int i = tid; i < a.M; ++i) p += s_ids[i] == id ? s_p[i] : 0.f;
-            const float q = yl > sv::kMaskFloor ? ex2((yl - st.x) * a.sL) : 0.f;
-            pg[id] = to_elem<T>(fmaf(kl, q, -us * p));
+    }
+    const bool own = id >= part.e0 && id < part.e1;
+    // the list's sum, where a factor needs it: every part sums the whole list
+    const bool need = !a.tail || st.z == neg_inf();
+    double P = 1.0;
+    float p = 0.f;
+    if (need) {
+        double x = id >= 0 ? exp((double)lp) : 0.0;
+        p = (float)x;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+        if (tid < SPEC_MAX_TOP && (tid & 31) == 0) s_d[tid >> 5] = x;
+        __syncthreads();
+        P = 0.0;
+        for (int i = 0; i < SPEC_MAX_TOP / 32; ++i) P += s_d[i];
+    } else if (own) {
+        p = (float)exp((double)lp);
+    }
+    if (tid < SPEC_MAX_TOP) {
+        s_ids[tid] = own ? id : -1;
+        s_p[tid] = p;
+    }
+    const float yl = own ? load1_rw(py + id) : neg_inf();
+    const int ei = part.edge(tid);
+    const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
+    __syncthreads();   // before anything is overwritten
+    const float ku = us * st.w, zo = st.z == neg_inf() ? 0.f : st.z;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = u * NT + tid;
+        if (i < n) grad_vec(part, out, i, w[u], ku, zo, a.sL);
+    }
+    if (ei >= 0) pg[ei] = to_elem<T>(ku * ex2((fmaxf(ey, sv::kMaskFloor) - zo) * a.sL));
+    __syncthreads();   // the listed tokens' values go over what was just written
+    if (own) {
+        bool once = true;
+        float sum = 0.f;
+        for (int i = 0; i < a.M; ++i)
+            if (s_ids[i] == id) {
+                if (i < tid) once = false;
+                sum += s_p[i];
+            }
+        if (once) {
+            const float kl = us * st.y * (a.tail && need ? (float)P : 1.f);
+            const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - st.x) * a.sL) : 0.f;
+            pg[id] = to_elem<T>(fmaf(kl, q, -us * (a.tail ? sum : sum * (float)(1.0 / P))));
         }
     }
 }
 
-template <typename T, bool kLoss, bool kGrad>
-cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
-    const size_t smem = kLoss ? ((size_t)a.V + 2 * Row<T>::E + 31) / 32 * 4 : 0;
+template <typename T, bool kGrad, int NT>
+static cudaError_t launch_distill(const DistillArgs &a, int S, cudaStream_t stream) {
+    const long long nvec = (long long)a.V / Row<T>::E / S + 1;
+    const size_t smem = (size_t)((16 + Row<T>::E * nvec + 8 + 31) / 32 + 4) / 4 * 16 + 16;
     if (smem > 40000) {
         static std::mutex mu;
         static bool done[64];
@@ -235,14 +514,33 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev & 63]) {
-            e = cudaFuncSetAttribute(distill_kernel<T, kLoss, kGrad>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     SPEC_MAX_V / 8 + 64);
+            e = cudaFuncSetAttribute(distill_kernel<T, kGrad, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     SPEC_MAX_V / 8 + 256);
             if (e != cudaSuccess) return e;
             done[dev & 63] = true;
         }
     }
-    distill_kernel<T, kLoss, kGrad><<<a.B * a.K, NT, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_cluster(distill_kernel<T, kGrad, NT>, (unsigned)((long long)a.B * a.K * S), NT, S, smem, stream, a, S);
+}
+
+template <typename T, bool kLoss, bool kGrad>
+cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
+    const long long rows = (long long)a.B * a.K, nvec = (long long)a.V / Row<T>::E;
+    if constexpr (!kLoss) {
+        const long long parts = nvec <= U * 256 ? 1 : (nvec + U * 256 - 1) / (U * 256);
+        if (rows * parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        grad_kernel<T, 256><<<(unsigned)(rows * parts), 256, 0, stream>>>(a, (int)parts);
+        return cudaGetLastError();
+    } else {
+        int S = 1;
+        if constexpr (kGrad) {
+            // the stretch in registers where a cluster can hold the row
+            while (S < kMaxCluster && nvec > (long long)S * U * 256) S *= 2;
+        }
+        while (S < kMaxCluster && rows * S * 2 <= 608 && nvec >= 2LL * S * 256) S *= 2;
+        if (kGrad && nvec > (long long)S * U * 256) return launch_distill<T, kGrad, 512>(a, S, stream);
+        return launch_distill<T, kGrad, 256>(a, S, stream);
+    }
 }
 
 template <bool kLoss, bool kGrad>

@@ -157,6 +157,7 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
         const float sc = a.scores[row];
         if (!(sc > neg_inf()) || sc == -neg_inf() || (a.finished && a.finished[row])) return;
     }
+    if (kCluster) cluster_arrive();   // waited for before the exchange: by then every CTA of the cluster runs
     const int b = row / a.K, kr = row - b * a.K;
     const Row<T> r(static_cast<const T *>(a.z) + b * a.batch_stride + kr * a.row_stride, a.V);
     const int k0 = kCluster ? (int)((long long)r.nvec * rank / S) : 0;
@@ -229,6 +230,7 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
     for (int i = tid; i < np; i += NT) best = fmaxf(best, s_c[i]);
     thr = block_bound(best, np, a.M, thr, s_b[2]);
     if (kCluster) {
+        cluster_wait();
         if (tid < S) {
             peer_store(peer(&s_x[0][rank], tid), thr);
             peer_store(peer(&s_x[1][rank], tid), mx);
