@@ -481,7 +481,8 @@ int spec_top_logprobs(const spec_rows_params *params, const void *logits, float 
  * spec_distill_step: loss and gradient (grad_loss = 1) in one call.
  * weight [B][K] f32 or NULL (1). dlogits may be the logits themselves
  * (in place, equal strides), and must not overlap them otherwise.
- * Precision: q and its sums in fp32, the list's terms in fp64.
+ * Precision: q and its sums in fp32, the list's sum P to 2e-10, the loss's
+ * terms added in fp64.
  */
 int spec_distill_loss(const spec_rows_params *params, const void *logits, const float *logprobs, const int32_t *ids,
                       const float *weight, float *loss, float *stats, int32_t *status, void *stream);

@@ -37,63 +37,6 @@ struct BeamArgs {
     int32_t *status;
 };
 
-// ---- two-float arithmetic: value = h + l ---------------------------------------
-
-__device__ __forceinline__ void two_sum(float a, float b, float &h, float &l) {
-    h = __fadd_rn(a, b);
-    const float t = __fsub_rn(h, a);
-    l = __fadd_rn(__fsub_rn(a, __fsub_rn(h, t)), __fsub_rn(b, t));
-}
-
-// e^x of x = z - M <= 0 as h + l, relative error about 2^-36: x = n ln2 + r with
-// ln2 in three floats, then e^r by its Taylor series, whose first terms carry
-// their roundings
-__device__ __forceinline__ void exp2f_of(float z, float M, float &h, float &l) {
-    float xh, xl;
-    two_sum(z, -M, xh, xl);
-    if (!(xh > -80.f)) {   // below 2e-35 of the maximum
-        h = l = 0.f;
-        return;
-    }
-    const float n = rintf(xh * kLog2e);
-    // ln2 = A + B + rest, A its first 12 bits, so that n A is exact
-    constexpr double kL = 0.69314718055994530942;
-    constexpr float A = (float)((double)(int)(kL * 4096.0) / 4096.0);
-    constexpr float B = (float)(kL - (double)A);
-    constexpr double kRest = kL - (double)A - (double)B;
-    float rh, rl, t;
-    two_sum(__fmaf_rn(-n, A, xh), xl, rh, rl);   // n A and the difference are exact
-    float nb = __fmul_rn(n, B), nbl = __fmaf_rn(n, B, -nb);
-    two_sum(rh, -nb, rh, t);
-    rl = rl + t - nbl - n * (float)kRest;
-    two_sum(rh, rl, rh, rl);
-    // e^r = 1 + r + r^2/2 + r^3 Q(r), |r| <= 0.35
-    const float r = rh;
-    float q = 1.f / 3628800.f;
-    q = fmaf(q, r, 1.f / 362880.f);
-    q = fmaf(q, r, 1.f / 40320.f);
-    q = fmaf(q, r, 1.f / 5040.f);
-    q = fmaf(q, r, 1.f / 720.f);
-    q = fmaf(q, r, 1.f / 120.f);
-    q = fmaf(q, r, 1.f / 24.f);
-    // r^3 (1/6 + r q): the leading 1/6 in two floats
-    const float r2 = __fmul_rn(r, r), r2l = __fmaf_rn(r, r, -r2);
-    const float r3 = __fmul_rn(r2, r), r3l = __fmaf_rn(r2, r, -r3) + r2l * r;
-    constexpr float s6 = 1.f / 6.f;
-    constexpr float s6l = (float)(1.0 / 6.0 - (double)s6);
-    const float c3 = __fmul_rn(r3, s6), c3l = __fmaf_rn(r3, s6, -c3) + r3l * s6 + r3 * s6l;
-    const float c4 = r2 * r2 * q;   // <= 6e-4: one rounding of 4e-11
-    float sh, sl, e1, e2, e3;
-    two_sum(1.f, r, sh, e1);
-    two_sum(sh, 0.5f * r2, sh, e2);
-    two_sum(sh, c3, sh, e3);
-    sl = e1 + e2 + e3 + (rl + r * rl + 0.5f * r2l + c3l + c4);
-    two_sum(sh, sl, sh, sl);
-    const float sc = __int_as_float(((int)n + 127) << 23);   // n >= -116
-    h = sh * sc;
-    l = sl * sc;
-}
-
 // ln of the row's sum against M, from two-float sums
 template <typename T>
 __device__ double precise_sum(const T *p, int V, float M, double *buf) {
@@ -101,7 +44,7 @@ __device__ double precise_sum(const T *p, int V, float M, double *buf) {
     float H = 0.f, L = 0.f;
     auto add = [&](float z) {
         float h, l, e;
-        exp2f_of(z, M, h, l);
+        exp_diff(z, M, h, l);
         two_sum(H, h, H, e);
         L += l + e;
     };

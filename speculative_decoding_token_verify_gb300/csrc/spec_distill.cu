@@ -131,15 +131,33 @@ __device__ __forceinline__ void zero_part(const Part<T> &p, const Out<T> &o) {
     if (i >= 0) o.g[i] = to_elem<T>(0.f);
 }
 
-// ku e^{s (y - mo)} for the part's vector i; masked logits give 0
+// The unlisted tokens' gradient ku e^{s (y - mo)} as ku2 2^{y sL - c}, c =
+// fl(mo sL) and its rounding in ku2: one FMA, one exponential, one product per
+// logit; masked logits give 0
+struct Factor {
+    float ku, c;
+};
+__device__ __forceinline__ Factor factor_of(float ku, float mo, float sL) {
+    const float c = mo * sL;
+    return {ku * ex2(-fmaf(mo, sL, -c)), c};
+}
+__device__ __forceinline__ float grad_one(const Factor &f, float y, float sL) { return f.ku * ex2(fmaf(y, sL, -f.c)); }
+
 template <typename T>
-__device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int i, const uint4 &w, float ku, float mo,
+__device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int i, const uint4 &w, const Factor &f,
                                          float sL) {
     constexpr int E = Part<T>::E;
     float z[E];
     Elem<T>::unpack(w, z);
+    const float2 L2 = make_float2(sL, sL), mc = make_float2(-f.c, -f.c), k2 = make_float2(f.ku, f.ku);
+    const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int j = 0; j < E; ++j) z[j] = ku * ex2((fmaxf(z[j], sv::kMaskFloor) - mo) * sL);
+    for (int j = 0; j < E / 2; ++j) {
+        const float2 y = sv::pfma(make_float2(z[2 * j], z[2 * j + 1]), L2, mc);
+        const float2 g = sv::pfma(make_float2(ex2(y.x), ex2(y.y)), k2, zero);
+        z[2 * j] = g.x;
+        z[2 * j + 1] = g.y;
+    }
     o.put(p, i, z);
 }
 
@@ -149,22 +167,53 @@ __device__ __forceinline__ uint4 ld_rw(const uint4 *p) {
     return v;
 }
 
-// what a CTA knows of its part
+// what a CTA knows of its part, and the row's total of it
 struct __align__(16) Known {
     float mo, So;    // unlisted tokens: maximum, sum of 2^{(y - mo) sL}
     float ml, Sl;    // listed tokens: the same, each once
     double P, B;     // sum of p, and of p (l - s y)
 };
 
+// a sum against m, moved to the larger maximum `to`
+__device__ __forceinline__ float moved(float sum, float m, float to, float sL) {
+    return sum != 0.f && m != to ? sum * ex2((m - to) * sL) : sum;
+}
+
+// the total over the first N lanes of a warp, N a power of two
+template <int N>
+__device__ __forceinline__ void known_total(Known &k, float sL) {
+#pragma unroll
+    for (int o = N / 2; o > 0; o >>= 1) {
+        const float mo = __shfl_xor_sync(kFull, k.mo, o), So = __shfl_xor_sync(kFull, k.So, o);
+        const float ml = __shfl_xor_sync(kFull, k.ml, o), Sl = __shfl_xor_sync(kFull, k.Sl, o);
+        const float a = fmaxf(k.mo, mo), c = fmaxf(k.ml, ml);
+        k.So = moved(k.So, k.mo, a, sL) + moved(So, mo, a, sL);
+        k.Sl = moved(k.Sl, k.ml, c, sL) + moved(Sl, ml, c, sL);
+        k.mo = a;
+        k.ml = c;
+        k.P += __shfl_xor_sync(kFull, k.P, o);
+        k.B += __shfl_xor_sync(kFull, k.B, o);
+    }
+}
+__device__ __forceinline__ Known known_nothing() { return {neg_inf(), 0.f, neg_inf(), 0.f, 0.0, 0.0}; }
+
+// what the gradient takes from the row's total
+struct Row2 {
+    float4 st;        // the statistics
+    float qscale;     // factor of a listed token's q (P where nothing is unlisted)
+    float norm;       // factor of p (1 / P with a renormalised list)
+    int rest, none;   // unlisted tokens with mass; no unmasked token at all
+    int empty;        // nothing to renormalise
+};
+
 template <typename T, bool kGrad, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S) {
     constexpr int E = Row<T>::E, NW = NT / 32;
     extern __shared__ __align__(16) uint8_t s_map[];
-    __shared__ float s_mx[2][NW], s_sm[2][NW];
-    __shared__ double s_d[2][NW];
     __shared__ int s_ids[SPEC_MAX_TOP], s_dup;
     __shared__ float s_p[SPEC_MAX_TOP];
-    __shared__ Known s_known[kMaxCluster];
+    __shared__ Known s_warp[NW], s_known[kMaxCluster];
+    __shared__ Row2 s_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / S, rank = blockIdx.x - row * S;
     const int b = row / a.K, kr = row - b * a.K;
@@ -273,146 +322,117 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         if (!(s_map[bit >> 3] >> (bit & 7) & 1)) sum_add1(acc, ey, a.sL, a.resc);
     }
 
-    // the part's maxima, then its sums
-    Known me;
+    // every warp's part, the CTA's, the row's
     {
-        const float x = warp_max(acc.mx), y = warp_max(yl);
-        if (lane == 0) {
-            s_mx[0][warp] = x;
-            s_mx[1][warp] = y;
-        }
-    }
-    const double p64 = own ? exp((double)lp) : 0.0;
-    double P = p64, B = p64 > 0.0 ? p64 * (yl > sv::kMaskFloor ? (double)lp - (double)a.s * (double)yl : INFINITY) : p64;
-    if (tid < SPEC_MAX_TOP) s_p[tid] = (float)p64;
-    if (warp < SPEC_MAX_TOP / 32) {
+        Known k = known_nothing();
+        k.mo = warp_max(acc.mx);
+        k.So = warp_sum(sum_at(acc, k.mo, a.sL));
+        if (warp < SPEC_MAX_TOP / 32) {
+            float ph = 0.f, pl = 0.f;
+            if (own) exp_diff(lp, 0.f, ph, pl);
+            s_p[tid] = ph;
+            const bool there = yl > sv::kMaskFloor;
+            k.ml = warp_max(yl);
+            k.Sl = warp_sum(once ? (there ? ex2((yl - k.ml) * a.sL) : yl == yl ? 0.f : yl) : 0.f);
+            k.P = (double)ph + (double)pl;
+            k.B = own && lp > -700.f ? (there ? k.P * ((double)lp - (double)a.s * (double)yl) : INFINITY) : k.P;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            P += __shfl_xor_sync(kFull, P, o);
-            B += __shfl_xor_sync(kFull, B, o);
+            for (int o = 16; o > 0; o >>= 1) {
+                k.P += __shfl_xor_sync(kFull, k.P, o);
+                k.B += __shfl_xor_sync(kFull, k.B, o);
+            }
         }
-        if (lane == 0) {
-            s_d[0][warp] = P;
-            s_d[1][warp] = B;
-        }
+        if (lane == 0) s_warp[warp] = k;
     }
     __syncthreads();
-    me.mo = s_mx[0][0];
-    me.ml = s_mx[1][0];
-#pragma unroll
-    for (int i = 1; i < NW; ++i) {
-        me.mo = fmaxf(me.mo, s_mx[0][i]);
-        me.ml = fmaxf(me.ml, s_mx[1][i]);
-    }
-    {
-        const float x = warp_sum(sum_at(acc, me.mo, a.sL));
-        const float y = warp_sum(once && yl > sv::kMaskFloor ? ex2((yl - me.ml) * a.sL) : yl == yl ? 0.f : yl);
-        if (lane == 0) {
-            s_sm[0][warp] = x;
-            s_sm[1][warp] = y;
-        }
-    }
-    __syncthreads();
-    if (warp == 0) {   // each lane one destination
-        me.So = me.Sl = 0.f;
-        for (int i = 0; i < NW; ++i) {
-            me.So += s_sm[0][i];
-            me.Sl += s_sm[1][i];
-        }
-        me.P = me.B = 0.0;
-        for (int i = 0; i < SPEC_MAX_TOP / 32; ++i) {
-            me.P += s_d[0][i];
-            me.B += s_d[1][i];
-        }
+    Known all = known_nothing();
+    if (warp == 0) {
+        if (lane < NW) all = s_warp[lane];
+        known_total<NW>(all, a.sL);
         if (S > 1) {
             cluster_wait();
-            if (lane < S) {
+            if (lane < S) {   // each lane one destination
                 const uint32_t at = peer(&s_known[rank], lane);
-                const unsigned long long *v = reinterpret_cast<const unsigned long long *>(&me);
+                const unsigned long long *v = reinterpret_cast<const unsigned long long *>(&all);
 #pragma unroll
                 for (int i = 0; i < (int)(sizeof(Known) / 8); ++i) peer_store(at + 8 * i, v[i]);
             }
-        } else if (lane == 0) {
-            s_known[0] = me;
         }
     }
     if (S > 1) {
         if (warp != 0) cluster_wait();
         cluster_arrive();
         cluster_wait();
-    } else {
-        __syncthreads();
+        if (warp == 0) {
+            all = known_nothing();
+            if (lane < S) all = s_known[lane];
+            known_total<kMaxCluster>(all, a.sL);
+        }
     }
-
-    // the row
-    float mo = neg_inf(), ml = neg_inf(), So = 0.f, Sl = 0.f;
-    P = 0.0;
-    for (int i = 0; i < S; ++i) {
-        mo = fmaxf(mo, s_known[i].mo);
-        ml = fmaxf(ml, s_known[i].ml);
-        P += s_known[i].P;
-    }
-    const float mx = fmaxf(mo, ml);
-    auto scaled = [&](float m, float sum, float to) { return sum != 0.f && m != to ? sum * ex2((m - to) * a.sL) : sum; };
-    for (int i = 0; i < S; ++i) {
-        So += scaled(s_known[i].mo, s_known[i].So, mo);
-        Sl += scaled(s_known[i].ml, s_known[i].Sl, mx);
-    }
-    if (!a.tail && P == 0.0) {   // nothing to renormalise: an empty list
-        dead();
-        return;
-    }
-    const bool some = mx > sv::kMaskFloor, rest = mo > sv::kMaskFloor || So != 0.f;
-    const float qo = scaled(mo, So, mx), Z = qo + Sl;
-    const double pT = a.tail ? fmax(0.0, 1.0 - P) : 0.0;
-    float4 st = make_float4(mx, 1.f / Z, mo, 0.f);
-    if (rest) st.w = (float)((double)qo / (double)Z - pT) / So;
-    else st.z = neg_inf();
-    const bool none = !some && Z == 0.f;   // no unmasked token
-    if (none) st = make_float4(0.f, 0.f, 0.f, 0.f);
-
-    if (kGrad) {
-        const float us = wt * a.s, ku = us * st.w, zo = rest ? mo : 0.f;
-        if (none) {
-            zero_part<T, NT>(part, out);
-        } else {
-            for (int it = its - 1; it >= 0; --it) {
-                if (it < its - 1) {
-#pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        const int i = (it * U + u) * NT + tid;
-                        if (i < n) w[u] = ld_rw(body + i);
-                    }
-                }
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int i = (it * U + u) * NT + tid;
-                    if (i < n) grad_vec(part, out, i, w[u], ku, zo, a.sL);
-                }
-            }
-            if (ei >= 0) pg[ei] = to_elem<T>(ku * ex2((fmaxf(ey, sv::kMaskFloor) - zo) * a.sL));
-            __syncthreads();   // the listed tokens' values go over what was just written
-            if (once) {
-                const float norm = a.tail ? 1.f : (float)(1.0 / P);
-                float p = s_p[tid];
-                if (s_dup)
-                    for (int i = tid + 1; i < a.M; ++i) p += s_ids[i] == id ? s_p[i] : 0.f;
-                const float kl = us * st.y * (a.tail && !rest ? (float)P : 1.f);
-                const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - st.x) * a.sL) : 0.f;
-                pg[id] = to_elem<T>(fmaf(kl, q, -us * (p * norm)));
+    if (warp == 0) {
+        const float mx = fmaxf(all.mo, all.ml);
+        const float qo = moved(all.So, all.mo, mx, a.sL), Z = qo + moved(all.Sl, all.ml, mx, a.sL);
+        Row2 r2;
+        r2.rest = all.mo > sv::kMaskFloor || all.So != 0.f;
+        r2.none = !(mx > sv::kMaskFloor) && Z == 0.f;
+        r2.empty = !a.tail && all.P == 0.0;
+        const float pT = a.tail ? (float)fmax(0.0, 1.0 - all.P) : 0.f;
+        r2.st = make_float4(mx, 1.f / Z, all.mo, 0.f);
+        if (r2.rest) r2.st.w = (qo / Z - pT) / all.So;
+        else r2.st.z = neg_inf();
+        if (r2.none) r2.st = make_float4(0.f, 0.f, 0.f, 0.f);
+        r2.qscale = a.tail && !r2.rest ? (float)all.P : 1.f;
+        r2.norm = a.tail ? 1.f : 1.f / (float)all.P;
+        if (lane == 0) s_row = r2;
+        if (rank == 0 && lane == 0) {
+            if (r2.empty) {
+                a.loss[row] = 0.f;
+                if (a.stats_out) a.stats_out[row] = make_float4(0.f, 0.f, 0.f, 0.f);
+            } else {
+                const double lse = (double)a.s * (double)mx + log((double)Z);
+                double kl = a.tail ? all.B + all.P * lse : all.B / all.P - log(all.P) + lse;
+                // ln(p_T / q_T), by parts where q_T is below fp32's range
+                if (r2.rest && pT > 0.f)
+                    kl += (double)pT * (qo > 1e-30f ? (double)logf(pT * (Z / qo))
+                                                    : (double)logf(pT * Z / all.So) + (double)a.s * ((double)mx - (double)all.mo));
+                if (!(mx > sv::kMaskFloor) || !(Z > 0.f) || mx == -neg_inf()) raise_status(a.status, SPEC_ERR_BAD_ROW);
+                if (r2.none) kl = INFINITY;
+                a.loss[row] = wt * (float)kl;
+                if (a.stats_out) a.stats_out[row] = r2.st;
             }
         }
     }
-    if (rank == 0 && tid == 0) {
-        double Bt = 0.0;
-        for (int i = 0; i < S; ++i) Bt += s_known[i].B;
-        const double lse = (double)a.s * (double)mx + log((double)Z);
-        double kl = a.tail ? Bt + P * lse : Bt / P - log(P) + lse;
-        if (rest && pT > 0.0) kl += pT * (log(pT) - ((double)a.s * (double)mo + log((double)So) - lse));
-        if (!some || !(Z > 0.f) || mx == -neg_inf()) raise_status(a.status, SPEC_ERR_BAD_ROW);
-        if (none) kl = INFINITY;
-        a.loss[row] = wt * (float)kl;
-        if (a.stats_out) a.stats_out[row] = st;
+    if (!kGrad) return;
+    __syncthreads();
+    const Row2 r2 = s_row;
+    if (r2.empty || r2.none) {
+        zero_part<T, NT>(part, out);
+        return;
+    }
+    const float us = wt * a.s;
+    const Factor f = factor_of(us * r2.st.w, r2.rest ? r2.st.z : 0.f, a.sL);
+    for (int it = its - 1; it >= 0; --it) {
+        if (it < its - 1) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int i = (it * U + u) * NT + tid;
+                if (i < n) w[u] = ld_rw(body + i);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = (it * U + u) * NT + tid;
+            if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
+        }
+    }
+    if (ei >= 0) pg[ei] = to_elem<T>(grad_one(f, ey, a.sL));
+    __syncthreads();   // the listed tokens' values go over what was just written
+    if (once) {
+        float p = s_p[tid];
+        if (s_dup)
+            for (int i = tid + 1; i < a.M; ++i) p += s_ids[i] == id ? s_p[i] : 0.f;
+        const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - r2.st.x) * a.sL) : 0.f;
+        pg[id] = to_elem<T>(fmaf(us * r2.st.y * r2.qscale, q, -us * (p * r2.norm)));
     }
 }
 
@@ -459,8 +479,10 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     double P = 1.0;
     float p = 0.f;
     if (need) {
-        double x = id >= 0 ? exp((double)lp) : 0.0;
-        p = (float)x;
+        float h = 0.f, l = 0.f;
+        if (id >= 0) exp_diff(lp, 0.f, h, l);
+        p = h;
+        double x = (double)h + (double)l;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
         if (tid < SPEC_MAX_TOP && (tid & 31) == 0) s_d[tid >> 5] = x;
@@ -468,7 +490,8 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
         P = 0.0;
         for (int i = 0; i < SPEC_MAX_TOP / 32; ++i) P += s_d[i];
     } else if (own) {
-        p = (float)exp((double)lp);
+        float l;
+        exp_diff(lp, 0.f, p, l);
     }
     if (tid < SPEC_MAX_TOP) {
         s_ids[tid] = own ? id : -1;
@@ -478,13 +501,13 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     const int ei = part.edge(tid);
     const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
     __syncthreads();   // before anything is overwritten
-    const float ku = us * st.w, zo = st.z == neg_inf() ? 0.f : st.z;
+    const Factor f = factor_of(us * st.w, st.z == neg_inf() ? 0.f : st.z, a.sL);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int i = u * NT + tid;
-        if (i < n) grad_vec(part, out, i, w[u], ku, zo, a.sL);
+        if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
     }
-    if (ei >= 0) pg[ei] = to_elem<T>(ku * ex2((fmaxf(ey, sv::kMaskFloor) - zo) * a.sL));
+    if (ei >= 0) pg[ei] = to_elem<T>(grad_one(f, ey, a.sL));
     __syncthreads();   // the listed tokens' values go over what was just written
     if (own) {
         bool once = true;

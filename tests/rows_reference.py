@@ -6,10 +6,16 @@ DS = 4e-6: an exponential's own error (2^-22), its argument's rounding, and
 the additions on a term's way into the sum (at most 32, each 2^-24 of the
 partial sum). An argument y = (z - M) s log2e carries two roundings, so an
 exponential of its own (a gradient's q) is off by |y| 2^-23 ln 2 besides.
+The list's sum P is formed from exponentials of relative error DP = 2e-10, and
+p_T = 1 - P is off by DP P: e^r, |r| <= 0.35, is summed as 1 + r + r^2/2 + r^3/6
+with every rounding carried, and r^4 Q(r) <= 6.3e-4 in plain fp32, of at most
+four roundings (its factors r^2, r^4, Q and the product): 6.3e-4 * 4 * 2^-24 =
+1.5e-10; the reduced argument and the final sum add less than 1e-11.
 U = 2^-24 is half a step of fp32 and `half(dtype)` that of the output."""
 import numpy as np
 
 DS = 4e-6
+DP = 2e-10
 U = 2.0 ** -24
 FLOOR = -1e29   # logits below count as masked
 
@@ -79,7 +85,7 @@ def distill(y, lp, ids, w=1.0, s=1.0, tail=True, up=1.0):
     kl = float((pn[pos] * (ln[pos] - lq[ids[pos]])).sum())
     target = np.zeros(V)
     np.add.at(target, ids, pn)
-    g, gt = q.copy(), np.zeros(V)
+    g, gt, kl_tol = q.copy(), np.zeros(V), 0.0
     inv = np.exp(s * m - L)
     stats, st = np.array([m, inv, -np.inf, 0.0]), np.array([0.0, inv * (DS + 2 * U), 0.0, 0.0])
 
@@ -95,6 +101,9 @@ def distill(y, lp, ids, w=1.0, s=1.0, tail=True, up=1.0):
         excess = qT - pT
         # q_T: two sums, and the exponential between the two maxima
         et = qT * (2 * DS + 4 * U * abs(s * (m - mo)))
+        if pT > 0:   # and the list's sum
+            et += DP * P
+            kl_tol += DP * P * (1 + abs(np.log(pT) - (Lo - L)))
         g = np.where(out, excess * r, q)
         gt = r * (et + abs(excess) * (DS + 2 * U * arg(y, mo) + 2.0 ** -22 + 8 * U))
         k = np.exp(s * mo - Lo)
@@ -105,7 +114,7 @@ def distill(y, lp, ids, w=1.0, s=1.0, tail=True, up=1.0):
     # listed: q's sum, argument and products, and p's rounding
     gt = np.where(out, gt, q * max(1.0, P) * (DS + 2 * U * arg(y, m) + 2.0 ** -22 + 8 * U) + 6 * U * target)
     f = abs(w * up * s)
-    return dict(loss=w * kl, loss_tol=abs(w) * (3 * DS + 4 * U * abs(kl)) if np.isfinite(kl) else 0.0, stats=stats,
+    return dict(loss=w * kl, loss_tol=abs(w) * (3 * DS + 4 * U * abs(kl) + kl_tol) if np.isfinite(kl) else 0.0, stats=stats,
                 stats_tol=st, grad=w * up * s * g, grad_tol=f * gt + 1e-37 * (1 + f))
 
 
