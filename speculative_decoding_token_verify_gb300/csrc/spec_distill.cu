@@ -29,8 +29,12 @@
 
 namespace sr {
 
-constexpr int U = 8;   // vectors per thread
+constexpr int UG = 8;   // vectors per thread of the gradient alone
 constexpr int kMaxCluster = 8;
+#ifndef STEP_U
+#define STEP_U 8
+#define STEP_NT 256
+#endif
 
 struct DistillArgs {
     const void *y;
@@ -171,12 +175,24 @@ __device__ __forceinline__ uint4 ld_rw(const uint4 *p) {
 struct __align__(16) Known {
     float mo, So;    // unlisted tokens: maximum, sum of 2^{(y - mo) sL}
     float ml, Sl;    // listed tokens: the same, each once
-    double P, B;     // sum of p, and of p (l - s y)
+    float Ph, Pl;    // sum of p, in two floats
+    float Bh, Bl;    // sum of p (l - s y), in two floats
 };
 
 // a sum against m, moved to the larger maximum `to`
 __device__ __forceinline__ float moved(float sum, float m, float to, float sL) {
     return sum != 0.f && m != to ? sum * ex2((m - to) * sL) : sum;
+}
+
+// a two-float sum with the lane o away; both lanes get the same bits
+__device__ __forceinline__ void pair_total(float &h, float &l, int o) {
+    const float a = __shfl_xor_sync(kFull, h, o), b = __shfl_xor_sync(kFull, l, o);
+    float e;
+    const bool big = fabsf(h) >= fabsf(a);   // one order in both lanes
+    const float x = big ? h : a, y = big ? a : h;
+    h = __fadd_rn(x, y);
+    e = __fsub_rn(y, __fsub_rn(h, x));
+    l = fabsf(h) < INFINITY ? (l + b) + e : 0.f;
 }
 
 // the total over the first N lanes of a warp, N a power of two
@@ -191,11 +207,11 @@ __device__ __forceinline__ void known_total(Known &k, float sL) {
         k.Sl = moved(k.Sl, k.ml, c, sL) + moved(Sl, ml, c, sL);
         k.mo = a;
         k.ml = c;
-        k.P += __shfl_xor_sync(kFull, k.P, o);
-        k.B += __shfl_xor_sync(kFull, k.B, o);
+        pair_total(k.Ph, k.Pl, o);
+        pair_total(k.Bh, k.Bl, o);
     }
 }
-__device__ __forceinline__ Known known_nothing() { return {neg_inf(), 0.f, neg_inf(), 0.f, 0.0, 0.0}; }
+__device__ __forceinline__ Known known_nothing() { return {neg_inf(), 0.f, neg_inf(), 0.f, 0.f, 0.f, 0.f, 0.f}; }
 
 // what the gradient takes from the row's total
 struct Row2 {
@@ -206,12 +222,12 @@ struct Row2 {
     int empty;        // nothing to renormalise
 };
 
-template <typename T, bool kGrad, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S) {
+template <typename T, bool kGrad, int NT, int U>
+__global__ void __launch_bounds__(NT, 8192 / (NT * U)) distill_kernel(DistillArgs a, int S) {
     constexpr int E = Row<T>::E, NW = NT / 32;
     extern __shared__ __align__(16) uint8_t s_map[];
     __shared__ int s_ids[SPEC_MAX_TOP], s_dup;
-    __shared__ float s_p[SPEC_MAX_TOP];
+    __shared__ float s_p[SPEC_MAX_TOP], s_yl[SPEC_MAX_TOP];
     __shared__ Known s_warp[NW], s_known[kMaxCluster];
     __shared__ Row2 s_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -257,23 +273,63 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         return;
     }
 
-    if (S > 1) cluster_arrive();   // waited for before the exchange: by then every CTA of the cluster runs
+    if (S > 1) cluster_arrive_relaxed();   // waited for before the exchange: by then every CTA of the cluster runs
 
-    // the part's own entries of the list
-    const bool own = id >= part.e0 && id < part.e1;
-    if (!own) id = -1;
-    if (tid < SPEC_MAX_TOP) s_ids[tid] = id;
-    float yl = neg_inf();
-    if (own) {
-        const int bit = map_bit(part, id);
-        const uint32_t m = 1u << (bit & 31);
-        if (atomicOr(reinterpret_cast<uint32_t *>(s_map) + (bit >> 5), m) & m) s_dup = 1;
-        yl = load1_rw(py + id);
+    // the part's own entries of the list, and while the row's loads arrive the
+    // list's part of what this warp knows
+    if (tid < SPEC_MAX_TOP) {
+        if (!(id >= part.e0 && id < part.e1)) id = -1;
+        s_ids[tid] = id;
+        if (id >= 0) {
+            const int bit = map_bit(part, id);
+            const uint32_t m = 1u << (bit & 31);
+            if (atomicOr(reinterpret_cast<uint32_t *>(s_map) + (bit >> 5), m) & m) s_dup = 1;
+            s_yl[tid] = load1_rw(py + id);
+        }
     }
     __syncthreads();
-    bool once = own;   // the first entry of its token
-    if (s_dup)
-        for (int i = 0; i < tid && i < a.M && once; ++i) once = s_ids[i] != id;
+    // the first entry of its token
+    auto once = [&](int t) {
+        const int v = s_ids[t];
+        bool f = v >= 0;
+        if (s_dup)
+            for (int i = 0; i < t && f; ++i) f = s_ids[i] != v;
+        return f;
+    };
+    {
+        Known k = known_nothing();
+        if (warp * 32 < a.M) {
+            float ph = 0.f, pl = 0.f, yl = neg_inf();
+            if (id >= 0) {
+                exp_diff(lp, 0.f, ph, pl);
+                yl = s_yl[tid];
+            }
+            s_p[tid] = ph;
+            const bool there = yl > sv::kMaskFloor;
+            k.ml = warp_max(yl);
+            k.Sl = warp_sum(once(tid) ? (there ? ex2((yl - k.ml) * a.sL) : yl == yl ? 0.f : yl) : 0.f);
+            k.Ph = ph;
+            k.Pl = pl;
+            if (id >= 0 && lp > -700.f) {
+                if (there) {   // p (l - s y), each product and sum with its rounding
+                    const float sy = __fmul_rn(a.s, yl), syl = __fmaf_rn(a.s, yl, -sy);
+                    float dh, dl;
+                    two_sum(lp, -sy, dh, dl);
+                    dl -= syl;
+                    k.Bh = __fmul_rn(ph, dh);
+                    k.Bl = __fmaf_rn(ph, dh, -k.Bh) + (ph * dl + pl * dh);
+                } else {
+                    k.Bh = INFINITY;
+                }
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                pair_total(k.Ph, k.Pl, o);
+                pair_total(k.Bh, k.Bl, o);
+            }
+        }
+        if (lane == 0) s_warp[warp] = k;
+    }
 
     // the unlisted tokens' sum
     Sum acc = sum_init(a.sL, a.resc);
@@ -315,34 +371,21 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         }
         sum_put(acc, v);
     }
-    const int ei = part.edge(tid);
-    const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
-    if (ei >= 0) {
-        const int bit = map_bit(part, ei);
-        if (!(s_map[bit >> 3] >> (bit & 7) & 1)) sum_add1(acc, ey, a.sL, a.resc);
+    {
+        const int i = part.edge(tid);
+        if (i >= 0) {
+            const int bit = map_bit(part, i);
+            if (!(s_map[bit >> 3] >> (bit & 7) & 1)) sum_add1(acc, load1_rw(py + i), a.sL, a.resc);
+        }
     }
 
     // every warp's part, the CTA's, the row's
     {
-        Known k = known_nothing();
-        k.mo = warp_max(acc.mx);
-        k.So = warp_sum(sum_at(acc, k.mo, a.sL));
-        if (warp < SPEC_MAX_TOP / 32) {
-            float ph = 0.f, pl = 0.f;
-            if (own) exp_diff(lp, 0.f, ph, pl);
-            s_p[tid] = ph;
-            const bool there = yl > sv::kMaskFloor;
-            k.ml = warp_max(yl);
-            k.Sl = warp_sum(once ? (there ? ex2((yl - k.ml) * a.sL) : yl == yl ? 0.f : yl) : 0.f);
-            k.P = (double)ph + (double)pl;
-            k.B = own && lp > -700.f ? (there ? k.P * ((double)lp - (double)a.s * (double)yl) : INFINITY) : k.P;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                k.P += __shfl_xor_sync(kFull, k.P, o);
-                k.B += __shfl_xor_sync(kFull, k.B, o);
-            }
+        const float m = warp_max(acc.mx), x = warp_sum(sum_at(acc, m, a.sL));
+        if (lane == 0) {
+            s_warp[warp].mo = m;
+            s_warp[warp].So = x;
         }
-        if (lane == 0) s_warp[warp] = k;
     }
     __syncthreads();
     Known all = known_nothing();
@@ -360,8 +403,12 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         }
     }
     if (S > 1) {
-        if (warp != 0) cluster_wait();
-        cluster_arrive();
+        if (warp != 0) {
+            cluster_wait();
+            cluster_arrive_relaxed();
+        } else {
+            cluster_arrive();
+        }
         cluster_wait();
         if (warp == 0) {
             all = known_nothing();
@@ -375,14 +422,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         Row2 r2;
         r2.rest = all.mo > sv::kMaskFloor || all.So != 0.f;
         r2.none = !(mx > sv::kMaskFloor) && Z == 0.f;
-        r2.empty = !a.tail && all.P == 0.0;
-        const float pT = a.tail ? (float)fmax(0.0, 1.0 - all.P) : 0.f;
+        const double P = (double)all.Ph + (double)all.Pl;
+        r2.empty = !a.tail && all.Ph == 0.f;
+        const float pT = a.tail ? (float)fmax(0.0, 1.0 - P) : 0.f;
         r2.st = make_float4(mx, 1.f / Z, all.mo, 0.f);
         if (r2.rest) r2.st.w = (qo / Z - pT) / all.So;
         else r2.st.z = neg_inf();
         if (r2.none) r2.st = make_float4(0.f, 0.f, 0.f, 0.f);
-        r2.qscale = a.tail && !r2.rest ? (float)all.P : 1.f;
-        r2.norm = a.tail ? 1.f : 1.f / (float)all.P;
+        r2.qscale = a.tail && !r2.rest ? all.Ph : 1.f;
+        r2.norm = a.tail ? 1.f : 1.f / all.Ph;
         if (lane == 0) s_row = r2;
         if (rank == 0 && lane == 0) {
             if (r2.empty) {
@@ -390,7 +438,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
                 if (a.stats_out) a.stats_out[row] = make_float4(0.f, 0.f, 0.f, 0.f);
             } else {
                 const double lse = (double)a.s * (double)mx + log((double)Z);
-                double kl = a.tail ? all.B + all.P * lse : all.B / all.P - log(all.P) + lse;
+                const double B = (double)all.Bh + (double)all.Bl;
+                double kl = a.tail ? B + P * lse : B / P - log(P) + lse;
                 // ln(p_T / q_T), by parts where q_T is below fp32's range
                 if (r2.rest && pT > 0.f)
                     kl += (double)pT * (qo > 1e-30f ? (double)logf(pT * (Z / qo))
@@ -425,14 +474,19 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
             if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
         }
     }
-    if (ei >= 0) pg[ei] = to_elem<T>(grad_one(f, ey, a.sL));
+    {
+        const int i = part.edge(tid);
+        if (i >= 0) pg[i] = to_elem<T>(grad_one(f, load1_rw(py + i), a.sL));
+    }
     __syncthreads();   // the listed tokens' values go over what was just written
-    if (once) {
+    if (tid < a.M && once(tid)) {
+        const int v = s_ids[tid];
         float p = s_p[tid];
         if (s_dup)
-            for (int i = tid + 1; i < a.M; ++i) p += s_ids[i] == id ? s_p[i] : 0.f;
+            for (int i = tid + 1; i < a.M; ++i) p += s_ids[i] == v ? s_p[i] : 0.f;
+        const float yl = s_yl[tid];
         const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - r2.st.x) * a.sL) : 0.f;
-        pg[id] = to_elem<T>(fmaf(us * r2.st.y * r2.qscale, q, -us * (p * r2.norm)));
+        pg[v] = to_elem<T>(fmaf(us * r2.st.y * r2.qscale, q, -us * (p * r2.norm)));
     }
 }
 
@@ -457,9 +511,9 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
         zero_part<T, NT>(part, out);
         return;
     }
-    uint4 w[U];
+    uint4 w[UG];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < UG; ++u) {
         const int i = u * NT + tid;
         if (i < n) w[u] = ld_rw(body + i);
     }
@@ -503,7 +557,7 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     __syncthreads();   // before anything is overwritten
     const Factor f = factor_of(us * st.w, st.z == neg_inf() ? 0.f : st.z, a.sL);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < UG; ++u) {
         const int i = u * NT + tid;
         if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
     }
@@ -525,7 +579,7 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     }
 }
 
-template <typename T, bool kGrad, int NT>
+template <typename T, bool kGrad, int NT, int U>
 static cudaError_t launch_distill(const DistillArgs &a, int S, cudaStream_t stream) {
     const long long nvec = (long long)a.V / Row<T>::E / S + 1;
     const size_t smem = (size_t)((16 + Row<T>::E * nvec + 8 + 31) / 32 + 4) / 4 * 16 + 16;
@@ -537,20 +591,20 @@ static cudaError_t launch_distill(const DistillArgs &a, int S, cudaStream_t stre
         if (e != cudaSuccess) return e;
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev & 63]) {
-            e = cudaFuncSetAttribute(distill_kernel<T, kGrad, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(distill_kernel<T, kGrad, NT, U>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      SPEC_MAX_V / 8 + 256);
             if (e != cudaSuccess) return e;
             done[dev & 63] = true;
         }
     }
-    return launch_cluster(distill_kernel<T, kGrad, NT>, (unsigned)((long long)a.B * a.K * S), NT, S, smem, stream, a, S);
+    return launch_cluster(distill_kernel<T, kGrad, NT, U>, (unsigned)((long long)a.B * a.K * S), NT, S, smem, stream, a, S);
 }
 
 template <typename T, bool kLoss, bool kGrad>
 cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
     const long long rows = (long long)a.B * a.K, nvec = (long long)a.V / Row<T>::E;
     if constexpr (!kLoss) {
-        const long long parts = nvec <= U * 256 ? 1 : (nvec + U * 256 - 1) / (U * 256);
+        const long long parts = nvec <= UG * 256 ? 1 : (nvec + UG * 256 - 1) / (UG * 256);
         if (rows * parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         grad_kernel<T, 256><<<(unsigned)(rows * parts), 256, 0, stream>>>(a, (int)parts);
         return cudaGetLastError();
@@ -558,11 +612,15 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
         int S = 1;
         if constexpr (kGrad) {
             // the stretch in registers where a cluster can hold the row
-            while (S < kMaxCluster && nvec > (long long)S * U * 256) S *= 2;
+            while (S < kMaxCluster && nvec > (long long)S * STEP_U * STEP_NT) S *= 2;
         }
         while (S < kMaxCluster && rows * S * 2 <= 608 && nvec >= 2LL * S * 256) S *= 2;
-        if (kGrad && nvec > (long long)S * U * 256) return launch_distill<T, kGrad, 512>(a, S, stream);
-        return launch_distill<T, kGrad, 256>(a, S, stream);
+        if constexpr (kGrad) {
+            if (nvec > (long long)S * STEP_U * STEP_NT) return launch_distill<T, kGrad, 512, 8>(a, S, stream);
+            return launch_distill<T, kGrad, STEP_NT, STEP_U>(a, S, stream);
+        } else {
+            return launch_distill<T, kGrad, 256, 8>(a, S, stream);
+        }
     }
 }
 

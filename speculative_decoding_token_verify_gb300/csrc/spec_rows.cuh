@@ -175,6 +175,13 @@ __device__ __forceinline__ void two_sum(float a, float b, float &h, float &l) {
     l = __fadd_rn(__fsub_rn(a, __fsub_rn(h, t)), __fsub_rn(b, t));
 }
 
+// (h, l) += (a, b)
+__device__ __forceinline__ void add2f(float &h, float &l, float a, float b) {
+    float e;
+    two_sum(h, a, h, e);
+    l += b + e;
+}
+
 // e^x of x = z - M as h + l, relative error about 1e-10 (0 below e^-87): x = n ln2 + r with
 // ln2 in three floats, then e^r by its Taylor series, whose first terms carry
 // their roundings
@@ -286,6 +293,8 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 
 // ---- thread-block clusters ----------------------------------------------------------
 
+// (relaxed: by threads that publish nothing)
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // the address of a shared variable in CTA `rank` of the cluster
