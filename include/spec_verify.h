@@ -420,7 +420,7 @@ int spec_irls_refit(int32_t K, void *state, float *est_params, double damping, d
  *
  * `status` is a device int32 or NULL: the largest code met is left there
  * (atomic maximum). These calls never clear it: the caller zeroes it. They
- * use no workspace except spec_beam_step. Asynchronous on `stream`, outputs
+ * use no workspace. Asynchronous on `stream`, outputs
  * bit-reproducible, B = 0 or K = 0 enqueues nothing.
  */
 typedef struct {
@@ -511,13 +511,10 @@ int spec_distill_step(const spec_rows_params *params, const void *logits, const 
  * differences of 1e-9: where fp32 sums leave the order of two selected
  * scores open, the kernel sums the beams' rows again in more bits.
  * eos in [0, V) or -1 (none; finished must then be NULL).
- * Workspace: spec_beam_workspace_size(params) bytes, 16-byte aligned, its
- * content ignored on entry, not to be shared by calls that can overlap.
  */
-size_t spec_beam_workspace_size(const spec_rows_params *params);
 int spec_beam_step(const spec_rows_params *params, const void *logits, const float *scores, const int32_t *finished,
                    int32_t eos, float *out_scores, int32_t *out_parent, int32_t *out_token, int32_t *out_finished,
-                   int32_t *status, void *workspace, size_t workspace_bytes, void *stream);
+                   int32_t *status, void *stream);
 
 /*
  * spec_beam_reorder -- states in the order of the surviving beams:

@@ -12,6 +12,6 @@ from .api import (  # noqa: F401
     workspace_size,
 )
 from .rows import (  # noqa: F401
-    MAX_BEAM_OUT, MAX_BEAMS, MAX_TOP, beam_reorder, beam_step, beam_workspace_size, distill_grad, distill_loss,
-    distill_step, top_logprobs,
+    MAX_BEAM_OUT, MAX_BEAMS, MAX_TOP, beam_reorder, beam_step, distill_grad, distill_loss, distill_step,
+    top_logprobs,
 )

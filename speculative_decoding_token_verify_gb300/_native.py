@@ -170,9 +170,7 @@ SIGNATURES = {
                                          ctypes.c_int64, _P, _P]),
     "spec_distill_step": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _P, _P, _P, ctypes.c_int64,
                                          ctypes.c_int64, _P, _P]),
-    "spec_beam_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(RowsParams)]),
-    "spec_beam_step": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P,
-                                      ctypes.c_size_t, _P]),
+    "spec_beam_step": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P]),
     "spec_beam_reorder": (ctypes.c_int, [ctypes.POINTER(ReorderParams), _P, _P, _P, _P, _P, _P]),
     "spec_get_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_I32)]),
     "spec_static_device_status": (ctypes.c_int, [ctypes.POINTER(_I32)]),

@@ -69,30 +69,6 @@ __device__ __forceinline__ uint4 pack_vec(const float (&z)[Elem<T>::kPerVec]) {
     else return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]), __float_as_uint(z[3]));
 }
 
-// a CTA's part of a row: vectors [k0, k0 + n), the row's head in the first
-// part and its tail in the last, elements [e0, e1) in all
-template <typename T>
-struct Part {
-    static constexpr int E = Row<T>::E;
-    Row<T> r;
-    int k0, n, e0, e1;
-    bool first, last;
-    __device__ __forceinline__ Part(const T *row, int V, int rank, int parts)
-        : r(row, V), first(rank == 0), last(rank == parts - 1) {
-        k0 = (int)((long long)r.nvec * rank / parts);
-        n = (int)((long long)r.nvec * (rank + 1) / parts) - k0;
-        e0 = first ? 0 : r.vec_index(k0);
-        e1 = last ? V : r.vec_index(k0 + n);
-    }
-    // the head's or tail's element of slot t, or -1
-    __device__ __forceinline__ int edge(int t) const {
-        if (t >= 2 * E) return -1;
-        const int i = r.edge_index(t);
-        return i >= 0 && (t < E ? first : last) ? i : -1;
-    }
-    __device__ __forceinline__ const uint4 *body() const { return r.body + k0; }
-};
-
 // the part's map of listed tokens: bit 16 + 8 i or 16 + 4 i starts vector i,
 // the head lies before it and the tail behind the last vector
 template <typename T>
@@ -612,11 +588,19 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
         int S = 1;
         if constexpr (kGrad) {
             // the stretch in registers where a cluster can hold the row
+#ifndef STEP_S
             while (S < kMaxCluster && nvec > (long long)S * STEP_U * STEP_NT) S *= 2;
+#else
+            S = rows >= 1000 ? STEP_S : 8;
+#endif
         }
         while (S < kMaxCluster && rows * S * 2 <= 608 && nvec >= 2LL * S * 256) S *= 2;
         if constexpr (kGrad) {
+            
+#ifndef STEP_S
             if (nvec > (long long)S * STEP_U * STEP_NT) return launch_distill<T, kGrad, 512, 8>(a, S, stream);
+#endif
+
             return launch_distill<T, kGrad, STEP_NT, STEP_U>(a, S, stream);
         } else {
             return launch_distill<T, kGrad, 256, 8>(a, S, stream);

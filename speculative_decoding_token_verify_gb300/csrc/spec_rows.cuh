@@ -53,6 +53,30 @@ struct Row {
     }
 };
 
+// a CTA's part of a row: vectors [k0, k0 + n), the row's head in the first
+// part and its tail in the last, elements [e0, e1) in all
+template <typename T>
+struct Part {
+    static constexpr int E = Row<T>::E;
+    Row<T> r;
+    int k0, n, e0, e1;
+    bool first, last;
+    __device__ __forceinline__ Part(const T *row, int V, int rank, int parts)
+        : r(row, V), first(rank == 0), last(rank == parts - 1) {
+        k0 = (int)((long long)r.nvec * rank / parts);
+        n = (int)((long long)r.nvec * (rank + 1) / parts) - k0;
+        e0 = first ? 0 : r.vec_index(k0);
+        e1 = last ? V : r.vec_index(k0 + n);
+    }
+    // the head's or tail's element of slot t, or -1
+    __device__ __forceinline__ int edge(int t) const {
+        if (t >= 2 * E) return -1;
+        const int i = r.edge_index(t);
+        return i >= 0 && (t < E ? first : last) ? i : -1;
+    }
+    __device__ __forceinline__ const uint4 *body() const { return r.body + k0; }
+};
+
 template <typename T>
 __device__ __forceinline__ float load1(const T *p) {
     return Elem<T>::load(p);

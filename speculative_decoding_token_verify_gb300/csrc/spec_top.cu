@@ -4,231 +4,38 @@
 // and the list in the order (logit descending, token ascending), which is the
 // order of the log-probabilities without their roundings.
 //
-// One pass. A cluster of S CTAs streams a row (S = 1 when there are rows
-// enough), each a stretch of it, and adds the sum as it goes. Beside it runs a
-// filter: with T such that at least M logits seen so far are >= T, only
-// vectors whose maximum reaches T can hold a listed token, and their indices
-// go to a short list in shared memory. T comes from the threads' own running
-// maxima: every warp sorts its 32, and with k = ceil(M / warps) the smallest
-// of the warps' k-th largest has M logits at or above it. It is taken after
-// iterations 1, 2, 4, 8, ..., and a stretch is read in U interleaved streams,
-// so that the first iteration samples all of it. About 7 M of a row's vectors
-// pass; the same bound over their maxima leaves about 1.5 M, whose logits are
-// looked at one by one and ranked by counting.
-//
-// Rows where more vectors pass than the list holds (runs of equal logits, all
-// large logits in one place) are finished by bisection: the M-th largest key
-// by counting passes over the row, tokens above it in any order, tokens at it
-// in ascending order.
+// One pass over the row by a cluster of S CTAs (S = 1 when there are rows
+// enough), each a part of it, with the filter of spec_top.cuh; the parts'
+// bounds, maxima and sums meet in one exchange through distributed shared
+// memory, and the first CTA ranks what passes the best bound.
 #include "spec_top.cuh"
-
-#include "spec_rows.cuh"
 
 namespace sr {
 
-constexpr int NT = 256;
-constexpr int NW = NT / 32;
-constexpr int U = 8;         // 16-byte loads in flight per thread
-constexpr int CAP = 2048;    // vectors that may pass the filter, per CTA
-constexpr int CAPE = 1024;   // logits that may pass the last bound, per row
-constexpr int kMaxCluster = 8;
-
-// the k-th largest of the warp's values (k = 1 .. 32)
-template <typename V>
-__device__ __forceinline__ V warp_kth(V v, int k) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-        for (int o = size >> 1; o > 0; o >>= 1) {
-            const V w = __shfl_xor_sync(kFull, v, o);
-            const bool big = ((lane & o) == 0) == ((lane & size) == 0);   // descending runs
-            v = big ? max(v, w) : min(v, w);
-        }
-    return __shfl_sync(kFull, v, k - 1);
-}
-
-// A bound with at least M of the block's `n` values (thread t holds the
-// largest of the values t, t + NT, ...) at or above it, or `none`.
-// buf: NW values, not written again before another barrier has passed.
-template <typename V>
-__device__ __forceinline__ V block_bound(V v, int n, int M, V none, V *buf) {
-    const int act = min(NW, n >> 5);   // warps whose lanes all hold a value
-    const int k = act ? (M + act - 1) / act : 33;
-    if (k > 32) return none;           // the same in every thread
-    const V t = warp_kth(v, k);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = t;
-    __syncthreads();
-    V r = buf[0];
-#pragma unroll
-    for (int i = 1; i < NW; ++i)
-        if (i < act) r = min(r, buf[i]);
-    return max(r, none);
-}
-
-template <typename T, typename F>
-__device__ __forceinline__ void each(const Row<T> &r, F f) {
-    constexpr int E = Row<T>::E;
-    if (threadIdx.x < 2 * E) {
-        const int i = r.edge_index(threadIdx.x);
-        if (i >= 0) f(load1(r.p + i), i);
-    }
-    for (int k = threadIdx.x; k < r.nvec; k += NT) {
-        float z[E];
-        Elem<T>::unpack(__ldg(r.body + k), z);
-#pragma unroll
-        for (int j = 0; j < E; ++j) f(z[j], r.vec_index(k) + j);
-    }
-}
-
-// The list by bisection; at least M keys of the row are >= t, or t = 1.
-// Leaves at most M candidates in s_el, in no order, and returns their number.
-template <typename T>
-__device__ __noinline__ int bisect(const Row<T> &r, int V, int M, uint32_t t, float mx, unsigned long long *s_el,
-                                   int *s_cnt, int *s_n) {
-    auto count = [&](uint32_t k) {   // tokens of key >= k, k > 0
-        int n = 0;
-        each(r, [&](float z, int) { n += order_key(z) >= k; });
-        n = __reduce_add_sync(kFull, n);
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) s_cnt[threadIdx.x >> 5] = n;
-        __syncthreads();
-        n = 0;
-        for (int i = 0; i < NW; ++i) n += s_cnt[i];
-        return n;
-    };
-    // the largest t with count(t) >= M, or 1 when the row has no more tokens
-    if (t > 1u || count(1u) > M) {
-        uint32_t hi = order_key(mx);   // count(hi + 1) == 0 < M
-        while (t < hi) {
-            const uint32_t mid = t + (hi - t) / 2 + ((hi - t) & 1u);
-            if (count(mid) >= M) t = mid;
-            else hi = mid - 1;
-        }
-    }
-    __syncthreads();
-    if (threadIdx.x == 0) *s_n = 0;
-    __syncthreads();
-    const bool all = t == 1u;
-    each(r, [&](float z, int i) {
-        const uint32_t key = order_key(z);
-        if (all ? key >= 1u : key > t) {
-            const int at = atomicAdd(s_n, 1);
-            if (at < M) s_el[at] = cand(key, i);
-        }
-    });
-    __syncthreads();
-    int n = min(*s_n, M);
-    if (!all) {   // tokens at the threshold, lowest index first
-        for (int i0 = 0; i0 < V && n < M; i0 += NT) {
-            const int i = i0 + threadIdx.x;
-            const bool at = i < V && order_key(load1(r.p + i)) == t;
-            const unsigned bal = __ballot_sync(kFull, at);
-            __syncthreads();
-            if ((threadIdx.x & 31) == 0) s_cnt[threadIdx.x >> 5] = __popc(bal);
-            __syncthreads();
-            int before = n + __popc(bal & ((1u << (threadIdx.x & 31)) - 1u)), total = 0;
-            for (int w = 0; w < NW; ++w) {
-                before += w < (int)(threadIdx.x >> 5) ? s_cnt[w] : 0;
-                total += s_cnt[w];
-            }
-            if (at && before < M) s_el[before] = cand(t, i);
-            n = min(n + total, M);
-        }
-        __syncthreads();
-    }
-    return n;
-}
+struct TopArgs {
+    const void *z;
+    long long batch_stride, row_stride;   // elements
+    int B, K, V, M;
+    float s, sL, rs;   // inverse temperature, s log2(e); how far a logit may exceed the sum's reference
+    float *val;        // [B * K][M]
+    int32_t *ids;      // [B * K][M]
+    float *lse;        // [B * K] or null
+    int32_t *status;
+};
 
 template <typename T, bool kCluster>
 __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
-    constexpr int E = Row<T>::E;
-    __shared__ float s_c[CAP];
-    __shared__ int s_code[CAP];
-    __shared__ __align__(16) unsigned long long s_el[CAPE];
-    __shared__ float s_b[3][NW], s_red[2][NW];
-    __shared__ uint32_t s_kb[NW];
-    __shared__ int s_n, s_ne, s_cnt[NW];
+    __shared__ TopShared s;
     __shared__ float s_x[4][kMaxCluster];   // per CTA of the cluster: bound, maximum, sum, overflow
     const int tid = threadIdx.x;
     const int row = kCluster ? blockIdx.x / S : blockIdx.x;
     const int rank = kCluster ? blockIdx.x - row * S : 0;
-    if (a.scores) {   // dead and finished beams: the whole cluster leaves
-        const float sc = a.scores[row];
-        if (!(sc > neg_inf()) || sc == -neg_inf() || (a.finished && a.finished[row])) return;
-    }
-    if (kCluster) cluster_arrive();   // waited for before the exchange: by then every CTA of the cluster runs
+    if (kCluster) cluster_arrive_relaxed();   // waited for before the exchange: by then every CTA of the cluster runs
     const int b = row / a.K, kr = row - b * a.K;
-    const Row<T> r(static_cast<const T *>(a.z) + b * a.batch_stride + kr * a.row_stride, a.V);
-    const int k0 = kCluster ? (int)((long long)r.nvec * rank / S) : 0;
-    const int n = (kCluster ? (int)((long long)r.nvec * (rank + 1) / S) : r.nvec) - k0;
-    const uint4 *body = r.body + k0;
-    if (tid == 0) s_n = s_ne = 0;
-    __syncthreads();
-
-    Sum acc = sum_init(a.sL, a.rs);
-    float thr = sv::kMaskFloor;
-    const int its = (n + U * NT - 1) / (U * NT), span = its * NT;
-    int refresh = 0;
-    for (int it = 0; it < its; ++it) {
-        uint4 w[U];
-        const int base = it * NT + tid;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = u * span + base;
-            w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
-        }
-        float c[U], cm;
-#pragma unroll
-        for (int u = 0; u < U; ++u) c[u] = vec_max<T>(w[u]);
-        cm = c[0];
-#pragma unroll
-        for (int u = 1; u < U; ++u) cm = fmaxf(cm, c[u]);
-        sum_see(acc, cm, a.sL, a.rs);
-        float v = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float z[E];
-            Elem<T>::unpack(w[u], z);
-            v += sum_terms<E>(acc, z, a.sL);
-        }
-        sum_put(acc, v);
-        if ((it & (it + 1)) == 0 && (it == 0 || it + 1 < its)) {
-            thr = block_bound(acc.mx, n, a.M, thr, s_b[refresh]);
-            refresh ^= 1;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (c[u] >= thr) {
-                const int at = atomicAdd(&s_n, 1);
-                if (at < CAP) {
-                    s_c[at] = c[u];
-                    s_code[at] = k0 + u * span + base;
-                }
-            }
-    }
-    if (tid < 2 * E) {   // the row's ends: single logits, coded by ~index
-        const int i = r.edge_index(tid);
-        if (i >= 0 && (tid < E ? rank == 0 : rank == S - 1)) {
-            const float z = load1(r.p + i);
-            sum_add1(acc, z, a.sL, a.rs);
-            if (z >= thr) {
-                const int at = atomicAdd(&s_n, 1);
-                if (at < CAP) {
-                    s_c[at] = z;
-                    s_code[at] = ~i;
-                }
-            }
-        }
-    }
-    float mx = block_max<NT>(acc.mx, s_red[0]);
-    float sum = block_sum<NT>(sum_at(acc, mx, a.sL), s_red[1]);
-    // (the barriers above also publish the list)
-    bool over = s_n > CAP;
-    const int np = min(s_n, CAP);
-    float best = neg_inf();
-    for (int i = tid; i < np; i += NT) best = fmaxf(best, s_c[i]);
-    thr = block_bound(best, np, a.M, thr, s_b[2]);
+    const T *z = static_cast<const T *>(a.z) + b * a.batch_stride + kr * a.row_stride;
+    const Part<T> part(z, a.V, rank, kCluster ? S : 1);
+    float mx, sum, thr;
+    bool over = stream_part(part, a.M, a.sL, a.rs, s, mx, sum, thr);
     if (kCluster) {
         cluster_wait();
         if (tid < S) {
@@ -250,32 +57,17 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
             sum += s_x[1][i] == m || !(s_x[2][i] > 0.f) ? s_x[2][i] : s_x[2][i] * ex2((s_x[1][i] - m) * a.sL);
         mx = m;
     }
-    // the passing vectors' logits, to the cluster's first CTA
-    const uint32_t el0 = kCluster ? peer(s_el, 0) : 0u, ne0 = kCluster ? peer(&s_ne, 0) : 0u;
-    auto put = [&](float z, int index) {
-        if (!(z >= thr)) return;
-        const uint32_t key = order_key(z);
-        if (key == 0u) return;
-        const int at = kCluster ? peer_add(ne0, 1) : atomicAdd(&s_ne, 1);
-        if (at < CAPE) {
-            if (kCluster) peer_store(el0 + 8u * at, cand(key, index));
-            else s_el[at] = cand(key, index);
-        }
-    };
-    if (!over)
-        for (int i = tid; i < np; i += NT) {
-            const float c = s_c[i];
-            if (!(c >= thr)) continue;
-            const int code = s_code[i];
-            if (code < 0) {
-                put(c, ~code);
-                continue;
+    // to the cluster's first CTA
+    if (!over) {
+        const uint32_t el0 = kCluster ? peer(s.el, 0) : 0u, ne0 = kCluster ? peer(&s.ne, 0) : 0u;
+        expand(part, thr, s, [&](uint32_t key, int index) {
+            const int at = kCluster ? peer_add(ne0, 1) : atomicAdd(&s.ne, 1);
+            if (at < CAPE) {
+                if (kCluster) peer_store(el0 + 8u * at, cand(key, index));
+                else s.el[at] = cand(key, index);
             }
-            float z[E];
-            Elem<T>::unpack(__ldg(r.body + code), z);
-#pragma unroll
-            for (int j = 0; j < E; ++j) put(z[j], r.vec_index(code) + j);
-        }
+        });
+    }
     if (kCluster) {
         cluster_arrive();
         cluster_wait();
@@ -283,43 +75,20 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
     } else {
         __syncthreads();
     }
-    int ne = s_ne;
-    if (over || ne > CAPE) ne = bisect(r, a.V, a.M, max(order_key(thr), 1u), mx, s_el, s_cnt, &s_n);
-    uint32_t bound = 0u;
-    if (ne > 128) {   // once more over single logits
-        uint32_t k = 0u;
-        for (int i = tid; i < ne; i += NT) k = max(k, cand_key(s_el[i]));
-        bound = block_bound(k, ne, a.M, 0u, s_kb);
-    }
-    if (bound) {   // gather what reaches it: s_c holds CAP 32-bit words, half as many candidates
-        unsigned long long *s_few = reinterpret_cast<unsigned long long *>(s_c);
-        if (tid == 0) s_n = 0;
-        __syncthreads();
-        for (int i = tid; i < ne; i += NT)
-            if (cand_key(s_el[i]) >= bound) s_few[atomicAdd(&s_n, 1)] = s_el[i];
-        __syncthreads();
-        ne = s_n;
-        for (int i = tid; i < ne; i += NT) s_el[i] = s_few[i];
-        __syncthreads();
-    }
+    int ne = s.ne;
+    if (over || ne > CAPE) ne = bisect(Part<T>(z, a.V, 0, 1), a.M, max(order_key(thr), 1u), mx, s);
+    ne = cut(ne, a.M, s);
     const bool some = mx > sv::kMaskFloor, bad = !(sum >= 0.f) || mx == -neg_inf();
     const float lnS = logf(sum);
-    for (int i = tid; i < ne; i += NT) {
-        const unsigned long long c = s_el[i];
-        int rk = 0;
-        for (int j = 0; j < ne; ++j) rk += s_el[j] > c;
-        if (rk < a.M) {
-            const float z = key_value(cand_key(c));
-            a.val[(size_t)row * a.M + rk] = a.stat ? z : fmaf(z - mx, a.s, -lnS);
-            a.ids[(size_t)row * a.M + rk] = cand_index(c);
-        }
-    }
+    ranked(ne, a.M, s, [&](unsigned long long c, int rk) {
+        a.val[(size_t)row * a.M + rk] = fmaf(key_value(cand_key(c)) - mx, a.s, -lnS);
+        a.ids[(size_t)row * a.M + rk] = cand_index(c);
+    });
     for (int i = ne + tid; i < a.M; i += NT) {
         a.val[(size_t)row * a.M + i] = neg_inf();
         a.ids[(size_t)row * a.M + i] = -1;
     }
     if (tid == 0) {
-        if (a.stat) a.stat[row] = make_float2(mx, sum);
         if (a.lse) a.lse[row] = bad ? __int_as_float(0x7fc00000) : some ? fmaf(mx, a.s, lnS) : neg_inf();
         if (bad) raise_status(a.status, SPEC_ERR_BAD_ROW);
     }
@@ -335,15 +104,15 @@ static int top_cluster(long long rows, int V, int es) {
 }
 
 template <typename T>
-static cudaError_t launch_top_t(const TopArgs &a, cudaStream_t stream) {
+static cudaError_t launch_t(const TopArgs &a, cudaStream_t stream) {
     const long long rows = (long long)a.B * a.K;
     const int S = top_cluster(rows, a.V, sizeof(T));
     if (S > 1) return launch_cluster(top_kernel<T, true>, (unsigned)(rows * S), NT, S, 0, stream, a, S);
     return launch_cluster(top_kernel<T, false>, (unsigned)rows, NT, 1, 0, stream, a, 1);
 }
 
-cudaError_t launch_top(const TopArgs &a, int bf16, cudaStream_t stream) {
-    return bf16 ? launch_top_t<__nv_bfloat16>(a, stream) : launch_top_t<float>(a, stream);
+static cudaError_t launch_top(const TopArgs &a, int bf16, cudaStream_t stream) {
+    return bf16 ? launch_t<__nv_bfloat16>(a, stream) : launch_t<float>(a, stream);
 }
 
 int check_rows(const spec_rows_params *p, int max_m, int max_k) {

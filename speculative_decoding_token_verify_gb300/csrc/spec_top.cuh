@@ -1,31 +1,276 @@
-// spec_top.cuh -- launch interface of the top-list kernel, shared by
-// spec_top.cu and spec_beam.cu. Internal to the library.
+// spec_top.cuh -- the M largest logits of a part of a row, found while the
+// part streams by: device code of the top lists and the beam step.
+//
+// Beside the softmax sum runs a filter: with T such that at least M logits
+// seen so far are >= T, only vectors whose maximum reaches T can hold a listed
+// token, and their indices go to a short list in shared memory. T comes from
+// the threads' own running maxima: every warp sorts its 32, and with k =
+// ceil(M / warps) the smallest of the warps' k-th largest has M logits at or
+// above it. It is taken after iterations 1, 2, 4, 8, ..., and the part is read
+// in U interleaved streams, so that the first iteration samples all of it.
+// About 7 M vectors of a row pass; the same bound over their maxima leaves
+// about 1.5 M, whose logits are looked at one by one and ranked by counting.
+//
+// Where more vectors pass than the list holds (runs of equal logits, all large
+// logits in one place) a bisection finishes: the M-th largest key by counting
+// passes, tokens above it in any order, tokens at it in ascending order.
 #pragma once
 
-#include <cuda_runtime.h>
-
-#include <cstdint>
+#include "spec_rows.cuh"
 
 namespace sr {
 
-struct TopArgs {
-    const void *z;
-    long long batch_stride, row_stride;   // elements
-    int B, K, V, M;
-    float s, sL, rs;              // inverse temperature, s log2(e); how far a logit may exceed the sum's reference
-    // the user's outputs (log-probabilities), or, for the beam step, raw logits
-    // and the row's (maximum, sum) in stat
-    float *val;                   // [B * K][M]
-    int32_t *ids;                 // [B * K][M]
-    float *lse;                   // [B * K] or null
-    float2 *stat;                 // null: val gets log-probabilities
-    // the beam step's rows that need no reading
-    const float *scores;          // [B * K] or null
-    const int32_t *finished;      // [B * K] or null
-    int32_t *status;
+constexpr int NT = 256;
+constexpr int NW = NT / 32;
+constexpr int U = 8;         // 16-byte loads in flight per thread
+constexpr int CAP = 2048;    // vectors that may pass the filter, per CTA
+constexpr int CAPE = 1024;   // logits that may pass the last bound, per row
+constexpr int kMaxCluster = 8;
+
+// the k-th largest of the warp's values (k = 1 .. 32)
+template <typename V>
+__device__ __forceinline__ V warp_kth(V v, int k) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int o = size >> 1; o > 0; o >>= 1) {
+            const V w = __shfl_xor_sync(kFull, v, o);
+            const bool big = ((lane & o) == 0) == ((lane & size) == 0);   // descending runs
+            v = big ? max(v, w) : min(v, w);
+        }
+    return __shfl_sync(kFull, v, k - 1);
+}
+
+// A bound with at least M of the block's `n` values (thread t holds the
+// largest of the values t, t + NT, ...) at or above it, or `none`.
+// buf: NW values, not written again before another barrier has passed.
+template <typename V>
+__device__ __forceinline__ V block_bound(V v, int n, int M, V none, V *buf) {
+    const int act = min(NW, n >> 5);   // warps whose lanes all hold a value
+    const int k = act ? (M + act - 1) / act : 33;
+    if (k > 32) return none;           // the same in every thread
+    const V t = warp_kth(v, k);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = t;
+    __syncthreads();
+    V r = buf[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i)
+        if (i < act) r = min(r, buf[i]);
+    return max(r, none);
+}
+
+
+struct TopShared {
+    float c[CAP];        // passing vectors: maximum and code (index in the row, or ~index of a single logit)
+    int code[CAP];
+    __align__(16) unsigned long long el[CAPE];   // candidates
+    float b[3][NW], red[2][NW];
+    uint32_t kb[NW];
+    int n, ne, cnt[NW];
 };
 
-// Enqueue on `stream`. Returns a cudaError_t.
-cudaError_t launch_top(const TopArgs &a, int bf16, cudaStream_t stream);
+template <typename T, typename F>
+__device__ __forceinline__ void each(const Part<T> &p, F f) {
+    constexpr int E = Row<T>::E;
+    const int e = p.edge(threadIdx.x);
+    if (e >= 0) f(load1(p.r.p + e), e);
+    for (int k = threadIdx.x; k < p.n; k += NT) {
+        float z[E];
+        Elem<T>::unpack(__ldg(p.body() + k), z);
+#pragma unroll
+        for (int j = 0; j < E; ++j) f(z[j], p.r.vec_index(p.k0 + k) + j);
+    }
+}
+
+// The part's list by bisection; at least M keys of the part are >= t, or t = 1.
+// Leaves at most M candidates in s.el, in no order, and returns their number.
+template <typename T>
+__device__ __noinline__ int bisect(const Part<T> &p, int M, uint32_t t, float mx, TopShared &s) {
+    auto count = [&](uint32_t k) {   // tokens of key >= k, k > 0
+        int n = 0;
+        each(p, [&](float z, int) { n += order_key(z) >= k; });
+        n = __reduce_add_sync(kFull, n);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) s.cnt[threadIdx.x >> 5] = n;
+        __syncthreads();
+        n = 0;
+        for (int i = 0; i < NW; ++i) n += s.cnt[i];
+        return n;
+    };
+    // the largest t with count(t) >= M, or 1 when the part has no more tokens
+    if (t > 1u || count(1u) > M) {
+        uint32_t hi = order_key(mx);   // count(hi + 1) == 0 < M
+        while (t < hi) {
+            const uint32_t mid = t + (hi - t) / 2 + ((hi - t) & 1u);
+            if (count(mid) >= M) t = mid;
+            else hi = mid - 1;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    const bool all = t == 1u;
+    each(p, [&](float z, int i) {
+        const uint32_t key = order_key(z);
+        if (all ? key >= 1u : key > t) {
+            const int at = atomicAdd(&s.n, 1);
+            if (at < M) s.el[at] = cand(key, i);
+        }
+    });
+    __syncthreads();
+    int n = min(s.n, M);
+    if (!all) {   // tokens at the threshold, lowest index first
+        for (int i0 = p.e0; i0 < p.e1 && n < M; i0 += NT) {
+            const int i = i0 + threadIdx.x;
+            const bool at = i < p.e1 && order_key(load1(p.r.p + i)) == t;
+            const unsigned bal = __ballot_sync(kFull, at);
+            __syncthreads();
+            if ((threadIdx.x & 31) == 0) s.cnt[threadIdx.x >> 5] = __popc(bal);
+            __syncthreads();
+            int before = n + __popc(bal & ((1u << (threadIdx.x & 31)) - 1u)), total = 0;
+            for (int w = 0; w < NW; ++w) {
+                before += w < (int)(threadIdx.x >> 5) ? s.cnt[w] : 0;
+                total += s.cnt[w];
+            }
+            if (at && before < M) s.el[before] = cand(t, i);
+            n = min(n + total, M);
+        }
+        __syncthreads();
+    }
+    return n;
+}
+
+// One pass over a part: its maximum and sum, a bound `thr` with at least M of
+// its logits at or above it (or the mask's floor), and the vectors that may
+// hold listed tokens. Returns whether more passed than the list holds; every
+// thread gets the same values.
+template <typename T>
+__device__ __forceinline__ bool stream_part(const Part<T> &p, int M, float sL, float rs, TopShared &s, float &mx,
+                                            float &sum, float &thr) {
+    constexpr int E = Row<T>::E;
+    const int tid = threadIdx.x, n = p.n;
+    const uint4 *body = p.body();
+    if (tid == 0) s.n = s.ne = 0;
+    __syncthreads();
+    Sum acc = sum_init(sL, rs);
+    thr = sv::kMaskFloor;
+    const int its = (n + U * NT - 1) / (U * NT), span = its * NT;
+    int refresh = 0;
+    for (int it = 0; it < its; ++it) {
+        uint4 w[U];
+        const int base = it * NT + tid;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = u * span + base;
+            w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
+        }
+        float c[U], cm;
+#pragma unroll
+        for (int u = 0; u < U; ++u) c[u] = vec_max<T>(w[u]);
+        cm = c[0];
+#pragma unroll
+        for (int u = 1; u < U; ++u) cm = fmaxf(cm, c[u]);
+        sum_see(acc, cm, sL, rs);
+        float v = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float z[E];
+            Elem<T>::unpack(w[u], z);
+            v += sum_terms<E>(acc, z, sL);
+        }
+        sum_put(acc, v);
+        if ((it & (it + 1)) == 0 && (it == 0 || it + 1 < its)) {
+            thr = block_bound(acc.mx, n, M, thr, s.b[refresh]);
+            refresh ^= 1;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c[u] >= thr) {
+                const int at = atomicAdd(&s.n, 1);
+                if (at < CAP) {
+                    s.c[at] = c[u];
+                    s.code[at] = p.k0 + u * span + base;
+                }
+            }
+    }
+    const int e = p.edge(tid);   // the row's ends: single logits
+    if (e >= 0) {
+        const float z = load1(p.r.p + e);
+        sum_add1(acc, z, sL, rs);
+        if (z >= thr) {
+            const int at = atomicAdd(&s.n, 1);
+            if (at < CAP) {
+                s.c[at] = z;
+                s.code[at] = ~e;
+            }
+        }
+    }
+    mx = block_max<NT>(acc.mx, s.red[0]);
+    sum = block_sum<NT>(sum_at(acc, mx, sL), s.red[1]);
+    // (the barriers above also publish the list)
+    const int np = min(s.n, CAP);
+    float best = neg_inf();
+    for (int i = tid; i < np; i += NT) best = fmaxf(best, s.c[i]);
+    thr = block_bound(best, np, M, thr, s.b[2]);
+    return s.n > CAP;
+}
+
+// the passing vectors' logits at or above thr
+template <typename T, typename F>
+__device__ __forceinline__ void expand(const Part<T> &p, float thr, TopShared &s, F put) {
+    constexpr int E = Row<T>::E;
+    const int np = min(s.n, CAP);
+    auto one = [&](float z, int index) {
+        const uint32_t key = order_key(z);
+        if (z >= thr && key != 0u) put(key, index);
+    };
+    for (int i = threadIdx.x; i < np; i += NT) {
+        const float c = s.c[i];
+        if (!(c >= thr)) continue;
+        const int code = s.code[i];
+        if (code < 0) {
+            one(c, ~code);
+            continue;
+        }
+        float z[E];
+        Elem<T>::unpack(__ldg(p.r.body + code), z);
+#pragma unroll
+        for (int j = 0; j < E; ++j) one(z[j], p.r.vec_index(code) + j);
+    }
+}
+
+// The candidates s.el[0 .. ne) cut down to few more than the M best; returns
+// their number. Called and left by all threads together.
+__device__ __forceinline__ int cut(int ne, int M, TopShared &s) {
+    if (ne <= 128) return ne;
+    uint32_t k = 0u;
+    for (int i = threadIdx.x; i < ne; i += NT) k = max(k, cand_key(s.el[i]));
+    const uint32_t bound = block_bound(k, ne, M, 0u, s.kb);
+    if (bound == 0u) return ne;
+    // s.c holds CAP 32-bit words: room for half as many candidates
+    unsigned long long *few = reinterpret_cast<unsigned long long *>(s.c);
+    static_assert(CAP >= 2 * CAPE, "the cut's buffer");
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < ne; i += NT)
+        if (cand_key(s.el[i]) >= bound) few[atomicAdd(&s.n, 1)] = s.el[i];
+    __syncthreads();
+    ne = s.n;
+    for (int i = threadIdx.x; i < ne; i += NT) s.el[i] = few[i];
+    __syncthreads();
+    return ne;
+}
+
+// f(candidate, rank) for the M best of s.el[0 .. ne)
+template <typename F>
+__device__ __forceinline__ void ranked(int ne, int M, const TopShared &s, F f) {
+    for (int i = threadIdx.x; i < ne; i += NT) {
+        const unsigned long long c = s.el[i];
+        int rk = 0;
+        for (int j = 0; j < ne; ++j) rk += s.el[j] > c;
+        if (rk < M) f(c, rk);
+    }
+}
 
 }  // namespace sr

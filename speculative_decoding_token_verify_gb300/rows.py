@@ -18,7 +18,7 @@ from typing import Optional
 import torch
 
 from . import _native
-from .api import BF16, F32, SPEC_ERR_INVALID_ARG, SPEC_OK, SpecError
+from .api import BF16, F32, SPEC_OK, SpecError
 
 MAX_TOP = 128
 MAX_BEAMS = 32
@@ -206,14 +206,12 @@ def distill_step(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
 
 def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Optional[torch.Tensor] = None,
               eos: int = -1, out: Optional[dict] = None, status: Optional[torch.Tensor] = None,
-              workspace: Optional[torch.Tensor] = None, stream: Optional[torch.cuda.Stream] = None) -> dict:
+              stream: Optional[torch.cuda.Stream] = None) -> dict:
     """One step of beam search (spec_beam_step): the N best continuations of
     the W beams of every sequence, from ``logits`` [B,W,V], cumulative
     ``scores`` [B,W] float32 (-inf: no beam; at the first step all but one) and
     ``finished`` [B,W] int32 or None. Returns ``scores`` [B,N] float32,
-    ``parent``, ``token`` and ``finished`` [B,N] int32. ``workspace`` is a
-    uint8 CUDA tensor of beam_workspace_size bytes or None (allocated for the
-    call on its stream)."""
+    ``parent``, ``token`` and ``finished`` [B,N] int32."""
     if logits.dim() != 3:
         raise ValueError("logits must be [B, W, V]")
     B, W, V, dt, bs, rs = _logits(logits, "logits")
@@ -221,34 +219,18 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Opti
     _tensor(scores, "scores", torch.float32, torch.Size((B, W)), dev, optional=False)
     _tensor(finished, "finished", torch.int32, torch.Size((B, W)), dev)
     _status(status, dev)
+    if not 1 <= N <= MAX_BEAM_OUT:
+        raise SpecError(2, f"beam_step: N must be in [1, {MAX_BEAM_OUT}]")
     p = _native.RowsParams(B, W, V, dt, N, 0, 1.0, 0, bs, rs)
-    L = _native.lib()
-    nbytes = L.spec_beam_workspace_size(ctypes.byref(p))
-    if nbytes == 0:
-        raise SpecError(SPEC_ERR_INVALID_ARG, _native.last_error())
-    if workspace is not None and (workspace.dtype != torch.uint8 or workspace.device != dev
-                                  or not workspace.is_contiguous()):
-        raise ValueError("workspace must be a contiguous uint8 tensor on the logits' device")
     with _On(logits, stream) as s:
-        if workspace is None:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
         sc = _out(out, "scores", torch.float32, (B, N), dev)
         par = _out(out, "parent", torch.int32, (B, N), dev)
         tok = _out(out, "token", torch.int32, (B, N), dev)
         fin = _out(out, "finished", torch.int32, (B, N), dev)
-        _check(L.spec_beam_step(ctypes.byref(p), logits.data_ptr(), scores.data_ptr(), _addr(finished), eos,
-                                sc.data_ptr(), par.data_ptr(), tok.data_ptr(), fin.data_ptr(), _addr(status),
-                                workspace.data_ptr(), workspace.numel(), s))
+        _check(_native.lib().spec_beam_step(ctypes.byref(p), logits.data_ptr(), scores.data_ptr(), _addr(finished),
+                                            eos, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), fin.data_ptr(),
+                                            _addr(status), s))
     return {"scores": sc, "parent": par, "token": tok, "finished": fin}
-
-
-def beam_workspace_size(B: int, W: int, V: int, N: int) -> int:
-    """Bytes of workspace beam_step needs."""
-    p = _native.RowsParams(B, W, V, F32, N, 0, 1.0, 0, 0, 0)
-    n = _native.lib().spec_beam_workspace_size(ctypes.byref(p))
-    if n == 0:
-        raise SpecError(SPEC_ERR_INVALID_ARG, _native.last_error())
-    return int(n)
 
 
 def _merged(shape, stride):

@@ -28,9 +28,7 @@ def _check(z, scores, N, finished=None, eos=-1, status_want=0):
     sv = _sv()
     B, W, V = z.shape
     status = torch.zeros(1, dtype=torch.int32, device=DEV)
-    nb = sv.beam_workspace_size(B, W, V, N)
-    ws = torch.full((nb,), 0x7F, dtype=torch.uint8, device=DEV)
-    out = sv.beam_step(z, scores, N, finished=finished, eos=eos, out=_poisoned(B, N), status=status, workspace=ws)
+    out = sv.beam_step(z, scores, N, finished=finished, eos=eos, out=_poisoned(B, N), status=status)
     torch.cuda.synchronize()
     assert int(status) == status_want
     zn, sn = z.float().cpu().numpy(), scores.cpu().numpy()
@@ -57,7 +55,8 @@ def _case(B, W, V, dtype, seed):
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("B,W,V,N", [(1, 1, 1, 1), (2, 1, 2, 4), (3, 2, 5, 4), (2, 3, 9, 64), (4, 4, 1000, 4),
                                      (1, 4, 32000, 8), (5, 8, 4097, 16), (2, 32, 2001, 64), (1, 5, 128256, 10),
-                                     (70, 2, 333, 3)])
+                                     (70, 2, 333, 3), (1, 1, 128256, 64), (1, 31, 32001, 64), (2, 12, 20000, 24),
+                                     (100, 3, 4099, 6), (200, 2, 2051, 4), (700, 1, 1031, 2), (1, 32, 40000, 64)])
 def test_against_reference(B, W, V, N, dtype):
     z, scores, _ = _case(B, W, V, dtype, B + W + V)
     _check(z, scores, N)
@@ -115,8 +114,10 @@ def test_scores_closer_than_fp32_sums_tell_apart(dtype, V):
             for _ in range(steps[w]):
                 s = np.nextafter(s, np.float32(0))
             scores[b, w] = float(s)
-    for N in (4, 6):
+    for N in (2, 4, 6):
         _check(z.to(DEV), scores.to(DEV), N)
+    for n in (1, 2, 3):   # one cluster
+        _check(z[:n].to(DEV), scores[:n].to(DEV), 4)
 
 
 def test_spoilt_beams():
@@ -269,10 +270,9 @@ def test_beam_drafts_verified_and_distilled():
     scores[:, 0] = 0
     toks = torch.zeros((B, W, K), dtype=torch.int32, device=DEV)
     rows = torch.zeros((B, W, K, V), device=DEV)
-    ws = torch.empty(sv.beam_workspace_size(B, W, V, W), dtype=torch.uint8, device=DEV)
     for i in range(K):
         z = torch.einsum("bwd,vd->bwv", state, head)
-        step = sv.beam_step(z, scores, W, workspace=ws)
+        step = sv.beam_step(z, scores, W)
         want = [ref.beam(z[b].cpu().numpy(), scores[b].cpu().numpy(), W) for b in range(B)]
         np.testing.assert_array_equal(step["parent"].cpu().numpy(), np.stack([x[1] for x in want]))
         np.testing.assert_array_equal(step["token"].cpu().numpy(), np.stack([x[2] for x in want]))

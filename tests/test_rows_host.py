@@ -81,9 +81,9 @@ def _step(L, p, z=FAKE, loss=FAKE, g=FAKE + 65536, bs=300, rs=100):
                                bs, rs, None, None)
 
 
-def _beam(L, p, z=FAKE, scores=FAKE, fin=None, eos=-1, out=FAKE + 4096, ws=FAKE, nb=1 << 30):
+def _beam(L, p, z=FAKE, scores=FAKE, fin=None, eos=-1, out=FAKE + 4096):
     return L.spec_beam_step(ctypes.byref(p) if p is not None else None, P(z), P(scores), P(fin) if fin else None, eos,
-                            P(out), P(FAKE), P(FAKE), P(FAKE + 8192), None, P(ws), nb, None)
+                            P(out), P(FAKE), P(FAKE), P(FAKE + 8192), None, None)
 
 
 @pytest.mark.parametrize("kw,code", BAD_ROWS)
@@ -125,12 +125,7 @@ def test_beam_arguments_refused(L):
     assert _beam(L, _rows(), eos=100) == 1 and _beam(L, _rows(), eos=-2) == 1
     assert _beam(L, _rows(), fin=FAKE, eos=-1) == 1
     assert _beam(L, _rows(), scores=0) == 1 and _beam(L, _rows(), out=0) == 1
-    assert _beam(L, _rows(), ws=0) == 1 and _beam(L, _rows(), ws=FAKE + 8) == 1 and _beam(L, _rows(), nb=100) == 1
     assert _beam(L, _rows(), scores=FAKE, out=FAKE) == 1          # in place with N != W
-    assert L.spec_beam_workspace_size(None) == 0
-    assert L.spec_beam_workspace_size(ctypes.byref(_rows(M=65))) == 0
-    n = L.spec_beam_workspace_size(ctypes.byref(_rows()))
-    assert n >= 4 * 3 * 8 * 8 and n % 16 == 0
 
 
 def test_reorder_arguments_refused(L):
@@ -171,8 +166,6 @@ def test_binding_refuses_host_and_misshapen_tensors():
               lambda: sv.beam_reorder(z, ids[..., 0])):
         with pytest.raises(ValueError):
             f()
-    with pytest.raises(sv.SpecError):
-        sv.beam_workspace_size(2, 40, 100, 4)
 
 
 def test_layouts_of_states():
