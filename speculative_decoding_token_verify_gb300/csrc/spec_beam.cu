@@ -77,7 +77,7 @@ struct BeamShared {
 // Dynamic shared memory: lists [units per CTA][N] (logit's key and place), and
 // at the first CTA candidates [W P N + W] and their scores.
 template <typename T>
-__global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P) {
+__global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, int P) {
     __shared__ BeamShared s;
     extern __shared__ __align__(16) unsigned char dyn[];
     const int tid = threadIdx.x;
@@ -116,13 +116,13 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P) {
             float thr;
             bool over = stream_part(p, N, kLog2e, sv::kRescale, s.top, mx, sum, thr);
             if (!over) {
-                expand(p, thr, s.top, [&](uint32_t key, int index) {
-                    const int at = atomicAdd(&s.top.ne, 1);
-                    if (at < CAPE) s.top.el[at] = cand(key, index);
+                over = expand(p, thr, s.top, [&](bool want, unsigned long long c) {
+                    const int at = take(want, &s.top.ne);
+                    if (want && at < CAPE) s.top.el[at] = c;
                 });
                 __syncthreads();
                 ne = s.top.ne;
-                over = ne > CAPE;
+                over |= ne > CAPE;
             }
             if (over) ne = bisect(p, N, max(order_key(thr), 1u), mx, s.top);
             ne = cut(ne, N, s.top);

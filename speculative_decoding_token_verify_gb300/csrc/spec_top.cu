@@ -24,7 +24,7 @@ struct TopArgs {
 };
 
 template <typename T, bool kCluster>
-__global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
+__global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
     __shared__ TopShared s;
     __shared__ float s_x[4][kMaxCluster];   // per CTA of the cluster: bound, maximum, sum, overflow
     const int tid = threadIdx.x;
@@ -57,16 +57,23 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
             sum += s_x[1][i] == m || !(s_x[2][i] > 0.f) ? s_x[2][i] : s_x[2][i] * ex2((s_x[1][i] - m) * a.sL);
         mx = m;
     }
-    // to the cluster's first CTA
+    // to the cluster's first CTA; a part with too many gives up for the row, by a count beyond the room
     if (!over) {
         const uint32_t el0 = kCluster ? peer(s.el, 0) : 0u, ne0 = kCluster ? peer(&s.ne, 0) : 0u;
-        expand(part, thr, s, [&](uint32_t key, int index) {
-            const int at = kCluster ? peer_add(ne0, 1) : atomicAdd(&s.ne, 1);
-            if (at < CAPE) {
-                if (kCluster) peer_store(el0 + 8u * at, cand(key, index));
-                else s.el[at] = cand(key, index);
+        const bool many = expand(part, thr, s, [&](bool want, unsigned long long c) {
+            if (kCluster) {
+                if (!want) return;
+                const int at = peer_add(ne0, 1);
+                if (at < CAPE) peer_store(el0 + 8u * at, c);
+            } else {
+                const int at = take(want, &s.ne);
+                if (want && at < CAPE) s.el[at] = c;
             }
         });
+        if (many && tid == 0) {
+            if (kCluster) peer_add(ne0, CAPE + 1);
+            else atomicAdd(&s.ne, CAPE + 1);
+        }
     }
     if (kCluster) {
         cluster_arrive();

@@ -22,7 +22,13 @@ namespace sr {
 
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
-constexpr int U = 8;         // 16-byte loads in flight per thread
+#ifndef TOP_U
+#define TOP_U 4
+#endif
+#ifndef TOP_OCC
+#define TOP_OCC 4
+#endif
+constexpr int U = TOP_U;         // 16-byte loads of an iteration per thread
 constexpr int CAP = 2048;    // vectors that may pass the filter, per CTA
 constexpr int CAPE = 1024;   // logits that may pass the last bound, per row
 constexpr int kMaxCluster = 8;
@@ -65,10 +71,21 @@ struct TopShared {
     float c[CAP];        // passing vectors: maximum and code (index in the row, or ~index of a single logit)
     int code[CAP];
     __align__(16) unsigned long long el[CAPE];   // candidates
+    int few[CAPE];       // codes of the vectors that pass the last bound
     float b[3][NW], red[2][NW];
     uint32_t kb[NW];
-    int n, ne, cnt[NW];
+    int n, nf, ne, cnt[NW];
 };
+
+// places for the lanes that want one, from a shared counter: one addition a warp
+__device__ __forceinline__ int take(bool want, int *counter) {
+    const unsigned m = __ballot_sync(kFull, want);
+    if (m == 0u) return 0;
+    const int lane = threadIdx.x & 31, lead = __ffs(m) - 1;
+    int at = 0;
+    if (lane == lead) at = atomicAdd(counter, __popc(m));
+    return __shfl_sync(kFull, at, lead) + __popc(m & ((1u << lane) - 1u));
+}
 
 template <typename T, typename F>
 __device__ __forceinline__ void each(const Part<T> &p, F f) {
@@ -151,20 +168,20 @@ __device__ __forceinline__ bool stream_part(const Part<T> &p, int M, float sL, f
     constexpr int E = Row<T>::E;
     const int tid = threadIdx.x, n = p.n;
     const uint4 *body = p.body();
-    if (tid == 0) s.n = s.ne = 0;
+    if (tid == 0) s.n = s.nf = s.ne = 0;
     __syncthreads();
     Sum acc = sum_init(sL, rs);
     thr = sv::kMaskFloor;
     const int its = (n + U * NT - 1) / (U * NT), span = its * NT;
     int refresh = 0;
-    for (int it = 0; it < its; ++it) {
-        uint4 w[U];
-        const int base = it * NT + tid;
+    auto load = [&](uint4 (&w)[U], int it) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int i = u * span + base;
-            w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
+            const int i = u * span + it * NT + tid;
+            w[u] = it < its && i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
         }
+    };
+    auto work = [&](const uint4 (&w)[U], int it) {
         float c[U], cm;
 #pragma unroll
         for (int u = 0; u < U; ++u) c[u] = vec_max<T>(w[u]);
@@ -190,9 +207,19 @@ __device__ __forceinline__ bool stream_part(const Part<T> &p, int M, float sL, f
                 const int at = atomicAdd(&s.n, 1);
                 if (at < CAP) {
                     s.c[at] = c[u];
-                    s.code[at] = p.k0 + u * span + base;
+                    s.code[at] = p.k0 + u * span + it * NT + tid;
                 }
             }
+    };
+    // the next iteration's loads are on their way while one is worked on
+    uint4 w0[U], w1[U];
+    load(w0, 0);
+    for (int it = 0; it < its; it += 2) {
+        load(w1, it + 1);
+        work(w0, it);
+        if (it + 1 >= its) break;
+        load(w0, it + 2);
+        work(w1, it + 1);
     }
     const int e = p.edge(tid);   // the row's ends: single logits
     if (e >= 0) {
@@ -216,28 +243,39 @@ __device__ __forceinline__ bool stream_part(const Part<T> &p, int M, float sL, f
     return s.n > CAP;
 }
 
-// the passing vectors' logits at or above thr
+// The passing vectors' logits at or above thr: put(wanted, candidate) is called
+// by whole warps. Returns whether more vectors reach thr than there is room for.
 template <typename T, typename F>
-__device__ __forceinline__ void expand(const Part<T> &p, float thr, TopShared &s, F put) {
+__device__ __forceinline__ bool expand(const Part<T> &p, float thr, TopShared &s, F put) {
     constexpr int E = Row<T>::E;
     const int np = min(s.n, CAP);
-    auto one = [&](float z, int index) {
-        const uint32_t key = order_key(z);
-        if (z >= thr && key != 0u) put(key, index);
-    };
-    for (int i = threadIdx.x; i < np; i += NT) {
-        const float c = s.c[i];
-        if (!(c >= thr)) continue;
-        const int code = s.code[i];
-        if (code < 0) {
-            one(c, ~code);
-            continue;
-        }
-        float z[E];
-        Elem<T>::unpack(__ldg(p.r.body + code), z);
-#pragma unroll
-        for (int j = 0; j < E; ++j) one(z[j], p.r.vec_index(code) + j);
+    for (int i0 = 0; i0 < np; i0 += NT) {
+        const int i = i0 + threadIdx.x;
+        const bool want = i < np && s.c[i] >= thr;
+        const int at = take(want, &s.nf);
+        if (want && at < CAPE) s.few[at] = s.code[i];
     }
+    __syncthreads();
+    const int nf = s.nf;
+    if (nf > CAPE) return true;
+    // one thread per logit
+    for (int i0 = 0; i0 < nf * E; i0 += 2 * NT) {
+        float z[2];
+        int at[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int i = i0 + k * NT + threadIdx.x, j = i & (E - 1);
+            const int code = i < nf * E ? s.few[i / E] : ~0;
+            at[k] = code >= 0 ? p.r.vec_index(code) + j : ~code;
+            z[k] = i < nf * E && (code >= 0 || j == 0) ? load1(p.r.p + at[k]) : neg_inf();
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t key = order_key(z[k]);
+            put(z[k] >= thr && key != 0u, cand(key, at[k]));
+        }
+    }
+    return false;
 }
 
 // The candidates s.el[0 .. ne) cut down to few more than the M best; returns
@@ -262,15 +300,28 @@ __device__ __forceinline__ int cut(int ne, int M, TopShared &s) {
     return ne;
 }
 
-// f(candidate, rank) for the M best of s.el[0 .. ne)
+// f(candidate, rank) for the M best of s.el[0 .. ne): each candidate's rank is
+// counted by G neighbouring lanes
+template <int G, typename F>
+__device__ __forceinline__ void ranked_by(int ne, int M, const TopShared &s, F f) {
+    const int g = threadIdx.x & (G - 1);
+    for (int i0 = 0; i0 < ne; i0 += NT / G) {
+        const int i = i0 + threadIdx.x / G;
+        const unsigned long long c = i < ne ? s.el[i] : 0ull;
+        int rk = 0;
+#pragma unroll 4
+        for (int j = g; j < ne; j += G) rk += s.el[j] > c;
+#pragma unroll
+        for (int o = G / 2; o > 0; o >>= 1) rk += __shfl_xor_sync(kFull, rk, o);
+        if (g == 0 && i < ne && rk < M) f(c, rk);
+    }
+}
 template <typename F>
 __device__ __forceinline__ void ranked(int ne, int M, const TopShared &s, F f) {
-    for (int i = threadIdx.x; i < ne; i += NT) {
-        const unsigned long long c = s.el[i];
-        int rk = 0;
-        for (int j = 0; j < ne; ++j) rk += s.el[j] > c;
-        if (rk < M) f(c, rk);
-    }
+    if (ne <= NT / 8) ranked_by<8>(ne, M, s, f);
+    else if (ne <= NT / 4) ranked_by<4>(ne, M, s, f);
+    else if (ne <= NT / 2) ranked_by<2>(ne, M, s, f);
+    else ranked_by<1>(ne, M, s, f);
 }
 
 }  // namespace sr
