@@ -2,11 +2,12 @@
 //
 // A sequence's N best continuations over W beams and V tokens are among each
 // beam's N best tokens. One launch: a cluster of C CTAs per sequence, which
-// splits every beam's row into P parts where W parts alone would not share out
-// (W P a multiple of C), streams its parts through the filter of spec_top.cuh
-// and keeps each part's N best logits. The parts' maxima, sums and N-th best
-// meet in every CTA; what can still reach the best part's N-th score goes to
-// the first CTA, which ranks it by
+// splits every beam's row into P parts where whole rows would not share out
+// (W P a multiple of C) and streams its parts through the filter of
+// spec_top.cuh. The parts' maxima, sums and bounds meet in every CTA: N
+// continuations reach the best part's bound as a score, so only vectors that
+// reach it too are looked at, a handful in a whole cluster. Their logits go to
+// the first CTA, which ranks them by
 //   score = cum + ((z - M) - ln S)
 // in fp64. What the order rests on in fewer bits is S alone: every S is off
 // by at most kTol / 2 relatively, so two candidates of different beams whose
@@ -57,37 +58,141 @@ __device__ double precise_sum(const Part<T> &p, float M, double *buf) {
     return S;
 }
 
-// score s at place p ranks before score o at place op
-__device__ __forceinline__ bool before(double s, int p, double o, int op) { return s > o || (s == o && p < op); }
+// fp64 scores as integers of the same order: GB300 compares those far faster
+__device__ __forceinline__ long long score_key(double s) {
+    const long long i = __double_as_longlong(s + 0.0);
+    return i < 0 ? i ^ 0x7fffffffffffffffll : i;
+}
+
+constexpr int kKeep = 128;   // vectors kept of a part when a CTA has several
 
 struct BeamShared {
     TopShared top;
-    float u_mx[kMaxUnits], u_sum[kMaxUnits], u_nth[kMaxUnits];   // of every part of the sequence
-    float cum[SPEC_MAX_BEAMS], base[SPEC_MAX_BEAMS];             // score; score - lse, roughly
+    float u_mx[kMaxUnits], u_sum[kMaxUnits], u_thr[kMaxUnits];   // of every part of the sequence
+    float cum[SPEC_MAX_BEAMS];
     float mx[SPEC_MAX_BEAMS], sum[SPEC_MAX_BEAMS];               // of every row
     int state[SPEC_MAX_BEAMS];                                   // 0 live, 1 finished, 2 none
     double lnS[SPEC_MAX_BEAMS], prec[SPEC_MAX_BEAMS][kMaxCluster], buf[NW];
     double sel[SPEC_MAX_BEAM_OUT + 1];
     int selw[SPEC_MAX_BEAM_OUT + 1], selp[SPEC_MAX_BEAM_OUT + 1];
-    float red[2][NW];
     unsigned need;   // beams to be summed again
     int count;       // candidates at the first CTA
+    int many;        // more candidates than room
 };
 
-// Dynamic shared memory: lists [units per CTA][N] (logit's key and place), and
-// at the first CTA candidates [W P N + W] and their scores.
+// At the first CTA: the N + 1 best of cands[0 .. n) and the finished beams, into
+// s.sel*; with `check` the beams whose order fp32 sums leave open, into s.need.
+// All threads call it; s.selw holds -1 before, a barrier follows.
+__device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s, unsigned long long *cands,
+                                                double *score, int n, bool check) {
+    const int tid = threadIdx.x, N = a.N;
+    __syncthreads();
+    if (check && tid < 32) {   // finished beams join the list, key 0
+        const bool fin = tid < a.W && s.state[tid] == 1;
+        const unsigned m = __ballot_sync(kFull, fin);
+        if (fin) cands[n + __popc(m & ((1u << tid) - 1u))] = (uint32_t)(tid * a.V + a.eos);
+        if (tid == 0) s.count = n + __popc(m);
+    }
+    __syncthreads();
+    n = s.count;
+    auto score_of = [&](unsigned long long c) {
+        const int w = (int)(uint32_t)c / a.V;
+        return cand_key(c) ? (double)s.cum[w] + (((double)key_value(cand_key(c)) - (double)s.mx[w]) - s.lnS[w])
+                           : (double)s.cum[w];
+    };
+    if (n > 64 && check) {   // drop what is well below N + 1 others
+        float best = neg_inf();
+        for (int i = tid; i < n; i += NT) best = fmaxf(best, (float)score_of(cands[i]));
+        float bound = block_bound(best, n, N + 1, neg_inf(), s.top.b[2]);
+        bound -= 1e-3f + 1e-5f * fabsf(bound);
+        if (bound > -1e28f) {   // (the same in every thread)
+            for (int i0 = 0; i0 < n; i0 += NT) {   // in place: a round's reads come before its writes
+                const int i = i0 + tid;
+                const unsigned long long c = i < n ? cands[i] : 0ull;
+                const bool want = i < n && (float)score_of(c) >= bound;
+                if (i0 == 0 && tid == 0) s.count = 0;
+                __syncthreads();
+                const int at = take(want, &s.count);
+                if (want) cands[at] = c;
+                __syncthreads();
+            }
+            n = s.count;
+        }
+    }
+    long long *keys = reinterpret_cast<long long *>(score);
+    for (int i = tid; i < n; i += NT) keys[i] = score_key(score_of(cands[i]));
+    __syncthreads();
+    for (int i = tid; i < n; i += NT) {
+        const long long k = keys[i];
+        const uint32_t place = (uint32_t)cands[i];
+        int rk = 0;
+#pragma unroll 4
+        for (int o = 0; o < n; ++o) {
+            const long long ko = keys[o];
+            rk += ko > k || (ko == k && (uint32_t)cands[o] < place);
+        }
+        if (rk <= N) {
+            s.sel[rk] = score_of(cands[i]);
+            s.selw[rk] = (int)place / a.V;
+            s.selp[rk] = (int)place;
+        }
+    }
+    if (!check) return;
+    __syncthreads();
+    // close neighbours among the selected, and all that is as close behind the last one
+    auto flag = [&](int w) {
+        if (s.state[w] == 0) atomicOr(&s.need, 1u << w);
+    };
+    if (tid < N && s.selw[tid] >= 0 && s.selw[tid + 1] >= 0 && s.selw[tid] != s.selw[tid + 1] &&
+        s.sel[tid] - s.sel[tid + 1] < kTol) {
+        flag(s.selw[tid]);
+        flag(s.selw[tid + 1]);
+    }
+    const int wl = s.selw[N - 1];
+    if (wl >= 0) {
+        const double last = s.sel[N - 1];
+        for (int i = tid; i < n; i += NT) {
+            const int w = (int)(uint32_t)cands[i] / a.V;
+            if (w == wl) continue;
+            const double sc = score_of(cands[i]);
+            if (sc <= last && last - sc < kTol) {
+                flag(w);
+                flag(wl);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ void write_beams(const BeamArgs &a, const BeamShared &s, int b) {
+    for (int i = threadIdx.x; i < a.N; i += NT) {
+        const size_t o = (size_t)b * a.N + i;
+        const int w = s.selw[i];
+        const int token = w >= 0 ? s.selp[i] - w * a.V : -1;
+        a.out_scores[o] = w >= 0 ? (float)s.sel[i] : neg_inf();
+        a.out_parent[o] = w;
+        a.out_token[o] = token;
+        a.out_finished[o] = w >= 0 && token == a.eos ? 1 : 0;
+    }
+}
+
+// Dynamic shared memory: with several parts per CTA their kept vectors (maxima,
+// codes); at the first CTA `room` candidates (logit's key and place; key 0: a
+// finished beam) and their scores.
 template <typename T>
-__global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, int P) {
+__global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, int P, int room) {
+    constexpr int E = Row<T>::E;
     __shared__ BeamShared s;
     extern __shared__ __align__(16) unsigned char dyn[];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 31;
     const int b = blockIdx.x / C, rank = blockIdx.x - b * C;
     const int units = a.W * P, N = a.N;
-    const int most = (units + C - 1) / C;               // parts a CTA may have, and
-    const int mine = (units - rank + C - 1) / C;        // parts this one has (units >= C)
-    unsigned long long *list = reinterpret_cast<unsigned long long *>(dyn);
-    unsigned long long *cands = list + (size_t)most * N;
-    double *score = reinterpret_cast<double *>(cands + (size_t)units * N + a.W);
+    const int most = (units + C - 1) / C;          // parts a CTA may have, and
+    const int mine = (units - rank + C - 1) / C;   // parts this one has (units >= C)
+    unsigned long long *cands = reinterpret_cast<unsigned long long *>(dyn);
+    double *score = reinterpret_cast<double *>(cands + room);
+    float *kept_c = reinterpret_cast<float *>(score + room);                  // [most][kKeep], most > 1
+    int *kept_code = reinterpret_cast<int *>(kept_c + (most > 1 ? most : 0) * kKeep);
+    int *kept = kept_code + (most > 1 ? most : 0) * kKeep;                    // [most] vectors kept, -1: too many
     if (C > 1) cluster_arrive_relaxed();   // waited for before the exchange: by then every CTA of the cluster runs
     if (tid < a.W) {
         const size_t row = (size_t)b * a.W + tid;
@@ -100,199 +205,211 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
     if (tid == 0) {
         s.count = 0;
         s.need = 0u;
+        s.many = 0;
     }
     __syncthreads();
-    auto part_of = [&](int u, int w) {
+    auto part_of = [&](int u) {
+        const int w = u / P;
         return Part<T>(static_cast<const T *>(a.z) + b * a.bs + w * a.rs, a.V, u - w * P, P);
     };
 
     // this CTA's parts
     for (int j = 0; j < mine; ++j) {
-        const int u = rank + j * C, w = u / P;
-        float mx = neg_inf(), sum = 0.f;
-        int ne = 0;
-        if (s.state[w] == 0) {
-            const Part<T> p = part_of(u, w);
-            float thr;
-            bool over = stream_part(p, N, kLog2e, sv::kRescale, s.top, mx, sum, thr);
-            if (!over) {
-                over = expand(p, thr, s.top, [&](bool want, unsigned long long c) {
-                    const int at = take(want, &s.top.ne);
-                    if (want && at < CAPE) s.top.el[at] = c;
-                });
-                __syncthreads();
-                ne = s.top.ne;
-                over |= ne > CAPE;
-            }
-            if (over) ne = bisect(p, N, max(order_key(thr), 1u), mx, s.top);
-            ne = cut(ne, N, s.top);
-            ranked(ne, N, s.top, [&](unsigned long long c, int rk) {
-                list[(size_t)j * N + rk] = ((unsigned long long)cand_key(c) << 32) | (uint32_t)(w * a.V + cand_index(c));
-                if (rk == N - 1) s.u_nth[u] = key_value(cand_key(c));
-            });
+        const int u = rank + j * C;
+        float mx = neg_inf(), sum = 0.f, thr = sv::kMaskFloor;
+        int n = 0;
+        if (s.state[u / P] == 0) {
+            stream_part(part_of(u), N, kLog2e, sv::kRescale, s.top, thr);
+            __syncthreads();
+            part_sum(s.top, kLog2e, mx, sum);
+            n = s.top.n > CAP ? -1 : s.top.n;
+            thr = closer_bound(thr, N, s.top);
         }
-        for (int i = ne + tid; i < N; i += NT) list[(size_t)j * N + i] = 0ull;
+        if (most > 1) {   // keep what still reaches the bound
+            if (n > 0) {
+                for (int i0 = 0; i0 < n; i0 += NT) {
+                    const int i = i0 + tid;
+                    const bool want = i < n && s.top.c[i] >= thr;
+                    const int at = take(want, &s.top.nf);
+                    if (want && at < kKeep) {
+                        kept_c[j * kKeep + at] = s.top.c[i];
+                        kept_code[j * kKeep + at] = s.top.code[i];
+                    }
+                }
+                __syncthreads();
+                n = s.top.nf > kKeep ? -1 : s.top.nf;
+            }
+        }
         if (tid == 0) {
             s.u_mx[u] = mx;
             s.u_sum[u] = sum;
-            if (ne < N) s.u_nth[u] = neg_inf();
+            s.u_thr[u] = thr;
+            kept[j] = n;
         }
-        __syncthreads();
+        if (most > 1) __syncthreads();
     }
     if (C > 1) {
         cluster_wait();
-        for (int i = tid; i < mine * C; i += NT) {   // every part to every CTA
-            const int u = rank + i / C * C, to = i % C;
-            if (to != rank) {
-                peer_store(peer(&s.u_mx[u], to), s.u_mx[u]);
-                peer_store(peer(&s.u_sum[u], to), s.u_sum[u]);
-                peer_store(peer(&s.u_nth[u], to), s.u_nth[u]);
+        if (most == 1) __syncwarp();   // written by this warp's first lane
+        if (tid < 32)
+            for (int i = lane; i < mine * C; i += 32) {   // every part to every CTA
+                const int u = rank + i / C * C, to = i % C;
+                if (to != rank) {
+                    peer_store(peer(&s.u_mx[u], to), s.u_mx[u]);
+                    peer_store(peer(&s.u_sum[u], to), s.u_sum[u]);
+                    peer_store(peer(&s.u_thr[u], to), s.u_thr[u]);
+                }
             }
-        }
-        cluster_arrive();
-        cluster_wait();
-    }
-
-    // rows from their parts
-    if (tid < a.W) {
-        float m = neg_inf(), sum = 0.f;
-        for (int i = 0; i < P; ++i) m = fmaxf(m, s.u_mx[tid * P + i]);
-        for (int i = 0; i < P; ++i) {
-            const float um = s.u_mx[tid * P + i], us = s.u_sum[tid * P + i];
-            sum += um == m || !(us > 0.f) ? us : us * ex2((um - m) * kLog2e);
-        }
-        if (rank == 0 && s.state[tid] == 0 && (!(sum >= 0.f) || m == -neg_inf())) raise_status(a.status, SPEC_ERR_BAD_ROW);
-        s.mx[tid] = m;
-        s.sum[tid] = sum;
-        s.base[tid] = s.cum[tid] - (m + logf(sum));
-    }
-    __syncthreads();
-    // a score that N continuations of one part reach
-    float bound = neg_inf(), mag = 0.f;
-    for (int u = tid; u < units; u += NT)
-        if (s.state[u / P] == 0) {
-            bound = fmaxf(bound, s.base[u / P] + s.u_nth[u]);
-            mag = fmaxf(mag, fabsf(s.cum[u / P]) + fabsf(s.mx[u / P]));
-        }
-    bound = block_max<NT>(bound, s.red[0]);
-    mag = block_max<NT>(mag, s.red[1]);
-    if (mag < INFINITY) bound -= 1e-3f + 1e-5f * (mag + fabsf(bound));   // these scores' roundings, many times over
-    else bound = neg_inf();
-    {
-        const uint32_t c0 = peer(cands, 0), n0 = peer(&s.count, 0);
-        for (int i = tid; i < mine * N; i += NT) {
-            const unsigned long long c = list[i];
-            if (c == 0ull) continue;
-            const int w = (int)(uint32_t)c / a.V;
-            if (!(s.base[w] + key_value(cand_key(c)) >= bound)) continue;
-            const int at = peer_add(n0, 1);   // room for every list of the sequence
-            peer_store(c0 + 8u * at, c);
-        }
-    }
-    if (rank == 0 && tid < a.W && s.state[tid] == 1)   // key 0: a finished beam
-        cands[atomicAdd(&s.count, 1)] = (uint32_t)(tid * a.V + a.eos);
-    if (C > 1) {
         cluster_arrive();
         cluster_wait();
     } else {
         __syncthreads();
     }
 
-    for (int round = 0; round < 2; ++round) {
+    // rows from their parts, in every warp: lane w has row w
+    float base = __int_as_float(0x7fc00000), mag = 0.f;   // score - lse, roughly; NaN: no continuations
+    if (lane < a.W && s.state[lane] == 0) {
+        float m = neg_inf(), sum = 0.f;
+        for (int i = 0; i < P; ++i) m = fmaxf(m, s.u_mx[lane * P + i]);
+        for (int i = 0; i < P; ++i) sum += moved(s.u_sum[lane * P + i], s.u_mx[lane * P + i], m, kLog2e);
+        const bool bad = !(sum >= 0.f) || m == -neg_inf();
+        if (m > sv::kMaskFloor && !bad) {
+            base = s.cum[lane] - (m + logf(sum));
+            mag = fabsf(s.cum[lane]) + fabsf(m);
+        }
+        if (tid < 32) {
+            if (rank == 0 && bad) raise_status(a.status, SPEC_ERR_BAD_ROW);
+            s.mx[lane] = m;
+            s.sum[lane] = sum;
+            if (rank == 0) s.lnS[lane] = log((double)sum);
+        }
+    }
+    // a score that N continuations of one part reach, less these scores'
+    // roundings many times over
+    float bound = neg_inf();
+    for (int u0 = 0; u0 < units; u0 += 32) {
+        const int u = min(u0 + lane, units - 1);
+        bound = fmaxf(bound, __shfl_sync(kFull, base, u / P) + s.u_thr[u]);
+    }
+    bound = warp_max(bound);
+    mag = warp_max(mag);
+    bound -= 1e-3f + 1e-5f * (mag + fabsf(bound));
+    if (!(bound > -1e28f)) bound = neg_inf();
+
+    // candidates are gathered in s.top.el, then handed over
+    auto push = [&](int w, float bw, float z, int index) {
+        const uint32_t key = order_key(z);
+        if (key == 0u || !(bw + z >= bound)) return;
+        const int at = atomicAdd(&s.top.ne, 1);
+        if (at < CAPE) s.top.el[at] = ((unsigned long long)key << 32) | (uint32_t)(w * a.V + index);
+    };
+    bool exact = false;   // every part's N best, found by bisection
+    for (;;) {
+        __syncthreads();
+        if (tid == 0) s.top.ne = 0;
+        __syncthreads();
+        for (int j = 0; j < mine; ++j) {
+            const int u = rank + j * C, w = u / P, n = kept[j];
+            const float bw = __shfl_sync(kFull, base, w);
+            if (!(bw == bw) || exact || n < 0) continue;   // (the same in every thread)
+            const Part<T> p = part_of(u);
+            const float *lc = most > 1 ? kept_c + j * kKeep : s.top.c;
+            const int *lcode = most > 1 ? kept_code + j * kKeep : s.top.code;
+            for (int i = tid; i < n; i += NT) {
+                const float c = lc[i];
+                if (!(bw + c >= bound)) continue;
+                const int code = lcode[i];
+                if (code < 0) {
+                    push(w, bw, c, ~code);
+                    continue;
+                }
+                float z[E];
+                Elem<T>::unpack(__ldg(p.r.body + code), z);
+#pragma unroll
+                for (int k = 0; k < E; ++k) push(w, bw, z[k], p.r.vec_index(code) + k);
+            }
+        }
+        __syncthreads();
+        {   // more than there is room for here counts as more than there is room for there
+            const int n = s.top.ne > CAPE ? CAPE + room : s.top.ne;
+            hand_over(n, [&](int i) { return s.top.el[min(i, CAPE - 1)]; }, cands, &s.count, room - a.W, &s.top.off);
+        }
+        for (int j = 0; j < mine; ++j) {
+            const int u = rank + j * C, w = u / P;
+            const float bw = __shfl_sync(kFull, base, w);
+            if (!(bw == bw) || !(exact || kept[j] < 0)) continue;
+            __syncthreads();
+            const int ne = bisect(part_of(u), N, 1u, s.u_mx[u], s.top);
+            hand_over(ne, [&](int i) {
+                const unsigned long long c = s.top.el[i];
+                return ((unsigned long long)cand_key(c) << 32) | (uint32_t)(w * a.V + cand_index(c));
+            }, cands, &s.count, room - a.W, &s.top.off);
+        }
+        if (C > 1) {
+            cluster_arrive();
+            cluster_wait();
+        } else {
+            __syncthreads();
+        }
         if (rank == 0) {
-            const int n = s.count;
-            if (round == 0 && tid < a.W) s.lnS[tid] = log((double)s.sum[tid]);
+            // the order, by scores in fp64
+            const bool many = s.count > room - a.W;
+            const int n = many ? 0 : s.count;
             if (tid <= N) s.selw[tid] = -1;
-            __syncthreads();
-            for (int i = tid; i < n; i += NT) {
-                const unsigned long long c = cands[i];
-                const int w = (int)(uint32_t)c / a.V;
-                score[i] = cand_key(c) ? (double)s.cum[w] + (((double)key_value(cand_key(c)) - (double)s.mx[w]) - s.lnS[w])
-                                       : (double)s.cum[w];
+            if (many) {
+                if (tid == 0) s.many = 1;
+                __syncthreads();   // everyone has read the count
+                if (tid == 0) s.count = 0;
+            } else {
+                rank_candidates(a, s, cands, score, n, true);
             }
             __syncthreads();
-            for (int i = tid; i < n; i += NT) {
-                const double sc = score[i];
-                const int place = (int)(uint32_t)cands[i];
-                int rk = 0;
-                for (int o = 0; o < n; ++o) rk += before(score[o], (int)(uint32_t)cands[o], sc, place);
-                if (rk <= N) {
-                    s.sel[rk] = sc;
-                    s.selw[rk] = place / a.V;
-                    s.selp[rk] = place;
-                }
-            }
-            __syncthreads();
-            if (round == 0) {
-                // close neighbours among the selected, and all that is as close behind the last one
-                auto flag = [&](int w) {
-                    if (s.state[w] == 0) atomicOr(&s.need, 1u << w);
-                };
-                if (tid < N && s.selw[tid] >= 0 && s.selw[tid + 1] >= 0 && s.selw[tid] != s.selw[tid + 1] &&
-                    s.sel[tid] - s.sel[tid + 1] < kTol) {
-                    flag(s.selw[tid]);
-                    flag(s.selw[tid + 1]);
-                }
-                const int wl = s.selw[N - 1];
-                if (wl >= 0) {
-                    const double last = s.sel[N - 1];
-                    for (int i = tid; i < n; i += NT) {
-                        const int w = (int)(uint32_t)cands[i] / a.V;
-                        if (w != wl && score[i] <= last && last - score[i] < kTol) {
-                            flag(w);
-                            flag(wl);
-                        }
-                    }
-                }
-                __syncthreads();
-                if (C > 1 && tid < C && tid > 0) {
-                    uint32_t at = peer(&s.need, tid);
-                    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(s.need) : "memory");
-                }
-            }
-        }
-        if (round == 1) break;
-        if (C > 1) {
-            cluster_arrive();
-            cluster_wait();
-        } else {
-            __syncthreads();
-        }
-        const unsigned need = s.need;
-        if (need == 0u) break;
-        for (int w = 0; w < a.W; ++w) {
-            if (!(need >> w & 1u)) continue;
-            const Part<T> p(static_cast<const T *>(a.z) + b * a.bs + w * a.rs, a.V, rank, C);
-            const double S = precise_sum(p, s.mx[w], s.buf);
-            if (tid == 0) {
-                const uint32_t at = peer(&s.prec[w][rank], 0);
-                peer_store(at, (unsigned long long)__double_as_longlong(S));
+            if (C > 1 && tid > 0 && tid < C) {
+                peer_store_u32(peer(&s.need, tid), s.need);
+                peer_store_u32(peer(&s.many, tid), many ? 1u : 0u);
             }
         }
         if (C > 1) {
             cluster_arrive();
+            if (rank == 0 && !s.many && s.need == 0u) write_beams(a, s, b);
             cluster_wait();
         } else {
             __syncthreads();
+            if (!s.many && s.need == 0u) write_beams(a, s, b);
         }
-        if (rank != 0) break;
-        if (tid < a.W && need >> tid & 1u) {
-            double S = 0.0;
-            for (int i = 0; i < C; ++i) S += s.prec[tid][i];
-            s.lnS[tid] = log(S);
-        }
+        if (!s.many || exact) break;
+        exact = true;
+        __syncthreads();
+        if (tid == 0) s.many = 0;   // (the first CTA publishes it again before it is read again)
+        __syncthreads();
+    }
+    const unsigned need = s.need;
+    if (need == 0u) return;
+
+    // the beams concerned once more, every CTA a part of each
+    for (int w = 0; w < a.W; ++w) {
+        if (!(need >> w & 1u)) continue;
+        const Part<T> p(static_cast<const T *>(a.z) + b * a.bs + w * a.rs, a.V, rank, C);
+        const double S = precise_sum(p, s.mx[w], s.buf);
+        if (tid == 0) peer_store(peer(&s.prec[w][rank], 0), (unsigned long long)__double_as_longlong(S));
+    }
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
         __syncthreads();
     }
     if (rank != 0) return;
-    for (int i = tid; i < N; i += NT) {
-        const size_t o = (size_t)b * N + i;
-        const int w = s.selw[i];
-        const int token = w >= 0 ? s.selp[i] - w * a.V : -1;
-        a.out_scores[o] = w >= 0 ? (float)s.sel[i] : neg_inf();
-        a.out_parent[o] = w;
-        a.out_token[o] = token;
-        a.out_finished[o] = w >= 0 && token == a.eos ? 1 : 0;
+    if (tid < a.W && need >> tid & 1u) {
+        double S = 0.0;
+        for (int i = 0; i < C; ++i) S += s.prec[tid][i];
+        s.lnS[tid] = log(S);
     }
+    if (tid <= N) s.selw[tid] = -1;
+    __syncthreads();
+    rank_candidates(a, s, cands, score, s.count, false);
+    __syncthreads();
+    write_beams(a, s, b);
 }
 
 // CTAs per sequence and parts per row. Clusters as large as fill the SMs' 608
@@ -311,14 +428,15 @@ static void beam_plan(const spec_rows_params *p, int es, int &C, int &P) {
 
 template <typename T>
 static cudaError_t launch_beam(const BeamArgs &a, int C, int P, cudaStream_t stream) {
-    const size_t units = (size_t)a.W * P, most = (units + C - 1) / C;
-    const size_t smem = (most * a.N + 2 * (units * a.N + a.W)) * 8;
+    const int units = a.W * P, most = (units + C - 1) / C;
+    const int room = (units * a.N > 1024 ? units * a.N : 1024) + a.W;
+    const size_t smem = (size_t)room * 16 + (most > 1 ? (size_t)most * kKeep * 8 : 0) + (size_t)most * 4;
     static std::mutex mu;
     static bool done[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (smem > 12 * 1024) {
+    if (smem > 8 * 1024) {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev & 63]) {
             e = cudaFuncSetAttribute(beam_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
@@ -326,7 +444,7 @@ static cudaError_t launch_beam(const BeamArgs &a, int C, int P, cudaStream_t str
             done[dev & 63] = true;
         }
     }
-    return launch_cluster(beam_kernel<T>, (unsigned)(a.B * C), NT, C, smem, stream, a, C, P);
+    return launch_cluster(beam_kernel<T>, (unsigned)(a.B * C), NT, C, smem, stream, a, C, P, room);
 }
 
 static int check_beam(const spec_rows_params *p) {

@@ -155,11 +155,6 @@ struct __align__(16) Known {
     float Bh, Bl;    // sum of p (l - s y), in two floats
 };
 
-// a sum against m, moved to the larger maximum `to`
-__device__ __forceinline__ float moved(float sum, float m, float to, float sL) {
-    return sum != 0.f && m != to ? sum * ex2((m - to) * sL) : sum;
-}
-
 // a two-float sum with the lane o away; both lanes get the same bits
 __device__ __forceinline__ void pair_total(float &h, float &l, int o) {
     const float a = __shfl_xor_sync(kFull, h, o), b = __shfl_xor_sync(kFull, l, o);

@@ -174,6 +174,11 @@ __device__ __forceinline__ float sum_at(const Sum &a, float M, float sL) {
     return a.mx > sv::kMaskFloor || S != 0.f ? S * ex2(fmaf(a.mr - M, sL, -a.eps)) : 0.f;
 }
 
+// a sum against the maximum m, moved to the larger maximum `to`
+__device__ __forceinline__ float moved(float sum, float m, float to, float sL) {
+    return sum != 0.f && m != to ? sum * ex2((m - to) * sL) : sum;
+}
+
 template <typename T>
 __device__ __forceinline__ float vec_max(const uint4 &w) {
     if constexpr (sizeof(T) == 2) {
@@ -318,9 +323,19 @@ __device__ __forceinline__ float block_sum(float v, float *buf) {
 // ---- thread-block clusters ----------------------------------------------------------
 
 // (relaxed: by threads that publish nothing)
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The aligned forms want whole warps.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // the address of a shared variable in CTA `rank` of the cluster
 __device__ __forceinline__ uint32_t peer(const void *p, int rank) {
     uint32_t a;
@@ -332,6 +347,9 @@ __device__ __forceinline__ void peer_store(uint32_t a, float v) {
 }
 __device__ __forceinline__ void peer_store(uint32_t a, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ void peer_store_u32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ int peer_add(uint32_t a, int v) {
     int r;

@@ -27,6 +27,7 @@ template <typename T, bool kCluster>
 __global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
     __shared__ TopShared s;
     __shared__ float s_x[4][kMaxCluster];   // per CTA of the cluster: bound, maximum, sum, overflow
+    __shared__ int s_ns;
     const int tid = threadIdx.x;
     const int row = kCluster ? blockIdx.x / S : blockIdx.x;
     const int rank = kCluster ? blockIdx.x - row * S : 0;
@@ -35,7 +36,11 @@ __global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
     const T *z = static_cast<const T *>(a.z) + b * a.batch_stride + kr * a.row_stride;
     const Part<T> part(z, a.V, rank, kCluster ? S : 1);
     float mx, sum, thr;
-    bool over = stream_part(part, a.M, a.sL, a.rs, s, mx, sum, thr);
+    stream_part(part, a.M, a.sL, a.rs, s, thr);
+    __syncthreads();
+    bool over = s.n > CAP;
+    thr = closer_bound(thr, a.M, s);
+    part_sum(s, a.sL, mx, sum);
     if (kCluster) {
         cluster_wait();
         if (tid < S) {
@@ -46,33 +51,30 @@ __global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
         }
         cluster_arrive();
         cluster_wait();
-        float m = neg_inf();
+        mx = neg_inf();
         for (int i = 0; i < S; ++i) {
             thr = fmaxf(thr, s_x[0][i]);
-            m = fmaxf(m, s_x[1][i]);
+            mx = fmaxf(mx, s_x[1][i]);
             over |= s_x[3][i] != 0.f;
         }
         sum = 0.f;
-        for (int i = 0; i < S; ++i)
-            sum += s_x[1][i] == m || !(s_x[2][i] > 0.f) ? s_x[2][i] : s_x[2][i] * ex2((s_x[1][i] - m) * a.sL);
-        mx = m;
+        for (int i = 0; i < S; ++i) sum += moved(s_x[2][i], s_x[1][i], mx, a.sL);
     }
-    // to the cluster's first CTA; a part with too many gives up for the row, by a count beyond the room
+    // to the cluster's first CTA, by way of the list of passing vectors, which
+    // is read by then; a part with too many gives up for the row, by a count
+    // beyond the room
+    if (kCluster && tid == 0) s_ns = 0;
     if (!over) {
-        const uint32_t el0 = kCluster ? peer(s.el, 0) : 0u, ne0 = kCluster ? peer(&s.ne, 0) : 0u;
+        unsigned long long *stage = reinterpret_cast<unsigned long long *>(s.c);
         const bool many = expand(part, thr, s, [&](bool want, unsigned long long c) {
-            if (kCluster) {
-                if (!want) return;
-                const int at = peer_add(ne0, 1);
-                if (at < CAPE) peer_store(el0 + 8u * at, c);
-            } else {
-                const int at = take(want, &s.ne);
-                if (want && at < CAPE) s.el[at] = c;
-            }
+            const int at = take(want, kCluster ? &s_ns : &s.ne);
+            if (want && at < CAPE) (kCluster ? stage : s.el)[at] = c;
         });
-        if (many && tid == 0) {
-            if (kCluster) peer_add(ne0, CAPE + 1);
-            else atomicAdd(&s.ne, CAPE + 1);
+        if (kCluster) {
+            __syncthreads();
+            hand_over(many ? CAPE + 1 : s_ns, [&](int i) { return stage[min(i, CAPE - 1)]; }, s.el, &s.ne, CAPE, &s.off);
+        } else if (many && tid == 0) {
+            s.ne = CAPE + 1;
         }
     }
     if (kCluster) {

@@ -72,9 +72,9 @@ struct TopShared {
     int code[CAP];
     __align__(16) unsigned long long el[CAPE];   // candidates
     int few[CAPE];       // codes of the vectors that pass the last bound
-    float b[3][NW], red[2][NW];
+    float b[3][NW], w_mx[NW], w_sum[NW];
     uint32_t kb[NW];
-    int n, nf, ne, cnt[NW];
+    int n, nf, ne, off, cnt[NW];
 };
 
 // places for the lanes that want one, from a shared counter: one addition a warp
@@ -158,13 +158,12 @@ __device__ __noinline__ int bisect(const Part<T> &p, int M, uint32_t t, float mx
     return n;
 }
 
-// One pass over a part: its maximum and sum, a bound `thr` with at least M of
-// its logits at or above it (or the mask's floor), and the vectors that may
-// hold listed tokens. Returns whether more passed than the list holds; every
-// thread gets the same values.
+// One pass over a part: a bound `thr` with at least M of its logits at or above
+// it (or the mask's floor; the same in every thread), the vectors that may hold
+// listed tokens in s.c and s.code, every warp's maximum and sum in s.w_mx and
+// s.w_sum. The caller's next barrier publishes all of it.
 template <typename T>
-__device__ __forceinline__ bool stream_part(const Part<T> &p, int M, float sL, float rs, TopShared &s, float &mx,
-                                            float &sum, float &thr) {
+__device__ __forceinline__ void stream_part(const Part<T> &p, int M, float sL, float rs, TopShared &s, float &thr) {
     constexpr int E = Row<T>::E;
     const int tid = threadIdx.x, n = p.n;
     const uint4 *body = p.body();
@@ -233,14 +232,42 @@ __device__ __forceinline__ bool stream_part(const Part<T> &p, int M, float sL, f
             }
         }
     }
-    mx = block_max<NT>(acc.mx, s.red[0]);
-    sum = block_sum<NT>(sum_at(acc, mx, sL), s.red[1]);
-    // (the barriers above also publish the list)
+    const float m = warp_max(acc.mx), v = warp_sum(sum_at(acc, m, sL));
+    if ((tid & 31) == 0) {
+        s.w_mx[tid >> 5] = m;
+        s.w_sum[tid >> 5] = v;
+    }
+}
+
+// the part's maximum and sum, after the barrier
+__device__ __forceinline__ void part_sum(const TopShared &s, float sL, float &mx, float &sum) {
+    mx = s.w_mx[0];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) mx = fmaxf(mx, s.w_mx[i]);
+    sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) sum += moved(s.w_sum[i], s.w_mx[i], mx, sL);
+}
+
+// a closer bound from the passing vectors' maxima
+__device__ __forceinline__ float closer_bound(float thr, int M, TopShared &s) {
     const int np = min(s.n, CAP);
     float best = neg_inf();
-    for (int i = tid; i < np; i += NT) best = fmaxf(best, s.c[i]);
-    thr = block_bound(best, np, M, thr, s.b[2]);
-    return s.n > CAP;
+    for (int i = threadIdx.x; i < np; i += NT) best = fmaxf(best, s.c[i]);
+    return block_bound(best, np, M, thr, s.b[2]);
+}
+
+// `n` words from this CTA's shared memory to the list `to` of the cluster's
+// first CTA, behind what other CTAs have put there; `counter` counts them all,
+// past `room` too. One remote addition per CTA: they are slow, and one after
+// another. All threads call it; a barrier follows.
+template <typename F>
+__device__ __forceinline__ void hand_over(int n, F word, unsigned long long *to, int *counter, int room, int *off) {
+    if (threadIdx.x == 0) *off = peer_add(peer(counter, 0), n);
+    __syncthreads();
+    const uint32_t at = peer(to, 0);
+    for (int i = threadIdx.x; i < n; i += NT)
+        if (*off + i < room) peer_store(at + 8u * (*off + i), word(i));
 }
 
 // The passing vectors' logits at or above thr: put(wanted, candidate) is called
