@@ -9,7 +9,7 @@
 // reach it too are looked at, a handful in a whole cluster. Their logits go to
 // the first CTA, which ranks them by
 //   score = cum + ((z - M) - ln S)
-// in fp64. What the order rests on in fewer bits is S alone: every S is off
+// in two floats. What the order rests on in fewer bits is S alone: every S is off
 // by at most kTol / 2 relatively, so two candidates of different beams whose
 // scores differ by less than kTol may be in the wrong order. Where that
 // touches a selected place, all CTAs sum the beams concerned again in two-float
@@ -23,7 +23,7 @@ namespace sr {
 // |relative error of S| <= kTol / 2: exponentials of 2^-22 and their
 // arguments' rounding (|y| 2^-25 ln 2, |y| <= 24 where the mass is), and
 // at most 32 roundings of 2^-24 on the way of a term into the sum
-constexpr double kTol = 8.0e-6;
+constexpr float kTol = 8.0e-6f;
 constexpr int kMaxUnits = SPEC_MAX_BEAMS * kMaxCluster;   // parts of a sequence
 
 struct BeamArgs {
@@ -58,10 +58,41 @@ __device__ double precise_sum(const Part<T> &p, float M, double *buf) {
     return S;
 }
 
-// fp64 scores as integers of the same order: GB300 compares those far faster
-__device__ __forceinline__ long long score_key(double s) {
-    const long long i = __double_as_longlong(s + 0.0);
-    return i < 0 ? i ^ 0x7fffffffffffffffll : i;
+// Scores are kept in two floats h + l, |l| <= half a step of h (about 2^-48 of
+// the score): GB300's fp64 rate makes the same sums in fp64 many times slower.
+struct Score {
+    float h, l;
+};
+// cum + (z - M) - lnS
+__device__ __forceinline__ Score score_sum(float cum, float z, float M, Score lnS) {
+    float h, l, e;
+    two_sum(z, -M, h, l);
+    two_sum(h, -lnS.h, h, e);
+    l += e - lnS.l;
+    two_sum(h, cum, h, e);
+    l += e;
+    two_sum(h, l, h, l);
+    return {h, l};
+}
+// as an integer of the same order
+__device__ __forceinline__ unsigned long long score_key(Score s) {
+    const auto ordered = [](float x) {
+        const int i = __float_as_int(x + 0.f);
+        return i < 0 ? ~(uint32_t)i : (uint32_t)i | 0x80000000u;
+    };
+    return ((unsigned long long)ordered(s.h) << 32) | ordered(s.l);
+}
+__device__ __forceinline__ float score_diff(Score a, Score b) { return (a.h - b.h) + (a.l - b.l); }
+
+// ln S in two floats: one Newton step from logf, S = Sh + Sl
+__device__ __forceinline__ Score ln_pair(float Sh, float Sl) {
+    const float g = logf(Sh);
+    float eh, el;
+    exp_diff(g, 0.f, eh, el);
+    const float r = ((Sh - eh) + (Sl - el)) / Sh;
+    float h, l;
+    two_sum(g, r, h, l);
+    return {h, l};
 }
 
 constexpr int kKeep = 128;   // vectors kept of a part when a CTA has several
@@ -72,8 +103,9 @@ struct BeamShared {
     float cum[SPEC_MAX_BEAMS];
     float mx[SPEC_MAX_BEAMS], sum[SPEC_MAX_BEAMS];               // of every row
     int state[SPEC_MAX_BEAMS];                                   // 0 live, 1 finished, 2 none
-    double lnS[SPEC_MAX_BEAMS], prec[SPEC_MAX_BEAMS][kMaxCluster], buf[NW];
-    double sel[SPEC_MAX_BEAM_OUT + 1];
+    Score lnS[SPEC_MAX_BEAMS];
+    double prec[SPEC_MAX_BEAMS][kMaxCluster], buf[NW];
+    Score sel[SPEC_MAX_BEAM_OUT + 1];
     int selw[SPEC_MAX_BEAM_OUT + 1], selp[SPEC_MAX_BEAM_OUT + 1];
     unsigned need;   // beams to be summed again
     int count;       // candidates at the first CTA
@@ -84,7 +116,7 @@ struct BeamShared {
 // s.sel*; with `check` the beams whose order fp32 sums leave open, into s.need.
 // All threads call it; s.selw holds -1 before, a barrier follows.
 __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s, unsigned long long *cands,
-                                                double *score, int n, bool check) {
+                                                unsigned long long *keys, int n, bool check) {
     const int tid = threadIdx.x, N = a.N;
     __syncthreads();
     if (check && tid < 32) {   // finished beams join the list, key 0
@@ -95,21 +127,21 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
     }
     __syncthreads();
     n = s.count;
-    auto score_of = [&](unsigned long long c) {
+    auto score_of = [&](unsigned long long c) -> Score {
         const int w = (int)(uint32_t)c / a.V;
-        return cand_key(c) ? (double)s.cum[w] + (((double)key_value(cand_key(c)) - (double)s.mx[w]) - s.lnS[w])
-                           : (double)s.cum[w];
+        if (!cand_key(c)) return {s.cum[w], 0.f};
+        return score_sum(s.cum[w], key_value(cand_key(c)), s.mx[w], s.lnS[w]);
     };
     if (n > 64 && check) {   // drop what is well below N + 1 others
         float best = neg_inf();
-        for (int i = tid; i < n; i += NT) best = fmaxf(best, (float)score_of(cands[i]));
+        for (int i = tid; i < n; i += NT) best = fmaxf(best, score_of(cands[i]).h);
         float bound = block_bound(best, n, N + 1, neg_inf(), s.top.b[2]);
         bound -= 1e-3f + 1e-5f * fabsf(bound);
         if (bound > -1e28f) {   // (the same in every thread)
             for (int i0 = 0; i0 < n; i0 += NT) {   // in place: a round's reads come before its writes
                 const int i = i0 + tid;
                 const unsigned long long c = i < n ? cands[i] : 0ull;
-                const bool want = i < n && (float)score_of(c) >= bound;
+                const bool want = i < n && score_of(c).h >= bound;
                 if (i0 == 0 && tid == 0) s.count = 0;
                 __syncthreads();
                 const int at = take(want, &s.count);
@@ -119,16 +151,15 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
             n = s.count;
         }
     }
-    long long *keys = reinterpret_cast<long long *>(score);
     for (int i = tid; i < n; i += NT) keys[i] = score_key(score_of(cands[i]));
     __syncthreads();
     for (int i = tid; i < n; i += NT) {
-        const long long k = keys[i];
+        const unsigned long long k = keys[i];
         const uint32_t place = (uint32_t)cands[i];
         int rk = 0;
 #pragma unroll 4
         for (int o = 0; o < n; ++o) {
-            const long long ko = keys[o];
+            const unsigned long long ko = keys[o];
             rk += ko > k || (ko == k && (uint32_t)cands[o] < place);
         }
         if (rk <= N) {
@@ -144,18 +175,18 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
         if (s.state[w] == 0) atomicOr(&s.need, 1u << w);
     };
     if (tid < N && s.selw[tid] >= 0 && s.selw[tid + 1] >= 0 && s.selw[tid] != s.selw[tid + 1] &&
-        s.sel[tid] - s.sel[tid + 1] < kTol) {
+        score_diff(s.sel[tid], s.sel[tid + 1]) < kTol) {
         flag(s.selw[tid]);
         flag(s.selw[tid + 1]);
     }
     const int wl = s.selw[N - 1];
     if (wl >= 0) {
-        const double last = s.sel[N - 1];
+        const Score last = s.sel[N - 1];
         for (int i = tid; i < n; i += NT) {
             const int w = (int)(uint32_t)cands[i] / a.V;
             if (w == wl) continue;
-            const double sc = score_of(cands[i]);
-            if (sc <= last && last - sc < kTol) {
+            const float d = score_diff(last, score_of(cands[i]));
+            if (d >= 0.f && d < kTol) {
                 flag(w);
                 flag(wl);
             }
@@ -168,7 +199,7 @@ __device__ __forceinline__ void write_beams(const BeamArgs &a, const BeamShared 
         const size_t o = (size_t)b * a.N + i;
         const int w = s.selw[i];
         const int token = w >= 0 ? s.selp[i] - w * a.V : -1;
-        a.out_scores[o] = w >= 0 ? (float)s.sel[i] : neg_inf();
+        a.out_scores[o] = w >= 0 ? s.sel[i].h : neg_inf();
         a.out_parent[o] = w;
         a.out_token[o] = token;
         a.out_finished[o] = w >= 0 && token == a.eos ? 1 : 0;
@@ -189,8 +220,8 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
     const int most = (units + C - 1) / C;          // parts a CTA may have, and
     const int mine = (units - rank + C - 1) / C;   // parts this one has (units >= C)
     unsigned long long *cands = reinterpret_cast<unsigned long long *>(dyn);
-    double *score = reinterpret_cast<double *>(cands + room);
-    float *kept_c = reinterpret_cast<float *>(score + room);                  // [most][kKeep], most > 1
+    unsigned long long *keys = cands + room;
+    float *kept_c = reinterpret_cast<float *>(keys + room);                  // [most][kKeep], most > 1
     int *kept_code = reinterpret_cast<int *>(kept_c + (most > 1 ? most : 0) * kKeep);
     int *kept = kept_code + (most > 1 ? most : 0) * kKeep;                    // [most] vectors kept, -1: too many
     if (C > 1) cluster_arrive_relaxed();   // waited for before the exchange: by then every CTA of the cluster runs
@@ -281,7 +312,7 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
             if (rank == 0 && bad) raise_status(a.status, SPEC_ERR_BAD_ROW);
             s.mx[lane] = m;
             s.sum[lane] = sum;
-            if (rank == 0) s.lnS[lane] = log((double)sum);
+            if (rank == 0) s.lnS[lane] = ln_pair(sum, 0.f);
         }
     }
     // a score that N continuations of one part reach, less these scores'
@@ -352,7 +383,6 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
             __syncthreads();
         }
         if (rank == 0) {
-            // the order, by scores in fp64
             const bool many = s.count > room - a.W;
             const int n = many ? 0 : s.count;
             if (tid <= N) s.selw[tid] = -1;
@@ -361,7 +391,7 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
                 __syncthreads();   // everyone has read the count
                 if (tid == 0) s.count = 0;
             } else {
-                rank_candidates(a, s, cands, score, n, true);
+                rank_candidates(a, s, cands, keys, n, true);
             }
             __syncthreads();
             if (C > 1 && tid > 0 && tid < C) {
@@ -403,11 +433,12 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
     if (tid < a.W && need >> tid & 1u) {
         double S = 0.0;
         for (int i = 0; i < C; ++i) S += s.prec[tid][i];
-        s.lnS[tid] = log(S);
+        const float h = (float)S;
+        s.lnS[tid] = ln_pair(h, (float)(S - (double)h));
     }
     if (tid <= N) s.selw[tid] = -1;
     __syncthreads();
-    rank_candidates(a, s, cands, score, s.count, false);
+    rank_candidates(a, s, cands, keys, s.count, false);
     __syncthreads();
     write_beams(a, s, b);
 }
