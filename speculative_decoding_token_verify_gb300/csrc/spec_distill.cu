@@ -31,10 +31,6 @@ namespace sr {
 
 constexpr int UG = 8;   // vectors per thread of the gradient alone
 constexpr int kMaxCluster = 8;
-#ifndef STEP_U
-#define STEP_U 8
-#define STEP_NT 256
-#endif
 
 struct DistillArgs {
     const void *y;
@@ -194,7 +190,7 @@ struct Row2 {
 };
 
 template <typename T, bool kGrad, int NT, int U>
-__global__ void __launch_bounds__(NT, 8192 / (NT * U)) distill_kernel(DistillArgs a, int S) {
+__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S) {
     constexpr int E = Row<T>::E, NW = NT / 32;
     extern __shared__ __align__(16) uint8_t s_map[];
     __shared__ int s_ids[SPEC_MAX_TOP], s_dup;
@@ -208,12 +204,15 @@ __global__ void __launch_bounds__(NT, 8192 / (NT * U)) distill_kernel(DistillArg
     const Part<T> part(py, a.V, rank, S);
     const int n = part.n, its = (n + U * NT - 1) / (U * NT);
     const uint4 *body = part.body();
-    uint4 w[U];
+    auto load = [&](uint4 (&w)[U], int it) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {   // on their way during the list's work
-        const int i = u * NT + tid;
-        w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
-    }
+        for (int u = 0; u < U; ++u) {
+            const int i = (it * U + u) * NT + tid;
+            w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
+        }
+    };
+    uint4 w0[U], w1[U];   // iterations it and it + 1; the first is on its way during the list's work
+    load(w0, 0);
 
     const float wt = a.weight ? a.weight[row] : 1.f;
     int id = -1;
@@ -304,14 +303,7 @@ __global__ void __launch_bounds__(NT, 8192 / (NT * U)) distill_kernel(DistillArg
 
     // the unlisted tokens' sum
     Sum acc = sum_init(a.sL, a.resc);
-    for (int it = 0; it < its; ++it) {
-        if (it > 0) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = (it * U + u) * NT + tid;
-                w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
-            }
-        }
+    auto work = [&](const uint4 (&w)[U], int it) {
         uint32_t bits[U];
         float cm = neg_inf();
 #pragma unroll
@@ -341,6 +333,13 @@ __global__ void __launch_bounds__(NT, 8192 / (NT * U)) distill_kernel(DistillArg
             v += sum_terms<E>(acc, z, a.sL);
         }
         sum_put(acc, v);
+    };
+    for (int it = 0; it < its; it += 2) {   // both buffers end up with the last two iterations
+        if (it + 1 < its) load(w1, it + 1);
+        work(w0, it);
+        if (it + 1 >= its) break;
+        if (it + 2 < its) load(w0, it + 2);
+        work(w1, it + 1);
     }
     {
         const int i = part.edge(tid);
@@ -431,19 +430,22 @@ __global__ void __launch_bounds__(NT, 8192 / (NT * U)) distill_kernel(DistillArg
     }
     const float us = wt * a.s;
     const Factor f = factor_of(us * r2.st.w, r2.rest ? r2.st.z : 0.f, a.sL);
-    for (int it = its - 1; it >= 0; --it) {
-        if (it < its - 1) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = (it * U + u) * NT + tid;
-                if (i < n) w[u] = ld_rw(body + i);
-            }
-        }
+    // backwards, from the two iterations at hand; the others come again, from L2
+    auto grad = [&](uint4 (&w)[U], int it) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = (it * U + u) * NT + tid;
             if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
         }
+        if (it < 2) return;
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid);
+    };
+    int it = its - 1;
+    if (it >= 0 && (it & 1) == 0) grad(w0, it--);
+    for (; it > 0; it -= 2) {
+        grad(w1, it);
+        grad(w0, it - 1);
     }
     {
         const int i = part.edge(tid);
@@ -581,25 +583,16 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
         return cudaGetLastError();
     } else {
         int S = 1;
-        if constexpr (kGrad) {
-            // the stretch in registers where a cluster can hold the row
-#ifndef STEP_S
-            while (S < kMaxCluster && nvec > (long long)S * STEP_U * STEP_NT) S *= 2;
+#ifdef DS_S
+        S = DS_S;
 #else
-            S = rows >= 1000 ? STEP_S : 8;
+        // with the gradient, the 608 / S rows in flight are read twice: they
+        // have to stay in L2
+        if (kGrad)
+            while (S < kMaxCluster && 608 / S * (long long)a.V * sizeof(T) > (80ll << 20)) S *= 2;
+        while (S < kMaxCluster && rows * S * 2 <= 640 && nvec >= 2LL * S * 512) S *= 2;
 #endif
-        }
-        while (S < kMaxCluster && rows * S * 2 <= 608 && nvec >= 2LL * S * 256) S *= 2;
-        if constexpr (kGrad) {
-            
-#ifndef STEP_S
-            if (nvec > (long long)S * STEP_U * STEP_NT) return launch_distill<T, kGrad, 512, 8>(a, S, stream);
-#endif
-
-            return launch_distill<T, kGrad, STEP_NT, STEP_U>(a, S, stream);
-        } else {
-            return launch_distill<T, kGrad, 256, 8>(a, S, stream);
-        }
+        return launch_distill<T, kGrad, 256, 4>(a, S, stream);
     }
 }
 

@@ -25,34 +25,32 @@ MAX_BEAMS = 32
 MAX_BEAM_OUT = 64
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
+_F32, _I32 = torch.float32, torch.int32
+_current_device = torch.cuda.current_device
 
 
-class _On:
-    """The device of ``t`` current, and ``stream`` too where one is given (so
-    that outputs are allocated on the stream that writes them)."""
+def _raw_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
 
-    __slots__ = ("ctx", "ptr")
 
-    def __init__(self, t: torch.Tensor, stream):
-        self.ctx = []
-        if t.device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(t.device))
-        if stream is not None:
-            if stream.device != t.device:
-                raise ValueError("stream must be a stream of the tensors' device")
-            self.ctx.append(torch.cuda.stream(stream))
-            self.ptr = stream.cuda_stream
-        else:
-            self.ptr = torch.cuda.current_stream(t.device).cuda_stream
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):   # the same number without the Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-        return self.ptr
 
-    def __exit__(self, *exc):
-        for c in reversed(self.ctx):
-            c.__exit__(*exc)
+def _run(t: torch.Tensor, stream, body):
+    """body(stream pointer) with the device of ``t`` current, and on ``stream``
+    where one is given (so that outputs are allocated on the stream that
+    writes them)."""
+    index = t.device.index
+    if stream is None:
+        if index == _current_device():
+            return body(_raw_stream(index))
+        with torch.cuda.device(index):
+            return body(_raw_stream(index))
+    if stream.device != t.device:
+        raise ValueError("stream must be a stream of the tensors' device")
+    with torch.cuda.device(index), torch.cuda.stream(stream):
+        return body(stream.cuda_stream)
 
 
 def _check(rc: int):
@@ -120,13 +118,16 @@ def top_logprobs(logits: torch.Tensor, M: int, inv_temperature: float = 1.0, out
     p = _native.RowsParams(B, K, V, dt, M, 0, inv_temperature, 0, bs, rs)
     if not 1 <= M <= MAX_TOP:
         raise SpecError(2, f"top_logprobs: M must be in [1, {MAX_TOP}]")
-    with _On(logits, stream) as s:
-        lp = _out(out, "logprobs", torch.float32, lead + (M,), dev)
-        ids = _out(out, "ids", torch.int32, lead + (M,), dev)
-        lse = _out(out, "lse", torch.float32, lead, dev)
+
+    def body(s):
+        lp = _out(out, "logprobs", _F32, lead + (M,), dev)
+        ids = _out(out, "ids", _I32, lead + (M,), dev)
+        lse = _out(out, "lse", _F32, lead, dev)
         _check(_native.lib().spec_top_logprobs(ctypes.byref(p), logits.data_ptr(), lp.data_ptr(), ids.data_ptr(),
                                                lse.data_ptr(), _addr(status), s))
-    return {"logprobs": lp, "ids": ids, "lse": lse}
+        return {"logprobs": lp, "ids": ids, "lse": lse}
+
+    return _run(logits, stream, body)
 
 
 def _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status):
@@ -149,12 +150,15 @@ def distill_loss(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
     top_logprobs returns them, ``weight`` [B,K] or None (1). Returns ``loss``
     [B,K] float32 and ``stats`` [B,K,4] float32, which distill_grad takes."""
     p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
-    with _On(logits, stream) as s:
-        loss = _out(out, "loss", torch.float32, tuple(lead), dev)
-        stats = _out(out, "stats", torch.float32, tuple(lead) + (4,), dev)
+
+    def body(s):
+        loss = _out(out, "loss", _F32, lead, dev)
+        stats = _out(out, "stats", _F32, lead + (4,), dev)
         _check(_native.lib().spec_distill_loss(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
                                                _addr(weight), loss.data_ptr(), stats.data_ptr(), _addr(status), s))
-    return {"loss": loss, "stats": stats}
+        return {"loss": loss, "stats": stats}
+
+    return _run(logits, stream, body)
 
 
 def _dlogits(out, logits):
@@ -179,12 +183,15 @@ def distill_grad(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
     p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
     _tensor(stats, "stats", torch.float32, lead + (4,), dev, optional=False)
     _tensor(grad_loss, "grad_loss", torch.float32, lead, dev)
-    with _On(logits, stream) as s:
+
+    def body(s):
         g, bs, rs = _dlogits(out, logits)
         _check(_native.lib().spec_distill_grad(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
                                                _addr(weight), stats.data_ptr(), _addr(grad_loss), g.data_ptr(), bs, rs,
                                                _addr(status), s))
-    return g
+        return g
+
+    return _run(logits, stream, body)
 
 
 def distill_step(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor,
@@ -196,12 +203,15 @@ def distill_step(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
     ``weight`` (a mean's 1/n, a loss scale). ``out['dlogits']`` may be the
     logits themselves."""
     p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
-    with _On(logits, stream) as s:
-        loss = _out(out, "loss", torch.float32, tuple(lead), dev)
+
+    def body(s):
+        loss = _out(out, "loss", _F32, lead, dev)
         g, bs, rs = _dlogits(None if out is None else out.get("dlogits"), logits)
         _check(_native.lib().spec_distill_step(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
                                                _addr(weight), loss.data_ptr(), g.data_ptr(), bs, rs, _addr(status), s))
-    return {"loss": loss, "dlogits": g}
+        return {"loss": loss, "dlogits": g}
+
+    return _run(logits, stream, body)
 
 
 def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Optional[torch.Tensor] = None,
@@ -216,21 +226,24 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Opti
         raise ValueError("logits must be [B, W, V]")
     B, W, V, dt, bs, rs = _logits(logits, "logits")
     dev = logits.device
-    _tensor(scores, "scores", torch.float32, torch.Size((B, W)), dev, optional=False)
-    _tensor(finished, "finished", torch.int32, torch.Size((B, W)), dev)
+    _tensor(scores, "scores", _F32, (B, W), dev, optional=False)
+    _tensor(finished, "finished", _I32, (B, W), dev)
     _status(status, dev)
     if not 1 <= N <= MAX_BEAM_OUT:
         raise SpecError(2, f"beam_step: N must be in [1, {MAX_BEAM_OUT}]")
     p = _native.RowsParams(B, W, V, dt, N, 0, 1.0, 0, bs, rs)
-    with _On(logits, stream) as s:
-        sc = _out(out, "scores", torch.float32, (B, N), dev)
-        par = _out(out, "parent", torch.int32, (B, N), dev)
-        tok = _out(out, "token", torch.int32, (B, N), dev)
-        fin = _out(out, "finished", torch.int32, (B, N), dev)
+
+    def body(s):
+        sc = _out(out, "scores", _F32, (B, N), dev)
+        par = _out(out, "parent", _I32, (B, N), dev)
+        tok = _out(out, "token", _I32, (B, N), dev)
+        fin = _out(out, "finished", _I32, (B, N), dev)
         _check(_native.lib().spec_beam_step(ctypes.byref(p), logits.data_ptr(), scores.data_ptr(), _addr(finished),
                                             eos, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), fin.data_ptr(),
                                             _addr(status), s))
-    return {"scores": sc, "parent": par, "token": tok, "finished": fin}
+        return {"scores": sc, "parent": par, "token": tok, "finished": fin}
+
+    return _run(logits, stream, body)
 
 
 def _merged(shape, stride):
@@ -289,7 +302,7 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
             state_v, dst_v = state.unsqueeze(-1), dst.unsqueeze(-1)
         else:
             state_v, dst_v = state, dst
-        if _try_layout(state_v, bd, ld) is None or _try_layout(dst_v, bd, ld) is None:
+        if _try_layout(state_v, bd, ld) is None or (dst is not state and _try_layout(dst_v, bd, ld) is None):
             ld = state_v.dim() - 1   # rows of evenly spaced segments
     else:
         ld = length_dim + nd if length_dim < 0 else length_dim
@@ -297,26 +310,30 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
             raise ValueError("length_dim must lie behind the beam axis")
         state_v, dst_v = state, dst
     O, B, W, H, T, unit, ss = _layout(state_v, bd, ld, "state")
-    O2, B2, N, H2, T2, unit2, ds = _layout(dst_v, bd, ld, "out")
-    want = list(state.shape)
-    want[bd + 1] = N
-    if list(dst.shape) != want:
-        raise ValueError("out must have the state's shape, but for the beam axis")
+    N, ds = W, ss
+    if dst is not state:
+        ds = _layout(dst_v, bd, ld, "out")[-1]
+        N = dst.shape[bd + 1]
+        if dst.shape[:bd + 1] != state.shape[:bd + 1] or dst.shape[bd + 2:] != state.shape[bd + 2:]:
+            raise ValueError("out must have the state's shape, but for the beam axis")
     if parent.dim() != 2 or parent.shape[0] != B or (dst is not state and parent.shape[1] != N):
         raise ValueError("parent must be int32 [B, N]")
     N = parent.shape[1]
-    _tensor(parent, "parent", torch.int32, torch.Size((B, N)), dev, optional=False)
-    _tensor(lengths, "lengths", torch.int32, torch.Size((B,)), dev)
+    _tensor(parent, "parent", _I32, (B, N), dev, optional=False)
+    _tensor(lengths, "lengths", _I32, (B,), dev)
     _status(status, dev)
     if unit == 0:
         return dst
     p = _native.ReorderParams(O, B, W, N, H, T, unit)
     p.src_stride[:] = ss
     p.dst_stride[:] = ds
-    with _On(state, stream) as s:
+
+    def body(s):
         _check(_native.lib().spec_beam_reorder(ctypes.byref(p), state.data_ptr(), dst.data_ptr(), parent.data_ptr(),
                                                _addr(lengths), _addr(status), s))
-    return dst
+        return dst
+
+    return _run(state, stream, body)
 
 
 def _try_layout(t, bd, ld):
