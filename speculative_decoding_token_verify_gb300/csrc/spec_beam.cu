@@ -58,13 +58,10 @@ __device__ double precise_sum(const Part<T> &p, float M, double *buf) {
     return S;
 }
 
-// Scores are kept in two floats h + l, |l| <= half a step of h (about 2^-48 of
-// the score): GB300's fp64 rate makes the same sums in fp64 many times slower.
-struct Score {
-    float h, l;
-};
+// Pairs are kept in two floats: GB300's fp64 rate makes the same sums in fp64
+// many times slower.
 // cum + (z - M) - lnS
-__device__ __forceinline__ Score score_sum(float cum, float z, float M, Score lnS) {
+__device__ __forceinline__ Pair score_sum(float cum, float z, float M, Pair lnS) {
     float h, l, e;
     two_sum(z, -M, h, l);
     two_sum(h, -lnS.h, h, e);
@@ -75,25 +72,14 @@ __device__ __forceinline__ Score score_sum(float cum, float z, float M, Score ln
     return {h, l};
 }
 // as an integer of the same order
-__device__ __forceinline__ unsigned long long score_key(Score s) {
+__device__ __forceinline__ unsigned long long score_key(Pair s) {
     const auto ordered = [](float x) {
         const int i = __float_as_int(x + 0.f);
         return i < 0 ? ~(uint32_t)i : (uint32_t)i | 0x80000000u;
     };
     return ((unsigned long long)ordered(s.h) << 32) | ordered(s.l);
 }
-__device__ __forceinline__ float score_diff(Score a, Score b) { return (a.h - b.h) + (a.l - b.l); }
-
-// ln S in two floats: one Newton step from logf, S = Sh + Sl
-__device__ __forceinline__ Score ln_pair(float Sh, float Sl) {
-    const float g = logf(Sh);
-    float eh, el;
-    exp_diff(g, 0.f, eh, el);
-    const float r = ((Sh - eh) + (Sl - el)) / Sh;
-    float h, l;
-    two_sum(g, r, h, l);
-    return {h, l};
-}
+__device__ __forceinline__ float score_diff(Pair a, Pair b) { return (a.h - b.h) + (a.l - b.l); }
 
 constexpr int kKeep = 128;   // vectors kept of a part when a CTA has several
 
@@ -103,9 +89,9 @@ struct BeamShared {
     float cum[SPEC_MAX_BEAMS];
     float mx[SPEC_MAX_BEAMS], sum[SPEC_MAX_BEAMS];               // of every row
     int state[SPEC_MAX_BEAMS];                                   // 0 live, 1 finished, 2 none
-    Score lnS[SPEC_MAX_BEAMS];
+    Pair lnS[SPEC_MAX_BEAMS];
     double prec[SPEC_MAX_BEAMS][kMaxCluster], buf[NW];
-    Score sel[SPEC_MAX_BEAM_OUT + 1];
+    Pair sel[SPEC_MAX_BEAM_OUT + 1];
     int selw[SPEC_MAX_BEAM_OUT + 1], selp[SPEC_MAX_BEAM_OUT + 1];
     unsigned need;   // beams to be summed again
     int count;       // candidates at the first CTA
@@ -127,7 +113,7 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
     }
     __syncthreads();
     n = s.count;
-    auto score_of = [&](unsigned long long c) -> Score {
+    auto score_of = [&](unsigned long long c) -> Pair {
         const int w = (int)(uint32_t)c / a.V;
         if (!cand_key(c)) return {s.cum[w], 0.f};
         return score_sum(s.cum[w], key_value(cand_key(c)), s.mx[w], s.lnS[w]);
@@ -181,7 +167,7 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
     }
     const int wl = s.selw[N - 1];
     if (wl >= 0) {
-        const Score last = s.sel[N - 1];
+        const Pair last = s.sel[N - 1];
         for (int i = tid; i < n; i += NT) {
             const int w = (int)(uint32_t)cands[i] / a.V;
             if (w == wl) continue;

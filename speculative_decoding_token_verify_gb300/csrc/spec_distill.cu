@@ -189,13 +189,192 @@ struct Row2 {
     int empty;        // nothing to renormalise
 };
 
+// a row's list in shared memory: this part's tokens (-1: none), probabilities
+// and logits; dup: some token is listed twice
+struct List {
+    int ids[SPEC_MAX_TOP];
+    float p[SPEC_MAX_TOP], yl[SPEC_MAX_TOP];
+    int dup;
+};
+
+// whether entry t is the first of its token
+__device__ __forceinline__ bool first_entry(const List &l, int t) {
+    const int v = l.ids[t];
+    bool f = v >= 0;
+    if (l.dup)
+        for (int i = 0; i < t && f; ++i) f = l.ids[i] != v;
+    return f;
+}
+
+// what a warp's 32 entries of the list give; l.p of them is written
+__device__ __forceinline__ Known list_known(const DistillArgs &a, List &l, int t, int id, float lp) {
+    Known k = known_nothing();
+    float ph = 0.f, pl = 0.f, yl = neg_inf();
+    if (id >= 0) {
+        exp_diff(lp, 0.f, ph, pl);
+        yl = l.yl[t];
+    }
+    l.p[t] = ph;
+    const bool there = yl > sv::kMaskFloor;
+    k.ml = warp_max(yl);
+    k.Sl = warp_sum(first_entry(l, t) ? (there ? ex2((yl - k.ml) * a.sL) : yl == yl ? 0.f : yl) : 0.f);
+    k.Ph = ph;
+    k.Pl = pl;
+    if (id >= 0 && lp > -700.f) {
+        if (there) {   // p (l - s y), each product and sum with its rounding
+            const float sy = __fmul_rn(a.s, yl), syl = __fmaf_rn(a.s, yl, -sy);
+            float dh, dl;
+            two_sum(lp, -sy, dh, dl);
+            dl -= syl;
+            k.Bh = __fmul_rn(ph, dh);
+            k.Bl = __fmaf_rn(ph, dh, -k.Bh) + (ph * dl + pl * dh);
+        } else {
+            k.Bh = INFINITY;
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        pair_total(k.Ph, k.Pl, o);
+        pair_total(k.Bh, k.Bl, o);
+    }
+    return k;
+}
+
+// U vectors' unlisted tokens into the sum; vector u is the part's i0 + u step
+template <typename T, int U>
+__device__ __forceinline__ void fold(Sum &acc, const uint4 (&w)[U], const uint8_t *map, int i0, int step, int n, float sL,
+                                     float resc) {
+    constexpr int E = Row<T>::E;
+    uint32_t bits[U];
+    float cm = neg_inf();
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = i0 + u * step;
+        bits[u] = i < n ? map_vec<T>(map, i) : 0u;
+        float c = vec_max<T>(w[u]);
+        if (bits[u]) {
+            float z[E];
+            Elem<T>::unpack(w[u], z);
+            c = neg_inf();
+#pragma unroll
+            for (int j = 0; j < E; ++j) c = bits[u] >> j & 1u ? c : fmaxf(c, z[j]);
+        }
+        cm = fmaxf(cm, c);
+    }
+    sum_see(acc, cm, sL, resc);
+    float v = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        float z[E];
+        Elem<T>::unpack(w[u], z);
+        if (bits[u]) {
+#pragma unroll
+            for (int j = 0; j < E; ++j) z[j] = bits[u] >> j & 1u ? neg_inf() : z[j];
+        }
+        v += sum_terms<E>(acc, z, sL);
+    }
+    sum_put(acc, v);
+}
+
+// the head's or tail's unlisted token of this thread into the sum
+template <typename T>
+__device__ __forceinline__ void fold_edge(Sum &acc, const Part<T> &part, const uint8_t *map, float sL, float resc) {
+    const int i = part.edge(threadIdx.x);
+    if (i < 0) return;
+    const int bit = map_bit(part, i);
+    if (!(map[bit >> 3] >> (bit & 7) & 1)) sum_add1(acc, load1_rw(part.r.p + i), sL, resc);
+}
+
+__device__ __forceinline__ float row_max(const Known &k) { return fmaxf(k.mo, k.ml); }
+__device__ __forceinline__ float row_sum(const DistillArgs &a, const Known &k, float &qo) {
+    const float mx = row_max(k);
+    qo = moved(k.So, k.mo, mx, a.sL);
+    return qo + moved(k.Sl, k.ml, mx, a.sL);
+}
+__device__ __forceinline__ float tail_mass(const DistillArgs &a, const Known &k) {
+    return a.tail ? fmaxf(0.f, (1.f - k.Ph) - k.Pl) : 0.f;   // 1 - Ph is exact near 1
+}
+
+__device__ __forceinline__ Row2 row_of(const DistillArgs &a, const Known &k) {
+    const float mx = row_max(k);
+    float qo;
+    const float Z = row_sum(a, k, qo);
+    Row2 r;
+    r.rest = k.mo > sv::kMaskFloor || k.So != 0.f;
+    r.none = !(mx > sv::kMaskFloor) && Z == 0.f;
+    r.empty = !a.tail && k.Ph == 0.f;
+    r.st = make_float4(mx, 1.f / Z, k.mo, 0.f);
+    if (r.rest) r.st.w = (qo / Z - tail_mass(a, k)) / k.So;
+    else r.st.z = neg_inf();
+    if (r.none || r.empty) r.st = make_float4(0.f, 0.f, 0.f, 0.f);
+    r.qscale = a.tail && !r.rest ? k.Ph : 1.f;
+    r.norm = a.tail ? 1.f : 1.f / k.Ph;
+    return r;
+}
+
+// the row's divergence, from its totals, in two floats
+__device__ float divergence(const DistillArgs &a, const Known &k, const Row2 &r) {
+    if (r.empty) return 0.f;
+    if (r.none) return INFINITY;
+    const float mx = row_max(k);
+    float qo;
+    const float Z = row_sum(a, k, qo);
+    // lse = s m + ln Z
+    const Pair lnZ = ln_pair(Z, 0.f);
+    const float sm = __fmul_rn(a.s, mx);
+    float lh, ll, h, l;
+    two_sum(sm, lnZ.h, lh, ll);
+    ll += __fmaf_rn(a.s, mx, -sm) + lnZ.l;
+    if (a.tail) {   // B + P lse
+        const float ph = __fmul_rn(k.Ph, lh);
+        two_sum(k.Bh, ph, h, l);
+        l += __fmaf_rn(k.Ph, lh, -ph) + (k.Ph * ll + k.Pl * lh) + k.Bl;
+    } else {        // B / P - ln P + lse
+        const float q = k.Bh / k.Ph;
+        const float rem = __fmaf_rn(-q, k.Ph, k.Bh) + (k.Bl - q * k.Pl);
+        const Pair lnP = ln_pair(k.Ph, k.Pl);
+        float e;
+        two_sum(q, lh, h, l);
+        two_sum(h, -lnP.h, h, e);
+        l += e + rem / k.Ph + ll - lnP.l;
+    }
+    if (!(fabsf(h) < INFINITY)) return h;
+    // p_T ln(p_T / q_T), by parts where q_T is below fp32's range
+    const float pT = tail_mass(a, k);
+    if (r.rest && pT > 0.f) {
+        if (qo > 1e-30f) l += pT * logf(pT * (Z / qo));
+        else l += pT * (logf(pT * Z / k.So) + a.s * (mx - k.mo));
+    }
+    return h + l;
+}
+
+__device__ __forceinline__ void put_loss(const DistillArgs &a, int row, float wt, const Known &k, const Row2 &r) {
+    float qo;
+    if (!r.empty && (!(row_max(k) > sv::kMaskFloor) || !(row_sum(a, k, qo) > 0.f) || row_max(k) == -neg_inf()))
+        raise_status(a.status, SPEC_ERR_BAD_ROW);
+    a.loss[row] = wt * divergence(a, k, r);
+    if (a.stats_out) a.stats_out[row] = r.st;
+}
+
+// the gradient at listed token entry t, over what was written there before
+template <typename T>
+__device__ __forceinline__ void put_listed(const DistillArgs &a, const List &l, int t, const Row2 &r, float us, T *pg) {
+    if (!first_entry(l, t)) return;
+    const int v = l.ids[t];
+    float p = l.p[t];
+    if (l.dup)
+        for (int i = t + 1; i < a.M; ++i) p += l.ids[i] == v ? l.p[i] : 0.f;
+    const float yl = l.yl[t];
+    const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - r.st.x) * a.sL) : 0.f;
+    pg[v] = to_elem<T>(fmaf(us * r.st.y * r.qscale, q, -us * (p * r.norm)));
+}
+
 template <typename T, bool kGrad, int NT, int U>
 __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S) {
     constexpr int E = Row<T>::E, NW = NT / 32;
     extern __shared__ __align__(16) uint8_t s_map[];
-    __shared__ int s_ids[SPEC_MAX_TOP], s_dup;
-    __shared__ float s_p[SPEC_MAX_TOP], s_yl[SPEC_MAX_TOP];
-    __shared__ Known s_warp[NW], s_known[kMaxCluster];
+    __shared__ List s_list;
+    __shared__ Known s_warp[NW], s_known[kMaxCluster], s_total;
     __shared__ Row2 s_row;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x / S, rank = blockIdx.x - row * S;
@@ -227,19 +406,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     }
     const uint32_t map_words = (16u + (uint32_t)E * n + 8u + 31u) / 32u;
     for (uint32_t i = tid; i < (map_words + 3u) / 4u; i += NT) reinterpret_cast<uint4 *>(s_map)[i] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) s_dup = 0;
+    if (tid == 0) s_list.dup = 0;
     const bool live = __syncthreads_or(id >= 0) && wt != 0.f;
     T *pg = kGrad ? static_cast<T *>(a.g) + b * a.gbs + kr * a.grs : nullptr;
     const Out<T> out(kGrad ? pg : const_cast<T *>(py), part);
-    auto dead = [&] {
+    if (!live) {   // the whole cluster alike
         if (rank == 0 && tid == 0) {
             a.loss[row] = 0.f;
             if (a.stats_out) a.stats_out[row] = make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (kGrad) zero_part<T, NT>(part, out);
-    };
-    if (!live) {   // the whole cluster alike
-        dead();
         return;
     }
 
@@ -249,105 +425,29 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     // list's part of what this warp knows
     if (tid < SPEC_MAX_TOP) {
         if (!(id >= part.e0 && id < part.e1)) id = -1;
-        s_ids[tid] = id;
+        s_list.ids[tid] = id;
         if (id >= 0) {
             const int bit = map_bit(part, id);
             const uint32_t m = 1u << (bit & 31);
-            if (atomicOr(reinterpret_cast<uint32_t *>(s_map) + (bit >> 5), m) & m) s_dup = 1;
-            s_yl[tid] = load1_rw(py + id);
+            if (atomicOr(reinterpret_cast<uint32_t *>(s_map) + (bit >> 5), m) & m) s_list.dup = 1;
+            s_list.yl[tid] = load1_rw(py + id);
         }
     }
     __syncthreads();
-    // the first entry of its token
-    auto once = [&](int t) {
-        const int v = s_ids[t];
-        bool f = v >= 0;
-        if (s_dup)
-            for (int i = 0; i < t && f; ++i) f = s_ids[i] != v;
-        return f;
-    };
     {
-        Known k = known_nothing();
-        if (warp * 32 < a.M) {
-            float ph = 0.f, pl = 0.f, yl = neg_inf();
-            if (id >= 0) {
-                exp_diff(lp, 0.f, ph, pl);
-                yl = s_yl[tid];
-            }
-            s_p[tid] = ph;
-            const bool there = yl > sv::kMaskFloor;
-            k.ml = warp_max(yl);
-            k.Sl = warp_sum(once(tid) ? (there ? ex2((yl - k.ml) * a.sL) : yl == yl ? 0.f : yl) : 0.f);
-            k.Ph = ph;
-            k.Pl = pl;
-            if (id >= 0 && lp > -700.f) {
-                if (there) {   // p (l - s y), each product and sum with its rounding
-                    const float sy = __fmul_rn(a.s, yl), syl = __fmaf_rn(a.s, yl, -sy);
-                    float dh, dl;
-                    two_sum(lp, -sy, dh, dl);
-                    dl -= syl;
-                    k.Bh = __fmul_rn(ph, dh);
-                    k.Bl = __fmaf_rn(ph, dh, -k.Bh) + (ph * dl + pl * dh);
-                } else {
-                    k.Bh = INFINITY;
-                }
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                pair_total(k.Ph, k.Pl, o);
-                pair_total(k.Bh, k.Bl, o);
-            }
-        }
+        const Known k = warp * 32 < a.M ? list_known(a, s_list, tid, id, lp) : known_nothing();
         if (lane == 0) s_warp[warp] = k;
     }
 
-    // the unlisted tokens' sum
     Sum acc = sum_init(a.sL, a.resc);
-    auto work = [&](const uint4 (&w)[U], int it) {
-        uint32_t bits[U];
-        float cm = neg_inf();
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = (it * U + u) * NT + tid;
-            bits[u] = i < n ? map_vec<T>(s_map, i) : 0u;
-            float c = vec_max<T>(w[u]);
-            if (bits[u]) {
-                float z[E];
-                Elem<T>::unpack(w[u], z);
-                c = neg_inf();
-#pragma unroll
-                for (int j = 0; j < E; ++j) c = bits[u] >> j & 1u ? c : fmaxf(c, z[j]);
-            }
-            cm = fmaxf(cm, c);
-        }
-        sum_see(acc, cm, a.sL, a.resc);
-        float v = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            float z[E];
-            Elem<T>::unpack(w[u], z);
-            if (bits[u]) {
-#pragma unroll
-                for (int j = 0; j < E; ++j) z[j] = bits[u] >> j & 1u ? neg_inf() : z[j];
-            }
-            v += sum_terms<E>(acc, z, a.sL);
-        }
-        sum_put(acc, v);
-    };
     for (int it = 0; it < its; it += 2) {   // both buffers end up with the last two iterations
         if (it + 1 < its) load(w1, it + 1);
-        work(w0, it);
+        fold<T, U>(acc, w0, s_map, it * U * NT + tid, NT, n, a.sL, a.resc);
         if (it + 1 >= its) break;
         if (it + 2 < its) load(w0, it + 2);
-        work(w1, it + 1);
+        fold<T, U>(acc, w1, s_map, (it + 1) * U * NT + tid, NT, n, a.sL, a.resc);
     }
-    {
-        const int i = part.edge(tid);
-        if (i >= 0) {
-            const int bit = map_bit(part, i);
-            if (!(s_map[bit >> 3] >> (bit & 7) & 1)) sum_add1(acc, load1_rw(py + i), a.sL, a.resc);
-        }
-    }
+    fold_edge(acc, part, s_map, a.sL, a.resc);
 
     // every warp's part, the CTA's, the row's
     {
@@ -387,38 +487,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         }
     }
     if (warp == 0) {
-        const float mx = fmaxf(all.mo, all.ml);
-        const float qo = moved(all.So, all.mo, mx, a.sL), Z = qo + moved(all.Sl, all.ml, mx, a.sL);
-        Row2 r2;
-        r2.rest = all.mo > sv::kMaskFloor || all.So != 0.f;
-        r2.none = !(mx > sv::kMaskFloor) && Z == 0.f;
-        const double P = (double)all.Ph + (double)all.Pl;
-        r2.empty = !a.tail && all.Ph == 0.f;
-        const float pT = a.tail ? (float)fmax(0.0, 1.0 - P) : 0.f;
-        r2.st = make_float4(mx, 1.f / Z, all.mo, 0.f);
-        if (r2.rest) r2.st.w = (qo / Z - pT) / all.So;
-        else r2.st.z = neg_inf();
-        if (r2.none) r2.st = make_float4(0.f, 0.f, 0.f, 0.f);
-        r2.qscale = a.tail && !r2.rest ? all.Ph : 1.f;
-        r2.norm = a.tail ? 1.f : 1.f / all.Ph;
-        if (lane == 0) s_row = r2;
-        if (rank == 0 && lane == 0) {
-            if (r2.empty) {
-                a.loss[row] = 0.f;
-                if (a.stats_out) a.stats_out[row] = make_float4(0.f, 0.f, 0.f, 0.f);
-            } else {
-                const double lse = (double)a.s * (double)mx + log((double)Z);
-                const double B = (double)all.Bh + (double)all.Bl;
-                double kl = a.tail ? B + P * lse : B / P - log(P) + lse;
-                // ln(p_T / q_T), by parts where q_T is below fp32's range
-                if (r2.rest && pT > 0.f)
-                    kl += (double)pT * (qo > 1e-30f ? (double)logf(pT * (Z / qo))
-                                                    : (double)logf(pT * Z / all.So) + (double)a.s * ((double)mx - (double)all.mo));
-                if (!(mx > sv::kMaskFloor) || !(Z > 0.f) || mx == -neg_inf()) raise_status(a.status, SPEC_ERR_BAD_ROW);
-                if (r2.none) kl = INFINITY;
-                a.loss[row] = wt * (float)kl;
-                if (a.stats_out) a.stats_out[row] = r2.st;
-            }
+        const Row2 r = row_of(a, all);
+        if (lane == 0) {
+            s_row = r;
+            s_total = all;
+            if (!kGrad && rank == 0) put_loss(a, row, wt, all, r);
         }
     }
     if (!kGrad) return;
@@ -426,41 +499,32 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     const Row2 r2 = s_row;
     if (r2.empty || r2.none) {
         zero_part<T, NT>(part, out);
-        return;
-    }
-    const float us = wt * a.s;
-    const Factor f = factor_of(us * r2.st.w, r2.rest ? r2.st.z : 0.f, a.sL);
-    // backwards, from the two iterations at hand; the others come again, from L2
-    auto grad = [&](uint4 (&w)[U], int it) {
+    } else {
+        const float us = wt * a.s;
+        const Factor f = factor_of(us * r2.st.w, r2.rest ? r2.st.z : 0.f, a.sL);
+        // backwards, from the two iterations at hand; the others come again, from L2
+        auto grad = [&](uint4 (&w)[U], int it) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = (it * U + u) * NT + tid;
-            if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
+            for (int u = 0; u < U; ++u) {
+                const int i = (it * U + u) * NT + tid;
+                if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
+            }
+            if (it < 2) return;
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid);
+        };
+        int it = its - 1;
+        if (it >= 0 && (it & 1) == 0) grad(w0, it--);
+        for (; it > 0; it -= 2) {
+            grad(w1, it);
+            grad(w0, it - 1);
         }
-        if (it < 2) return;
-#pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid);
-    };
-    int it = its - 1;
-    if (it >= 0 && (it & 1) == 0) grad(w0, it--);
-    for (; it > 0; it -= 2) {
-        grad(w1, it);
-        grad(w0, it - 1);
-    }
-    {
         const int i = part.edge(tid);
         if (i >= 0) pg[i] = to_elem<T>(grad_one(f, load1_rw(py + i), a.sL));
+        __syncthreads();   // the listed tokens' values go over what was just written
+        if (tid < a.M) put_listed(a, s_list, tid, r2, us, pg);
     }
-    __syncthreads();   // the listed tokens' values go over what was just written
-    if (tid < a.M && once(tid)) {
-        const int v = s_ids[tid];
-        float p = s_p[tid];
-        if (s_dup)
-            for (int i = tid + 1; i < a.M; ++i) p += s_ids[i] == v ? s_p[i] : 0.f;
-        const float yl = s_yl[tid];
-        const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - r2.st.x) * a.sL) : 0.f;
-        pg[v] = to_elem<T>(fmaf(us * r2.st.y * r2.qscale, q, -us * (p * r2.norm)));
-    }
+    if (rank == 0 && tid == NT - 1) put_loss(a, row, wt, s_total, r2);
 }
 
 // the gradient from a row's statistics: a CTA per part of a row

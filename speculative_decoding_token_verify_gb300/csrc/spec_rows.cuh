@@ -261,6 +261,22 @@ __device__ __forceinline__ void exp_diff(float z, float M, float &h, float &l) {
     l = sl * sc;
 }
 
+// a value h + l, |l| <= half a step of h
+struct Pair {
+    float h, l;
+};
+
+// ln S in two floats: one Newton step from logf, S = Sh + Sl
+__device__ __forceinline__ Pair ln_pair(float Sh, float Sl) {
+    const float g = logf(Sh);
+    float eh, el;
+    exp_diff(g, 0.f, eh, el);
+    const float r = ((Sh - eh) + (Sl - el)) / Sh;
+    float h, l;
+    two_sum(g, r, h, l);
+    return {h, l};
+}
+
 // ---- ordered keys --------------------------------------------------------------
 //
 // Larger logit, larger key; both zeros alike; masked logits (-inf, or below

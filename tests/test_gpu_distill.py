@@ -101,6 +101,57 @@ def test_many_rows(dtype):
     _check(y, lp, ids, w)
 
 
+@pytest.mark.parametrize("dtype,V", [("bf16", 40003), ("f32", 40003), ("bf16", 262147), ("f32", 131077), ("bf16", 9),
+                                     ("f32", 3), ("bf16", 16385)])
+@pytest.mark.parametrize("tail", [True, False])
+def test_many_rows_of_many_lengths(dtype, V, tail):
+    """Batches that stream row behind row: four student rows repeated over 150
+    sequences (stride 0), rows of weight zero and empty lists strewn in. Every
+    copy of a row has the same bits; the first copies match the reference."""
+    sv = _sv()
+    B = 150
+    y, lp, ids, w = _case(1, 4, V, 24, dtype, V)
+    yy = y.expand(B, 4, V)
+    lp, ids = lp.repeat(B, 1, 1), ids.repeat(B, 1, 1)
+    w = w.repeat(B, 1)
+    g = torch.Generator().manual_seed(V)
+    off = torch.rand((B, 4), generator=g) < 0.3
+    off[:1] = False
+    off[40:60] = True                 # a long run of rows that are not read
+    w[off.to(DEV)] = 0
+    ids[-20:-10, 1] = -1
+    dead = off.clone()
+    dead[-20:-10, 1] = True
+    a = sv.distill_loss(yy, lp, ids, w, tail=tail)
+    st = sv.distill_step(yy, lp, ids, w, tail=tail, out={"dlogits": torch.full((B, 4, V), 3e38, dtype=DT[dtype],
+                                                                            device=DEV)})
+    torch.cuda.synchronize()
+    live = (~dead).to(DEV)[..., None]
+    zero = torch.zeros((), device=DEV)
+    assert torch.equal(a["loss"], torch.where(live[..., 0], a["loss"][:1], zero))
+    assert torch.equal(a["stats"], torch.where(live, a["stats"][:1], zero))
+    assert torch.equal(st["loss"], torch.where(live[..., 0], st["loss"][:1], zero))
+    assert torch.equal(st["dlogits"], torch.where(live, st["dlogits"][:1], zero.to(DT[dtype])))
+    for k in range(4):
+        r = ref.distill(y[0, k].float().cpu().numpy(), lp[0, k].cpu().numpy(), ids[0, k].cpu().numpy(), float(w[0, k]), 1.0,
+                        tail)
+        assert abs(float(a["loss"][0, k]) - r["loss"]) <= r["loss_tol"]
+        assert abs(float(st["loss"][0, k]) - r["loss"]) <= r["loss_tol"]
+        d = np.abs(st["dlogits"][0, k].float().cpu().numpy() - r["grad"])
+        assert np.all(d <= r["grad_tol"] + ref.half(dtype == "bf16") * (np.abs(r["grad"]) + r["grad_tol"]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_many_rows_in_place(dtype):
+    sv = _sv()
+    for V in (2053, 70001):
+        y, lp, ids, w = _case(2, 4, V, 24, dtype, V)
+        y, lp, ids, w = (t.repeat((80,) + (1,) * (t.dim() - 1)) for t in (y, lp, ids, w))
+        want = sv.distill_step(y, lp, ids, w)
+        got = sv.distill_step(y, lp, ids, w, out={"dlogits": y})
+        assert torch.equal(y, want["dlogits"]) and torch.equal(got["loss"], want["loss"])
+
+
 @pytest.mark.parametrize("s", [0.1, 0.5, 2.0, 20.0])
 @pytest.mark.parametrize("tail", [True, False])
 def test_temperatures(s, tail):
