@@ -137,6 +137,32 @@ __device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int 
     o.put(p, i, z);
 }
 
+// L2 policies: rows read twice are kept for the second read, then let go
+__device__ __forceinline__ uint64_t l2_keep() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint64_t l2_drop() {
+    uint64_t p;
+    asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ uint4 ldg_stream(const uint4 *p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
+    return v;
+}
+__device__ __forceinline__ uint4 ld_rw(const uint4 *p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ uint4 ld_rw(const uint4 *p) {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
@@ -240,26 +266,36 @@ __device__ __forceinline__ Known list_known(const DistillArgs &a, List &l, int t
     return k;
 }
 
-// U vectors' unlisted tokens into the sum; vector u is the part's i0 + u step
-template <typename T, int U>
-__device__ __forceinline__ void fold(Sum &acc, const uint4 (&w)[U], const uint8_t *map, int i0, int step, int n, float sL,
+// the vector with its listed tokens masked
+template <typename T>
+__device__ __forceinline__ void mask_listed(uint4 &w, uint32_t bits) {
+    uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 2) {
+            if (bits >> (2 * k) & 1u) v[k] = (v[k] & 0xffff0000u) | 0xff80u;
+            if (bits >> (2 * k + 1) & 1u) v[k] = (v[k] & 0xffffu) | 0xff800000u;
+        } else {
+            if (bits >> k & 1u) v[k] = 0xff800000u;
+        }
+    }
+    w = make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// U vectors' unlisted tokens into the sum; vector u is the part's i0 + u step.
+// Listed tokens are masked in w itself: the gradient there comes later. kFull:
+// all of the vectors are in the part.
+template <typename T, bool kFull, int U>
+__device__ __forceinline__ void fold(Sum &acc, uint4 (&w)[U], const uint8_t *map, int i0, int step, int n, float sL,
                                      float resc) {
     constexpr int E = Row<T>::E;
-    uint32_t bits[U];
     float cm = neg_inf();
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int i = i0 + u * step;
-        bits[u] = i < n ? map_vec<T>(map, i) : 0u;
-        float c = vec_max<T>(w[u]);
-        if (bits[u]) {
-            float z[E];
-            Elem<T>::unpack(w[u], z);
-            c = neg_inf();
-#pragma unroll
-            for (int j = 0; j < E; ++j) c = bits[u] >> j & 1u ? c : fmaxf(c, z[j]);
-        }
-        cm = fmaxf(cm, c);
+        const uint32_t bits = kFull || i < n ? map_vec<T>(map, i) : 0u;
+        if (bits) mask_listed<T>(w[u], bits);
+        cm = fmaxf(cm, vec_max<T>(w[u]));
     }
     sum_see(acc, cm, sL, resc);
     float v = 0.f;
@@ -267,10 +303,6 @@ __device__ __forceinline__ void fold(Sum &acc, const uint4 (&w)[U], const uint8_
     for (int u = 0; u < U; ++u) {
         float z[E];
         Elem<T>::unpack(w[u], z);
-        if (bits[u]) {
-#pragma unroll
-            for (int j = 0; j < E; ++j) z[j] = bits[u] >> j & 1u ? neg_inf() : z[j];
-        }
         v += sum_terms<E>(acc, z, sL);
     }
     sum_put(acc, v);
@@ -383,11 +415,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     const Part<T> part(py, a.V, rank, S);
     const int n = part.n, its = (n + U * NT - 1) / (U * NT);
     const uint4 *body = part.body();
+    // whether iteration it is full: all but the last are
+    auto full = [&](int it) { return (it + 1) * U * NT <= n; };
     auto load = [&](uint4 (&w)[U], int it) {
+        const uint4 *p = body + it * U * NT + tid;
+        const uint64_t policy = kGrad && it + 2 < its ? l2_keep() : l2_drop();
+        if (full(it)) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = (it * U + u) * NT + tid;
-            w[u] = i < n ? sv::ldg_stream(body + i) : masked_vec<T>();
+            for (int u = 0; u < U; ++u) w[u] = ldg_stream(p + u * NT, policy);
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) w[u] = (it * U + u) * NT + tid < n ? ldg_stream(p + u * NT, policy) : masked_vec<T>();
         }
     };
     uint4 w0[U], w1[U];   // iterations it and it + 1; the first is on its way during the list's work
@@ -440,12 +478,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     }
 
     Sum acc = sum_init(a.sL, a.resc);
+    auto work = [&](uint4 (&w)[U], int it) {
+        if (full(it)) fold<T, true, U>(acc, w, s_map, it * U * NT + tid, NT, n, a.sL, a.resc);
+        else fold<T, false, U>(acc, w, s_map, it * U * NT + tid, NT, n, a.sL, a.resc);
+    };
     for (int it = 0; it < its; it += 2) {   // both buffers end up with the last two iterations
         if (it + 1 < its) load(w1, it + 1);
-        fold<T, U>(acc, w0, s_map, it * U * NT + tid, NT, n, a.sL, a.resc);
+        work(w0, it);
         if (it + 1 >= its) break;
         if (it + 2 < its) load(w0, it + 2);
-        fold<T, U>(acc, w1, s_map, (it + 1) * U * NT + tid, NT, n, a.sL, a.resc);
+        work(w1, it + 1);
     }
     fold_edge(acc, part, s_map, a.sL, a.resc);
 
@@ -504,14 +546,18 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         const Factor f = factor_of(us * r2.st.w, r2.rest ? r2.st.z : 0.f, a.sL);
         // backwards, from the two iterations at hand; the others come again, from L2
         auto grad = [&](uint4 (&w)[U], int it) {
+            const int i0 = it * U * NT + tid;
+            if (full(it)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = (it * U + u) * NT + tid;
-                if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
+                for (int u = 0; u < U; ++u) grad_vec(part, out, i0 + u * NT, w[u], f, a.sL);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (i0 + u * NT < n) grad_vec(part, out, i0 + u * NT, w[u], f, a.sL);
             }
             if (it < 2) return;
 #pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid);
+            for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid, l2_drop());
         };
         int it = its - 1;
         if (it >= 0 && (it & 1) == 0) grad(w0, it--);
