@@ -240,7 +240,6 @@ __global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, in
             __syncthreads();
             part_sum(s.top, kLog2e, mx, sum);
             n = s.top.n > CAP ? -1 : s.top.n;
-            thr = closer_bound(thr, N, s.top);
         }
         if (most > 1) {   // keep what still reaches the bound
             if (n > 0) {

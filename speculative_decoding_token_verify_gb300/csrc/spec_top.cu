@@ -39,7 +39,6 @@ __global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
     stream_part(part, a.M, a.sL, a.rs, s, thr);
     __syncthreads();
     bool over = s.n > CAP;
-    thr = closer_bound(thr, a.M, s);
     part_sum(s, a.sL, mx, sum);
     if (kCluster) {
         cluster_wait();

@@ -237,6 +237,8 @@ __device__ __forceinline__ void stream_part(const Part<T> &p, int M, float sL, f
         s.w_mx[tid >> 5] = m;
         s.w_sum[tid >> 5] = v;
     }
+    // a last bound, from all of the part (its barrier, or the caller's)
+    if (its > 1) thr = block_bound(acc.mx, n, M, thr, s.b[2]);
 }
 
 // the part's maximum and sum, after the barrier
@@ -247,14 +249,6 @@ __device__ __forceinline__ void part_sum(const TopShared &s, float sL, float &mx
     sum = 0.f;
 #pragma unroll
     for (int i = 0; i < NW; ++i) sum += moved(s.w_sum[i], s.w_mx[i], mx, sL);
-}
-
-// a closer bound from the passing vectors' maxima
-__device__ __forceinline__ float closer_bound(float thr, int M, TopShared &s) {
-    const int np = min(s.n, CAP);
-    float best = neg_inf();
-    for (int i = threadIdx.x; i < np; i += NT) best = fmaxf(best, s.c[i]);
-    return block_bound(best, np, M, thr, s.b[2]);
 }
 
 // `n` words from this CTA's shared memory to the list `to` of the cluster's
