@@ -196,7 +196,7 @@ __device__ __forceinline__ void write_beams(const BeamArgs &a, const BeamShared 
 // codes); at the first CTA `room` candidates (logit's key and place; key 0: a
 // finished beam) and their scores.
 template <typename T>
-__global__ void __launch_bounds__(NT, TOP_OCC) beam_kernel(BeamArgs a, int C, int P, int room) {
+__global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, int room) {
     constexpr int E = Row<T>::E;
     __shared__ BeamShared s;
     extern __shared__ __align__(16) unsigned char dyn[];

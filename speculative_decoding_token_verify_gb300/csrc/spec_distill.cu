@@ -693,15 +693,15 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
         return cudaGetLastError();
     } else {
         int S = 1;
-#ifdef DS_S
-        S = DS_S;
-#else
-        // with the gradient, the 608 / S rows in flight are read twice: they
-        // have to stay in L2
+        // with the gradient, the 608 / S rows in flight are read twice and have to
+        // stay in L2: 2048 rows of 128256 bf16 take 215 us at S = 1, 192 at 2, 202
+        // at 4; rows of 32000 57 us at 1, 79 at 2
         if (kGrad)
-            while (S < kMaxCluster && 608 / S * (long long)a.V * sizeof(T) > (80ll << 20)) S *= 2;
+            while (S < kMaxCluster && 608 / S * (long long)a.V * (long long)sizeof(T) > (80ll << 20)) S *= 2;
+        // few rows are split while there are SM slots and a part keeps two vectors
+        // per thread: 32 rows of 128256 take 8.1 us at S = 8 and 14.6 at 1, 320 rows
+        // 18.1 at 2 and 21.7 at 1 (the loss)
         while (S < kMaxCluster && rows * S * 2 <= 640 && nvec >= 2LL * S * 512) S *= 2;
-#endif
         return launch_distill<T, kGrad, 256, 4>(a, S, stream);
     }
 }

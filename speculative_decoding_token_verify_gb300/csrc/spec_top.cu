@@ -24,7 +24,7 @@ struct TopArgs {
 };
 
 template <typename T, bool kCluster>
-__global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
+__global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
     __shared__ TopShared s;
     __shared__ float s_x[4][kMaxCluster];   // per CTA of the cluster: bound, maximum, sum, overflow
     __shared__ int s_ns;
@@ -102,12 +102,15 @@ __global__ void __launch_bounds__(NT, TOP_OCC) top_kernel(TopArgs a, int S) {
     }
 }
 
-// CTAs per row: rows are split while there are SM slots to fill (4 CTAs on
-// each of 152 SMs) and a CTA keeps a vector per thread
+// CTAs per row: rows are split while half of the SMs' slots (4 CTAs on each of
+// 152 SMs) are free and a part keeps four vectors per thread: an exchange
+// costs more than it saves beyond. bf16, M = 64, S = 1 / 2 / 4 / 8: 8 rows of
+// 128256 16.3 / 13.8 / 12.0 / 10.6 us, 128 rows 16.7 / 16.4 / 19.3 / 24.7 us;
+// 128 rows of 32000 10.1 / 11.3 / 14.1 / 20.7 us.
 static int top_cluster(long long rows, int V, int es) {
     const long long nvec = (long long)V * es / 16;
     int S = 1;
-    while (S < kMaxCluster && rows * S * 2 <= 608 && nvec >= 2LL * S * NT) S *= 2;
+    while (S < kMaxCluster && rows * S * 2 <= 304 && nvec >= 2LL * S * U * NT) S *= 2;
     return S;
 }
 

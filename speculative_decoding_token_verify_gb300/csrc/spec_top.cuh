@@ -22,13 +22,10 @@ namespace sr {
 
 constexpr int NT = 256;
 constexpr int NW = NT / 32;
-#ifndef TOP_U
-#define TOP_U 4
-#endif
-#ifndef TOP_OCC
-#define TOP_OCC 4
-#endif
-constexpr int U = TOP_U;         // 16-byte loads of an iteration per thread
+// 16-byte loads of an iteration per thread. Two iterations are in registers, at
+// 64 of them a thread and 4 CTAs per SM: 2048 rows of 128256 bf16 take 110 us;
+// 2 loads and 5 CTAs 119 us, 3 loads 120 us, 8 loads and 2 CTAs 133 us.
+constexpr int U = 4;
 constexpr int CAP = 2048;    // vectors that may pass the filter, per CTA
 constexpr int CAPE = 1024;   // logits that may pass the last bound, per row
 constexpr int kMaxCluster = 8;
