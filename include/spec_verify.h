@@ -50,6 +50,7 @@
  *    slice, token) against the buffer it addresses before the access, and
  *    on a failed check skip the access and raise SPEC_ERR_INDEX in the
  *    status word. They are for testing; the default build has no checks.
+ *    (The row operators at the end have the same code in both builds.)
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H

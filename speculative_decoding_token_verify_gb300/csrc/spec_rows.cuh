@@ -300,7 +300,7 @@ __device__ __forceinline__ unsigned long long cand(uint32_t key, int index) {
 __device__ __forceinline__ int cand_index(unsigned long long c) { return (int)~(uint32_t)c; }
 __device__ __forceinline__ uint32_t cand_key(unsigned long long c) { return (uint32_t)(c >> 32); }
 
-// ---- block reductions (fixed order) ---------------------------------------------
+// ---- warp reductions (fixed order) ----------------------------------------------
 
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll
@@ -311,29 +311,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     return v;
-}
-
-// every thread gets the block's maximum; `buf`: NT / 32 floats, free to reuse
-// after the next barrier
-template <int NT>
-__device__ __forceinline__ float block_max(float v, float *buf) {
-    v = warp_max(v);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = buf[0];
-#pragma unroll
-    for (int i = 1; i < NT / 32; ++i) r = fmaxf(r, buf[i]);
-    return r;
-}
-template <int NT>
-__device__ __forceinline__ float block_sum(float v, float *buf) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float r = buf[0];
-#pragma unroll
-    for (int i = 1; i < NT / 32; ++i) r += buf[i];
-    return r;
 }
 
 // ---- thread-block clusters ----------------------------------------------------------
@@ -394,8 +371,7 @@ cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, unsigned nt, uns
 // ---- host-side checks shared by the row operators --------------------------------
 
 int check_rows(const spec_rows_params *p, int max_m, int max_k);
-int check_strided(const char *name, const void *base, int64_t batch_stride, int64_t row_stride, int es, bool out, int B,
-                  int K, int V);
+int check_strided(const void *base, int64_t batch_stride, int64_t row_stride, int es, bool out, int B, int K, int V);
 
 }  // namespace sr
 

@@ -8,6 +8,13 @@
 // enough), each a part of it, with the filter of spec_top.cuh; the parts'
 // bounds, maxima and sums meet in one exchange through distributed shared
 // memory, and the first CTA ranks what passes the best bound.
+//
+// Measured: 2048 rows of 128256 bf16, M = 64: 103 us, 5.1 TB/s, 76% of the
+// measured copy rate. The stream with its sums alone takes 86 us; looking at
+// what passed and ranking it the rest (46 thousand warp instructions a row, a
+// third of them there, issue slots 66% busy). A CTA that goes on to further
+// rows with the next one's first loads in flight took 110 us, whole iterations
+// without bounds 110 us (registers spill).
 #include "spec_top.cuh"
 
 namespace sr {
@@ -144,8 +151,7 @@ int check_rows(const spec_rows_params *p, int max_m, int max_k) {
 
 // Strides of an input are >= 0. Rows of an output must not overlap: one of the
 // two axes steps over the whole extent of the other.
-int check_strided(const char *name, const void *base, int64_t bs, int64_t rs, int es, bool out, int B, int K, int V) {
-    (void)name;
+int check_strided(const void *base, int64_t bs, int64_t rs, int es, bool out, int B, int K, int V) {
     if (!base) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "logits / dlogits is NULL");
     if (reinterpret_cast<uintptr_t>(base) % es)
         return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "logits / dlogits must be aligned to the element size");
@@ -170,7 +176,7 @@ extern "C" int spec_top_logprobs(const spec_rows_params *p, const void *logits, 
     if (rc != SPEC_OK) return rc;
     if (p->tail != 0) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "top_logprobs: tail must be 0");
     if ((int64_t)p->B * p->K == 0) return spec_internal_set_error(SPEC_OK, "");
-    rc = check_strided("logits", logits, p->batch_stride, p->row_stride, p->dtype == SPEC_BF16 ? 2 : 4, false, p->B,
+    rc = check_strided(logits, p->batch_stride, p->row_stride, p->dtype == SPEC_BF16 ? 2 : 4, false, p->B,
                        p->K, p->V);
     if (rc != SPEC_OK) return rc;
     if (!logprobs || !ids) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "logprobs / ids is NULL");

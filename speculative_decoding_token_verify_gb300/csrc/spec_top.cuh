@@ -6,10 +6,11 @@
 // token, and their indices go to a short list in shared memory. T comes from
 // the threads' own running maxima: every warp sorts its 32, and with k =
 // ceil(M / warps) the smallest of the warps' k-th largest has M logits at or
-// above it. It is taken after iterations 1, 2, 4, 8, ..., and the part is read
-// in U interleaved streams, so that the first iteration samples all of it.
-// About 7 M vectors of a row pass; the same bound over their maxima leaves
-// about 1.5 M, whose logits are looked at one by one and ranked by counting.
+// above it. It is taken after iterations 1, 2, 4, 8, ... and once more at the
+// end, and the part is read in U interleaved streams, so that the first
+// iteration samples all of it. About 7 M vectors of a row of 128256 pass; the
+// last bound leaves about 1.5 M, whose logits are looked at one by one and
+// ranked by counting.
 //
 // Where more vectors pass than the list holds (runs of equal logits, all large
 // logits in one place) a bisection finishes: the M-th largest key by counting

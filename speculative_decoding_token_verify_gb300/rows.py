@@ -18,11 +18,13 @@ from typing import Optional
 import torch
 
 from . import _native
-from .api import BF16, F32, SPEC_OK, SpecError
+from .api import BF16, F32, MAX_V, SPEC_ERR_UNSUPPORTED, SPEC_OK, SpecError
 
 MAX_TOP = 128
 MAX_BEAMS = 32
 MAX_BEAM_OUT = 64
+MAX_B = 1 << 24
+MAX_K_ROWS = 4096
 
 _DTYPES = {torch.bfloat16: BF16, torch.float32: F32}
 _F32, _I32 = torch.float32, torch.int32
@@ -80,6 +82,8 @@ def _logits(z: torch.Tensor, name: str):
         raise ValueError(f"{name} must be [B, K, V] or [R, V]")
     if vs != 1 and V > 1:
         raise ValueError(f"{name}: the vocabulary axis must be contiguous")
+    if B > MAX_B or K > MAX_K_ROWS or V > MAX_V:   # before the C ABI's 32-bit fields
+        raise SpecError(SPEC_ERR_UNSUPPORTED, f"{name}: {tuple(shape)} is outside the supported range")
     return B, K, V, dt, bs, rs
 
 
@@ -97,12 +101,19 @@ def _status(status, device):
         raise ValueError("status must be an int32 tensor of one element on the logits' device")
 
 
+def _written(t):
+    """Tell autograd that the library writes into ``t``."""
+    if t.requires_grad:
+        torch.autograd.graph.increment_version(t)
+    return t
+
+
 def _out(out, name, dtype, shape, device):
     t = None if out is None else out.get(name)
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _tensor(t, f"out['{name}']", dtype, torch.Size(shape), device)
-    return t
+    return _written(t)
 
 
 def top_logprobs(logits: torch.Tensor, M: int, inv_temperature: float = 1.0, out: Optional[dict] = None,
@@ -115,9 +126,9 @@ def top_logprobs(logits: torch.Tensor, M: int, inv_temperature: float = 1.0, out
     B, K, V, dt, bs, rs = _logits(logits, "logits")
     dev, lead = logits.device, tuple(logits.shape[:-1])
     _status(status, dev)
-    p = _native.RowsParams(B, K, V, dt, M, 0, inv_temperature, 0, bs, rs)
     if not 1 <= M <= MAX_TOP:
-        raise SpecError(2, f"top_logprobs: M must be in [1, {MAX_TOP}]")
+        raise SpecError(SPEC_ERR_UNSUPPORTED, f"top_logprobs: M must be in [1, {MAX_TOP}]")
+    p = _native.RowsParams(B, K, V, dt, M, 0, inv_temperature, 0, bs, rs)
 
     def body(s):
         lp = _out(out, "logprobs", _F32, lead + (M,), dev)
@@ -168,7 +179,7 @@ def _dlogits(out, logits):
     elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
         raise ValueError("dlogits must have the logits' dtype, shape and device")
     _, _, _, _, bs, rs = _logits(out, "dlogits")
-    return out, bs, rs
+    return _written(out), bs, rs
 
 
 def distill_grad(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor, stats: torch.Tensor,
@@ -230,7 +241,9 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Opti
     _tensor(finished, "finished", _I32, (B, W), dev)
     _status(status, dev)
     if not 1 <= N <= MAX_BEAM_OUT:
-        raise SpecError(2, f"beam_step: N must be in [1, {MAX_BEAM_OUT}]")
+        raise SpecError(SPEC_ERR_UNSUPPORTED, f"beam_step: N must be in [1, {MAX_BEAM_OUT}]")
+    if not -1 <= eos < V:
+        raise ValueError("eos must be -1 or a token")
     p = _native.RowsParams(B, W, V, dt, N, 0, 1.0, 0, bs, rs)
 
     def body(s):
@@ -324,6 +337,9 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
     _status(status, dev)
     if unit == 0:
         return dst
+    if O > 65535 or H > 65535 or B > MAX_B or T >= 1 << 31 or unit > 1 << 30:   # before 32-bit fields
+        raise SpecError(SPEC_ERR_UNSUPPORTED, "beam_reorder: the state's axes are outside the supported range")
+    _written(dst)
     p = _native.ReorderParams(O, B, W, N, H, T, unit)
     p.src_stride[:] = ss
     p.dst_stride[:] = ds

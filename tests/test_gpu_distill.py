@@ -314,3 +314,71 @@ def test_streams_graphs_and_repeats():
     assert torch.equal(gr, sv.distill_grad(y, lp, ids, st["stats"], weight=w))
     empty = sv.distill_step(y[:0], lp[:0], ids[:0], w[:0])
     assert empty["dlogits"].shape == (0, 2, 20011)
+
+
+def test_rows_without_a_batch_axis():
+    sv = _sv()
+    y, lp, ids, w = _case(6, 1, 3001, 12, "bf16", 17)
+    want = sv.distill_step(y, lp, ids, w)
+    two = [t[:, 0].contiguous() for t in (y, lp, ids, w)]
+    got = sv.distill_step(*two)
+    assert got["dlogits"].shape == (6, 3001) and got["loss"].shape == (6,)
+    a = sv.distill_loss(*two)
+    g = sv.distill_grad(two[0], two[1], two[2], a["stats"], weight=two[3])
+    for r in range(6):   # another view of the same rows: the same alignments
+        assert torch.equal(got["dlogits"][r], want["dlogits"][r, 0])
+    assert torch.equal(got["loss"], want["loss"][:, 0]) and g.shape == (6, 3001)
+
+
+def test_offsets_beyond_32_bits():
+    """Student and gradient rows that start past 2^31 elements."""
+    V = 5003
+    buf = torch.zeros((2 ** 31 + 8 * V,), dtype=torch.bfloat16, device=DEV)
+    far = buf.as_strided((2, 1, V), (2 ** 31 + 3 * V, V, 1))
+    y, lp, ids, w = _case(2, 1, V, 16, "bf16", 18)
+    far.copy_(y)
+    _check(far, lp, ids, w)
+    want = _sv().distill_step(far, lp, ids, w)
+    got = _sv().distill_step(far, lp, ids, w, out={"dlogits": far})
+    assert torch.equal(far, want["dlogits"]) and torch.equal(got["loss"], want["loss"])
+
+
+def test_two_calls_and_two_graphs_at_once():
+    """No call keeps anything that another could meet."""
+    sv = _sv()
+    a = _case(40, 2, 9001, 20, "bf16", 19)
+    b = _case(3, 3, 60000, 100, "f32", 20)
+    want = [sv.distill_step(*x) for x in (a, b)]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append((sv.distill_step(*a, stream=s1), sv.distill_step(*b, stream=s2)))
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(sv.distill_step(*x))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, (s1, s2)):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    got.append(tuple(outs))
+    for pair in got:
+        for w, g in zip(want, pair):
+            assert all(torch.equal(w[k], g[k]) for k in w)
+
+
+def test_in_place_writes_are_seen_by_autograd():
+    sv = _sv()
+    y, lp, ids, w = _case(2, 2, 300, 8, "f32", 21)
+    x = y.clone().requires_grad_()
+    z = x * 1.0
+    loss = (z * z).sum()              # keeps z for its backward pass
+    sv.distill_step(z, lp, ids, w, out={"dlogits": z})
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()

@@ -168,6 +168,23 @@ def test_binding_refuses_host_and_misshapen_tensors():
             f()
 
 
+class _Fake:
+    """A tensor's outline: shapes beyond the C ABI's 32-bit fields."""
+    is_cuda, dtype = True, torch.float32
+
+    def __init__(self, shape):
+        self.shape = torch.Size(shape)
+
+    def stride(self):
+        return (0,) * (len(self.shape) - 1) + (1,)
+
+
+@pytest.mark.parametrize("shape", [(2 ** 32 + 1, 2, 10), (2, 4097, 10), (2, 2, 2 ** 32 + 5), (2 ** 33, 7)])
+def test_binding_refuses_shapes_before_they_wrap(shape):
+    with pytest.raises(sv.SpecError):
+        rows._logits(_Fake(shape), "logits")
+
+
 def test_layouts_of_states():
     t = torch.zeros((2, 3, 4, 5, 6, 8))
     assert rows._layout(t, 1, 4, "t") == (2, 3, 4, 5, 6, 32, [3 * 4 * 240 * 4, 960 * 4, 240 * 4, 48 * 4])
