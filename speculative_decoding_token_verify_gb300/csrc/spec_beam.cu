@@ -104,21 +104,11 @@ struct BeamShared {
     int many;        // more candidates than room
 };
 
-// At the first CTA: the N + 1 best of cands[0 .. n) and the finished beams, into
-// s.sel*; with `check` the beams whose order fp32 sums leave open, into s.need.
+// At the first CTA: the N + 1 best of cands[0 .. n), into s.sel*; with `check` the beams whose order fp32 sums leave open, into s.need.
 // All threads call it; s.selw holds -1 before, a barrier follows.
 __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s, unsigned long long *cands,
                                                 unsigned long long *keys, int n, bool check) {
     const int tid = threadIdx.x, N = a.N;
-    __syncthreads();
-    if (check && tid < 32) {   // finished beams join the list, key 0
-        const bool fin = tid < a.W && s.state[tid] == 1;
-        const unsigned m = __ballot_sync(kFull, fin);
-        if (fin) cands[n + __popc(m & ((1u << tid) - 1u))] = (uint32_t)(tid * a.V + a.eos);
-        if (tid == 0) s.count = n + __popc(m);
-    }
-    __syncthreads();
-    n = s.count;
     auto score_of = [&](unsigned long long c) -> Pair {
         const int w = (int)(uint32_t)c / a.V;
         if (!cand_key(c)) return {s.cum[w], 0.f};
@@ -145,16 +135,20 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
     }
     for (int i = tid; i < n; i += NT) keys[i] = score_key(score_of(cands[i]));
     __syncthreads();
-    for (int i = tid; i < n; i += NT) {
-        const unsigned long long k = keys[i];
-        const uint32_t place = (uint32_t)cands[i];
+    // ranks by counting, G neighbouring lanes per candidate
+    const int G = n <= NT / 8 ? 8 : n <= NT / 4 ? 4 : n <= NT / 2 ? 2 : 1, g = tid & (G - 1);
+    for (int i0 = 0; i0 < n; i0 += NT / G) {
+        const int i = i0 + tid / G;
+        const unsigned long long k = i < n ? keys[i] : 0ull;
+        const uint32_t place = i < n ? (uint32_t)cands[i] : 0u;
         int rk = 0;
 #pragma unroll 4
-        for (int o = 0; o < n; ++o) {
+        for (int o = g; o < n; o += G) {
             const unsigned long long ko = keys[o];
             rk += ko > k || (ko == k && (uint32_t)cands[o] < place);
         }
-        if (rk <= N) {
+        for (int o = G / 2; o > 0; o >>= 1) rk += __shfl_xor_sync(kFull, rk, o);
+        if (g == 0 && i < n && rk <= N) {
             s.sel[rk] = score_of(cands[i]);
             s.selw[rk] = (int)place / a.V;
             s.selp[rk] = (int)place;
@@ -330,6 +324,14 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
         __syncthreads();
         if (tid == 0) s.top.ne = 0;
         __syncthreads();
+        if (rank == 0 && tid < 32) {   // finished beams, key 0
+            const bool fin = lane < a.W && s.state[lane] == 1;
+            const unsigned m = __ballot_sync(kFull, fin);
+            int at = 0;
+            if (lane == 0 && m) at = peer_add(peer(&s.count, 0), __popc(m));
+            at = __shfl_sync(kFull, at, 0) + __popc(m & ((1u << lane) - 1u));
+            if (fin && at < room) cands[at] = (uint32_t)(lane * a.V + a.eos);
+        }
         for (int j = 0; j < mine; ++j) {
             const int u = rank + j * C, w = u / P, n = kept[j];
             const float bw = __shfl_sync(kFull, base, w);
@@ -354,7 +356,7 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
         __syncthreads();
         {   // more than there is room for here counts as more than there is room for there
             const int n = s.top.ne > CAPE ? CAPE + room : s.top.ne;
-            hand_over(n, [&](int i) { return s.top.el[min(i, CAPE - 1)]; }, cands, &s.count, room - a.W, &s.top.off);
+            hand_over(n, [&](int i) { return s.top.el[min(i, CAPE - 1)]; }, cands, &s.count, room, &s.top.off);
         }
         for (int j = 0; j < mine; ++j) {
             const int u = rank + j * C, w = u / P;
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
             hand_over(ne, [&](int i) {
                 const unsigned long long c = s.top.el[i];
                 return ((unsigned long long)cand_key(c) << 32) | (uint32_t)(w * a.V + cand_index(c));
-            }, cands, &s.count, room - a.W, &s.top.off);
+            }, cands, &s.count, room, &s.top.off);
         }
         if (C > 1) {
             cluster_arrive();
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
             __syncthreads();
         }
         if (rank == 0) {
-            const bool many = s.count > room - a.W;
+            const bool many = s.count > room;
             const int n = many ? 0 : s.count;
             if (tid <= N) s.selw[tid] = -1;
             if (many) {
