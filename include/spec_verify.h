@@ -526,9 +526,9 @@ int spec_beam_step(const spec_rows_params *params, const void *logits, const flo
  * was; a parent outside [-1, W) does too and raises SPEC_ERR_BAD_PARENT.
  * dst may be src (in place, any map including repeated parents; N <= W and
  * equal strides; rows that keep their place are not touched), and must not
- * overlap it otherwise. Strides in bytes, multiples of 1; rows and segments
- * of dst must not overlap. All of base, strides and unit_bytes multiples of
- * 16 is the fastest case.
+ * overlap it otherwise. Strides in bytes, of any alignment; rows and segments
+ * of dst must not overlap. A beam stride that is a multiple of 16 (and, out of
+ * place, a dst aligned like src) is the fastest case.
  */
 typedef struct {
     int32_t O;            /* outer count (layers), 0 .. 65535                 */

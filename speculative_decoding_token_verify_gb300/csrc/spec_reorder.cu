@@ -21,12 +21,14 @@ struct ReorderArgs {
     int32_t *status;
     int B, W, N, H, T;
     long long unit, ss[4], ds[4];
-    long long seg_tiles;   // tiles of NTR vectors per segment
+    long long seg_tiles;   // tiles of NTR CP vectors per segment, at least 1
     int in_place;
 };
 
-template <typename Vec, int WB>
-__global__ void __launch_bounds__(NTR) reorder_kernel(ReorderArgs a) {
+// WB: beams a thread has registers for; CP: columns per thread, so that few beams
+// too have several loads in flight
+template <typename Vec, int WB, int CP>
+__global__ void __launch_bounds__(NTR, 2) reorder_kernel(ReorderArgs a) {
     __shared__ int s_par[SPEC_MAX_BEAMS];
     const int o = blockIdx.z;
     const int h = (int)(blockIdx.x / a.seg_tiles);
@@ -45,31 +47,56 @@ __global__ void __launch_bounds__(NTR) reorder_kernel(ReorderArgs a) {
         __syncthreads();
         const long long units = a.lengths ? min(max(a.lengths[b], 0), a.T) : a.T;
         const long long bytes = units * a.unit;
-        const long long at = (tile * NTR + threadIdx.x) * (long long)sizeof(Vec);
-        if (at >= bytes) continue;
-        const char *src = a.src + o * a.ss[0] + b * a.ss[1] + h * a.ss[3] + at;
-        char *dst = a.dst + o * a.ds[0] + b * a.ds[1] + h * a.ds[3] + at;
-        Vec v[WB];
+        const char *src = a.src + o * a.ss[0] + b * a.ss[1] + h * a.ss[3];
+        char *dst = a.dst + o * a.ds[0] + b * a.ds[1] + h * a.ds[3];
+        // bytes up to an aligned address (the same for all beams), vectors, bytes
+        const long long head = min(bytes, (long long)(-reinterpret_cast<uintptr_t>(src) & (sizeof(Vec) - 1)));
+        const long long vecs = (bytes - head) / (long long)sizeof(Vec);
+        const long long i0 = tile * (NTR * CP) + threadIdx.x;
+        Vec v[CP][WB];
 #pragma unroll
-        for (int n = 0; n < WB; ++n)
-            if (n < a.N && s_par[n] >= 0) v[n] = *reinterpret_cast<const Vec *>(src + s_par[n] * a.ss[2]);
+        for (int c = 0; c < CP; ++c)
+            if (i0 + c * NTR < vecs) {
+                const char *p = src + head + (i0 + c * NTR) * (long long)sizeof(Vec);
 #pragma unroll
-        for (int n = 0; n < WB; ++n)
-            if (n < a.N && s_par[n] >= 0) *reinterpret_cast<Vec *>(dst + n * a.ds[2]) = v[n];
+                for (int n = 0; n < WB; ++n)
+                    if (n < a.N && s_par[n] >= 0) v[c][n] = *reinterpret_cast<const Vec *>(p + s_par[n] * a.ss[2]);
+            }
+#pragma unroll
+        for (int c = 0; c < CP; ++c)
+            if (i0 + c * NTR < vecs) {
+                char *p = dst + head + (i0 + c * NTR) * (long long)sizeof(Vec);
+#pragma unroll
+                for (int n = 0; n < WB; ++n)
+                    if (n < a.N && s_par[n] >= 0) *reinterpret_cast<Vec *>(p + n * a.ds[2]) = v[c][n];
+            }
+        // head and tail bytes: a segment's first tile has threads for all of them
+        const long long rest = bytes - vecs * (long long)sizeof(Vec);
+        if (sizeof(Vec) > 1 && tile == 0 && threadIdx.x < rest) {
+            const long long at = threadIdx.x < head ? threadIdx.x : bytes - rest + threadIdx.x;
+            char w[WB];
+#pragma unroll
+            for (int n = 0; n < WB; ++n)
+                if (n < a.N && s_par[n] >= 0) w[n] = src[at + s_par[n] * a.ss[2]];
+#pragma unroll
+            for (int n = 0; n < WB; ++n)
+                if (n < a.N && s_par[n] >= 0) dst[at + n * a.ds[2]] = w[n];
+        }
     }
 }
 
 template <typename Vec>
 static cudaError_t launch_vec(ReorderArgs &a, int O, cudaStream_t stream) {
+    const int cp = a.N <= 4 ? 4 : a.N <= 8 ? 2 : 1;
     const long long seg = (long long)a.T * a.unit / (long long)sizeof(Vec);
-    a.seg_tiles = (seg + NTR - 1) / NTR;
+    a.seg_tiles = seg > 0 ? (seg + NTR * cp - 1) / (NTR * cp) : 1;
     const long long gx = a.seg_tiles * a.H;
     if (gx > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const dim3 grid((unsigned)gx, (unsigned)(a.B < 65535 ? a.B : 65535), (unsigned)O);
-    if (a.N <= 4) reorder_kernel<Vec, 4><<<grid, NTR, 0, stream>>>(a);
-    else if (a.N <= 8) reorder_kernel<Vec, 8><<<grid, NTR, 0, stream>>>(a);
-    else if (a.N <= 16) reorder_kernel<Vec, 16><<<grid, NTR, 0, stream>>>(a);
-    else reorder_kernel<Vec, 32><<<grid, NTR, 0, stream>>>(a);
+    if (a.N <= 4) reorder_kernel<Vec, 4, 4><<<grid, NTR, 0, stream>>>(a);
+    else if (a.N <= 8) reorder_kernel<Vec, 8, 2><<<grid, NTR, 0, stream>>>(a);
+    else if (a.N <= 16) reorder_kernel<Vec, 16, 1><<<grid, NTR, 0, stream>>>(a);
+    else reorder_kernel<Vec, 32, 1><<<grid, NTR, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -142,16 +169,22 @@ extern "C" int spec_beam_reorder(const spec_reorder_params *p, const void *src, 
     a.H = p->H;
     a.T = p->T;
     a.unit = p->unit_bytes;
-    uint64_t bits = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) | (uint64_t)p->unit_bytes;
     for (int i = 0; i < 4; ++i) {
         a.ss[i] = sc[i] > 1 ? p->src_stride[i] : 0;
         a.ds[i] = dc[i] > 1 ? p->dst_stride[i] : 0;
-        bits |= (uint64_t)(a.ss[i] | a.ds[i]);
     }
+    // Vectors as wide as all beams of a segment, and its rows in src and dst, are
+    // aligned alike; a segment's own alignment, and a length that ends inside a
+    // vector, cost bytes at its ends.
+    uint64_t bits = (uint64_t)(a.ss[2] | a.ds[2]);
+    if (!a.in_place)
+        bits |= (uint64_t)((a.ss[0] - a.ds[0]) | (a.ss[1] - a.ds[1]) | (a.ss[3] - a.ds[3])) |
+                (reinterpret_cast<uintptr_t>(src) - reinterpret_cast<uintptr_t>(dst));
     spec_internal_set_error(SPEC_OK, "");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (bits % 16 == 0) e = launch_vec<uint4>(a, p->O, st);
+    if (bits % 16 == 0 && a.N <= 16) e = launch_vec<uint4>(a, p->O, st);
+    else if (bits % 8 == 0) e = launch_vec<uint2>(a, p->O, st);   // 32 beams' wider vectors leave one CTA an SM
     else if (bits % 4 == 0) e = launch_vec<uint32_t>(a, p->O, st);
     else if (bits % 2 == 0) e = launch_vec<uint16_t>(a, p->O, st);
     else e = launch_vec<uint8_t>(a, p->O, st);

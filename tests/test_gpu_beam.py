@@ -202,6 +202,37 @@ def test_reorder(dtype, D, W):
         np.testing.assert_array_equal((s.view(torch.int16) if kind else s).cpu().numpy(), want)
 
 
+@pytest.mark.parametrize("off", [0, 1, 2, 3, 7, 15])
+@pytest.mark.parametrize("T,D", [(64, 33), (16, 40), (48, 1), (5, 3), (1, 1)])
+def test_reorder_of_bytes_at_every_alignment(off, T, D):
+    """Segments that start and lengths that end anywhere in a vector; beams a
+    multiple of 16 bytes apart, or not; nothing beside the rows is touched."""
+    sv = _sv()
+    O, B, W, H = 2, 3, 4, 2
+    for pad in (0, 5):
+        row = H * T * D
+        beam = (row + 15) // 16 * 16 + pad
+        buf = torch.randint(0, 256, (off + O * B * W * beam + 32,), dtype=torch.uint8, device=DEV)
+        s = buf.as_strided((O, B, W, H, T, D), (B * W * beam, W * beam, beam, T * D, D, 1), off)
+        parent = torch.tensor([[3, 0, 1, 2], [0, 0, 3, -1], [1, 1, 1, 1]], dtype=torch.int32, device=DEV)
+        ln = torch.tensor([T, T // 2, max(T - 1, 0)], dtype=torch.int32, device=DEV)
+        host = buf.cpu().numpy().copy()
+        view = np.lib.stride_tricks.as_strided(host[off:], s.shape, s.stride())
+        view[...] = ref.reorder(view, parent.cpu().numpy(), ln.cpu().numpy())
+        before = s.clone()
+        sv.beam_reorder(s, parent, lengths=ln, batch_dim=1, length_dim=4)
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(buf.cpu().numpy(), host)
+        out = torch.randint(0, 256, (off + 3 + O * B * W * beam,), dtype=torch.uint8, device=DEV)
+        for shift in (0, 3):
+            d = out.as_strided(s.shape, s.stride(), off + shift)
+            want = torch.from_numpy(ref.reorder(before.cpu().numpy(), parent.cpu().numpy(), ln.cpu().numpy()))
+            d.copy_(before)
+            sv.beam_reorder(before.contiguous(), parent, lengths=ln, batch_dim=1, length_dim=4, out=d)
+            torch.cuda.synchronize()
+            assert torch.equal(d.cpu(), want)
+
+
 def test_reorder_out_of_place_and_fewer_beams():
     sv = _sv()
     state = _state((4, 6, 50), torch.float32, 1)                    # [B, W, X]
