@@ -591,12 +591,14 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     __shared__ int s_ids[SPEC_MAX_TOP];
     __shared__ float s_p[SPEC_MAX_TOP];
     __shared__ double s_d[SPEC_MAX_TOP / 32];
+    __shared__ uint32_t s_seen[32];   // a hash of the part's tokens: bits met twice may be a token listed twice
+    __shared__ int s_dup;
     const int tid = threadIdx.x;
     const int row = blockIdx.x / parts, rank = blockIdx.x - row * parts;
     const int b = row / a.K, kr = row - b * a.K;
     const T *py = static_cast<const T *>(a.y) + b * a.bs + kr * a.rs;
     T *pg = static_cast<T *>(a.g) + b * a.gbs + kr * a.grs;
-    const Part<T> part(py, a.V, rank, parts);
+    const Part<T> part(py, a.V, rank, parts, UG * NT);
     const Out<T> out(pg, part);
     const int n = part.n;
     const uint4 *body = part.body();
@@ -606,12 +608,18 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
         zero_part<T, NT>(part, out);
         return;
     }
+    const bool full = n == UG * NT;
     uint4 w[UG];
+    if (full) {
 #pragma unroll
-    for (int u = 0; u < UG; ++u) {
-        const int i = u * NT + tid;
-        if (i < n) w[u] = ld_rw(body + i);
+        for (int u = 0; u < UG; ++u) w[u] = ld_rw(body + u * NT + tid);
+    } else {
+#pragma unroll
+        for (int u = 0; u < UG; ++u)
+            if (u * NT + tid < n) w[u] = ld_rw(body + u * NT + tid);
     }
+    if (tid < 32) s_seen[tid] = 0u;
+    if (tid == 0) s_dup = 0;
     int id = -1;
     float lp = neg_inf();
     if (tid < a.M) {
@@ -647,25 +655,36 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
         s_p[tid] = p;
     }
     const float yl = own ? load1_rw(py + id) : neg_inf();
+    if (!need) __syncthreads();   // (the sum's barrier, where there was one)
+    if (own) {
+        const uint32_t m = 1u << (id & 31);
+        if (atomicOr(&s_seen[id >> 5 & 31], m) & m) s_dup = 1;
+    }
     const int ei = part.edge(tid);
     const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
     __syncthreads();   // before anything is overwritten
     const Factor f = factor_of(us * st.w, st.z == neg_inf() ? 0.f : st.z, a.sL);
+    if (full) {
 #pragma unroll
-    for (int u = 0; u < UG; ++u) {
-        const int i = u * NT + tid;
-        if (i < n) grad_vec(part, out, i, w[u], f, a.sL);
+        for (int u = 0; u < UG; ++u) grad_vec(part, out, u * NT + tid, w[u], f, a.sL);
+    } else {
+#pragma unroll
+        for (int u = 0; u < UG; ++u)
+            if (u * NT + tid < n) grad_vec(part, out, u * NT + tid, w[u], f, a.sL);
     }
     if (ei >= 0) pg[ei] = to_elem<T>(grad_one(f, ey, a.sL));
     __syncthreads();   // the listed tokens' values go over what was just written
     if (own) {
         bool once = true;
-        float sum = 0.f;
-        for (int i = 0; i < a.M; ++i)
-            if (s_ids[i] == id) {
-                if (i < tid) once = false;
-                sum += s_p[i];
-            }
+        float sum = p;
+        if (s_dup) {
+            sum = 0.f;
+            for (int i = 0; i < a.M; ++i)
+                if (s_ids[i] == id) {
+                    if (i < tid) once = false;
+                    sum += s_p[i];
+                }
+        }
         if (once) {
             const float kl = us * st.y * (a.tail && need ? (float)P : 1.f);
             const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - st.x) * a.sL) : 0.f;

@@ -65,6 +65,16 @@ struct Part {
         : r(row, V), first(rank == 0), last(rank == parts - 1) {
         k0 = (int)((long long)r.nvec * rank / parts);
         n = (int)((long long)r.nvec * (rank + 1) / parts) - k0;
+        ends(V);
+    }
+    // parts of `size` vectors, the last one shorter
+    __device__ __forceinline__ Part(const T *row, int V, int rank, int parts, int size)
+        : r(row, V), first(rank == 0), last(rank == parts - 1) {
+        k0 = min(r.nvec, rank * size);
+        n = last ? r.nvec - k0 : min(size, r.nvec - k0);
+        ends(V);
+    }
+    __device__ __forceinline__ void ends(int V) {
         e0 = first ? 0 : r.vec_index(k0);
         e1 = last ? V : r.vec_index(k0 + n);
     }
