@@ -72,10 +72,7 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
     if (kCluster && tid == 0) s_ns = 0;
     if (!over) {
         unsigned long long *stage = reinterpret_cast<unsigned long long *>(s.c);
-        const bool many = expand(part, thr, s, [&](bool want, unsigned long long c) {
-            const int at = take(want, kCluster ? &s_ns : &s.ne);
-            if (want && at < CAPE) (kCluster ? stage : s.el)[at] = c;
-        });
+        const bool many = expand(part, thr, s, kCluster ? stage : s.el, kCluster ? &s_ns : &s.ne);
         if (kCluster) {
             __syncthreads();
             hand_over(many ? CAPE + 1 : s_ns, [&](int i) { return stage[min(i, CAPE - 1)]; }, s.el, &s.ne, CAPE, &s.off);

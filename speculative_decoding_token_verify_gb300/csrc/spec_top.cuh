@@ -262,12 +262,13 @@ __device__ __forceinline__ void hand_over(int n, F word, unsigned long long *to,
         if (*off + i < room) peer_store(at + 8u * (*off + i), word(i));
 }
 
-// The passing vectors' logits at or above thr: put(wanted, candidate) is called
-// by whole warps. Returns whether more vectors reach thr than there is room for.
-template <typename T, typename F>
-__device__ __forceinline__ bool expand(const Part<T> &p, float thr, TopShared &s, F put) {
-    constexpr int E = Row<T>::E;
-    const int np = min(s.n, CAP);
+// The passing vectors' logits at or above thr, as candidates in dst[0 .. CAPE),
+// counted in *counter past CAPE too. Returns whether more vectors reach thr than
+// there is room for. A barrier follows.
+template <typename T>
+__device__ __forceinline__ bool expand(const Part<T> &p, float thr, TopShared &s, unsigned long long *dst, int *counter) {
+    constexpr int E = Row<T>::E, G = 4;   // logits per thread and round, loaded together
+    const int np = min(s.n, CAP), lane = threadIdx.x & 31;
     for (int i0 = 0; i0 < np; i0 += NT) {
         const int i = i0 + threadIdx.x;
         const bool want = i < np && s.c[i] >= thr;
@@ -277,21 +278,32 @@ __device__ __forceinline__ bool expand(const Part<T> &p, float thr, TopShared &s
     __syncthreads();
     const int nf = s.nf;
     if (nf > CAPE) return true;
-    // one thread per logit
-    for (int i0 = 0; i0 < nf * E; i0 += 2 * NT) {
-        float z[2];
-        int at[2];
+    for (int i0 = 0; i0 < nf * E; i0 += G * NT) {
+        float z[G];
+        int index[G];
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < G; ++k) {
             const int i = i0 + k * NT + threadIdx.x, j = i & (E - 1);
             const int code = i < nf * E ? s.few[i / E] : ~0;
-            at[k] = code >= 0 ? p.r.vec_index(code) + j : ~code;
-            z[k] = i < nf * E && (code >= 0 || j == 0) ? load1(p.r.p + at[k]) : neg_inf();
+            index[k] = code >= 0 ? p.r.vec_index(code) + j : ~code;
+            z[k] = i < nf * E && (code >= 0 || j == 0) ? load1(p.r.p + index[k]) : neg_inf();
         }
+        unsigned m[G];
+        int total = 0;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const uint32_t key = order_key(z[k]);
-            put(z[k] >= thr && key != 0u, cand(key, at[k]));
+        for (int k = 0; k < G; ++k) {
+            m[k] = __ballot_sync(kFull, z[k] >= thr && order_key(z[k]) != 0u);
+            total += __popc(m[k]);
+        }
+        if (total == 0) continue;
+        int at = 0;
+        if (lane == 0) at = atomicAdd(counter, total);
+        at = __shfl_sync(kFull, at, 0);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+            const int to = at + __popc(m[k] & ((1u << lane) - 1u));
+            if ((m[k] >> lane & 1u) && to < CAPE) dst[to] = cand(order_key(z[k]), index[k]);
+            at += __popc(m[k]);
         }
     }
     return false;
