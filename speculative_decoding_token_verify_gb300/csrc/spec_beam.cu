@@ -15,7 +15,7 @@
 // touches a selected place, all CTAs sum the beams concerned again in two-float
 // arithmetic (relative error about 1e-10) and the ranking is repeated.
 //
-// Measured: 64 sequences of 8 beams, V = 128256 bf16, N = 16: 41 us, 2.9 TB/s of
+// Measured: 64 sequences of 8 beams, V = 128256 bf16, N = 16: 40 us, 2.9 TB/s of
 // the live rows; the stream takes 29 us of it (512 rows in one wave, whose CTAs
 // start and end together), the exchange, candidates and ranking the rest. With
 // scores compared in fp64 the call took 76 to 119 us, with the top lists as a

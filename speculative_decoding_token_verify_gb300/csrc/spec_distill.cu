@@ -28,8 +28,8 @@
 //
 // Measured (bf16, M = 64; of the measured copy rate, 6691 GB/s): the loss of 1920 rows of
 // 152064 85 us, 6.2 TB/s, 93%; the step of 2048 rows of 128256 190 us, 5.3 TB/s
-// of read and written gradient bytes, 79%; the gradient of 320 rows of 128256 29
-// us, 80%. The step is bound by loads in flight in its second pass (issue slots
+// of read and written gradient bytes, 79%; the gradient of 320 rows of 128256 25
+// us, 92%. The step is bound by loads in flight in its second pass (issue slots
 // 49% busy, long-scoreboard stalls first); without the L2 policies it took 222 us,
 // with S = 8 and the whole part in registers 285 us (a part's fixed cost, about
 // 7 us, eight times a row), with a persistent CTA per SM fed by bulk copies into a

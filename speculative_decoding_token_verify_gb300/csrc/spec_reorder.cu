@@ -5,9 +5,12 @@
 // stores any. Rows that keep their place are neither read nor written, and what
 // lies behind a sequence's length is skipped by whole tiles.
 //
-// Measured: a 2 GB bf16 cache, 8 beams of which about a third stay, 287 us: 6.9
+// Measured: a 2 GB bf16 cache, 8 beams of which about a third stay, 280 us: 7.0
 // TB/s of moved bytes (parents that go on twice are read from L2 the second
-// time), the rate of a plain copy.
+// time), the rate of a plain copy; with one column per thread 308 us. 16 beams
+// run at 84% of that, 3 beams at 65%: loads of beams that stay leave their
+// registers idle. Listing the beams that move first, so that few leave room for
+// more columns, spilled and was slower throughout (317 us).
 #include "spec_rows.cuh"
 
 namespace sr {

@@ -9,12 +9,11 @@
 // bounds, maxima and sums meet in one exchange through distributed shared
 // memory, and the first CTA ranks what passes the best bound.
 //
-// Measured: 2048 rows of 128256 bf16, M = 64: 103 us, 5.1 TB/s, 76% of the
-// measured copy rate. The stream with its sums alone takes 86 us; looking at
-// what passed and ranking it the rest (46 thousand warp instructions a row, a
-// third of them there, issue slots 66% busy). A CTA that goes on to further
-// rows with the next one's first loads in flight took 110 us, whole iterations
-// without bounds 110 us (registers spill).
+// Measured: 2048 rows of 128256 bf16, M = 64: 102 us, 5.2 TB/s, 77% of the
+// measured copy rate. The stream with its sums alone takes 86 us; the bounds,
+// looking at what passed and ranking it the rest (issue slots 66% busy). A CTA
+// that goes on to further rows with the next one's first loads in flight took
+// 110 us, whole iterations without bounds 105 to 110 us.
 #include "spec_top.cuh"
 
 namespace sr {
