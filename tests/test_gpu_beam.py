@@ -120,6 +120,17 @@ def test_scores_closer_than_fp32_sums_tell_apart(dtype, V):
         _check(z[:n].to(DEV), scores[:n].to(DEV), 4)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_longest_rows_and_most_beams(dtype):
+    z, scores, _ = _case(1, 32, 1 << 20, dtype, 7)
+    z[0, 3] = z[0, 2]                 # identical beams at equal scores
+    scores[0, 3] = scores[0, 2]
+    _check(z, scores, 64)
+    z[0, 5:9] = 0.25                  # rows of equal logits among the best
+    scores[0, 5:9] = 20.0
+    _check(z, scores, 64)
+
+
 def test_spoilt_beams():
     sv = _sv()
     z, scores, _ = _case(3, 3, 400, "f32", 4)
@@ -283,6 +294,33 @@ def test_reorder_strided_views_and_large_offsets():
     s[0, 1] = torch.arange(1024, device=DEV).to(torch.uint8)
     sv.beam_reorder(s, torch.tensor([[1, 1]], dtype=torch.int32, device=DEV))
     assert torch.equal(s[0, 0], s[0, 1]) and int(s[0, 0].long().sum()) > 0
+
+
+def test_reorder_in_a_graph_and_on_a_stream():
+    sv = _sv()
+    state = _state((2, 3, 4, 2, 50, 16), torch.bfloat16, 5)
+    parent = torch.tensor([[1, 0, 3, 3], [0, 0, 0, 0], [3, 2, 1, 0]], dtype=torch.int32, device=DEV)
+    ln = torch.tensor([50, 7, 0], dtype=torch.int32, device=DEV)
+    kw = dict(lengths=ln, batch_dim=1, length_dim=4)
+    once = sv.beam_reorder(state.clone(), parent, **kw)
+    twice = sv.beam_reorder(once.clone(), parent, **kw)
+    s = torch.cuda.Stream()
+    a = state.clone()
+    torch.cuda.synchronize()
+    sv.beam_reorder(a, parent, stream=s, **kw)
+    s.synchronize()
+    assert torch.equal(a, once)
+    b = state.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.beam_reorder(b, parent, **kw)
+    b.copy_(state)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b, once)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(b, twice)
 
 
 # ---- a run of them ------------------------------------------------------------------------------

@@ -146,6 +146,20 @@ def test_offsets_beyond_32_bits():
     _check(rows, 16)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_longest_rows(dtype):
+    """V = 2^20, split over a cluster and, repeated, one CTA a row."""
+    sv = _sv()
+    V = 1 << 20
+    g = torch.Generator().manual_seed(8)
+    z = _rows("normal", 2, V, g).view(2, 1, V).to(DT[dtype]).to(DEV)
+    z[1, 0, :] = torch.sort(z[1, 0]).values          # ascending: the filter lets everything through
+    out = _check(z, 128)
+    many = sv.top_logprobs(z.expand(2, 400, V), 128)
+    assert torch.equal(many["ids"], out["ids"].expand_as(many["ids"]))
+    assert torch.equal(many["logprobs"], many["logprobs"][:, :1].expand_as(many["logprobs"]))
+
+
 def test_spoilt_rows_stay_alone():
     sv = _sv()
     g = torch.Generator().manual_seed(6)
