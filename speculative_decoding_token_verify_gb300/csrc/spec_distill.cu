@@ -22,19 +22,22 @@
 // list's tokens in its part, and what the CTAs know (maxima, sums, P, the
 // loss's terms) meets in one exchange through distributed shared memory. The
 // step goes over its part a second time, backwards: the last two iterations
-// are still in registers, the others come again from L2, where they were kept
-// by policy, so HBM reads a row once and writes its gradient once. The gradient
-// alone needs no exchange: a CTA per 256 UG vectors.
+// are still in registers, up to three more in shared memory, the others come
+// again from L2, where they were kept by policy, so HBM reads a row once and
+// writes its gradient once. The gradient alone needs no exchange: a CTA per 256
+// UG vectors.
 //
-// Measured (bf16, M = 64; of the measured copy rate, 6691 GB/s): the loss of 1920 rows of
-// 152064 85 us, 6.2 TB/s, 93%; the step of 2048 rows of 128256 190 us, 5.3 TB/s
-// of read and written gradient bytes, 79%; the gradient of 320 rows of 128256 25
-// us, 92%. The step is bound by loads in flight in its second pass (issue slots
-// 49% busy, long-scoreboard stalls first); without the L2 policies it took 222 us,
-// with S = 8 and the whole part in registers 285 us (a part's fixed cost, about
-// 7 us, eight times a row), with a persistent CTA per SM fed by bulk copies into a
-// ring of chunks 244 us (and the loss 132-156 us): 16 warps do not hide the
-// ring's waits.
+// Measured (bf16, M = 64; shares of the measured copy rate, 6691 GB/s): the loss
+// of 1920 rows of 152064 85 us, 6.2 TB/s, 93%; the step of 2048 rows of 128256
+// 186 us, 5.4 TB/s of read and written bytes, 80%; the gradient of 320 rows of
+// 128256 25 us, 92%. The step is bound by loads in flight in its second pass
+// (issue slots half busy, long-scoreboard stalls first). Without the held
+// iterations it took 190 us, without the L2 policies too 222 us, with S = 8 and
+// the whole part in registers 285 us (a part's fixed cost, about 7 us, eight
+// times a row), with a persistent CTA per SM fed by bulk copies into a ring of
+// chunks 244 us (and the loss 132 to 156 us): 16 warps do not hide the ring's
+// waits. 256 threads, 4 loads an iteration and 4 CTAs per SM: 190 us then; 2 or 3
+// loads and 5 or 6 CTAs 197 to 217, 128 or 512 threads 214 and 212.
 #include <mutex>
 
 #include "spec_rows.cuh"
@@ -414,7 +417,7 @@ __device__ __forceinline__ void put_listed(const DistillArgs &a, const List &l, 
 }
 
 template <typename T, bool kGrad, int NT, int U>
-__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S) {
+__global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, int S, int held) {
     constexpr int E = Row<T>::E, NW = NT / 32;
     extern __shared__ __align__(16) uint8_t s_map[];
     __shared__ List s_list;
@@ -431,7 +434,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     auto full = [&](int it) { return (it + 1) * U * NT <= n; };
     auto load = [&](uint4 (&w)[U], int it) {
         const uint4 *p = body + it * U * NT + tid;
-        const uint64_t policy = kGrad && it + 2 < its ? l2_keep() : l2_drop();
+        const uint64_t policy = kGrad && it < its - 2 - held ? l2_keep() : l2_drop();
         if (full(it)) {
 #pragma unroll
             for (int u = 0; u < U; ++u) w[u] = ldg_stream(p + u * NT, policy);
@@ -490,9 +493,16 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     }
 
     Sum acc = sum_init(a.sL, a.resc);
+    // `held` iterations before the last two go to shared memory for the second pass
+    uint4 *s_held = reinterpret_cast<uint4 *>(s_map + (map_words + 3u) / 4u * 16u) + tid;
+    const int held0 = max(its - 2 - held, 0);
     auto work = [&](uint4 (&w)[U], int it) {
         if (full(it)) fold<T, true, U>(acc, w, s_map, it * U * NT + tid, NT, n, a.sL, a.resc);
         else fold<T, false, U>(acc, w, s_map, it * U * NT + tid, NT, n, a.sL, a.resc);
+        if (kGrad && it >= held0 && it < its - 2) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) s_held[((it - held0) * U + u) * NT] = w[u];
+        }
     };
     for (int it = 0; it < its; it += 2) {   // both buffers end up with the last two iterations
         if (it + 1 < its) load(w1, it + 1);
@@ -568,8 +578,13 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
                     if (i0 + u * NT < n) grad_vec(part, out, i0 + u * NT, w[u], f, a.sL);
             }
             if (it < 2) return;
+            if (it - 2 >= held0) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid, l2_drop());
+                for (int u = 0; u < U; ++u) w[u] = s_held[((it - 2 - held0) * U + u) * NT];
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; ++u) w[u] = ld_rw(body + ((it - 2) * U + u) * NT + tid, l2_drop());
+            }
         };
         int it = its - 1;
         if (it >= 0 && (it & 1) == 0) grad(w0, it--);
@@ -696,7 +711,14 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
 template <typename T, bool kGrad, int NT, int U>
 static cudaError_t launch_distill(const DistillArgs &a, int S, cudaStream_t stream) {
     const long long nvec = (long long)a.V / Row<T>::E / S + 1;
-    const size_t smem = (size_t)((16 + Row<T>::E * nvec + 8 + 31) / 32 + 4) / 4 * 16 + 16;
+    size_t smem = (size_t)((16 + Row<T>::E * nvec + 8 + 31) / 32 + 4) / 4 * 16 + 16;
+    // iterations held in shared memory, while 1024 / NT CTAs fit an SM (54 KB each)
+    int held = 0;
+    if (kGrad) {
+        const long long its = (nvec + U * NT - 1) / (U * NT);
+        while (held < its - 2 && held < 3 && smem + (size_t)(held + 1) * U * NT * 16 <= 54000 * NT / 256) ++held;
+        smem += (size_t)held * U * NT * 16;
+    }
     if (smem > 40000) {
         static std::mutex mu;
         static bool done[64];
@@ -711,7 +733,7 @@ static cudaError_t launch_distill(const DistillArgs &a, int S, cudaStream_t stre
             done[dev & 63] = true;
         }
     }
-    return launch_cluster(distill_kernel<T, kGrad, NT, U>, (unsigned)((long long)a.B * a.K * S), NT, S, smem, stream, a, S);
+    return launch_cluster(distill_kernel<T, kGrad, NT, U>, (unsigned)((long long)a.B * a.K * S), NT, S, smem, stream, a, S, held);
 }
 
 template <typename T, bool kLoss, bool kGrad>
@@ -725,10 +747,11 @@ cudaError_t launch(const DistillArgs &a, cudaStream_t stream) {
     } else {
         int S = 1;
         // with the gradient, the 608 / S rows in flight are read twice and have to
-        // stay in L2: 2048 rows of 128256 bf16 take 215 us at S = 1, 192 at 2, 202
-        // at 4; rows of 32000 57 us at 1, 79 at 2
+        // stay in L2 (116 MB of 129): 2048 rows of 128256 bf16 take 241 us at S = 1,
+        // 187 at 2, 208 at 4; 1536 rows of 180000 198 at 2, 207 at 4, of 235000 345
+        // at 2, 263 at 4; 2048 rows of 32000 57 at 1, 72 at 2
         if (kGrad)
-            while (S < kMaxCluster && 608 / S * (long long)a.V * (long long)sizeof(T) > (80ll << 20)) S *= 2;
+            while (S < kMaxCluster && 608 / S * (long long)a.V * (long long)sizeof(T) > (116ll << 20)) S *= 2;
         // few rows are split while there are SM slots and a part keeps two vectors
         // per thread: 32 rows of 128256 take 8.1 us at S = 8 and 14.6 at 1, 320 rows
         // 18.1 at 2 and 21.7 at 1 (the loss)
