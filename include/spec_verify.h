@@ -467,10 +467,11 @@ int spec_top_logprobs(const spec_rows_params *params, const void *logits, float 
  * (with tail = 0 p_T = 0; with tail = 1 and no unlisted token P q_v for q_v).
  * A token listed twice carries both probabilities and counts once in q_T.
  * A row of weight 0 or with an empty list (no id, or with tail = 0 no
- * probability above 0) has loss 0 and gradient 0 whatever its logits. A listed token that the student masks makes the loss
- * +inf, the gradient stays finite. A student row without unmasked tokens:
- * loss +inf, gradient 0, SPEC_ERR_BAD_ROW. An id outside [-1, V) is taken as
- * absent and raises SPEC_ERR_BAD_TOKEN.
+ * probability above 0) has loss 0 and gradient 0 whatever its logits. A listed
+ * token that the student masks makes the loss +inf, the gradient stays finite.
+ * A student row without unmasked tokens: loss +inf, gradient 0,
+ * SPEC_ERR_BAD_ROW. An id outside [-1, V) is taken as absent and raises
+ * SPEC_ERR_BAD_TOKEN.
  *
  * spec_distill_loss: loss [B][K] f32 out, stats [B][K][4] f32 out (16-byte
  *   aligned): the row's maximum m, 1 / sum_v exp(s (y_v - m)), the unlisted
@@ -483,7 +484,7 @@ int spec_top_logprobs(const spec_rows_params *params, const void *logits, float 
  * weight [B][K] f32 or NULL (1). dlogits may be the logits themselves
  * (in place, equal strides), and must not overlap them otherwise.
  * Precision: q and its sums in fp32, the list's sum P to 2e-10, the loss's
- * terms added in fp64.
+ * terms added in two floats.
  */
 int spec_distill_loss(const spec_rows_params *params, const void *logits, const float *logprobs, const int32_t *ids,
                       const float *weight, float *loss, float *stats, int32_t *status, void *stream);

@@ -152,7 +152,9 @@ __device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int 
     o.put(p, i, z);
 }
 
-// L2 policies: rows read twice are kept for the second read, then let go
+// L2 policies: rows read twice are kept for the second read, then let go. No
+// load takes the read-only path: the step may write over its logits (and the
+// path gains nothing, 186 us with it as without).
 __device__ __forceinline__ uint64_t l2_keep() {
     uint64_t p;
     asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
@@ -163,9 +165,9 @@ __device__ __forceinline__ uint64_t l2_drop() {
     asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
-__device__ __forceinline__ uint4 ldg_stream(const uint4 *p, uint64_t policy) {
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p, uint64_t policy) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p), "l"(policy));
     return v;
@@ -437,10 +439,10 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         const uint64_t policy = kGrad && it < its - 2 - held ? l2_keep() : l2_drop();
         if (full(it)) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = ldg_stream(p + u * NT, policy);
+            for (int u = 0; u < U; ++u) w[u] = ld_stream(p + u * NT, policy);
         } else {
 #pragma unroll
-            for (int u = 0; u < U; ++u) w[u] = (it * U + u) * NT + tid < n ? ldg_stream(p + u * NT, policy) : masked_vec<T>();
+            for (int u = 0; u < U; ++u) w[u] = (it * U + u) * NT + tid < n ? ld_stream(p + u * NT, policy) : masked_vec<T>();
         }
     };
     uint4 w0[U], w1[U];   // iterations it and it + 1; the first is on its way during the list's work
