@@ -414,8 +414,8 @@ int spec_irls_refit(int32_t K, void *state, float *est_params, double damping, d
  * i * row_stride. Strides are in elements and may be 0 (a repeated row) for
  * inputs; a stride smaller than V otherwise overlaps rows, which inputs may
  * and outputs may not. Any alignment to the element works; no stride or
- * length needs to be a multiple of anything. A logit of -inf or below -1e29
- * is masked (the token has probability 0). NaN or +inf logits spoil their own
+ * length needs to be a multiple of anything. A logit of -inf or up to -1e29f
+ * is masked (the token has probability 0); finite ones may be of any size. NaN or +inf logits spoil their own
  * row's outputs only (its floats are NaN or infinite) and raise
  * SPEC_ERR_BAD_ROW.
  *

@@ -236,9 +236,11 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
         float mx = neg_inf(), sum = 0.f, thr = sv::kMaskFloor;
         int n = 0;
         if (s.state[u / P] == 0) {
-            stream_part(part_of(u), N, kLog2e, sv::kRescale, s.top, thr);
+            const Part<T> p = part_of(u);
+            stream_part(p, N, kLog2e, sv::kRescale, s.top, thr);
             __syncthreads();
             part_sum(s.top, kLog2e, mx, sum);
+            if (far_max(mx, kLog2e)) sum = count_equal(p, mx, s.top);
             n = s.top.n > CAP ? -1 : s.top.n;
         }
         if (most > 1) {   // keep what still reaches the bound

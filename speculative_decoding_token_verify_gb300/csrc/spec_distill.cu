@@ -28,11 +28,11 @@
 // UG vectors.
 //
 // Measured (bf16, M = 64; shares of the measured copy rate, 6691 GB/s): the loss
-// of 1920 rows of 152064 85 us, 6.2 TB/s, 93%; the step of 2048 rows of 128256
-// 186 us, 5.4 TB/s of read and written bytes, 80%; the gradient of 320 rows of
-// 128256 25 us, 92%. The step is bound by loads in flight in its second pass
+// of 1920 rows of 152064 87 us, 6.1 TB/s, 91%; the step of 2048 rows of 128256
+// 185 us, 5.4 TB/s of read and written bytes, 81%; the gradient of 320 rows of
+// 128256 26 us, 90%. The step is bound by loads in flight in its second pass
 // (issue slots half busy, long-scoreboard stalls first). Without the held
-// iterations it took 190 us, without the L2 policies too 222 us, with S = 8 and
+// iterations it takes 190 us, without the L2 policies too 222 us, with S = 8 and
 // the whole part in registers 285 us (a part's fixed cost, about 7 us, eight
 // times a row), with a persistent CTA per SM fed by bulk copies into a ring of
 // chunks 244 us (and the loss 132 to 156 us): 16 warps do not hide the ring's
@@ -122,17 +122,11 @@ __device__ __forceinline__ void zero_part(const Part<T> &p, const Out<T> &o) {
     if (i >= 0) o.g[i] = to_elem<T>(0.f);
 }
 
-// The unlisted tokens' gradient ku e^{s (y - mo)} as ku2 2^{y sL - c}, c =
-// fl(mo sL) and its rounding in ku2: one FMA, one exponential, one product per
-// logit; masked logits give 0
+// The unlisted tokens' gradient ku e^{s (y - mo)}; masked logits give 0
 struct Factor {
-    float ku, c;
+    float ku, mo;
 };
-__device__ __forceinline__ Factor factor_of(float ku, float mo, float sL) {
-    const float c = mo * sL;
-    return {ku * ex2(-fmaf(mo, sL, -c)), c};
-}
-__device__ __forceinline__ float grad_one(const Factor &f, float y, float sL) { return f.ku * ex2(fmaf(y, sL, -f.c)); }
+__device__ __forceinline__ float grad_one(const Factor &f, float y, float sL) { return f.ku * ex2((y - f.mo) * sL); }
 
 template <typename T>
 __device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int i, const uint4 &w, const Factor &f,
@@ -140,11 +134,11 @@ __device__ __forceinline__ void grad_vec(const Part<T> &p, const Out<T> &o, int 
     constexpr int E = Part<T>::E;
     float z[E];
     Elem<T>::unpack(w, z);
-    const float2 L2 = make_float2(sL, sL), mc = make_float2(-f.c, -f.c), k2 = make_float2(f.ku, f.ku);
+    const float2 L2 = make_float2(sL, sL), mo = make_float2(-f.mo, -f.mo), k2 = make_float2(f.ku, f.ku);
     const float2 zero = make_float2(0.f, 0.f);
 #pragma unroll
     for (int j = 0; j < E / 2; ++j) {
-        const float2 y = sv::pfma(make_float2(z[2 * j], z[2 * j + 1]), L2, mc);
+        const float2 y = sv::pfma(sv::padd(make_float2(z[2 * j], z[2 * j + 1]), mo), L2, zero);
         const float2 g = sv::pfma(make_float2(ex2(y.x), ex2(y.y)), k2, zero);
         z[2 * j] = g.x;
         z[2 * j + 1] = g.y;
@@ -191,7 +185,7 @@ struct __align__(16) Known {
     float mo, So;    // unlisted tokens: maximum, sum of 2^{(y - mo) sL}
     float ml, Sl;    // listed tokens: the same, each once
     float Ph, Pl;    // sum of p, in two floats
-    float Bh, Bl;    // sum of p (l - s y), in two floats
+    float Bh, Bl;    // sum of p (l - s (y - y0)), in two floats
 };
 
 // a two-float sum with the lane o away; both lanes get the same bits
@@ -233,12 +227,21 @@ struct Row2 {
 };
 
 // a row's list in shared memory: this part's tokens (-1: none), probabilities
-// and logits; dup: some token is listed twice
+// and logits; the warps' largest logits of the whole row's list; dup: some token
+// is listed twice
 struct List {
     int ids[SPEC_MAX_TOP];
-    float p[SPEC_MAX_TOP], yl[SPEC_MAX_TOP];
+    float p[SPEC_MAX_TOP], yl[SPEC_MAX_TOP], top[SPEC_MAX_TOP / 32];
     int dup;
 };
+
+// y0, the largest unmasked logit of the list (or 0): the loss's terms are taken
+// against it, so that rows far from 0 lose nothing
+__device__ __forceinline__ float list_top(const List &l) {
+    const float m = fmaxf(fmaxf(l.top[0], l.top[1]), fmaxf(l.top[2], l.top[3]));
+    static_assert(SPEC_MAX_TOP == 128, "four warps hold a list");
+    return m > sv::kMaskFloor ? m : 0.f;
+}
 
 // whether entry t is the first of its token
 __device__ __forceinline__ bool first_entry(const List &l, int t) {
@@ -264,9 +267,10 @@ __device__ __forceinline__ Known list_known(const DistillArgs &a, List &l, int t
     k.Ph = ph;
     k.Pl = pl;
     if (id >= 0 && lp > -700.f) {
-        if (there) {   // p (l - s y), each product and sum with its rounding
-            const float sy = __fmul_rn(a.s, yl), syl = __fmaf_rn(a.s, yl, -sy);
+        if (there) {   // p (l - s (y - y0)), each product and sum with its rounding
             float dh, dl;
+            two_sum(yl, -list_top(l), dh, dl);
+            const float sy = __fmul_rn(a.s, dh), syl = __fmaf_rn(a.s, dh, -sy) + a.s * dl;
             two_sum(lp, -sy, dh, dl);
             dl -= syl;
             k.Bh = __fmul_rn(ph, dh);
@@ -303,7 +307,7 @@ __device__ __forceinline__ void mask_listed(uint4 &w, uint32_t bits) {
 // Listed tokens are masked in w itself: the gradient there comes later. kFull:
 // all of the vectors are in the part.
 template <typename T, bool kFull, int U>
-__device__ __forceinline__ void fold(Sum &acc, uint4 (&w)[U], const uint8_t *map, int i0, int step, int n, float sL,
+__device__ __forceinline__ void fold(DiffSum &acc, uint4 (&w)[U], const uint8_t *map, int i0, int step, int n, float sL,
                                      float resc) {
     constexpr int E = Row<T>::E;
     float cm = neg_inf();
@@ -327,7 +331,7 @@ __device__ __forceinline__ void fold(Sum &acc, uint4 (&w)[U], const uint8_t *map
 
 // the head's or tail's unlisted token of this thread into the sum
 template <typename T>
-__device__ __forceinline__ void fold_edge(Sum &acc, const Part<T> &part, const uint8_t *map, float sL, float resc) {
+__device__ __forceinline__ void fold_edge(DiffSum &acc, const Part<T> &part, const uint8_t *map, float sL, float resc) {
     const int i = part.edge(threadIdx.x);
     if (i < 0) return;
     const int bit = map_bit(part, i);
@@ -362,18 +366,19 @@ __device__ __forceinline__ Row2 row_of(const DistillArgs &a, const Known &k) {
 }
 
 // the row's divergence, from its totals, in two floats
-__device__ float divergence(const DistillArgs &a, const Known &k, const Row2 &r) {
+__device__ float divergence(const DistillArgs &a, const Known &k, const Row2 &r, float y0) {
     if (r.empty) return 0.f;
     if (r.none) return INFINITY;
     const float mx = row_max(k);
     float qo;
     const float Z = row_sum(a, k, qo);
-    // lse = s m + ln Z
+    // lse - s y0 = s (m - y0) + ln Z
     const Pair lnZ = ln_pair(Z, 0.f);
-    const float sm = __fmul_rn(a.s, mx);
     float lh, ll, h, l;
+    two_sum(mx, -y0, h, l);
+    const float sm = __fmul_rn(a.s, h), sml = __fmaf_rn(a.s, h, -sm) + a.s * l;
     two_sum(sm, lnZ.h, lh, ll);
-    ll += __fmaf_rn(a.s, mx, -sm) + lnZ.l;
+    ll += sml + lnZ.l;
     if (a.tail) {   // B + P lse
         const float ph = __fmul_rn(k.Ph, lh);
         two_sum(k.Bh, ph, h, l);
@@ -397,11 +402,11 @@ __device__ float divergence(const DistillArgs &a, const Known &k, const Row2 &r)
     return h + l;
 }
 
-__device__ __forceinline__ void put_loss(const DistillArgs &a, int row, float wt, const Known &k, const Row2 &r) {
+__device__ __forceinline__ void put_loss(const DistillArgs &a, int row, float wt, const Known &k, const Row2 &r, float y0) {
     float qo;
     if (!r.empty && (!(row_max(k) > sv::kMaskFloor) || !(row_sum(a, k, qo) > 0.f) || row_max(k) == -neg_inf()))
         raise_status(a.status, SPEC_ERR_BAD_ROW);
-    a.loss[row] = wt * divergence(a, k, r);
+    a.loss[row] = wt * divergence(a, k, r, y0);
     if (a.stats_out) a.stats_out[row] = r.st;
 }
 
@@ -479,13 +484,15 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     // the part's own entries of the list, and while the row's loads arrive the
     // list's part of what this warp knows
     if (tid < SPEC_MAX_TOP) {
+        const float y = id >= 0 ? load1_rw(py + id) : neg_inf(), top = warp_max(y);
+        if (lane == 0) s_list.top[warp] = top;
         if (!(id >= part.e0 && id < part.e1)) id = -1;
         s_list.ids[tid] = id;
         if (id >= 0) {
             const int bit = map_bit(part, id);
             const uint32_t m = 1u << (bit & 31);
             if (atomicOr(reinterpret_cast<uint32_t *>(s_map) + (bit >> 5), m) & m) s_list.dup = 1;
-            s_list.yl[tid] = load1_rw(py + id);
+            s_list.yl[tid] = y;
         }
     }
     __syncthreads();
@@ -494,7 +501,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         if (lane == 0) s_warp[warp] = k;
     }
 
-    Sum acc = sum_init(a.sL, a.resc);
+    DiffSum acc = diff_init(a.resc);
     // `held` iterations before the last two go to shared memory for the second pass
     uint4 *s_held = reinterpret_cast<uint4 *>(s_map + (map_words + 3u) / 4u * 16u) + tid;
     const int held0 = max(its - 2 - held, 0);
@@ -557,7 +564,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         if (lane == 0) {
             s_row = r;
             s_total = all;
-            if (!kGrad && rank == 0) put_loss(a, row, wt, all, r);
+            if (!kGrad && rank == 0) put_loss(a, row, wt, all, r, list_top(s_list));
         }
     }
     if (!kGrad) return;
@@ -567,7 +574,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         zero_part<T, NT>(part, out);
     } else {
         const float us = wt * a.s;
-        const Factor f = factor_of(us * r2.st.w, r2.rest ? r2.st.z : 0.f, a.sL);
+        const Factor f = {us * r2.st.w, r2.rest ? r2.st.z : 0.f};
         // backwards, from the two iterations at hand; the others come again, from L2
         auto grad = [&](uint4 (&w)[U], int it) {
             const int i0 = it * U * NT + tid;
@@ -599,7 +606,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         __syncthreads();   // the listed tokens' values go over what was just written
         if (tid < a.M) put_listed(a, s_list, tid, r2, us, pg);
     }
-    if (rank == 0 && tid == NT - 1) put_loss(a, row, wt, s_total, r2);
+    if (rank == 0 && tid == NT - 1) put_loss(a, row, wt, s_total, r2, list_top(s_list));
 }
 
 // the gradient from a row's statistics: a CTA per part of a row
@@ -680,7 +687,7 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     const int ei = part.edge(tid);
     const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
     __syncthreads();   // before anything is overwritten
-    const Factor f = factor_of(us * st.w, st.z == neg_inf() ? 0.f : st.z, a.sL);
+    const Factor f = {us * st.w, st.z == neg_inf() ? 0.f : st.z};
     if (full) {
 #pragma unroll
         for (int u = 0; u < UG; ++u) grad_vec(part, out, u * NT + tid, w[u], f, a.sL);

@@ -116,15 +116,24 @@ __device__ __forceinline__ float load1_rw(const T *p) {
 // the reference moves and at the end. Chunks of a few vectors are summed
 // apart and added with a compensation, so that a term meets at most about
 // twenty roundings on its way into the sum, however long the row.
+//
+// Beyond |z sL| = 2^30 (masks of -1e9 at a low temperature, of -1e20 at any) eps
+// would overflow 2^eps. So the reference starts at -2^30 / sL: logits below add
+// nothing. They are 64 or more apart in the exponent, so that a sum against a
+// maximum out there is the number of logits equal to it, which a pass of its
+// own counts where a part's maximum turns out to lie there, or as far above 0.
 struct Sum {
     float mr, mrL, eps, mrh;
     float mx;      // largest logit seen
     float S, lo;   // the sum is S - lo
 };
 
+constexpr float kFar = 1073741824.f;
+__device__ __forceinline__ bool far_max(float m, float sL) { return m > sv::kMaskFloor && fabsf(m * sL) > kFar; }
+
 __device__ __forceinline__ Sum sum_init(float sL, float rs) {
     Sum a;
-    a.mr = sv::kMaskFloor;
+    a.mr = rs * (-kFar / (sv::kRescale * kLog2e));   // rs = kRescale / s
     a.mrL = a.mr * sL;
     a.eps = fmaf(a.mr, sL, -a.mrL);
     a.mrh = a.mr + rs;
@@ -166,7 +175,8 @@ __device__ __forceinline__ float sum_terms(const Sum &a, const float (&z)[E], fl
 }
 
 // a chunk's sum into the running one (Kahan)
-__device__ __forceinline__ void sum_put(Sum &a, float v) {
+template <typename S>
+__device__ __forceinline__ void sum_put(S &a, float v) {
     const float y = __fsub_rn(v, a.lo);
     const float t = __fadd_rn(a.S, y);
     a.lo = __fsub_rn(__fsub_rn(t, a.S), y);
@@ -181,7 +191,51 @@ __device__ __forceinline__ void sum_add1(Sum &a, float z, float sL, float rs) {
 // the sum against the maximum M
 __device__ __forceinline__ float sum_at(const Sum &a, float M, float sL) {
     const float S = a.S - a.lo;
-    return a.mx > sv::kMaskFloor || S != 0.f ? S * ex2(fmaf(a.mr - M, sL, -a.eps)) : 0.f;
+    return S != 0.f ? S * ex2(fmaf(a.mr - M, sL, -a.eps)) : 0.f;
+}
+
+// The same sum with the exponent (z - mr) sL, two operations a logit in place of
+// one: right for logits of any size without a second pass, and where memory
+// bounds the kernel no slower.
+struct DiffSum {
+    float mr, mrh, mx, S, lo;
+};
+__device__ __forceinline__ DiffSum diff_init(float rs) {
+    const float mr = sv::kMaskFloor * (1.f - 0x1p-23f);   // the least unmasked logit
+    return {mr, mr + rs, neg_inf(), 0.f, 0.f};
+}
+__device__ __forceinline__ void sum_see(DiffSum &a, float c, float sL, float rs) {
+    a.mx = fmaxf(a.mx, c);
+    if (c > a.mrh) {
+        const float al = ex2((a.mr - c) * sL);
+        a.S *= al;
+        a.lo *= al;
+        a.mr = c;
+        a.mrh = c + rs;
+    }
+}
+template <int E>
+__device__ __forceinline__ float sum_terms(const DiffSum &a, const float (&z)[E], float sL) {
+    const float2 L2 = make_float2(sL, sL), ml = make_float2(-a.mr, -a.mr), zero = make_float2(0.f, 0.f);
+    float2 e[E / 2];
+#pragma unroll
+    for (int j = 0; j < E / 2; ++j) {
+        const float2 y = sv::pfma(sv::padd(make_float2(z[2 * j], z[2 * j + 1]), ml), L2, zero);
+        e[j] = make_float2(ex2(y.x), ex2(y.y));
+    }
+#pragma unroll
+    for (int w = E / 4; w > 0; w >>= 1)
+#pragma unroll
+        for (int j = 0; j < w; ++j) e[j] = sv::padd(e[j], e[j + w]);
+    return e[0].x + e[0].y;
+}
+__device__ __forceinline__ void sum_add1(DiffSum &a, float z, float sL, float rs) {
+    sum_see(a, z, sL, rs);
+    sum_put(a, ex2((z - a.mr) * sL));
+}
+__device__ __forceinline__ float sum_at(const DiffSum &a, float M, float sL) {
+    const float S = a.S - a.lo;
+    return S != 0.f ? S * ex2((a.mr - M) * sL) : 0.f;
 }
 
 // a sum against the maximum m, moved to the larger maximum `to`
@@ -221,14 +275,14 @@ __device__ __forceinline__ void add2f(float &h, float &l, float a, float b) {
     l += b + e;
 }
 
-// e^x of x = z - M as h + l, relative error about 1e-10 (0 below e^-87): x = n ln2 + r with
+// e^x of x = z - M as h + l, relative error about 1e-10 (0 below e^-87, inf above e^87): x = n ln2 + r with
 // ln2 in three floats, then e^r by its Taylor series, whose first terms carry
 // their roundings
 __device__ __forceinline__ void exp_diff(float z, float M, float &h, float &l) {
     float xh, xl;
     two_sum(z, -M, xh, xl);
-    if (!(xh > -87.f)) {
-        h = xh == xh ? 0.f : xh;
+    if (!(fabsf(xh) < 87.f)) {
+        h = xh > 0.f ? INFINITY : xh == xh ? 0.f : xh;
         l = 0.f;
         return;
     }

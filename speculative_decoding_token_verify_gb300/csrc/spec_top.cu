@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(NT, 4) top_kernel(TopArgs a, int S) {
     int ne = s.ne;
     if (over || ne > CAPE) ne = bisect(Part<T>(z, a.V, 0, 1), a.M, max(order_key(thr), 1u), mx, s);
     ne = cut(ne, a.M, s);
+    if (far_max(mx, a.sL)) sum = count_equal(Part<T>(z, a.V, 0, 1), mx, s);
     const bool some = mx > sv::kMaskFloor, bad = !(sum >= 0.f) || mx == -neg_inf();
     const float lnS = logf(sum);
     ranked(ne, a.M, s, [&](unsigned long long c, int rk) {

@@ -239,7 +239,22 @@ __device__ __forceinline__ void stream_part(const Part<T> &p, int M, float sL, f
     if (its > 1) thr = block_bound(acc.mx, n, M, thr, s.b[2]);
 }
 
-// the part's maximum and sum, after the barrier
+// the part's logits equal to mx; NaN where some are infinite or NaN
+template <typename T>
+__device__ __forceinline__ float count_equal(const Part<T> &p, float mx, TopShared &s) {
+    int n = 0;
+    each(p, [&](float z, int) { n = z != z ? n | 1 << 24 : n + (z == mx); });
+    n = mx < INFINITY ? __reduce_add_sync(kFull, min(n, 1 << 24)) : 1 << 24;
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s.cnt[threadIdx.x >> 5] = n;
+    __syncthreads();
+    n = 0;
+    for (int i = 0; i < NW; ++i) n += min(s.cnt[i], 1 << 24);
+    return n < 1 << 24 ? (float)n : NAN;
+}
+
+// the part's maximum and sum, after the barrier; where the maximum is far out
+// count_equal is the sum
 __device__ __forceinline__ void part_sum(const TopShared &s, float sL, float &mx, float &sum) {
     mx = s.w_mx[0];
 #pragma unroll

@@ -2,9 +2,10 @@
 the tolerances their fp32 kernels are held to.
 
 Tolerances. S is a row's sum of exponentials. Its relative error is at most
-DS = 4e-6: an exponential's own error (2^-22), its argument's rounding, and
-the additions on a term's way into the sum (at most 32, each 2^-24 of the
-partial sum). An argument y = (z - M) s log2e carries two roundings, so an
+DS = 4e-6: an exponential's own error (2^-22), its argument's two roundings
+(2^-24 |y| ln 2 in all, 1e-6 at |y| = 24; smaller terms carry no mass), and the
+additions on a term's way into the sum (at most 32, each 2^-24 of the partial
+sum, 1.9e-6): 3.2e-6. An argument y = (z - M) s log2e carries two roundings, so an
 exponential of its own (a gradient's q) is off by |y| 2^-23 ln 2 besides.
 The list's sum P is formed from exponentials of relative error DP = 2e-10, and
 p_T = 1 - P is off by DP P: e^r, |r| <= 0.35, is summed as 1 + r + r^2/2 + r^3/6
@@ -17,7 +18,8 @@ import numpy as np
 DS = 4e-6
 DP = 2e-10
 U = 2.0 ** -24
-FLOOR = -1e29   # logits below count as masked
+TINY = 2.0 ** -125   # two steps (a quotient and a difference) that lose what is below fp32's normal range, 2^-126
+FLOOR = float(np.float32(-1e29))   # logits up to it count as masked
 
 
 def half(bf16):
@@ -26,13 +28,19 @@ def half(bf16):
 
 def _masked(z):
     z = np.asarray(z, np.float64)
-    return np.where(z < FLOOR, -np.inf, z)
+    return np.where(z <= FLOOR, -np.inf, z)
+
+
+def max_lnsum(z, s=1.0):
+    """m = max z and ln sum e^{s (z - m)}: apart, because s m of 1e20 has no room for the other in fp64."""
+    z = _masked(z)
+    m = z.max()
+    return (m, 0.0) if m == -np.inf else (m, np.log(np.exp(s * (z - m)).sum()))
 
 
 def lse(z, s=1.0):
-    z = _masked(z) * s
-    m = z.max()
-    return -np.inf if m == -np.inf else m + np.log(np.exp(z - m).sum())
+    m, lnS = max_lnsum(z, s)
+    return s * m + lnS
 
 
 def order(z, m):
@@ -45,15 +53,14 @@ def order(z, m):
 def top(z, M, s=1.0):
     """(logprobs [M], ids [M], lse, tolerance of logprobs, tolerance of lse)."""
     z = _masked(z)
-    L = lse(z, s)
+    m, lnS = max_lnsum(z, s)
+    L = s * m + lnS
     at = order(z, M)
     lp, ids, tol = np.full(M, -np.inf), np.full(M, -1, np.int32), np.zeros(M)
-    lp[:len(at)] = s * z[at] - L if len(at) else 0.0
+    lp[:len(at)] = s * (z[at] - m) - lnS if len(at) else 0.0
     ids[:len(at)] = at
     if not len(at):
         return lp, ids, L, tol, 0.0
-    m = z.max()
-    lnS = L - s * m
     # roundings: z - M, its product with s, ln S, the difference
     tol[:len(at)] = DS + U * (3 * np.abs(s * (z[at] - m)) + 2 * abs(lnS) + np.abs(lp[:len(at)]))
     return lp, ids, L, tol, DS + U * (2 * abs(s * m) + 2 * abs(lnS) + 2 * abs(L))
@@ -70,14 +77,13 @@ def distill(y, lp, ids, w=1.0, s=1.0, tail=True, up=1.0):
     zero = dict(loss=0.0, stats=np.zeros(4), grad=np.zeros(V), loss_tol=0.0, stats_tol=np.zeros(4), grad_tol=np.zeros(V))
     if w == 0 or not len(ids) or (not tail and P == 0):
         return zero
-    L = lse(y, s)
-    if L == -np.inf:
+    m, lnS = max_lnsum(y, s)
+    if m == -np.inf:
         return {**zero, "loss": np.inf if w > 0 else -np.inf}
-    lq = s * y - L
+    lq = s * (y - m) - lnS
     q = np.exp(lq)
     out = np.ones(V, bool)
     out[ids] = False
-    m = y.max()
     mo = y[out].max() if out.any() else -np.inf
     pT = max(0.0, 1.0 - P) if tail else 0.0
     ln, pn = (lp, p) if tail else (lp - np.log(P), p / P)
@@ -86,28 +92,29 @@ def distill(y, lp, ids, w=1.0, s=1.0, tail=True, up=1.0):
     target = np.zeros(V)
     np.add.at(target, ids, pn)
     g, gt, kl_tol = q.copy(), np.zeros(V), 0.0
-    inv = np.exp(s * m - L)
+    inv = np.exp(-lnS)
     stats, st = np.array([m, inv, -np.inf, 0.0]), np.array([0.0, inv * (DS + 2 * U), 0.0, 0.0])
 
     def arg(z, ref_):   # |argument| where an exponential is more than 0
         return np.where(np.isfinite(z), np.abs(s * (z - ref_)), 0.0)
 
     if mo > -np.inf:
-        Lo = lse(np.where(out, y, -np.inf), s)
-        qT = np.exp(Lo - L)
-        r = np.where(out, np.exp(s * y - Lo), 0.0)
+        lnSo = max_lnsum(np.where(out, y, -np.inf), s)[1]
+        lqT = s * (mo - m) + lnSo - lnS
+        qT = np.exp(lqT)
+        r = np.where(out, np.exp(s * (y - mo) - lnSo), 0.0)
         if pT > 0:
-            kl += pT * (np.log(pT) - (Lo - L))
+            kl += pT * (np.log(pT) - lqT)
         excess = qT - pT
         # q_T: two sums, and the exponential between the two maxima
         et = qT * (2 * DS + 4 * U * abs(s * (m - mo)))
         if pT > 0:   # and the list's sum
             et += DP * P
-            kl_tol += DP * P * (1 + abs(np.log(pT) - (Lo - L)))
+            kl_tol += DP * P * (1 + abs(np.log(pT) - lqT))
         g = np.where(out, excess * r, q)
         gt = r * (et + abs(excess) * (DS + 2 * U * arg(y, mo) + 2.0 ** -22 + 8 * U))
-        k = np.exp(s * mo - Lo)
-        stats[2:], st[2:] = [mo, excess * k], [0.0, k * (et + abs(excess) * (DS + 2 * U))]
+        k = np.exp(-lnSo)
+        stats[2:], st[2:] = [mo, excess * k], [0.0, k * (et + abs(excess) * (DS + 2 * U)) + TINY]
     elif tail:
         g = P * q
     g = np.where(out, g, g - target)
@@ -128,9 +135,9 @@ def beam(z, scores, N, finished=None, eos=-1):
         if finished is not None and finished[w]:
             pool.append((-float(scores[w]), w * V + eos, 0.0))
             continue
-        L = lse(z[w])
+        m, lnS = max_lnsum(z[w])
         for v in order(z[w], N):
-            sc = float(scores[w]) + (float(z[w][v]) - L)
+            sc = float(scores[w]) + ((float(z[w][v]) - m) - lnS)
             pool.append((-sc, w * V + int(v), DS))
     pool.sort()
     pool = pool[:N]

@@ -377,3 +377,37 @@ def test_beam_drafts_verified_and_distilled():
             assert abs(float(r["loss"][b, k]) - x["loss"]) <= x["loss_tol"]
             d = np.abs(r["dlogits"][b, k].cpu().numpy() - x["grad"])
             assert np.all(d <= x["grad_tol"] + ref.U * (np.abs(x["grad"]) + x["grad_tol"]))
+
+
+def test_logits_at_the_mask_floor_are_masked():
+    """fp32 -1e29 as a mask value gives what -inf gives, to the bit."""
+    sv = _sv()
+    z, scores, _ = _case(3, 4, 2003, "f32", 78)
+    mask = torch.zeros_like(z, dtype=torch.bool)
+    mask[0, 1] = True
+    mask[0, 2, 5:] = True
+    mask[1] = True
+    mask[2, :, ::3] = True
+    got = []
+    for value in (-1e29, -float("inf")):
+        status = torch.zeros(1, dtype=torch.int32, device=DEV)
+        out = sv.beam_step(z.masked_fill(mask, value), scores, 8, status=status)
+        got.append((out["scores"], out["parent"], out["token"], out["finished"], status))
+    for at, inf in zip(*got):
+        assert torch.equal(at, inf)
+
+
+@pytest.mark.parametrize("value", [-1e9, -3e9, -1e10, -7e15, -1e20, -9e28, 2e10])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_logits_far_out(dtype, value):
+    """Masks of ordinary size (-1e9, -1e20) and whole rows out there."""
+    for V in (2003, 40003):
+        z, scores, g = _case(4, 4, V, dtype, 79)
+        mask = (torch.rand(z.shape, generator=g) < 0.95).to(DEV)
+        mask[1, 1] = True
+        mask[1, 2] = True
+        mask[1, 2, 7:9] = False
+        mask[2] = True
+        z = z.masked_fill(mask, value)
+        z[3, 1] = (value * (1 + torch.rand((V,), generator=g))).to(z)
+        _check(z, scores, 8)

@@ -382,3 +382,47 @@ def test_in_place_writes_are_seen_by_autograd():
     sv.distill_step(z, lp, ids, w, out={"dlogits": z})
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         loss.backward()
+
+
+def test_logits_at_the_mask_floor_are_masked():
+    """fp32 -1e29 as a mask value gives what -inf gives, to the bit."""
+    sv = _sv()
+    y, lp, ids, w = _case(4, 3, 1501, 12, "f32", 31)
+    listed = torch.zeros_like(y).scatter_(-1, ids.long(), 1.0) > 0
+    mask = torch.zeros_like(listed)
+    mask[0] = ~listed[0]                                   # only listed tokens have mass
+    mask[1, 0] = True                                      # none has
+    mask[1, 1, ::2] = True
+    mask[2] = torch.rand(mask[2].shape, device=DEV) < 0.9
+    mask[2, :, -1] = False
+    for tail in (True, False):
+        got = []
+        for value in (-1e29, -INF):
+            z = y.masked_fill(mask, value)
+            status = torch.zeros(1, dtype=torch.int32, device=DEV)
+            a = sv.distill_loss(z, lp, ids, w, tail=tail, status=status)
+            g = sv.distill_grad(z, lp, ids, a["stats"], weight=w, tail=tail)
+            step = sv.distill_step(z, lp, ids, w, tail=tail)
+            got.append((a["loss"], a["stats"], g, step["loss"], step["dlogits"], status))
+        for at, inf in zip(*got):
+            assert torch.equal(at, inf)
+        assert int(got[0][-1]) == sv.api.SPEC_ERR_BAD_ROW
+
+
+@pytest.mark.parametrize("s", [0.05, 1.0, 20.0])
+@pytest.mark.parametrize("value", [-1e9, -3e9, -1e10, -7e15, -1e20, -9e28, 2e10])
+def test_logits_far_out(value, s):
+    """Masks of ordinary size (-1e9, -1e20) and whole rows out there."""
+    for dtype, V in (("f32", 3001), ("bf16", 40003)):
+        y, lp, ids, w = _case(3, 3, V, 12, dtype, 32, s=s)
+        listed = torch.zeros(y.shape, device=DEV).scatter_(-1, ids.long(), 1.0) > 0
+        gen = torch.Generator().manual_seed(33)
+        mask = (torch.rand(y.shape, generator=gen) < 0.9).to(DEV)
+        mask[..., -1] = False
+        mask[1] = ~listed[1]                                   # all unlisted tokens
+        mask[2] = True                                         # all tokens,
+        mask[2, 2, ids[2, 2, 0].long()] = False                # or all but a listed one
+        z = y.masked_fill(mask, value)
+        z[2, 1] = (value * (1 + torch.rand((V,), generator=gen))).to(z)   # a row spread out there
+        for tail in (True, False):
+            _check(z, lp, ids, w, s=s, tail=tail)

@@ -208,3 +208,38 @@ def test_other_stream_and_graph():
     g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(out[k], want[k].flip(0)) for k in want)
+
+
+@pytest.mark.parametrize("V", [3, 1037, 40003])
+def test_logits_at_the_mask_floor_are_masked(V):
+    """fp32 -1e29 as a mask value gives what -inf gives, to the bit."""
+    sv = _sv()
+    g = torch.Generator().manual_seed(77)
+    z = 3.0 * torch.randn((6, V), generator=g).to(DEV)
+    mask = torch.zeros_like(z, dtype=torch.bool)
+    mask[0] = True
+    mask[1, 1:] = True
+    mask[2, ::2] = True
+    mask[3, : V // 2] = True
+    a = sv.top_logprobs(z.masked_fill(mask, -1e29), 8)
+    b = sv.top_logprobs(z.masked_fill(mask, -INF), 8)
+    for key in ("logprobs", "ids", "lse"):
+        assert torch.equal(a[key], b[key]), key
+
+
+@pytest.mark.parametrize("s", [0.05, 1.0, 20.0])
+@pytest.mark.parametrize("value", [-1e9, -3e9, -1e10, -7e15, -1e20, -9e28, 2e10])
+def test_logits_far_out(value, s):
+    """Masks of ordinary size (-1e9, -1e20) and whole rows out there."""
+    for dtype, V, n in (("f32", 1037, 1), ("bf16", 40003, 1), ("bf16", 40003, 120)):
+        g = torch.Generator().manual_seed(34)
+        z = 3.0 * torch.randn((n, 5, V), generator=g)
+        mask = torch.rand(z.shape, generator=g) < 0.95
+        mask[:, 1] = True
+        mask[:, 1, 5:9] = False
+        mask[:, 2] = True
+        mask[:, 2, -1] = False
+        mask[:, 3] = True
+        z = z.masked_fill(mask, value)
+        z[:, 4] = value * (1 + torch.rand((n, V), generator=g))
+        _check(z.to(DT[dtype]).to(DEV), 16, s)
