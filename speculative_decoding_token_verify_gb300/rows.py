@@ -189,7 +189,8 @@ def distill_grad(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
     """Gradient of sum(grad_loss * loss) by the logits (spec_distill_grad),
     from distill_loss's ``stats`` and the same other arguments; ``grad_loss``
     [B,K] or None (1). ``out`` may be any tensor of the logits' shape and
-    dtype, the logits themselves too. Returns the gradient, which
+    dtype, the logits themselves too (else it must not overlap them). Returns
+    the gradient, which
     ``logits.backward(gradient)`` takes on through the draft model."""
     p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
     _tensor(stats, "stats", torch.float32, lead + (4,), dev, optional=False)
@@ -212,7 +213,7 @@ def distill_step(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
     """Loss and gradient in one call (spec_distill_step): ``loss`` [B,K]
     float32 and ``dlogits`` [B,K,V], the gradient of loss.sum(); scale it by
     ``weight`` (a mean's 1/n, a loss scale). ``out['dlogits']`` may be the
-    logits themselves."""
+    logits themselves, and must not overlap them otherwise."""
     p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
 
     def body(s):
@@ -299,7 +300,8 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
     int32, -1 leaves the row. Axis ``batch_dim`` is the sequence, the next one
     the beam. With ``lengths`` [B] int32 only the first lengths[b] entries of
     axis ``length_dim`` move. In place (``out`` None or ``state``), else into
-    ``out``, whose beam axis has N rows. Any dtype."""
+    ``out``, whose beam axis has N rows and which must not overlap the state.
+    Any dtype."""
     if not state.is_cuda:
         raise ValueError("state must be a CUDA tensor")
     dst = state if out is None else out

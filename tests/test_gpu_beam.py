@@ -411,3 +411,17 @@ def test_logits_far_out(dtype, value):
         z = z.masked_fill(mask, value)
         z[3, 1] = (value * (1 + torch.rand((V,), generator=g))).to(z)
         _check(z, scores, 8)
+
+
+@pytest.mark.parametrize("V", [9, 2003, 40003])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_spoilt_beams_far_out(V, bad):
+    sv = _sv()
+    z = torch.full((1, 2, V), -1e20, device=DEV)
+    z[0, 1, V // 2] = bad
+    scores = torch.tensor([[-1.0, 5.0]], device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = sv.beam_step(z, scores, 3, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == sv.api.SPEC_ERR_BAD_ROW
+    assert out["parent"].tolist() == [[0, 0, 0]] and out["token"].tolist() == [[0, 1, 2]]

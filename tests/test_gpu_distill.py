@@ -426,3 +426,28 @@ def test_logits_far_out(value, s):
         z[2, 1] = (value * (1 + torch.rand((V,), generator=gen))).to(z)   # a row spread out there
         for tail in (True, False):
             _check(z, lp, ids, w, s=s, tail=tail)
+
+
+@pytest.mark.parametrize("s", [1e-4, 1e4])
+@pytest.mark.parametrize("tail", [True, False])
+def test_extreme_temperatures(s, tail):
+    for dtype, V in (("f32", 3001), ("bf16", 40003)):
+        y, lp, ids, w = _case(2, 3, V, 12, dtype, 35, s=s)
+        _check(y, lp, ids, w, s=s, tail=tail)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_spoilt_rows_far_out(bad):
+    sv = _sv()
+    y, lp, ids, w = _case(1, 3, 2001, 10, "f32", 37)
+    y[:] = -1e20
+    clean = sv.distill_step(y, lp, ids, w)
+    unlisted = next(v for v in range(2001) if v not in ids[0, 1].tolist())
+    y[0, 1, unlisted] = bad
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    got = sv.distill_step(y, lp, ids, w, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == sv.api.SPEC_ERR_BAD_ROW and not torch.isfinite(got["loss"][0, 1])
+    for k in (0, 2):
+        assert torch.equal(got["loss"][0, k], clean["loss"][0, k])
+        assert torch.equal(got["dlogits"][0, k], clean["dlogits"][0, k])

@@ -243,3 +243,26 @@ def test_logits_far_out(value, s):
         z = z.masked_fill(mask, value)
         z[:, 4] = value * (1 + torch.rand((n, V), generator=g))
         _check(z.to(DT[dtype]).to(DEV), 16, s)
+
+
+@pytest.mark.parametrize("s", [1e-4, 1e4])
+def test_extreme_temperatures(s):
+    for dtype, V, n in (("f32", 1037, 2), ("bf16", 40003, 2), ("f32", 40003, 130)):
+        z = 3.0 * torch.randn((n, 5, V), generator=torch.Generator().manual_seed(36))
+        _check(z.to(DT[dtype]).to(DEV), 16, s)
+
+
+@pytest.mark.parametrize("V", [9, 1037, 40003])
+@pytest.mark.parametrize("bad", [float("nan"), INF])
+def test_spoilt_rows_far_out(V, bad):
+    sv = _sv()
+    z = torch.full((3, V), -1e20, device=DEV)
+    z[1, V // 2] = bad
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    out = sv.top_logprobs(z, 4, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == sv.api.SPEC_ERR_BAD_ROW and not torch.isfinite(out["lse"][1])
+    for r in (0, 2):
+        assert out["ids"][r].tolist() == [0, 1, 2, 3]
+        assert torch.equal(out["logprobs"][r], out["logprobs"][r, :1].expand(4))
+        assert abs(float(out["logprobs"][r, 0]) + np.log(V)) <= ref.DS + 4 * ref.U * np.log(V)
