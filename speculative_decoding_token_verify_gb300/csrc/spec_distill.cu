@@ -370,10 +370,11 @@ __device__ float divergence(const DistillArgs &a, const Known &k, const Row2 &r,
     if (r.empty) return 0.f;
     if (r.none) return INFINITY;
     const float mx = row_max(k);
-    float qo;
-    const float Z = row_sum(a, k, qo);
+    const float qo = moved(k.So, k.mo, mx, a.sL);
+    float Z, Zl;   // with its rounding: the tail's term takes qo / Z again
+    two_sum(qo, moved(k.Sl, k.ml, mx, a.sL), Z, Zl);
     // lse - s y0 = s (m - y0) + ln Z
-    const Pair lnZ = ln_pair(Z, 0.f);
+    const Pair lnZ = ln_pair(Z, Zl);
     float lh, ll, h, l;
     two_sum(mx, -y0, h, l);
     const float sm = __fmul_rn(a.s, h), sml = __fmaf_rn(a.s, h, -sm) + a.s * l;
@@ -393,11 +394,26 @@ __device__ float divergence(const DistillArgs &a, const Known &k, const Row2 &r,
         l += e + rem / k.Ph + ll - lnP.l;
     }
     if (!(fabsf(h) < INFINITY)) return h;
-    // p_T ln(p_T / q_T), by parts where q_T is below fp32's range
+    // p_T ln(p_T / q_T): in two floats, or where the list holds little mass and
+    // the divergence is small it would be off by 2^-23; by parts where q_T is below
+    // fp32's range
     const float pT = tail_mass(a, k);
     if (r.rest && pT > 0.f) {
-        if (qo > 1e-30f) l += pT * logf(pT * (Z / qo));
-        else l += pT * (logf(pT * Z / k.So) + a.s * (mx - k.mo));
+        if (qo > 1e-30f) {
+            float th, tl, e;
+            two_sum(1.f, -k.Ph, th, tl);
+            tl -= k.Pl;
+            two_sum(th, tl, th, tl);
+            const float nh = __fmul_rn(th, Z), nl = __fmaf_rn(th, Z, -nh) + (th * Zl + tl * Z);
+            const float qh = nh / qo;
+            const Pair ln = ln_pair(qh, (__fmaf_rn(-qh, qo, nh) + nl) / qo);
+            const float t = __fmul_rn(th, ln.h);
+            l += __fmaf_rn(th, ln.h, -t) + (th * ln.l + tl * ln.h);
+            two_sum(h, t, h, e);
+            l += e;
+        } else {
+            l += pT * (logf(pT * Z / k.So) + a.s * (mx - k.mo));
+        }
     }
     return h + l;
 }

@@ -451,3 +451,26 @@ def test_spoilt_rows_far_out(bad):
     for k in (0, 2):
         assert torch.equal(got["loss"][0, k], clean["loss"][0, k])
         assert torch.equal(got["dlogits"][0, k], clean["dlogits"][0, k])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,M,noise", [(2003, 1, 0.1), (2003, 5, 0.02), (40003, 1, 0.3), (40003, 30, 0.01), (300, 150, 0.01)])
+def test_small_divergences(V, M, noise, dtype):
+    """Lists of little mass. With Z = So + Sl the sums' relative errors enter the
+    divergence as P dZ + p_T (dZ - dSo) = (q_T - p_T) dSo + (1 - q_T) dSl, each at
+    most DS; beside them stand the list's sum, two roundings of the result and 1e-9
+    for the terms in two floats."""
+    sv = _sv()
+    y, lp, ids, _ = _case(2, 4, V, min(M, 128), dtype, 38, noise=noise, sigma=1.0)
+    got = sv.distill_loss(y, lp, ids)["loss"].cpu().numpy().astype(np.float64)
+    step = sv.distill_step(y, lp, ids)["loss"].cpu().numpy().astype(np.float64)
+    yn, lpn, idn = y.float().cpu().numpy().astype(np.float64), lp.cpu().numpy().astype(np.float64), ids.cpu().numpy()
+    for b in range(2):
+        for k in range(4):
+            want = ref.distill(yn[b, k], lpn[b, k], idn[b, k])["loss"]
+            q = np.exp(yn[b, k] - ref.lse(yn[b, k]))
+            listed = q[idn[b, k]].sum()
+            P = np.exp(lpn[b, k]).sum()
+            tol = (abs(P - listed) + listed) * ref.DS + 2 * ref.U * abs(want) + 1e-9
+            tol += ref.DP * P * (1 + abs(np.log((1 - P) / (1 - listed))))
+            assert abs(got[b, k] - want) <= tol and abs(step[b, k] - want) <= tol, (got[b, k], step[b, k], want, tol)
