@@ -462,9 +462,11 @@ int spec_top_logprobs(const spec_rows_params *params, const void *logits, float 
  *   tail = 0: the list renormalised, p_m / P and l_m - ln P for p_m and l_m,
  *     without the last term.
  * loss = weight * KL, and the gradient of grad_loss * loss by y_v is
- *   grad_loss * weight * s * (q_v - sum_m p_m [id_m = v])     at listed v,
- *   grad_loss * weight * s * (q_T - p_T) q_v / q_T            at unlisted v
- * (with tail = 0 p_T = 0; with tail = 1 and no unlisted token P q_v for q_v).
+ *   grad_loss * weight * s * (c q_v - sum_m p_m [id_m = v])   at listed v,
+ *   grad_loss * weight * s * (c q_T - p_T) q_v / q_T          at unlisted v
+ * with c = P + p_T: 1, or P where the list's probabilities sum to more than 1 (P
+ * up to 1 + 2^-15, the rounding of fp32 log-probabilities, counts as 1 here).
+ * With tail = 0 c = 1 and p_T = 0; with tail = 1 and no unlisted token c = P.
  * A token listed twice carries both probabilities and counts once in q_T.
  * A row of weight 0 or with an empty list (no id, or with tail = 0 no
  * probability above 0) has loss 0 and gradient 0 whatever its logits. A listed

@@ -4,10 +4,10 @@
 // With q = softmax(s y), the list's probabilities p_m, the unlisted tokens'
 // teacher mass p_T = 1 - P and student mass q_T:
 //   KL = sum_m p_m (l_m - ln q(id_m)) + p_T (ln p_T - ln q_T)
-//   dKL / dy_v = s (q_v - sum_m p_m [id_m = v])   at listed v
-//              = s (q_T - p_T) r_v                at unlisted v,
+//   dKL / dy_v = s (c q_v - sum_m p_m [id_m = v])   at listed v
+//              = s (c q_T - p_T) r_v                at unlisted v,
 // r = the softmax over the unlisted tokens alone: their part of q rescaled to
-// the teacher's mass.
+// the teacher's mass; c = P + p_T is the teacher's mass, 1 unless P is more.
 //
 // The unlisted tokens have a maximum and a sum of their own, so neither q_T =
 // 1 - Q (which cancels when the list holds nearly all of the mass) nor q_T /
@@ -217,10 +217,20 @@ __device__ __forceinline__ void known_total(Known &k, float sL) {
 }
 __device__ __forceinline__ Known known_nothing() { return {neg_inf(), 0.f, neg_inf(), 0.f, 0.f, 0.f, 0.f, 0.f}; }
 
+// The factor c of q in the gradient: the teacher's mass, P + p_T, and P alone where
+// nothing is unlisted. Where P passes 1, p_T is 0, so that c multiplies the unlisted
+// tokens' statistic too. P up to 1 + 2^-15 counts as 1: log-probabilities
+// s z - lse of two terms up to 256, each rounded to fp32 by at most 2^-17, are off
+// by 2^-16, so a list of the whole mass may come with as much more.
+constexpr float kMassOne = 1.f + 0x1p-15f;
+__device__ __forceinline__ float mass_factor(int tail, bool rest, float P) {
+    return tail && (!rest || P > kMassOne) ? P : 1.f;
+}
+
 // what the gradient takes from the row's total
 struct Row2 {
     float4 st;        // the statistics
-    float qscale;     // factor of a listed token's q (P where nothing is unlisted)
+    float qscale;     // the factor of q
     float norm;       // factor of p (1 / P with a renormalised list)
     int rest, none;   // unlisted tokens with mass; no unmasked token at all
     int empty;        // nothing to renormalise
@@ -360,7 +370,7 @@ __device__ __forceinline__ Row2 row_of(const DistillArgs &a, const Known &k) {
     if (r.rest) r.st.w = (qo / Z - tail_mass(a, k)) / k.So;
     else r.st.z = neg_inf();
     if (r.none || r.empty) r.st = make_float4(0.f, 0.f, 0.f, 0.f);
-    r.qscale = a.tail && !r.rest ? k.Ph : 1.f;
+    r.qscale = mass_factor(a.tail, r.rest, k.Ph);
     r.norm = a.tail ? 1.f : 1.f / k.Ph;
     return r;
 }
@@ -590,7 +600,7 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
         zero_part<T, NT>(part, out);
     } else {
         const float us = wt * a.s;
-        const Factor f = {us * r2.st.w, r2.rest ? r2.st.z : 0.f};
+        const Factor f = {us * r2.st.w * r2.qscale, r2.rest ? r2.st.z : 0.f};
         // backwards, from the two iterations at hand; the others come again, from L2
         auto grad = [&](uint4 (&w)[U], int it) {
             const int i0 = it * U * NT + tid;
@@ -631,6 +641,7 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     __shared__ int s_ids[SPEC_MAX_TOP];
     __shared__ float s_p[SPEC_MAX_TOP];
     __shared__ double s_d[SPEC_MAX_TOP / 32];
+    __shared__ float s_f[SPEC_MAX_TOP / 32];
     __shared__ uint32_t s_seen[32];   // a hash of the part's tokens: bits met twice may be a token listed twice
     __shared__ int s_dup;
     const int tid = threadIdx.x;
@@ -671,8 +682,10 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
         }
     }
     const bool own = id >= part.e0 && id < part.e1;
-    // the list's sum, where a factor needs it: every part sums the whole list
-    const bool need = !a.tail || st.z == neg_inf();
+    // the list's sum: every part sums the whole list, in more bits where P scales
+    // every row, in fp32 (relative error 2^-22 and eight roundings, like q's own)
+    // where only a mass above 1 does (0.2 us a call; by exp_diff 0.35)
+    const bool rest = st.z != neg_inf(), need = !a.tail || !rest;
     double P = 1.0;
     float p = 0.f;
     if (need) {
@@ -702,8 +715,15 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     }
     const int ei = part.edge(tid);
     const float ey = ei >= 0 ? load1_rw(py + ei) : neg_inf();
+    if (!need && tid < SPEC_MAX_TOP) {   // (under the loads)
+        const float x = warp_sum(id >= 0 ? ex2(lp * kLog2e) : 0.f);
+        if ((tid & 31) == 0) s_f[tid >> 5] = x;
+    }
     __syncthreads();   // before anything is overwritten
-    const Factor f = {us * st.w, st.z == neg_inf() ? 0.f : st.z};
+    const float Pf = need ? (float)P : (s_f[0] + s_f[1]) + (s_f[2] + s_f[3]);
+    static_assert(SPEC_MAX_TOP == 128, "four warps hold a list");
+    const float c = mass_factor(a.tail, rest, Pf);
+    const Factor f = {us * st.w * c, rest ? st.z : 0.f};
     if (full) {
 #pragma unroll
         for (int u = 0; u < UG; ++u) grad_vec(part, out, u * NT + tid, w[u], f, a.sL);
@@ -726,7 +746,7 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
                 }
         }
         if (once) {
-            const float kl = us * st.y * (a.tail && need ? (float)P : 1.f);
+            const float kl = us * st.y * c;
             const float q = yl > sv::kMaskFloor || yl != yl ? ex2((yl - st.x) * a.sL) : 0.f;
             pg[id] = to_elem<T>(fmaf(kl, q, -us * (a.tail ? sum : sum * (float)(1.0 / P))));
         }
