@@ -101,11 +101,11 @@ def _status(status, device):
         raise ValueError("status must be an int32 tensor of one element on the logits' device")
 
 
-def _written(t):
-    """Tell autograd that the library writes into ``t``."""
-    if t.requires_grad:
-        torch.autograd.graph.increment_version(t)
-    return t
+# Tells autograd that a call has written into tensors of the caller's. All of them
+# count: a detached alias shares its counter with a tensor that a backward pass may
+# need, and so does a tensor without a gradient that another's backward pass keeps.
+# Called after the write, so that a refused call leaves the counters alone.
+_written = torch.autograd.graph.increment_version
 
 
 def _out(out, name, dtype, shape, device):
@@ -113,7 +113,7 @@ def _out(out, name, dtype, shape, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _tensor(t, f"out['{name}']", dtype, torch.Size(shape), device)
-    return _written(t)
+    return t
 
 
 def top_logprobs(logits: torch.Tensor, M: int, inv_temperature: float = 1.0, out: Optional[dict] = None,
@@ -136,6 +136,8 @@ def top_logprobs(logits: torch.Tensor, M: int, inv_temperature: float = 1.0, out
         lse = _out(out, "lse", _F32, lead, dev)
         _check(_native.lib().spec_top_logprobs(ctypes.byref(p), logits.data_ptr(), lp.data_ptr(), ids.data_ptr(),
                                                lse.data_ptr(), _addr(status), s))
+        if out is not None:
+            _written((lp, ids, lse))
         return {"logprobs": lp, "ids": ids, "lse": lse}
 
     return _run(logits, stream, body)
@@ -167,6 +169,8 @@ def distill_loss(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
         stats = _out(out, "stats", _F32, lead + (4,), dev)
         _check(_native.lib().spec_distill_loss(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
                                                _addr(weight), loss.data_ptr(), stats.data_ptr(), _addr(status), s))
+        if out is not None:
+            _written((loss, stats))
         return {"loss": loss, "stats": stats}
 
     return _run(logits, stream, body)
@@ -179,7 +183,7 @@ def _dlogits(out, logits):
     elif out.dtype != logits.dtype or out.shape != logits.shape or out.device != logits.device:
         raise ValueError("dlogits must have the logits' dtype, shape and device")
     _, _, _, _, bs, rs = _logits(out, "dlogits")
-    return _written(out), bs, rs
+    return out, bs, rs
 
 
 def distill_grad(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor, stats: torch.Tensor,
@@ -201,6 +205,8 @@ def distill_grad(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
         _check(_native.lib().spec_distill_grad(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
                                                _addr(weight), stats.data_ptr(), _addr(grad_loss), g.data_ptr(), bs, rs,
                                                _addr(status), s))
+        if out is not None:
+            _written(g)
         return g
 
     return _run(logits, stream, body)
@@ -221,6 +227,8 @@ def distill_step(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
         g, bs, rs = _dlogits(None if out is None else out.get("dlogits"), logits)
         _check(_native.lib().spec_distill_step(ctypes.byref(p), logits.data_ptr(), logprobs.data_ptr(), ids.data_ptr(),
                                                _addr(weight), loss.data_ptr(), g.data_ptr(), bs, rs, _addr(status), s))
+        if out is not None:
+            _written((loss, g))
         return {"loss": loss, "dlogits": g}
 
     return _run(logits, stream, body)
@@ -255,6 +263,8 @@ def beam_step(logits: torch.Tensor, scores: torch.Tensor, N: int, finished: Opti
         _check(_native.lib().spec_beam_step(ctypes.byref(p), logits.data_ptr(), scores.data_ptr(), _addr(finished),
                                             eos, sc.data_ptr(), par.data_ptr(), tok.data_ptr(), fin.data_ptr(),
                                             _addr(status), s))
+        if out is not None:
+            _written((sc, par, tok, fin))
         return {"scores": sc, "parent": par, "token": tok, "finished": fin}
 
     return _run(logits, stream, body)
@@ -341,7 +351,6 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
         return dst
     if O > 65535 or H > 65535 or B > MAX_B or T >= 1 << 31 or unit > 1 << 30:   # before 32-bit fields
         raise SpecError(SPEC_ERR_UNSUPPORTED, "beam_reorder: the state's axes are outside the supported range")
-    _written(dst)
     p = _native.ReorderParams(O, B, W, N, H, T, unit)
     p.src_stride[:] = ss
     p.dst_stride[:] = ds
@@ -349,6 +358,7 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
     def body(s):
         _check(_native.lib().spec_beam_reorder(ctypes.byref(p), state.data_ptr(), dst.data_ptr(), parent.data_ptr(),
                                                _addr(lengths), _addr(status), s))
+        _written(dst)
         return dst
 
     return _run(state, stream, body)
