@@ -309,7 +309,8 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
     (..., b, n, ...) becomes row (..., b, parent[b, n], ...), ``parent`` [B,N]
     int32, -1 leaves the row. Axis ``batch_dim`` is the sequence, the next one
     the beam. With ``lengths`` [B] int32 only the first lengths[b] entries of
-    axis ``length_dim`` move. In place (``out`` None or ``state``), else into
+    axis ``length_dim`` move; without, whole rows do, of a state cut out of a
+    larger buffer along any one axis too. In place (``out`` None or ``state``), else into
     ``out``, whose beam axis has N rows and which must not overlap the state.
     Any dtype."""
     if not state.is_cuda:
@@ -327,8 +328,10 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
             state_v, dst_v = state.unsqueeze(-1), dst.unsqueeze(-1)
         else:
             state_v, dst_v = state, dst
-        if _try_layout(state_v, bd, ld) is None or (dst is not state and _try_layout(dst_v, bd, ld) is None):
-            ld = state_v.dim() - 1   # rows of evenly spaced segments
+        # whole rows: any axis may divide them, the first that fits gives the longest segments
+        while ld < state_v.dim() - 1 and (_try_layout(state_v, bd, ld) is None or
+                                          (dst is not state and _try_layout(dst_v, bd, ld) is None)):
+            ld += 1
     else:
         ld = length_dim + nd if length_dim < 0 else length_dim
         if not bd + 2 <= ld < nd:
