@@ -317,8 +317,11 @@ def beam_reorder(state: torch.Tensor, parent: torch.Tensor, lengths: Optional[to
         raise ValueError("state must be a CUDA tensor")
     dst = state if out is None else out
     nd, dev = state.dim(), state.device
-    if dst.dim() != nd or dst.dtype != state.dtype or dst.device != dev:
-        raise ValueError("out must have the state's dtype, device and number of axes")
+    if dst is not state:
+        if dst.dim() != nd or dst.dtype != state.dtype or dst.device != dev:
+            raise ValueError("out must have the state's dtype, device and number of axes")
+        if dst.is_conj() != state.is_conj() or dst.is_neg() != state.is_neg():   # bytes are moved, not values
+            raise ValueError("out and state must both be conjugated or negated views, or neither")
     bd = batch_dim + nd if batch_dim < 0 else batch_dim
     if not 0 <= bd < nd - 1:
         raise ValueError("state must have a batch and a beam axis")

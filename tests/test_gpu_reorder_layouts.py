@@ -81,3 +81,17 @@ def test_states_that_no_axis_splits_are_refused():
             sv.beam_reorder(bad, parent)
     with pytest.raises(ValueError):
         sv.beam_reorder(torch.zeros((2, 2, 4, 6, 8, 10), device=DEV), parent, out=t.transpose(3, 5).expand(2, 2, 4, 10, 8, 6))
+
+
+def test_views_that_stand_for_other_values_are_refused():
+    """A conjugated or negated view's memory is not its values."""
+    sv = _sv()
+    parent = torch.tensor([[1, 0]], dtype=torch.int32, device=DEV)
+    z = torch.randn((1, 2, 5), dtype=torch.complex64, device=DEV)
+    with pytest.raises(ValueError):
+        sv.beam_reorder(z.conj(), parent, out=torch.empty_like(z))
+    with pytest.raises(ValueError):
+        sv.beam_reorder(torch._neg_view(z.real.contiguous()), parent, out=torch.empty((1, 2, 5), device=DEV))
+    want = z.flip(1)
+    w = z.conj()
+    assert torch.equal(sv.beam_reorder(w, parent), want.conj()) and torch.equal(z, want)   # both alike: in place
