@@ -506,7 +506,8 @@ int spec_distill_step(const spec_rows_params *params, const void *logits, const 
  * finished beam (finished[b][w] != 0; finished may be NULL) has one
  * continuation, the token eos at its own score; its logits are not read. A
  * beam of score -inf has none; a score of NaN or +inf counts as -inf and
- * raises SPEC_ERR_BAD_ROW.
+ * raises SPEC_ERR_BAD_ROW. A continuation whose score lies below fp32's range
+ * is none either.
  * The N best of a sequence, best first, equal scores by w * V + v:
  * out_scores, out_parent (w), out_token (v), out_finished (1 if the token is
  * eos), each [B][N]; where there are fewer: -inf, -1, -1, 0. out_scores

@@ -66,7 +66,7 @@ __device__ double precise_sum(const Part<T> &p, float M, double *buf) {
 
 // Pairs are kept in two floats: GB300's fp64 rate makes the same sums in fp64
 // many times slower.
-// cum + (z - M) - lnS
+// cum + (z - M) - lnS; below fp32's range -inf (the error terms are NaN there)
 __device__ __forceinline__ Pair score_sum(float cum, float z, float M, Pair lnS) {
     float h, l, e;
     two_sum(z, -M, h, l);
@@ -75,6 +75,7 @@ __device__ __forceinline__ Pair score_sum(float cum, float z, float M, Pair lnS)
     two_sum(h, cum, h, e);
     l += e;
     two_sum(h, l, h, l);
+    if (!(fabsf(h) < INFINITY)) return {neg_inf(), 0.f};
     return {h, l};
 }
 // as an integer of the same order
@@ -149,9 +150,12 @@ __device__ __forceinline__ void rank_candidates(const BeamArgs &a, BeamShared &s
         }
         for (int o = G / 2; o > 0; o >>= 1) rk += __shfl_xor_sync(kFull, rk, o);
         if (g == 0 && i < n && rk <= N) {
-            s.sel[rk] = score_of(cands[i]);
-            s.selw[rk] = (int)place / a.V;
-            s.selp[rk] = (int)place;
+            const Pair sc = score_of(cands[i]);
+            if (sc.h > neg_inf()) {
+                s.sel[rk] = sc;
+                s.selw[rk] = (int)place / a.V;
+                s.selp[rk] = (int)place;
+            }
         }
     }
     if (!check) return;
