@@ -99,7 +99,8 @@ static cudaError_t launch_vec(ReorderArgs &a, int O, cudaStream_t stream) {
     if (a.N <= 4) reorder_kernel<Vec, 4, 4><<<grid, NTR, 0, stream>>>(a);
     else if (a.N <= 8) reorder_kernel<Vec, 8, 2><<<grid, NTR, 0, stream>>>(a);
     else if (a.N <= 16) reorder_kernel<Vec, 16, 1><<<grid, NTR, 0, stream>>>(a);
-    else reorder_kernel<Vec, 32, 1><<<grid, NTR, 0, stream>>>(a);
+    else if constexpr (sizeof(Vec) < 16) reorder_kernel<Vec, 32, 1><<<grid, NTR, 0, stream>>>(a);
+    else return cudaErrorInvalidValue;   // (more than 16 beams take narrower vectors)
     return cudaGetLastError();
 }
 
