@@ -443,7 +443,10 @@ typedef struct {
  * logits in ascending token order), as logprobs[m] = s z - lse and its token
  * ids[m]. Masked tokens are never listed: with fewer than M unmasked tokens
  * the remaining entries are -inf and -1. A row without unmasked tokens has
- * lse = -inf and an empty list (no error: rows past a sequence's end).
+ * lse = -inf and an empty list (no error: rows past a sequence's end). Rows where
+ * thousands of logits tie with the M-th largest (a fill value such as -1e9, which is
+ * a logit like any other, around fewer than M tokens) are many times slower than
+ * rows masked by -inf: the list is then found by bisection, in up to 34 passes.
  * logprobs [B][K][M] f32 and ids [B][K][M] int32 out; lse [B][K] f32 out or
  * NULL. One read of the logits.
  */
@@ -513,8 +516,11 @@ int spec_distill_step(const spec_rows_params *params, const void *logits, const 
  * eos), each [B][N]; where there are fewer: -inf, -1, -1, 0. out_scores
  * may be scores and out_finished finished (N = W).
  * The order is that of exact arithmetic on the logits and scores, down to
- * differences of 1e-9: where fp32 sums leave the order of two selected
- * scores open, the kernel sums the beams' rows again in more bits.
+ * differences of 1e-9 or, where that is more, 2^-44 of the size of the scores and
+ * logits: where fp32 sums leave the order of two selected scores open, the
+ * kernel sums the beams' rows again in more bits. The scores themselves are
+ * those of fp32 sums otherwise (absolute error at most 4e-6, and their rounding).
+ * Rows of ties are slow here as in spec_top_logprobs.
  * eos in [0, V) or -1 (none; finished must then be NULL).
  */
 int spec_beam_step(const spec_rows_params *params, const void *logits, const float *scores, const int32_t *finished,

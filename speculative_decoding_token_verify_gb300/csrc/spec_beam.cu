@@ -17,7 +17,8 @@
 //
 // Measured: 64 sequences of 8 beams, V = 128256 bf16, N = 16: 40 us, 2.9 TB/s of
 // the live rows; the stream takes 29 us of it (512 rows in one wave, whose CTAs
-// start and end together), the exchange, candidates and ranking the rest. With
+// start and end together), the exchange, candidates and ranking the rest; f32 59 us,
+// a first step (one live beam each) 35 us. With
 // scores compared in fp64 the call took 76 to 119 us, with the top lists as a
 // launch of their own 53 us.
 #include <mutex>
@@ -444,7 +445,11 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
 
 // CTAs per sequence and parts per row. Clusters as large as fill the SMs' 608
 // slots; parts so that the W P units share out evenly, while a part keeps a
-// vector per thread and the candidates of all parts fit (4096).
+// vector per thread and the candidates of all parts fit (4096). V = 128256 bf16, N =
+// 2 W: 64 sequences of 8 beams 47 us, of 5, 7 and 11 beams (several parts a CTA,
+// one after another) 76, 100 and 170 us; one sequence of 4, 8 and 16 beams 15, 19
+// and 35 us. With several parts a CTA and N near 64 more vectors reach a part's
+// bound than are kept of it, and bisection takes over: 32 beams, N = 64, 1286 us.
 static void beam_plan(const spec_rows_params *p, int es, int &C, int &P) {
     const long long nvec = (long long)p->V * es / 16;
     C = kMaxCluster;

@@ -9,7 +9,9 @@
 // TB/s of moved bytes (parents that go on twice are read from L2 the second
 // time), the rate of a plain copy; with one column per thread 308 us. 16 beams
 // run at 84% of that, 3 beams at 65%: loads of beams that stay leave their
-// registers idle. Listing the beams that move first, so that few leave room for
+// registers idle. Random permutations of whole rows, moved bytes against a copy's rate: 2
+// beams (half of the rows stay) 63%, 3 beams 91%, 4 and 8 beams all of it, 16 beams
+// 92%, 24 beams 91%, 32 beams 80%. Listing the beams that move first, so that few leave room for
 // more columns, spilled and was slower throughout (317 us).
 #include "spec_rows.cuh"
 

@@ -11,7 +11,8 @@
 //
 // Measured: 2048 rows of 128256 bf16, M = 64: 102 us, 5.2 TB/s, 77% of the
 // measured copy rate. The stream with its sums alone takes 86 us; the bounds,
-// looking at what passed and ranking it the rest (issue slots 66% busy). A CTA
+// looking at what passed and ranking it the rest (issue slots 66% busy); f32 175 us,
+// 6.0 TB/s, 90%. A CTA
 // that goes on to further rows with the next one's first loads in flight took
 // 110 us, whole iterations without bounds 105 to 110 us.
 #include "spec_top.cuh"

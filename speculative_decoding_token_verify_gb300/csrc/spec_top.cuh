@@ -14,7 +14,10 @@
 //
 // Where more vectors pass than the list holds (runs of equal logits, all large
 // logits in one place) a bisection finishes: the M-th largest key by counting
-// passes, tokens above it in any order, tokens at it in ascending order.
+// passes, tokens above it in any order, tokens at it in ascending order. One CTA
+// does that for its whole row: 8 rows of 128256 bf16 with ten tokens at large and
+// the others at -1e9 take 570 us in place of 11 (M = 64), 256 rows 690 us in place
+// of 21. Masked logits never get there (8 us for the same rows masked by -inf).
 #pragma once
 
 #include "spec_rows.cuh"

@@ -161,7 +161,9 @@ def distill_loss(logits: torch.Tensor, logprobs: torch.Tensor, ids: torch.Tensor
     """Distillation loss of the student's ``logits`` [B,K,V] from a teacher's
     top list (spec_distill_loss): ``logprobs`` and ``ids`` [B,K,M] as
     top_logprobs returns them, ``weight`` [B,K] or None (1). Returns ``loss``
-    [B,K] float32 and ``stats`` [B,K,4] float32, which distill_grad takes."""
+    [B,K] float32 and ``stats`` [B,K,4] float32, which distill_grad takes. The
+    loss is no part of an autograd graph, whether or not the logits are: its
+    gradient comes from distill_grad or distill_step."""
     p, dev, lead = _distill_args(logits, logprobs, ids, weight, inv_temperature, tail, status)
 
     def body(s):
