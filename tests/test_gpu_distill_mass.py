@@ -139,3 +139,31 @@ def test_reference_holds_up_to_mass_one():
             loss, g = gradient(y[k].double(), lp[k].double(), ids[k], 1.0, tail)
             r = ref.distill(y[k].numpy(), lp[k].numpy(), ids[k].numpy(), tail=tail)
             assert abs(r["loss"] - loss) < 1e-9 and np.abs(r["grad"] - g.numpy()).max() < 1e-9
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_little_teacher_mass_left(dtype):
+    """M equal probabilities that leave the unlisted tokens 1e-7 or so of the
+    teacher's mass, and a student that leaves them none: the gradient there is
+    -p_T r, as good as the list's sum (DP of P)."""
+    import speculative_decoding_token_verify_gb300 as sv
+    sv.build()
+    V, lists = 300, [2, 3, 5, 7, 11, 23, 45, 64, 90, 91, 128]
+    for M in lists:
+        l = np.float32(-np.log(M))
+        while M * np.exp(float(l)) >= 1.0:
+            l = np.nextafter(l, np.float32(-100))
+        lp = torch.full((1, 1, M), float(l))
+        ids = torch.arange(M, dtype=torch.int32)[None, None] * 2
+        y = torch.full((1, 1, V), -60.0)
+        y[..., ids[0, 0].long()] = 1.0
+        y = y.to(DT[dtype])
+        a = sv.distill_loss(y.to(DEV), lp.to(DEV), ids.to(DEV))
+        g = sv.distill_grad(y.to(DEV), lp.to(DEV), ids.to(DEV), a["stats"])
+        step = sv.distill_step(y.to(DEV), lp.to(DEV), ids.to(DEV))["dlogits"]
+        r = ref.distill(y[0, 0].float().numpy(), lp[0, 0].numpy(), ids[0, 0].numpy())
+        tol = r["grad_tol"] + ref.half(dtype == "bf16") * (np.abs(r["grad"]) + r["grad_tol"])
+        for got in (g, step):
+            off = np.abs(got[0, 0].float().cpu().double().numpy() - r["grad"])
+            assert np.all(off <= tol), (M, float((off / tol).max()))
