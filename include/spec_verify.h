@@ -463,7 +463,7 @@ int spec_top_logprobs(const spec_rows_params *params, const void *logits, float 
  *       KL = sum_m p_m (l_m - ln q(id_m)) + p_T (ln p_T - ln q_T).
  *     The last term is left out where p_T = 0 or no unlisted token is unmasked.
  *   tail = 0: the list renormalised, p_m / P and l_m - ln P for p_m and l_m,
- *     without the last term.
+ *     without the last term. Only differences of the l_m count (logits will do).
  * loss = weight * KL, and the gradient of grad_loss * loss by y_v is
  *   grad_loss * weight * s * (c q_v - sum_m p_m [id_m = v])   at listed v,
  *   grad_loss * weight * s * (c q_T - p_T) q_v / q_T          at unlisted v
@@ -471,8 +471,8 @@ int spec_top_logprobs(const spec_rows_params *params, const void *logits, float 
  * up to 1 + 2^-15, the rounding of fp32 log-probabilities, counts as 1 here).
  * With tail = 0 c = 1 and p_T = 0; with tail = 1 and no unlisted token c = P.
  * A token listed twice carries both probabilities and counts once in q_T.
- * A row of weight 0 or with an empty list (no id, or with tail = 0 no
- * probability above 0) has loss 0 and gradient 0 whatever its logits. A listed
+ * A row of weight 0 or with an empty list (no id, or with tail = 0 only
+ * l_m = -inf) has loss 0 and gradient 0 whatever its logits. A listed
  * token that the student masks makes the loss +inf, the gradient stays finite.
  * A student row without unmasked tokens: loss +inf, gradient 0,
  * SPEC_ERR_BAD_ROW. An id outside [-1, V) is taken as absent and raises

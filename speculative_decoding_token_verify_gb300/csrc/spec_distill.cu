@@ -187,8 +187,8 @@ __device__ __forceinline__ uint4 ld_rw(const uint4 *p) {
 struct __align__(16) Known {
     float mo, So;    // unlisted tokens: maximum, sum of 2^{(y - mo) sL}
     float ml, Sl;    // listed tokens: the same, each once
-    float Ph, Pl;    // sum of p, in two floats
-    float Bh, Bl;    // sum of p (l - s (y - y0)), in two floats
+    float Ph, Pl;    // sum of p = e^(l - l0), in two floats
+    float Bh, Bl;    // sum of p (l - l0 - s (y - y0)), in two floats
 };
 
 // a two-float sum with the lane o away; both lanes get the same bits
@@ -240,11 +240,11 @@ struct Row2 {
 };
 
 // a row's list in shared memory: this part's tokens (-1: none), probabilities
-// and logits; the warps' largest logits of the whole row's list; dup: some token
-// is listed twice
+// and logits; the warps' largest logits and log-probabilities of the whole row's
+// list; dup: some token is listed twice
 struct List {
     int ids[SPEC_MAX_TOP];
-    float p[SPEC_MAX_TOP], yl[SPEC_MAX_TOP], top[SPEC_MAX_TOP / 32];
+    float p[SPEC_MAX_TOP], yl[SPEC_MAX_TOP], top[SPEC_MAX_TOP / 32], lmax[SPEC_MAX_TOP / 32];
     int dup;
 };
 
@@ -254,6 +254,14 @@ __device__ __forceinline__ float list_top(const List &l) {
     const float m = fmaxf(fmaxf(l.top[0], l.top[1]), fmaxf(l.top[2], l.top[3]));
     static_assert(SPEC_MAX_TOP == 128, "four warps hold a list");
     return m > sv::kMaskFloor ? m : 0.f;
+}
+
+// l0, what a list's log-probabilities are taken against: 0, or where only their
+// differences count (a renormalised list) the largest one, so that no level of
+// them leaves fp32's range. lmax: the four warps' largest
+__device__ __forceinline__ float list_level(int tail, const float *lmax) {
+    const float m = fmaxf(fmaxf(lmax[0], lmax[1]), fmaxf(lmax[2], lmax[3]));
+    return !tail && fabsf(m) < INFINITY ? m : 0.f;
 }
 
 // whether entry t is the first of its token
@@ -269,8 +277,9 @@ __device__ __forceinline__ bool first_entry(const List &l, int t) {
 __device__ __forceinline__ Known list_known(const DistillArgs &a, List &l, int t, int id, float lp) {
     Known k = known_nothing();
     float ph = 0.f, pl = 0.f, yl = neg_inf();
+    const float l0 = list_level(a.tail, l.lmax);
     if (id >= 0) {
-        exp_diff(lp, 0.f, ph, pl);
+        exp_diff(lp, l0, ph, pl);
         yl = l.yl[t];
     }
     l.p[t] = ph;
@@ -279,13 +288,14 @@ __device__ __forceinline__ Known list_known(const DistillArgs &a, List &l, int t
     k.Sl = warp_sum(first_entry(l, t) ? (there ? ex2((yl - k.ml) * a.sL) : yl == yl ? 0.f : yl) : 0.f);
     k.Ph = ph;
     k.Pl = pl;
-    if (id >= 0 && lp > -700.f) {
-        if (there) {   // p (l - s (y - y0)), each product and sum with its rounding
-            float dh, dl;
+    if (id >= 0 && lp - l0 > -700.f) {
+        if (there) {   // p (l - l0 - s (y - y0)), each product and sum with its rounding
+            float dh, dl, lh, ll;
             two_sum(yl, -list_top(l), dh, dl);
             const float sy = __fmul_rn(a.s, dh), syl = __fmaf_rn(a.s, dh, -sy) + a.s * dl;
-            two_sum(lp, -sy, dh, dl);
-            dl -= syl;
+            two_sum(lp, -l0, lh, ll);
+            two_sum(lh, -sy, dh, dl);
+            dl += ll - syl;
             k.Bh = __fmul_rn(ph, dh);
             k.Bl = __fmaf_rn(ph, dh, -k.Bh) + (ph * dl + pl * dh);
         } else {
@@ -514,7 +524,11 @@ __global__ void __launch_bounds__(NT, 1024 / NT) distill_kernel(DistillArgs a, i
     // list's part of what this warp knows
     if (tid < SPEC_MAX_TOP) {
         const float y = id >= 0 ? load1_rw(py + id) : neg_inf(), top = warp_max(y);
-        if (lane == 0) s_list.top[warp] = top;
+        const float lmax = warp_max(id >= 0 ? lp : neg_inf());
+        if (lane == 0) {
+            s_list.top[warp] = top;
+            s_list.lmax[warp] = lmax;
+        }
         if (!(id >= part.e0 && id < part.e1)) id = -1;
         s_list.ids[tid] = id;
         if (id >= 0) {
@@ -692,8 +706,16 @@ __global__ void __launch_bounds__(NT, 4) grad_kernel(DistillArgs a, int parts) {
     double P = 1.0;
     float p = 0.f;
     if (need) {
-        float h = 0.f, l = 0.f;
-        if (id >= 0) exp_diff(lp, 0.f, h, l);
+        float h = 0.f, l = 0.f, l0 = 0.f;
+        if (!a.tail) {
+            if (tid < SPEC_MAX_TOP) {
+                const float m = warp_max(id >= 0 ? lp : neg_inf());
+                if ((tid & 31) == 0) s_f[tid >> 5] = m;
+            }
+            __syncthreads();
+            l0 = list_level(0, s_f);
+        }
+        if (id >= 0) exp_diff(lp, l0, h, l);
         p = h;
         double x = (double)h + (double)l;
 #pragma unroll

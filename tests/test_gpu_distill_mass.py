@@ -167,3 +167,44 @@ def test_little_teacher_mass_left(dtype):
         for got in (g, step):
             off = np.abs(got[0, 0].float().cpu().double().numpy() - r["grad"])
             assert np.all(off <= tol), (M, float((off / tol).max()))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,M", [(40, 6), (2001, 24), (40003, 128)])
+def test_renormalised_lists_of_any_level(V, M, dtype):
+    """With tail = 0 only differences of the list's log-probabilities count: levels
+    whose probabilities all leave fp32's range."""
+    import speculative_decoding_token_verify_gb300 as sv
+    sv.build()
+    levels = [-600.0, -103.0, -90.0, 89.0, 300.0]
+    K = len(levels)
+    for repeats in (False, True):
+        y, lp, ids = _case(K, V, M, dtype, [1.0] * K, repeats, V + M, 1.0)
+        lp = (lp.double() + torch.tensor(levels, dtype=torch.float64)[:, None]).float()
+        ids[0, M // 2] = -1
+        lp[1, M - 1] = -float("inf")
+        w = torch.linspace(0.25, 1.0, K)
+        yd, lpd, idd = y[None].to(DEV), lp[None].to(DEV), ids[None].to(DEV)
+        kw = dict(weight=w[None].to(DEV), tail=False)
+        a = sv.distill_loss(yd, lpd, idd, **kw)
+        g = sv.distill_grad(yd, lpd, idd, a["stats"], **kw)
+        step = sv.distill_step(yd, lpd, idd, **kw)
+        half = ref.half(dtype == "bf16")
+        for k in range(K):
+            keep = (ids[k] >= 0) & (lp[k] > -float("inf"))
+            l, i = lp[k][keep].double(), ids[k][keep]
+            loss, want = gradient(y[k].double(), l, i, 1.0, False)
+            f = float(w[k])
+            lt = f * (ref.DS + 4 * ref.U * abs(loss) + 2e-8)
+            for got in (a["loss"], step["loss"]):
+                assert abs(float(got[0, k]) - f * loss) <= lt, (repeats, k, float(got[0, k]), f * loss)
+            tol = _tolerance(y[k], l, i, 1.0, False, f, half)
+            exact = want * f
+            tol = tol + half * (exact.abs() + tol) + 1e-37
+            for got in (step["dlogits"], g):
+                off = (got[0, k].double().cpu() - exact).abs()
+                assert bool((off <= tol).all()), (repeats, k, float((off / tol).max()))
+    lp.fill_(-float("inf"))                   # no probability at all: an empty list
+    a = sv.distill_loss(yd, lp[None].to(DEV), idd, **kw)
+    assert not a["loss"].any() and not a["stats"].any()
