@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(NT, 4) beam_kernel(BeamArgs a, int C, int P, i
     float bound = neg_inf();
     for (int u0 = 0; u0 < units; u0 += 32) {
         const int u = min(u0 + lane, units - 1);
-        bound = fmaxf(bound, __shfl_sync(kFull, base, u / P) + s.u_thr[u]);
+        const float bw = __shfl_sync(kFull, base, u / P), thr = s.u_thr[u];
+        if (thr > sv::kMaskFloor) bound = fmaxf(bound, bw + thr);   // (the floor is no bound)
     }
     bound = warp_max(bound);
     mag = warp_max(mag);
