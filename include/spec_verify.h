@@ -415,9 +415,10 @@ int spec_irls_refit(int32_t K, void *state, float *est_params, double damping, d
  * inputs; a stride smaller than V otherwise overlaps rows, which inputs may
  * and outputs may not. Any alignment to the element works; no stride or
  * length needs to be a multiple of anything. A logit of -inf or up to -1e29f
- * is masked (the token has probability 0); finite ones may be of any size. NaN or +inf logits spoil their own
- * row's outputs only (its floats are NaN or infinite) and raise
- * SPEC_ERR_BAD_ROW.
+ * is masked (the token has probability 0); finite ones may be of any size
+ * (beyond 2^120 / s a log-probability or a loss may overflow to an infinity).
+ * NaN or +inf logits spoil their own row's outputs only (its floats are NaN or
+ * infinite) and raise SPEC_ERR_BAD_ROW.
  *
  * `status` is a device int32 or NULL: the largest code met is left there
  * (atomic maximum). These calls never clear it: the caller zeroes it. They

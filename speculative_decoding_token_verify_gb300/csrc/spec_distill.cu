@@ -29,7 +29,7 @@
 //
 // Measured (bf16, M = 64; shares of the measured copy rate, 6691 GB/s): the loss
 // of 1920 rows of 152064 87 us, 6.1 TB/s, 91%; the step of 2048 rows of 128256
-// 185 us, 5.4 TB/s of read and written bytes, 81%; the gradient of 2048 rows of
+// 186 us, 5.4 TB/s of read and written bytes, 81%; the gradient of 2048 rows of
 // 128256 151 us, 7.0 TB/s, the rate of a copy; of 320 rows, a tenth of them without
 // weight, 25 us in a graph over three input sets (the 82 MB written stay in L2) and
 // 28 us called one by one. f32, 2048 rows of 128256: loss 156 us, gradient 297 us, step
