@@ -72,7 +72,11 @@ extern "C" {
 #define SPEC_ERR_BAD_TOKEN 6     /* device status: a draft token was outside [0,V) */
 #define SPEC_ERR_BAD_TEMPERATURE 7 /* device status: an inverse temperature was out of range */
 #define SPEC_ERR_INDEX 8         /* device status, checked builds only: an index check failed */
-#define SPEC_ERR_BAD_PARENT 9    /* device status: a parent beam was outside [-1, W) */
+#define SPEC_ERR_BAD_PARENT 9    /* device status: a parent (beam or node) was out of range */
+#define SPEC_ERR_BAD_PAGE 10     /* device status: a page was outside [0, P) where one is needed */
+#define SPEC_ERR_BAD_LENGTH 11   /* device status: a length or count was out of range */
+#define SPEC_ERR_NO_PAGES 12     /* device status: fewer free pages than wanted */
+#define SPEC_ERR_BAD_PATH 13     /* device status: a path does not ascend */
 
 /* limits */
 #define SPEC_MAX_B (1 << 24)     /* sequences per call                      */
@@ -85,8 +89,9 @@ extern "C" {
 #define SPEC_MAX_TOP 128         /* entries of a top list (M)               */
 #define SPEC_MAX_BEAMS 32        /* beams per sequence (W)                  */
 #define SPEC_MAX_BEAM_OUT 64     /* continuations kept per sequence (N)     */
+#define SPEC_MAX_NODES 128       /* nodes of a tree of drafts (N)           */
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype;
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 /* spec_tree_attention only */ } spec_dtype;
 
 typedef enum {
     SPEC_STOCHASTIC = 0, /* [SD] lossless rejection rule + residual/bonus draw */
@@ -554,6 +559,157 @@ typedef struct {
 } spec_reorder_params;
 int spec_beam_reorder(const spec_reorder_params *params, const void *src, void *dst, const int32_t *parent,
                       const int32_t *lengths, int32_t *status, void *stream);
+
+/*
+ * Trees of drafts over a cache held in pages. A draft model that proposes more
+ * than one continuation (beams, top lists) gives a tree: node 0 is the last
+ * token of the context, whose keys and values are not in the cache yet, node n
+ * the token after node parents[n] < n. One pass of the target over all nodes
+ * scores them, the walk along the target's choices keeps one path, and the
+ * cache keeps that path's keys and values. The calls: spec_pages_resize (pages
+ * for the nodes), spec_tree_attention in every layer, spec_tree_accept,
+ * spec_pages_compact; spec_pages_fork for beams.
+ *
+ * A cache is a pool of P pages of `page` slots each. table [rows][M] int32
+ * holds a row's (sequence's or beam's) pages in order, -1 for none: token t of
+ * row r lies in slot t % page of page table[r][t / page]. lengths are tokens.
+ * refs [P] int32 counts the table entries that name a page (several rows may
+ * share one, and entries of other tables count too); a page is free where it
+ * is 0, and there is no other list of free pages.
+ *
+ * These calls never read or write outside the tensors that they are given,
+ * whatever tables, lengths, parents and paths hold: entries out of range are
+ * treated as the calls say and raise a code in `status` (device int32 or NULL;
+ * atomic maximum, never cleared here). They keep nothing between calls.
+ * Asynchronous on `stream`, outputs bit-reproducible.
+ */
+
+/*
+ * spec_tree_attention -- attention of N nodes a sequence over its pages.
+ * Row (b, n, h) sees the keys of tokens t < lengths[b], and of the nodes
+ * n = a_0, a_1 = parents[n], .. up to a root (parent -1); node i's key lies at
+ * token lengths[b] + i (the caller has written it). With s_t = scale q . k_t
+ * over what it sees:
+ *   out = sum_t e^{s_t} v_t / sum_t e^{s_t},  lse = ln sum_t e^{s_t}.
+ * Query head h reads key head h / (Hq / Hkv). counts[b] (NULL: N) of the nodes
+ * exist; rows of the others have out = 0 and lse = -inf. parents NULL: a chain
+ * (parents[n] = n - 1); N = 1: an ordinary decoding step.
+ * Keys and values that a row does not see do not reach it, NaN and infinities
+ * among them (slots never written, other branches). What it sees may make it NaN,
+ * and so do scores beyond fp32's range.
+ * parents outside [-1, n) count as -1 (SPEC_ERR_BAD_PARENT). counts are clamped to
+ * [0, N], lengths to [0, M page - counts[b]] (SPEC_ERR_BAD_LENGTH). Where a page that a
+ * sequence needs is outside [0, P), SPEC_ERR_BAD_PAGE is raised and that
+ * sequence's outputs are unspecified.
+ * Precision: scores and sums in fp32; the probabilities are rounded to the
+ * inputs' type before they multiply the values (relative error 2^-9 each in bf16).
+ * q, k and v: strides in elements, multiples of 8 and > 0 (where the axis has more
+ * than one entry), 16-byte aligned, D contiguous. out [B][N][Hq][D] in the inputs' type, lse
+ * [B][N][Hq] f32 or NULL, contiguous; out must not overlap an input.
+ */
+typedef struct {
+    int32_t B;            /* sequences, 0 .. 65535                            */
+    int32_t N;            /* nodes per sequence, 0 .. SPEC_MAX_NODES          */
+    int32_t Hq, Hkv;      /* heads; Hq a multiple of Hkv, at most 128 times   */
+    int32_t D;            /* head size: a multiple of 8, 8 .. 128             */
+    int32_t dtype;        /* SPEC_BF16 or SPEC_F16                            */
+    int32_t P, page, M;   /* pages, slots a page (a power of two >= 8), entries a row */
+    float scale;          /* finite                                           */
+    int64_t q_stride[3];  /* of b, node, head                                 */
+    int64_t k_stride[3];  /* of page, slot, head                              */
+    int64_t v_stride[3];
+    int64_t parents_stride; /* 0: one tree for all sequences, else >= N       */
+} spec_attend_params;
+/* Bytes of device workspace (16-byte aligned); 0 if the parameters are invalid. */
+size_t spec_tree_attention_workspace_size(const spec_attend_params *params);
+int spec_tree_attention(const spec_attend_params *params, const void *q, const void *k, const void *v,
+                        const int32_t *table, const int32_t *lengths, const int32_t *parents, const int32_t *counts,
+                        void *out, float *lse, void *workspace, size_t workspace_bytes, int32_t *status, void *stream);
+
+/*
+ * spec_tree_accept -- the accepted path of a tree. choice[b][n] is the target's
+ * token after node n: its argmax, or a draw from its distribution there (the
+ * emitted tokens then follow the target's distribution exactly). From node 0 on,
+ * the walk goes to the lowest child c with tokens[b][c] == choice[b][current],
+ * until there is none. path[b] holds its nodes (0 first), out_tokens[b] the
+ * choices at them (the accepted drafts and one token more), both [B][N] filled
+ * up with -1; accepted_len[b] counts the drafts (nodes but node 0). tokens and
+ * outputs contiguous int32; choice with strides in elements. counts NULL: N; a
+ * sequence of count 0 has accepted_len 0 and nothing but -1. parents as for
+ * spec_tree_attention (NULL: a chain); nodes with parent -1 other than node 0
+ * are never reached. N in [1, SPEC_MAX_NODES].
+ */
+int spec_tree_accept(int32_t B, int32_t N, const int32_t *tokens, const int32_t *parents, int64_t parents_stride,
+                     const int32_t *choice, int64_t choice_batch_stride, int64_t choice_node_stride,
+                     const int32_t *counts, int32_t *accepted_len, int32_t *out_tokens, int32_t *path,
+                     int32_t *status, void *stream);
+
+/* A cache's layout: O outer entries (layers, keys and values) of P pages; a page
+ * is H segments (heads) of `page` slots of unit_bytes each, slots contiguous.
+ * Strides in bytes, of any alignment (multiples of 16 are fastest). */
+typedef struct {
+    int32_t O, P, H, page;  /* O and H 0 .. 65535                             */
+    int64_t unit_bytes;     /* 1 .. 2^30                                      */
+    int64_t stride[3];      /* of outer entry, page, segment                  */
+} spec_cache_params;
+
+/*
+ * spec_pages_compact -- the kept nodes moved to the end of the context: slot
+ * lengths[b] + i receives slot lengths[b] + path[b][i], i = 0, 1, .., in all
+ * outer entries and segments, in place. path [B][N] int32, ends at its first -1;
+ * it must ascend (path[i] >= i follows): an entry that does not, or is outside
+ * [0, N), ends it and raises SPEC_ERR_BAD_PATH. out_lengths[b] = lengths[b] + entries kept;
+ * out_lengths must not overlap lengths. A move whose page is missing is left out
+ * (SPEC_ERR_BAD_PAGE); lengths outside [0, M page] move nothing and stay
+ * (SPEC_ERR_BAD_LENGTH). Rows must not share pages behind lengths. Several caches
+ * with one table take one call each. N in [1, SPEC_MAX_NODES].
+ */
+int spec_pages_compact(const spec_cache_params *params, void *cache, int32_t B, int32_t N, int32_t M,
+                       const int32_t *table, const int32_t *lengths, const int32_t *path, int32_t *out_lengths,
+                       int32_t *status, void *stream);
+
+/*
+ * spec_pages_resize -- rows get exactly the pages that lengths [R] ask for,
+ * ceil(lengths[r] / page): entries behind them are dropped (-1, and one
+ * reference less), then missing ones are filled with free pages, the lowest
+ * first, in order of row and entry, with one reference each. Length 0 gives a
+ * row's pages back. Where free pages run out the remaining entries stay -1
+ * (SPEC_ERR_NO_PAGES). Entries outside [-1, P) count as -1 (SPEC_ERR_BAD_PAGE),
+ * lengths are clamped to [0, M page] (SPEC_ERR_BAD_LENGTH). out_table may be table and
+ * out_refs refs, which must not overlap otherwise. workspace: P int32.
+ */
+typedef struct {
+    int32_t B, W, N;        /* sequences, rows of each before and after (resize: B W rows, N = W) */
+    int32_t M, P, page;     /* entries a row, pages, slots a page             */
+} spec_pages_params;
+int spec_pages_resize(const spec_pages_params *params, const int32_t *table, const int32_t *refs,
+                      const int32_t *lengths, int32_t *out_table, int32_t *out_refs, int32_t *workspace,
+                      int32_t *status, void *stream);
+
+/*
+ * spec_pages_fork -- tables in the order of the surviving beams: row (b, n)
+ * continues row (b, parent[b][n]) of table [B][W][M] and lengths [B][W]; parent
+ * -1 continues its own row (none where n >= W: the new row is empty). Full pages are shared. A
+ * page that holds the row's last tokens and is not full goes to the first new row that
+ * continues with it, if no other entry names it; for every other such row a free
+ * page (the lowest first, in the rows' order, those that the call itself frees
+ * among them) takes its place and an entry in
+ * copies [B][N][4]: source page, page, slots to copy, 0 (page -1: nothing to
+ * copy), which spec_pages_copy carries out. Pages behind a row's length are
+ * dropped. out_table [B][N][M], out_lengths [B][N] and copies must not overlap
+ * inputs; out_refs may be refs. Rows without a free page get -1 there
+ * (SPEC_ERR_NO_PAGES). A parent outside [-1, W) counts as -1
+ * (SPEC_ERR_BAD_PARENT); entries and lengths as in spec_pages_resize, a
+ * missing page among those that a length asks for raises SPEC_ERR_BAD_PAGE and stays -1.
+ * workspace: 2 P int32.
+ */
+int spec_pages_fork(const spec_pages_params *params, const int32_t *table, const int32_t *refs, const int32_t *lengths,
+                    const int32_t *parent, int32_t *out_table, int32_t *out_refs, int32_t *out_lengths,
+                    int32_t *copies, int32_t *workspace, int32_t *status, void *stream);
+/* The first slots of pages copied, in all outer entries: copies [count][4] as
+ * spec_pages_fork leaves them (entries out of range are left out; no page may
+ * be a source and a destination). */
+int spec_pages_copy(const spec_cache_params *params, void *cache, const int32_t *copies, int32_t count, void *stream);
 
 /*
  * Synchronously read the device status word of a workspace last used by

@@ -15,3 +15,6 @@ from .rows import (  # noqa: F401
     MAX_BEAM_OUT, MAX_BEAMS, MAX_TOP, beam_reorder, beam_step, distill_grad, distill_loss, distill_step,
     top_logprobs,
 )
+from .tree import (  # noqa: F401
+    MAX_NODES, pages_compact, pages_fork, pages_resize, tree_accept, tree_attention,
+)

@@ -22,7 +22,7 @@ LIB_PATH = os.path.join(_PKG, "libspecverify.so")
 # for tests
 CHECKED_LIB_PATH = os.path.join(_PKG, "libspecverify_checked.so")
 SOURCES = ("spec_verify.cu", "spec_nucleus.cu", "spec_estimator.cu", "spec_irls.cu", "spec_av.cu", "spec_ngram.cu",
-           "spec_top.cu", "spec_distill.cu", "spec_beam.cu", "spec_reorder.cu")
+           "spec_top.cu", "spec_distill.cu", "spec_beam.cu", "spec_reorder.cu", "spec_attend.cu", "spec_pages.cu")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 _lock = threading.Lock()
@@ -137,6 +137,50 @@ class ReorderParams(ctypes.Structure):
     ]
 
 
+class AttendParams(ctypes.Structure):
+    """Mirror of ``spec_attend_params``."""
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("Hq", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("P", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("M", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("q_stride", ctypes.c_int64 * 3),
+        ("k_stride", ctypes.c_int64 * 3),
+        ("v_stride", ctypes.c_int64 * 3),
+        ("parents_stride", ctypes.c_int64),
+    ]
+
+
+class CacheParams(ctypes.Structure):
+    """Mirror of ``spec_cache_params``."""
+    _fields_ = [
+        ("O", ctypes.c_int32),
+        ("P", ctypes.c_int32),
+        ("H", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("unit_bytes", ctypes.c_int64),
+        ("stride", ctypes.c_int64 * 3),
+    ]
+
+
+class PagesParams(ctypes.Structure):
+    """Mirror of ``spec_pages_params``."""
+    _fields_ = [
+        ("B", ctypes.c_int32),
+        ("W", ctypes.c_int32),
+        ("N", ctypes.c_int32),
+        ("M", ctypes.c_int32),
+        ("P", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+    ]
+
+
 # (name, restype, argtypes) of every symbol include/spec_verify.h declares
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -172,6 +216,15 @@ SIGNATURES = {
                                          ctypes.c_int64, _P, _P]),
     "spec_beam_step": (ctypes.c_int, [ctypes.POINTER(RowsParams), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P]),
     "spec_beam_reorder": (ctypes.c_int, [ctypes.POINTER(ReorderParams), _P, _P, _P, _P, _P, _P]),
+    "spec_tree_attention_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(AttendParams)]),
+    "spec_tree_attention": (ctypes.c_int, [ctypes.POINTER(AttendParams), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                           ctypes.c_size_t, _P, _P]),
+    "spec_tree_accept": (ctypes.c_int, [_I32, _I32, _P, _P, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64, _P, _P,
+                                        _P, _P, _P, _P]),
+    "spec_pages_compact": (ctypes.c_int, [ctypes.POINTER(CacheParams), _P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _P]),
+    "spec_pages_resize": (ctypes.c_int, [ctypes.POINTER(PagesParams), _P, _P, _P, _P, _P, _P, _P, _P]),
+    "spec_pages_fork": (ctypes.c_int, [ctypes.POINTER(PagesParams), _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "spec_pages_copy": (ctypes.c_int, [ctypes.POINTER(CacheParams), _P, _P, _I32, _P]),
     "spec_get_device_status": (ctypes.c_int, [_P, ctypes.POINTER(_I32)]),
     "spec_static_device_status": (ctypes.c_int, [ctypes.POINTER(_I32)]),
     "spec_debug_set_wait_limit": (ctypes.c_uint32, [ctypes.c_uint32]),

@@ -28,6 +28,10 @@ SPEC_ERR_BAD_TOKEN = 6
 SPEC_ERR_BAD_TEMPERATURE = 7
 SPEC_ERR_INDEX = 8
 SPEC_ERR_BAD_PARENT = 9
+SPEC_ERR_BAD_PAGE = 10
+SPEC_ERR_BAD_LENGTH = 11
+SPEC_ERR_NO_PAGES = 12
+SPEC_ERR_BAD_PATH = 13
 MAX_K = 31
 MAX_V = 1 << 20
 

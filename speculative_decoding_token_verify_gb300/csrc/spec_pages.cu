@@ -1,0 +1,730 @@
+// spec_pages.cu -- the upkeep of a cache held in pages: rows resized, forked and
+// compacted, and the walk down a tree of drafts.
+//
+// The tables are small (megabytes at most) and every decision is a count: which
+// entries are dropped, how many pages are wanted before this one, which pages are
+// free before that one. One cluster of CTAs makes them in one launch, with a
+// cluster barrier between the phases. Each warp owns a contiguous stretch of entries (and later of pages),
+// so that a rank is a sum of ballots: over the warp's own stretch, the CTA's earlier
+// warps, and the cluster's earlier CTAs. Reference counts change by integer
+// atomics, whose order cannot be seen.
+#include <climits>
+
+#include "spec_rows.cuh"
+
+namespace sr {
+
+constexpr int NTP = 1024;
+constexpr int NWP = NTP / 32;
+constexpr int kMaxPagesCluster = 8;
+
+struct PagesArgs {
+    const int32_t *table, *refs, *lengths, *parent;
+    int32_t *out_table, *out_refs, *out_lengths, *copies;
+    int32_t *list, *claim;   // workspace: free pages in order; the first row that wants a page
+    int32_t *status;
+    int B, W, N, M, P, page;
+};
+
+struct PagesShared {
+    int warp[NWP];            // a count per warp
+    int cta[2][16];           // and per CTA of the cluster, for two counts
+};
+
+__device__ __forceinline__ void cluster_sync_all(int C) {
+    if (C > 1) {
+        cluster_arrive();
+        cluster_wait();
+    } else {
+        __syncthreads();
+    }
+}
+
+// From every warp's count: how many come before this warp in the cluster, and in
+// all. Ends with a cluster barrier, before which the caller's writes also count.
+__device__ __forceinline__ void ranks(PagesShared &sh, int slot, int mine, int C, int rank, int &before, int &total) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) sh.warp[warp] = mine;
+    __syncthreads();
+    if (threadIdx.x < C) {
+        int sum = 0;
+        for (int w = 0; w < NWP; ++w) sum += sh.warp[w];
+        if (C > 1) peer_store_u32(peer(&sh.cta[slot][rank], threadIdx.x), (uint32_t)sum);
+        else sh.cta[slot][0] = sum;
+    }
+    before = 0;
+    for (int w = 0; w < warp; ++w) before += sh.warp[w];
+    cluster_sync_all(C);
+    total = 0;
+    for (int c = 0; c < C; ++c) {
+        if (c < rank) before += sh.cta[slot][c];
+        total += sh.cta[slot][c];
+    }
+}
+
+// A warp's stretch of n entries, in whole groups of 32.
+struct Stretch {
+    long long lo, hi;
+    __device__ __forceinline__ Stretch(long long n, int warp, int warps) {
+        const long long groups = (n + 31) / 32, per = (groups + warps - 1) / warps;
+        lo = min(n, warp * per * 32);
+        hi = min(n, (warp + 1) * per * 32);
+    }
+};
+
+__device__ __forceinline__ int lanes_below(unsigned ballot) {
+    return __popc(ballot & ((1u << (threadIdx.x & 31)) - 1));
+}
+
+// list[k] = the k-th lowest free page, for k < wanted; the number of free pages
+__device__ __forceinline__ int free_pages(const PagesArgs &a, PagesShared &sh, int wanted, int C, int rank, int gw) {
+    const int lane = threadIdx.x & 31;
+    const Stretch s(a.P, gw, C * NWP);
+    int count = 0, before, total;
+    for (long long i = s.lo + lane; i < s.hi + lane; i += 32)
+        count += __popc(__ballot_sync(kFull, i < s.hi && __ldcg(a.out_refs + i) == 0));
+    ranks(sh, 1, count, C, rank, before, total);
+    for (long long i = s.lo + lane; i < s.hi + lane && before < wanted; i += 32) {
+        const bool free = i < s.hi && __ldcg(a.out_refs + i) == 0;
+        const unsigned all = __ballot_sync(kFull, free);
+        const int k = before + lanes_below(all);
+        if (free && k < wanted) a.list[k] = (int)i;
+        before += __popc(all);
+    }
+    cluster_sync_all(C);
+    return total;
+}
+
+__device__ __forceinline__ int pages_for(const PagesArgs &a, int length) {
+    const long long most = (long long)a.M * a.page;
+    if (length < 0 || length > most) {
+        raise_status(a.status, SPEC_ERR_BAD_LENGTH);
+        length = length < 0 ? 0 : (int)most;
+    }
+    return (int)(((long long)length + a.page - 1) / a.page);
+}
+
+// entry i of a table as (row, place), moved on by 32 without a division most of the time
+struct Place {
+    int r, m;
+    __device__ __forceinline__ Place(long long i, int M) : r((int)(i / max(M, 1))), m((int)(i - (long long)r * M)) {}
+    __device__ __forceinline__ void next(int M) {
+        m += 32;
+        if (m >= M) {
+            const int q = m / M;
+            r += q;
+            m -= q * M;
+        }
+    }
+};
+
+// Rows of exactly the pages that their lengths ask for.
+__global__ void __launch_bounds__(NTP, 1) resize_kernel(PagesArgs a, int C) {
+    __shared__ PagesShared sh;
+    const int rank = C > 1 ? blockIdx.x : 0, lane = threadIdx.x & 31, gw = rank * NWP + (threadIdx.x >> 5);
+    if (a.out_refs != a.refs)
+        for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) a.out_refs[i] = a.refs[i];
+    cluster_sync_all(C);   // (from here on every CTA of the cluster has shared memory to write to)
+    const Stretch s((long long)a.B * a.W * a.M, gw, C * NWP);
+    int wants = 0, before, wanted;
+    {
+        Place at(s.lo + lane, a.M);
+        int row = -1, need = 0;
+        for (long long i = s.lo + lane; i < s.hi + lane; i += 32, at.next(a.M)) {
+            bool want = false;
+            if (i < s.hi) {
+                if (at.r != row) need = pages_for(a, a.lengths[row = at.r]);
+                const int e = a.table[i];
+                const bool has = e >= 0 && e < a.P;
+                if (!has && e != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                want = !has && at.m < need;
+                if (has && at.m >= need) atomicAdd(a.out_refs + e, -1);
+            }
+            wants += __popc(__ballot_sync(kFull, want));
+        }
+    }
+    ranks(sh, 0, wants, C, rank, before, wanted);
+    int nfree = 0;
+    if (wanted > 0) nfree = free_pages(a, sh, wanted, C, rank, gw);
+    if (nfree < wanted && rank == 0 && threadIdx.x == 0) raise_status(a.status, SPEC_ERR_NO_PAGES);
+    {
+        Place at(s.lo + lane, a.M);
+        int row = -1, need = 0;
+        for (long long i = s.lo + lane; i < s.hi + lane; i += 32, at.next(a.M)) {
+            int e = -1;
+            bool want = false;
+            if (i < s.hi) {
+                if (at.r != row) need = pages_for(a, a.lengths[row = at.r]);
+                e = a.table[i];
+                const bool has = e >= 0 && e < a.P;
+                want = !has && at.m < need;
+                if (!has || at.m >= need) e = -1;
+            }
+            const unsigned all = __ballot_sync(kFull, want);
+            const int k = before + lanes_below(all);
+            if (want && k < nfree) {
+                e = __ldcg(a.list + k);
+                a.out_refs[e] = 1;
+            }
+            before += __popc(all);
+            if (i < s.hi) a.out_table[i] = e;
+        }
+    }
+}
+
+// What new row (b, n) continues: its old row's index (-1: none) and length.
+__device__ __forceinline__ int source_row(const PagesArgs &a, int r, int &length) {
+    const int b = r / a.N, n = r - b * a.N;
+    int w = a.parent[r];
+    if (w < -1 || w >= a.W) {
+        raise_status(a.status, SPEC_ERR_BAD_PARENT);
+        w = -1;
+    }
+    if (w < 0) w = n < a.W ? n : -1;
+    length = 0;
+    if (w < 0) return -1;
+    const int src = b * a.W + w;
+    length = a.lengths[src];
+    const long long most = (long long)a.M * a.page;
+    if (length < 0 || length > most) {
+        raise_status(a.status, SPEC_ERR_BAD_LENGTH);
+        length = length < 0 ? 0 : (int)most;
+    }
+    return src;
+}
+
+__device__ __forceinline__ int entry(const PagesArgs &a, int row, int m) {
+    const int e = a.table[(long long)row * a.M + m];
+    if (e >= 0 && e < a.P) return e;
+    if (e != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+    return -1;
+}
+
+// Tables in the order of the surviving beams.
+__global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
+    __shared__ PagesShared sh;
+    const int rank = C > 1 ? blockIdx.x : 0, lane = threadIdx.x & 31, gw = rank * NWP + (threadIdx.x >> 5);
+    for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) {
+        if (a.out_refs != a.refs) a.out_refs[i] = a.refs[i];
+        a.claim[i] = INT_MAX;
+    }
+    cluster_sync_all(C);
+    // full pages: the old row's entries lose a reference, the new row's gain one
+    {
+        const Stretch s((long long)a.B * a.N * a.M, gw, C * NWP);
+        Place at(s.lo + lane, a.M);
+        int row = -1, src = -1, length = 0, full = 0, own = -1;
+        for (long long i = s.lo + lane; i < s.hi; i += 32, at.next(a.M)) {
+            if (at.r != row) {
+                row = at.r;
+                src = source_row(a, row, length);
+                full = length / a.page;
+                const int b = row / a.N, n = row - b * a.N;
+                own = n < a.W ? b * a.W + n : -1;
+            }
+            int e = -1;
+            if (src >= 0 && (at.m < full || (at.m == full && length % a.page))) {
+                e = entry(a, src, at.m);
+                if (e < 0) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+            }
+            if (at.m == full && e >= 0) {
+                atomicMin(a.claim + e, row);
+                e = -1;   // decided below
+            }
+            const int old = own >= 0 ? entry(a, own, at.m) : -1;
+            if (old != e) {
+                if (old >= 0) atomicAdd(a.out_refs + old, -1);
+                if (e >= 0) atomicAdd(a.out_refs + e, 1);
+            }
+            a.out_table[i] = e;
+        }
+    }
+    if (a.N < a.W) {   // old rows without a new one in their place
+        const int gone = a.W - a.N;
+        const Stretch s((long long)a.B * gone * a.M, gw, C * NWP);
+        Place at(s.lo + lane, a.M);
+        for (long long i = s.lo + lane; i < s.hi; i += 32, at.next(a.M)) {
+            const int b = at.r / gone, old = entry(a, b * a.W + a.N + at.r - b * gone, at.m);
+            if (old >= 0) atomicAdd(a.out_refs + old, -1);
+        }
+    }
+    cluster_sync_all(C);
+    // pages that are not full: kept by the first row that wants them, or copied
+    const Stretch s((long long)a.B * a.N, gw, C * NWP);
+    int wants = 0, before, wanted;
+    for (long long r = s.lo + lane; r < s.hi + lane; r += 32) {
+        bool want = false;
+        if (r < s.hi) {
+            int length;
+            const int src = source_row(a, (int)r, length), full = length / a.page, part = length % a.page;
+            const int last = src >= 0 && part ? entry(a, src, full) : -1;
+            if (last >= 0) {
+                want = __ldcg(a.claim + last) != (int)r || __ldcg(a.out_refs + last) != 0;
+                if (!want) {
+                    a.out_refs[last] = 1;   // (only the first row reads this count)
+                    a.out_table[r * a.M + full] = last;
+                }
+            }
+            a.out_lengths[r] = length;
+            int32_t *c = a.copies + r * 4;
+            c[0] = want ? last : -1;
+            c[1] = -1;
+            c[2] = want ? part : 0;
+            c[3] = 0;
+        }
+        wants += __popc(__ballot_sync(kFull, want));
+    }
+    ranks(sh, 0, wants, C, rank, before, wanted);
+    if (wanted == 0) return;   // (nothing of the cluster's shared memory is read any more)
+    const int nfree = free_pages(a, sh, wanted, C, rank, gw);
+    if (nfree < wanted && rank == 0 && threadIdx.x == 0) raise_status(a.status, SPEC_ERR_NO_PAGES);
+    for (long long r = s.lo + lane; r < s.hi + lane; r += 32) {
+        int32_t *c = a.copies + r * 4;
+        const bool want = r < s.hi && c[0] >= 0;   // (written by this thread)
+        const unsigned all = __ballot_sync(kFull, want);
+        const int k = before + lanes_below(all);
+        if (want && k < nfree) {
+            const int e = __ldcg(a.list + k);
+            int length;
+            source_row(a, (int)r, length);
+            c[1] = e;
+            a.out_refs[e] = 1;
+            a.out_table[r * a.M + length / a.page] = e;
+        }
+        before += __popc(all);
+    }
+}
+
+// ---- bytes of pages ------------------------------------------------------------------
+
+struct CacheArgs {
+    char *cache;
+    const int32_t *copies, *table, *lengths, *path;
+    int32_t *out_lengths, *status;
+    long long unit, ss[3];
+    int O, P, H, page, B, N, M;
+    long long vecs;   // vectors a segment (copy) or a unit (compact)
+};
+
+constexpr int NTC = 256;
+
+// copies[y]: the first slots of a page, CP vectors a thread
+template <typename Vec, int CP>
+__global__ void __launch_bounds__(NTC) copy_kernel(CacheArgs a, int count) {
+    for (int c = blockIdx.y; c < count; c += gridDim.y) {
+        const int src = a.copies[c * 4LL], dst = a.copies[c * 4LL + 1], slots = min(a.copies[c * 4LL + 2], a.page);
+        if (src < 0 || src >= a.P || dst < 0 || dst >= a.P || slots <= 0) continue;
+        const long long n = slots * a.unit / (long long)sizeof(Vec);
+        for (long long oh = blockIdx.z; oh < (long long)a.O * a.H; oh += gridDim.z) {
+            const long long o = oh / a.H, off = o * a.ss[0] + (oh - o * a.H) * a.ss[2];
+            const Vec *from = reinterpret_cast<const Vec *>(a.cache + off + src * a.ss[1]);
+            Vec *to = reinterpret_cast<Vec *>(a.cache + off + dst * a.ss[1]);
+            for (long long i0 = (long long)blockIdx.x * NTC * CP + threadIdx.x; i0 < n; i0 += (long long)gridDim.x * NTC * CP) {
+                Vec v[CP];
+#pragma unroll
+                for (int k = 0; k < CP; ++k)
+                    if (i0 + k * NTC < n) v[k] = from[i0 + k * NTC];
+#pragma unroll
+                for (int k = 0; k < CP; ++k)
+                    if (i0 + k * NTC < n) to[i0 + k * NTC] = v[k];
+            }
+        }
+    }
+}
+
+// The kept nodes of row b = blockIdx.y. A thread owns one vector of a unit and
+// makes its moves in order, eight loads ahead of their stores: a source path[j]
+// lies behind every place i <= j that was written before it is read.
+template <typename Vec>
+__global__ void __launch_bounds__(NTC) compact_kernel(CacheArgs a) {
+    __shared__ long long s_src[SPEC_MAX_NODES], s_dst[SPEC_MAX_NODES];
+    __shared__ int s_kept;
+    constexpr int U = 8;
+    const bool lead = blockIdx.x == 0;
+    for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
+        const int L = a.lengths[b];
+        const bool bad = L < 0 || L > (long long)a.M * a.page;
+        const int32_t *path = a.path + (long long)b * a.N;
+        __syncthreads();
+        if (threadIdx.x == 0) s_kept = bad ? 0 : a.N;
+        __syncthreads();
+        if (threadIdx.x < a.N && !bad) {
+            const int i = threadIdx.x, p = path[i], q = i ? path[i - 1] : -1;
+            if (p <= q || p >= a.N) {   // (ends at the first -1, too)
+                atomicMin(&s_kept, i);
+            }
+        }
+        __syncthreads();
+        const int kept = s_kept;
+        if (threadIdx.x < kept) {
+            const int i = threadIdx.x, p = path[i];
+            const int from = L + p, to = L + i;
+            long long so = -1, dof = 0;
+            if (p != i) {
+                const int mf = from / a.page, mt = to / a.page;
+                const int pf = mf < a.M ? a.table[(long long)b * a.M + mf] : -1;
+                const int pt = mt < a.M ? a.table[(long long)b * a.M + mt] : -1;
+                if (pf >= 0 && pf < a.P && pt >= 0 && pt < a.P) {
+                    so = pf * a.ss[1] + (from - mf * a.page) * a.unit;
+                    dof = pt * a.ss[1] + (to - mt * a.page) * a.unit;
+                } else if (lead) {
+                    raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                }
+            }
+            s_src[i] = so;
+            s_dst[i] = dof;
+        }
+        if (lead && threadIdx.x == 0) {
+            a.out_lengths[b] = L + kept;
+            if (bad) raise_status(a.status, SPEC_ERR_BAD_LENGTH);
+            if (!bad && kept < a.N && path[kept] != -1) raise_status(a.status, SPEC_ERR_BAD_PATH);
+        }
+        __syncthreads();
+        const long long columns = (long long)a.O * a.H * a.vecs;
+        for (long long x = (long long)blockIdx.x * NTC + threadIdx.x; x < columns; x += (long long)gridDim.x * NTC) {
+            const long long oh = x / a.vecs, o = oh / a.H;
+            char *base = a.cache + o * a.ss[0] + (oh - o * a.H) * a.ss[2] + (x - oh * a.vecs) * (long long)sizeof(Vec);
+            for (int i = 0; i < kept; i += U) {
+                Vec v[U];
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if (i + k < kept && s_src[i + k] >= 0) v[k] = *reinterpret_cast<const Vec *>(base + s_src[i + k]);
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    if (i + k < kept && s_src[i + k] >= 0) *reinterpret_cast<Vec *>(base + s_dst[i + k]) = v[k];
+            }
+        }
+    }
+}
+
+// ---- the walk down a tree --------------------------------------------------------------
+
+struct AcceptArgs {
+    const int32_t *tokens, *parents, *choice, *counts;
+    int32_t *accepted, *out, *path, *status;
+    long long ps, cb, cn;
+    int B, N;
+};
+
+constexpr int kPerLane = SPEC_MAX_NODES / 32;
+constexpr int NTA = 128;
+
+// A warp per sequence; lane l holds nodes l, l + 32, ..: a step of the walk is a
+// comparison and a ballot for each.
+__global__ void __launch_bounds__(NTA) accept_kernel(AcceptArgs a) {
+    __shared__ int32_t s_choice[NTA / 32][SPEC_MAX_NODES];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const long long b = (long long)blockIdx.x * (NTA / 32) + w;
+    if (b >= a.B) return;
+    const int N = a.N;
+    int count = a.counts ? a.counts[b] : N;
+    int bad = 0;
+    if (count < 0 || count > N) {
+        bad = SPEC_ERR_BAD_LENGTH;
+        count = count < 0 ? 0 : N;
+    }
+    int tok[kPerLane], par[kPerLane];
+#pragma unroll
+    for (int k = 0; k < kPerLane; ++k) {
+        const int n = lane + 32 * k;
+        tok[k] = 0;
+        par[k] = -1;
+        if (n < count) {
+            tok[k] = a.tokens[b * N + n];
+            s_choice[w][n] = a.choice[b * a.cb + n * a.cn];
+            par[k] = a.parents ? a.parents[b * a.ps + n] : n - 1;
+            if (par[k] < -1 || par[k] >= n) {
+                bad = max(bad, SPEC_ERR_BAD_PARENT);
+                par[k] = -1;
+            }
+        }
+    }
+    if (bad) raise_status(a.status, bad);
+    __syncwarp();
+    int cur = count > 0 ? 0 : -1, kept = 0;
+    while (cur >= 0) {   // parents lie before their children: at most count steps
+        const int said = s_choice[w][cur];
+        if (lane == 0) {
+            a.path[b * N + kept] = cur;
+            a.out[b * N + kept] = said;
+        }
+        ++kept;
+        int next = -1;
+#pragma unroll
+        for (int k = kPerLane - 1; k >= 0; --k) {
+            const unsigned hit = __ballot_sync(kFull, par[k] == cur && tok[k] == said);
+            if (hit) next = 32 * k + __ffs(hit) - 1;
+        }
+        cur = next;
+    }
+    for (int i = kept + lane; i < N; i += 32) a.path[b * N + i] = a.out[b * N + i] = -1;
+    if (lane == 0) a.accepted[b] = kept ? kept - 1 : 0;
+}
+
+// ---- host ---------------------------------------------------------------------------------
+
+static int check_pages(const spec_pages_params *p, bool fork) {
+    if (!p) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "params is NULL");
+    if (p->B < 0 || p->W < 0 || p->N < 0 || p->M < 0 || p->P < 0)
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages: B, W, N, M and P must be >= 0");
+    if (p->page < 1) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages: page must be >= 1");
+    if (!fork && p->N != p->W) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_resize: N must be W");
+    const int64_t rows = (int64_t)p->B * (p->W > p->N ? p->W : p->N);
+    if (rows > (1 << 24) || p->P > (1 << 30) || (rows && p->M > (INT32_MAX - 65536) / rows) ||
+        (int64_t)p->M * p->page > INT32_MAX)
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "pages: tables, pools or rows outside the supported range");
+    return SPEC_OK;
+}
+
+static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
+
+// Small tables are one CTA's work (cluster barriers cost more than they share out).
+static int pages_cluster(long long ints) {
+    int c = 1;
+    while (c < kMaxPagesCluster && ints > 8192LL * c) c *= 2;
+    return c;
+}
+
+static int check_cache(const spec_cache_params *p, const void *cache) {
+    if (!p) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "params is NULL");
+    if (p->O < 0 || p->P < 0 || p->H < 0 || p->page < 1)
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: O, P and H must be >= 0, page >= 1");
+    if (p->O > 65535 || p->H > 65535 || p->P > (1 << 30))
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "cache: O, P or H out of range");
+    if (p->unit_bytes < 1 || p->unit_bytes > (1 << 30))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: unit_bytes must be in [1, 2^30]");
+    const int64_t n[3] = {p->O, p->P, p->H};
+    for (int i = 0; i < 3; ++i)
+        if (p->stride[i] < 0 || (n[i] > 1 && p->stride[i] > (INT64_MAX >> 4) / n[i]))
+            return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: strides must be >= 0 and not too large");
+    const int64_t bytes = (int64_t)p->page * p->unit_bytes;
+    // segments, pages and outer entries that do not overlap: ordered by stride, each
+    // axis steps over the whole extent of the smaller ones
+    int order[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (p->stride[order[j]] < p->stride[order[i]]) {
+                const int t = order[i];
+                order[i] = order[j];
+                order[j] = t;
+            }
+    int64_t extent = bytes;
+    for (int i = 0; i < 3; ++i) {
+        const int k = order[i];
+        if (n[k] <= 1) continue;
+        if (p->stride[k] < extent) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: pages overlap");
+        extent += (n[k] - 1) * p->stride[k];
+    }
+    (void)cache;
+    return SPEC_OK;
+}
+
+static void cache_args(CacheArgs &a, const spec_cache_params *p, void *cache) {
+    a.cache = static_cast<char *>(cache);
+    a.unit = p->unit_bytes;
+    a.O = p->O;
+    a.P = p->P;
+    a.H = p->H;
+    a.page = p->page;
+    const int n[3] = {p->O, p->P, p->H};
+    for (int i = 0; i < 3; ++i) a.ss[i] = n[i] > 1 ? p->stride[i] : 0;
+}
+
+// the widest vector that every unit starts and ends on
+static int vec_bytes(const CacheArgs &a) {
+    const uint64_t bits = (uint64_t)(a.unit | a.ss[0] | a.ss[1] | a.ss[2]) | reinterpret_cast<uintptr_t>(a.cache);
+    return bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : bits % 2 == 0 ? 2 : 1;
+}
+
+template <typename Vec>
+static cudaError_t launch_copy(CacheArgs &a, int count, cudaStream_t st) {
+    constexpr int CP = 4;
+    const long long n = (long long)a.page * a.unit / (long long)sizeof(Vec), oh = (long long)a.O * a.H;
+    const long long gx = (n + NTC * CP - 1) / (NTC * CP);
+    const dim3 grid((unsigned)(gx < 1024 ? gx : 1024), (unsigned)(count < 65535 ? count : 65535),
+                    (unsigned)(oh < 65535 ? oh : 65535));
+    copy_kernel<Vec, CP><<<grid, NTC, 0, st>>>(a, count);
+    return cudaGetLastError();
+}
+
+template <typename Vec>
+static cudaError_t launch_compact(CacheArgs &a, cudaStream_t st) {
+    a.vecs = a.unit / (long long)sizeof(Vec);
+    const long long columns = (long long)a.O * a.H * a.vecs, gx = (columns + NTC - 1) / NTC;
+    const dim3 grid((unsigned)(gx < 65536 ? (gx > 0 ? gx : 1) : 65536), (unsigned)(a.B < 65535 ? a.B : 65535));
+    compact_kernel<Vec><<<grid, NTC, 0, st>>>(a);
+    return cudaGetLastError();
+}
+
+static int done(cudaError_t e) {
+    return e == cudaSuccess ? SPEC_OK : spec_internal_set_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
+}
+
+}  // namespace sr
+
+extern "C" int spec_pages_resize(const spec_pages_params *p, const int32_t *table, const int32_t *refs,
+                                 const int32_t *lengths, int32_t *out_table, int32_t *out_refs, int32_t *workspace,
+                                 int32_t *status, void *stream) {
+    using namespace sr;
+    const int rc = check_pages(p, false);
+    if (rc != SPEC_OK) return rc;
+    const int64_t rows = (int64_t)p->B * p->W, entries = rows * p->M;
+    if (entries == 0 && p->P == 0) return spec_internal_set_error(SPEC_OK, "");
+    if ((entries && (!table || !out_table || !lengths)) || (p->P && (!refs || !out_refs || !workspace)))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_resize: an argument is NULL");
+    const int64_t tb = entries * 4, rb = (int64_t)p->P * 4;
+    if ((out_table != table && overlap(out_table, tb, table, tb)) || (out_refs != refs && overlap(out_refs, rb, refs, rb)) ||
+        overlap(out_table, tb, out_refs, rb) || overlap(out_table, tb, refs, rb) || overlap(out_table, tb, lengths, rows * 4) ||
+        overlap(out_refs, rb, table, tb) || overlap(out_refs, rb, lengths, rows * 4) || overlap(workspace, rb, table, tb) ||
+        overlap(workspace, rb, refs, rb) || overlap(workspace, rb, lengths, rows * 4) || overlap(workspace, rb, out_table, tb) ||
+        overlap(workspace, rb, out_refs, rb))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_resize: arguments overlap");
+    spec_internal_set_error(SPEC_OK, "");
+    PagesArgs a{};
+    a.table = table;
+    a.refs = refs;
+    a.lengths = lengths;
+    a.out_table = out_table;
+    a.out_refs = out_refs;
+    a.list = workspace;
+    a.status = status;
+    a.B = p->B;
+    a.W = p->W;
+    a.N = p->N;
+    a.M = p->M;
+    a.P = p->P;
+    a.page = p->page;
+    const int C = pages_cluster(entries + p->P);
+    return done(launch_cluster(resize_kernel, C, NTP, C, 0, static_cast<cudaStream_t>(stream), a, C));
+}
+
+extern "C" int spec_pages_fork(const spec_pages_params *p, const int32_t *table, const int32_t *refs,
+                               const int32_t *lengths, const int32_t *parent, int32_t *out_table, int32_t *out_refs,
+                               int32_t *out_lengths, int32_t *copies, int32_t *workspace, int32_t *status,
+                               void *stream) {
+    using namespace sr;
+    const int rc = check_pages(p, true);
+    if (rc != SPEC_OK) return rc;
+    const int64_t rows = (int64_t)p->B * p->W, out_rows = (int64_t)p->B * p->N;
+    if (rows == 0 && out_rows == 0 && p->P == 0) return spec_internal_set_error(SPEC_OK, "");
+    if ((rows * p->M && !table) || (rows && !lengths) || (out_rows * p->M && !out_table) ||
+        (out_rows && (!parent || !out_lengths || !copies)) || (p->P && (!refs || !out_refs || !workspace)))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_fork: an argument is NULL");
+    const int64_t rb = (int64_t)p->P * 4;
+    const void *in[4] = {table, lengths, parent, refs};
+    const int64_t in_bytes[4] = {rows * p->M * 4, rows * 4, out_rows * 4, rb};
+    const void *out[5] = {out_table, out_lengths, copies, workspace, out_refs};
+    const int64_t out_bytes[5] = {out_rows * p->M * 4, out_rows * 4, out_rows * 16, 2 * rb, rb};
+    for (int i = 0; i < 5; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlap(out[i], out_bytes[i], in[j], in_bytes[j]) && !(i == 4 && j == 3 && out_refs == refs))
+                return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_fork: an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (overlap(out[i], out_bytes[i], out[j], out_bytes[j]))
+                return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_fork: outputs overlap");
+    }
+    spec_internal_set_error(SPEC_OK, "");
+    PagesArgs a{};
+    a.table = table;
+    a.refs = refs;
+    a.lengths = lengths;
+    a.parent = parent;
+    a.out_table = out_table;
+    a.out_refs = out_refs;
+    a.out_lengths = out_lengths;
+    a.copies = copies;
+    a.list = workspace;
+    a.claim = workspace + p->P;
+    a.status = status;
+    a.B = p->B;
+    a.W = p->W;
+    a.N = p->N;
+    a.M = p->M;
+    a.P = p->P;
+    a.page = p->page;
+    const int C = pages_cluster((rows + out_rows) * p->M + p->P);
+    return done(launch_cluster(fork_kernel, C, NTP, C, 0, static_cast<cudaStream_t>(stream), a, C));
+}
+
+extern "C" int spec_pages_copy(const spec_cache_params *p, void *cache, const int32_t *copies, int32_t count,
+                               void *stream) {
+    using namespace sr;
+    const int rc = check_cache(p, cache);
+    if (rc != SPEC_OK) return rc;
+    if (count < 0) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_copy: count must be >= 0");
+    if (count == 0 || p->O == 0 || p->H == 0 || p->P == 0) return spec_internal_set_error(SPEC_OK, "");
+    if (!cache || !copies) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_copy: cache or copies is NULL");
+    spec_internal_set_error(SPEC_OK, "");
+    CacheArgs a{};
+    cache_args(a, p, cache);
+    a.copies = copies;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (vec_bytes(a)) {
+        case 16: return done(launch_copy<uint4>(a, count, st));
+        case 4: return done(launch_copy<uint32_t>(a, count, st));
+        case 2: return done(launch_copy<uint16_t>(a, count, st));
+        default: return done(launch_copy<uint8_t>(a, count, st));
+    }
+}
+
+extern "C" int spec_pages_compact(const spec_cache_params *p, void *cache, int32_t B, int32_t N, int32_t M,
+                                  const int32_t *table, const int32_t *lengths, const int32_t *path,
+                                  int32_t *out_lengths, int32_t *status, void *stream) {
+    using namespace sr;
+    const int rc = check_cache(p, cache);
+    if (rc != SPEC_OK) return rc;
+    if (B < 0 || M < 0) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_compact: B and M must be >= 0");
+    if (B > SPEC_MAX_B || N < 1 || N > SPEC_MAX_NODES || (int64_t)M * p->page > INT32_MAX - SPEC_MAX_NODES)
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "pages_compact: B, N or M out of range");
+    if (B == 0) return spec_internal_set_error(SPEC_OK, "");
+    if (!lengths || !path || !out_lengths || (M && !table) || (p->O && p->H && p->P && !cache))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_compact: an argument is NULL");
+    if (overlap(out_lengths, B * 4LL, lengths, B * 4LL) || overlap(out_lengths, B * 4LL, path, (int64_t)B * N * 4) ||
+        overlap(out_lengths, B * 4LL, table, (int64_t)B * M * 4))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_compact: out_lengths overlaps an input");
+    spec_internal_set_error(SPEC_OK, "");
+    CacheArgs a{};
+    cache_args(a, p, cache);
+    a.table = table;
+    a.lengths = lengths;
+    a.path = path;
+    a.out_lengths = out_lengths;
+    a.status = status;
+    a.B = B;
+    a.N = N;
+    a.M = M;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    switch (vec_bytes(a)) {
+        case 16: return done(launch_compact<uint4>(a, st));
+        case 4: return done(launch_compact<uint32_t>(a, st));
+        case 2: return done(launch_compact<uint16_t>(a, st));
+        default: return done(launch_compact<uint8_t>(a, st));
+    }
+}
+
+extern "C" int spec_tree_accept(int32_t B, int32_t N, const int32_t *tokens, const int32_t *parents,
+                                int64_t parents_stride, const int32_t *choice, int64_t choice_batch_stride,
+                                int64_t choice_node_stride, const int32_t *counts, int32_t *accepted_len,
+                                int32_t *out_tokens, int32_t *path, int32_t *status, void *stream) {
+    using namespace sr;
+    if (B < 0) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: B must be >= 0");
+    if (B > SPEC_MAX_B || N < 1 || N > SPEC_MAX_NODES)
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "tree_accept: B or N out of range");
+    if (parents && parents_stride != 0 && parents_stride < N)
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: parents_stride must be 0 or >= N");
+    if (choice_batch_stride < 0 || choice_node_stride < 0 || choice_batch_stride > (INT64_MAX >> 4) / (B + 1) ||
+        choice_node_stride > (INT64_MAX >> 12) || parents_stride > (INT64_MAX >> 4) / (B + 1))
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: strides must be >= 0 and not too large");
+    if (B == 0) return spec_internal_set_error(SPEC_OK, "");
+    if (!tokens || !choice || !accepted_len || !out_tokens || !path)
+        return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: an argument is NULL");
+    spec_internal_set_error(SPEC_OK, "");
+    const AcceptArgs a{tokens, parents, choice, counts, accepted_len, out_tokens, path, status,
+                       parents_stride, choice_batch_stride, choice_node_stride, B, N};
+    const unsigned grid = (unsigned)((B + NTA / 32 - 1) / (NTA / 32));
+    accept_kernel<<<grid, NTA, 0, static_cast<cudaStream_t>(stream)>>>(a);
+    return done(cudaGetLastError());
+}
