@@ -43,7 +43,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=(), checked: b
     path."""
     srcs = [os.path.join(_CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(_CSRC, "spec_device.cuh"), os.path.join(_CSRC, "spec_nucleus.cuh"),
-            os.path.join(_CSRC, "spec_rows.cuh"), os.path.join(_CSRC, "spec_top.cuh"),
+            os.path.join(_CSRC, "spec_rows.cuh"), os.path.join(_CSRC, "spec_top.cuh"), os.path.join(_CSRC, "spec_tc.cuh"),
             os.path.join(_INCLUDE, "spec_verify.h")]
     targets = [(LIB_PATH, [])] + ([(CHECKED_LIB_PATH, ["-DSPEC_CHECKED"])] if checked else [])
     newest = max(os.path.getmtime(d) for d in deps)

@@ -1,19 +1,57 @@
 // spec_attend.cu -- attention of a tree's nodes over a cache held in pages.
+//
+// Rows. The query rows of one key head's group, (node, head) in node order, fill
+// tiles of 128 rows: floor(128 / G) nodes each. S = Q K^T (128 rows x 128
+// keys) and O += P V run on the tensor cores with S, P and O in tensor memory;
+// a thread owns a row of S and keeps its running maximum and sum.
+//
+// Streams. A CTA has two streams, each with an S, an O and a warpgroup for the
+// softmax, so that one multiplies while the other exponentiates. A group of one tile
+// gives the streams every other tile of keys and merges them at the end; two
+// tiles of rows get a stream each and share the keys.
+//
+// Work. All tiles of keys of all (sequence, head, pair of row tiles) stand in one line that is
+// cut into equal parts, one per CTA, from lengths that only the GPU knows; a
+// part's ends may lie inside a sequence. Those pieces go to the workspace unnormalised, and a
+// second kernel joins them.
+//
+// What a row must not see. Keys behind the context are masked by a bit per node. A
+// probability of 0 does not stop a NaN value, so a warp of its own looks at the values behind the
+// context before they are multiplied: slots that no node owns become 0, and of the nodes' own values the NaN and infinities
+// do, and are added back at the end to the rows that see them.
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cfloat>
+#include <cmath>
+#include <mutex>
+
 #include "spec_rows.cuh"
+#include "spec_tc.cuh"
 
 namespace sr {
 
+constexpr int kTile = 128;             // keys a tile, and rows a tile
+constexpr int kChunk = kTile * 128;    // bytes of 64 elements of a tile's rows
+constexpr int kNT = 384;               // copies, products, values' check, idle; two softmax warpgroups
+constexpr unsigned kSpin = 1u << 20;   // polls of a wait before it gives up
+constexpr int kSegRing = 8;            // segments whose flags of non-finite values are kept
+constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
+
 struct AttendArgs {
-    const void *q, *k, *v;
+    const void *v;
     const int32_t *table, *lengths, *parents, *counts;
     void *out;
     float *lse;
     int32_t *status;
-    int B, N, Hq, Hkv, G, D, P, page, M;
-    float sL;   // scale log2 e
-    long long qs[3], ks[3], vs[3], ps;
+    float *part_o;    // [CTA][2][tile][row][D padded]: unnormalised outputs of a sequence's pieces
+    float2 *part_ml;  // [CTA][2][tile][row]: their reference (log2) and sum
+    int4 *joins;      // [CTA]: sequence (-1: none), head, pair of tiles, last CTA of what begins here and ends elsewhere
+    int B, N, Hq, Hkv, G, D, P, page, M, fill;
+    int nodes;        // a tile
+    float sL;         // |scale| log2 e
+    int neg;          // scale < 0
+    long long vs[3], ps;
 };
 
 // What a sequence holds: tokens before the nodes, and nodes.
@@ -46,59 +84,633 @@ __device__ __forceinline__ int parent_of(const AttendArgs &a, int b, int n) {
 }
 
 template <typename T>
-__device__ __forceinline__ float to_f(T x);
+struct Half;
 template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <>
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-template <typename T>
-__device__ __forceinline__ T from_f(float x);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ __half from_f(float x) { return __float2half_rn(x); }
-
-// A warp per row (b, n, h); lane l holds elements 4 l .. 4 l + 3. One key after
-// another, with the running maximum and sum of a softmax.
-template <typename T>
-__global__ void __launch_bounds__(128) attend_simple_kernel(AttendArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (row >= (long long)a.B * a.N * a.Hq) return;
-    const int h = (int)(row % a.Hq), n = (int)(row / a.Hq % a.N), b = (int)(row / a.Hq / a.N), hk = h / a.G;
-    int L, count;
-    sequence(a, b, L, count);
-    const bool mine = 4 * lane < a.D;
-    const T *q = static_cast<const T *>(a.q) + b * a.qs[0] + n * a.qs[1] + h * a.qs[2] + 4 * lane;
-    float x[4] = {0, 0, 0, 0}, o[4] = {0, 0, 0, 0}, m = neg_inf(), l = 0.f;
-    if (mine)
-        for (int i = 0; i < 4; ++i) x[i] = to_f(q[i]);
-    auto see = [&](int t) {
-        const int p = a.table[(long long)b * a.M + t / a.page];
-        if (p < 0 || p >= a.P) {
-            raise_status(a.status, SPEC_ERR_BAD_PAGE);
-            return;
-        }
-        const int slot = t % a.page;
-        const T *k = static_cast<const T *>(a.k) + p * a.ks[0] + slot * a.ks[1] + hk * a.ks[2] + 4 * lane;
-        const T *v = static_cast<const T *>(a.v) + p * a.vs[0] + slot * a.vs[1] + hk * a.vs[2] + 4 * lane;
-        float s = 0.f;
-        if (mine)
-            for (int i = 0; i < 4; ++i) s += x[i] * to_f(k[i]);
-        s = warp_sum(s) * a.sL;
-        const float mx = fmaxf(m, s), w = ex2(s - mx), keep = ex2(m - mx);
-        l = l * keep + w;
-        m = mx;
-        if (mine)
-            for (int i = 0; i < 4; ++i) o[i] = o[i] * keep + w * to_f(v[i]);
-    };
-    if (n < count) {
-        for (int t = 0; t < L; ++t) see(t);
-        for (int j = n; j >= 0; j = parent_of(a, b, j)) see(L + j);
+struct Half<__nv_bfloat16> {
+    static constexpr int kBf16 = 1;
+    static constexpr uint32_t kExp = 0x7f80;
+    __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
     }
-    T *out = static_cast<T *>(a.out) + row * a.D + 4 * lane;
-    if (mine)
-        for (int i = 0; i < 4; ++i) out[i] = from_f<T>(l != 0.f ? o[i] / l : 0.f);
+    __device__ static __forceinline__ float value(uint32_t h) { return __uint_as_float(h << 16); }
+};
+template <>
+struct Half<__half> {
+    static constexpr int kBf16 = 0;
+    static constexpr uint32_t kExp = 0x7c00;
+    __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    __device__ static __forceinline__ float value(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
+};
+
+// One piece of a CTA's work: tiles [t0, t1) of `tiles` of (b, h, pair).
+struct Segment {
+    int b, h, pair, t0, t1, tiles, L, count, act;
+    long long left;   // units of the pair from t0 on
+    __device__ __forceinline__ int jobs() const { return act == 2 ? 2 * (t1 - t0) : t1 - t0; }
+    __device__ __forceinline__ int keys(int t) const { return min(kTile, L + count - t * kTile); }
+    __device__ __forceinline__ bool tail(int t) const { return (t + 1) * kTile > L; }
+    // the tile and the stream of a job
+    __device__ __forceinline__ int tile(int j) const { return t0 + (act == 2 ? j >> 1 : j); }
+};
+
+// Every role walks the CTA's segments by itself.
+struct Walk {
+    int b;
+    long long off, left;
+    __device__ __forceinline__ bool next(const AttendArgs &a, Segment &s) {
+        while (left > 0) {
+            sequence(a, b, s.L, s.count);
+            const int pairs = (s.count + 2 * a.nodes - 1) / (2 * a.nodes);
+            s.tiles = (s.L + s.count + kTile - 1) / kTile;
+            const long long head = (long long)pairs * s.tiles, all = head * a.Hkv;
+            if (off >= all) {
+                off -= all;
+                ++b;
+                continue;
+            }
+            s.b = b;
+            s.h = (int)(off / head);
+            const long long in = off - s.h * head;
+            s.pair = (int)(in / s.tiles);
+            s.t0 = (int)(in - (long long)s.pair * s.tiles);
+            s.left = s.tiles - s.t0;
+            s.t1 = s.t0 + (int)min(s.left, left);
+            s.act = s.count - s.pair * 2 * a.nodes > a.nodes ? 2 : 1;
+            off += s.t1 - s.t0;
+            left -= s.t1 - s.t0;
+            return true;
+        }
+        return false;
+    }
+};
+
+template <int DC>
+struct AttendSmem {
+    static constexpr int kStage = DC * kChunk;
+    static constexpr int kStages = DC == 2 ? 5 : 10;
+    static constexpr int kQ = 2 * kStage;
+    static constexpr int kTiles = kQ + kStages * kStage;
+};
+
+struct AttendBars {
+    uint64_t full[10], empty[10], fixed[10], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, o_free, merge, drain;
+};
+
+// behind the tiles in shared memory
+struct AttendShared {
+    AttendBars bars;
+    float2 ml[2][kTile];
+    long long sum[kNT / 32], off;
+    uint32_t tmem, bad[kSegRing][4];
+    int abort, b0;
+};
+
+template <typename T, int DC>
+__global__ void __launch_bounds__(kNT, 1)
+    attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
+                  const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int box) {
+    using SM = AttendSmem<DC>;
+    constexpr int S = SM::kStages, DP = DC * 64;
+    extern __shared__ __align__(1024) char dyn[];   // (the kernel has no other shared memory, so that this holds)
+    AttendShared &sh = *reinterpret_cast<AttendShared *>(dyn + SM::kTiles);
+    AttendBars &bars = sh.bars;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t base = tc::smem(dyn), ring = base + SM::kQ;
+
+    // ---- which part of the line is this CTA's ----------------------------------------
+    const int G = gridDim.x, me = blockIdx.x;
+    const int per_thread = (a.B + kNT - 1) / kNT;
+    const int b_lo = min(a.B, (int)threadIdx.x * per_thread), b_hi = min(a.B, b_lo + per_thread);
+    auto units = [&](int b) -> long long {
+        int L, count;
+        sequence(a, b, L, count);
+        return (long long)a.Hkv * ((count + 2 * a.nodes - 1) / (2 * a.nodes)) * ((L + count + kTile - 1) / kTile);
+    };
+    long long mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += units(b);
+    long long upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const long long v = __shfl_up_sync(kFull, upto, o);
+        if (lane >= o) upto += v;
+    }
+    if (lane == 31) sh.sum[warp] = upto;
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        sh.b0 = a.B;
+        sh.off = 0;
+        for (int i = 0; i < S; ++i) {
+            tc::bar_init(tc::smem(&bars.full[i]), 1);
+            tc::bar_init(tc::smem(&bars.empty[i]), 2);   // the products and the values' check
+            tc::bar_init(tc::smem(&bars.fixed[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(tc::smem(&bars.s_full[i]), 1);
+            tc::bar_init(tc::smem(&bars.p_ready[i]), 4);
+            tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
+        }
+        tc::bar_init(tc::smem(&bars.q_full), 1);
+        tc::bar_init(tc::smem(&bars.q_empty), 1);
+        tc::bar_init(tc::smem(&bars.o_free), 8);
+        tc::bar_init(tc::smem(&bars.merge), 8);
+        tc::bar_init(tc::smem(&bars.drain), 1);
+        tc::fence_barrier_init();
+    }
+    if (warp == 1) tc::tmem_alloc(tc::smem(&sh.tmem), 512);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    long long total = 0;
+    for (int w = 0; w < kNT / 32; ++w) {
+        if (w < warp) upto += sh.sum[w];
+        total += sh.sum[w];
+    }
+    const long long per = (total + G - 1) / G, u0 = min(total, me * per), u1 = min(total, u0 + per);
+    if (u0 < u1 && u0 >= upto - mine && u0 < upto) {   // the thread whose sequences hold u0
+        long long at = upto - mine;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const long long n = units(b);
+            if (u0 < at + n) {
+                sh.b0 = b;
+                sh.off = u0 - at;
+                break;
+            }
+            at += n;
+        }
+    }
+    if (a.fill) {   // rows of nodes that do not exist
+        const long long rows = (long long)a.B * a.N * a.Hq;
+        for (long long r = (long long)me * kNT + threadIdx.x; r < rows; r += (long long)G * kNT) {
+            const int b = (int)(r / ((long long)a.N * a.Hq)), n = (int)(r / a.Hq % a.N);
+            int L, count;
+            sequence(a, b, L, count);
+            if (n < count) continue;
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + r * a.D);
+            for (int i = 0; i < a.D / 8; ++i) o[i] = make_uint4(0, 0, 0, 0);
+            if (a.lse) a.lse[r] = neg_inf();
+        }
+    }
+    __syncthreads();
+    Walk walk{sh.b0, sh.off, u1 - u0};
+    Segment s;
+    const uint32_t tmem = sh.tmem;
+    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + DP};
+    constexpr uint32_t kIdS = tc::shape(Half<T>::kBf16, kTile, false), kIdO = tc::shape(Half<T>::kBf16, DP, true);
+
+    // A wait that gives up: the CTA's other waits then do, too.
+    auto wait = [&](const uint64_t *bar, uint32_t parity) -> bool {
+        const uint32_t addr = tc::smem(bar);
+        for (unsigned i = 0; i < kSpin; ++i) {
+            if (tc::bar_try(addr, parity)) return true;
+            if (*(volatile int *)&sh.abort) return false;
+        }
+        *(volatile int *)&sh.abort = 1;
+        raise_status(a.status, SPEC_ERR_TIMEOUT);
+        return false;
+    };
+    auto wait_warp = [&](const uint64_t *bar, uint32_t parity) -> bool {
+        const bool ok = wait(bar, parity);
+        return __all_sync(kFull, ok);
+    };
+
+    if (warp == 0) {
+        // ---- copies: keys two jobs ahead of the values ---------------------------------
+        unsigned n = 0, segs = 0;
+        bool ok = true;
+        if (lane == 0) {
+            tc::prefetch_map(&qmap);
+            tc::prefetch_map(&kmap);
+            tc::prefetch_map(&vmap);
+        }
+        auto tile = [&](const CUtensorMap *map, int t) {
+            const int st = n % S;
+            if (n >= S && !wait_warp(&bars.empty[st], (n / S + 1) & 1)) return false;
+            const int keys = s.keys(t), boxes = (keys + box - 1) / box, at0 = t * kTile;
+            const uint32_t bar = tc::smem(&bars.full[st]), dst = ring + st * SM::kStage;
+            if (lane == 0) tc::bar_expect(bar, (uint32_t)boxes * box * 128 * DC);
+            __syncwarp();
+            for (int i = lane; i < boxes * DC; i += 32) {
+                const int bx = DC == 2 ? i >> 1 : i, c = DC == 2 ? i & 1 : 0, key = at0 + bx * box;
+                int p = a.table[(long long)s.b * a.M + key / a.page];
+                if (p < 0 || p >= a.P) {
+                    raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                    p = -1;   // (the copy fills zeros)
+                }
+                tc::load_tile(dst + c * kChunk + bx * box * 128, map, bar, c * 64, s.h, key % a.page, p);
+            }
+            ++n;
+            return true;
+        };
+        while (ok && walk.next(a, s)) {
+            const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
+            for (int t = 0; ok && t < min(nt, ahead); ++t) ok = tile(&kmap, s.t0 + t);
+            if (!ok || (segs > 0 && !wait_warp(&bars.q_empty, (segs + 1) & 1))) break;
+            if (lane == 0) {
+                const uint32_t bar = tc::smem(&bars.q_full);
+                tc::bar_expect(bar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
+                for (int m = 0; m < s.act; ++m)
+                    for (int c = 0; c < DC; ++c)
+                        tc::load_tile(base + m * SM::kStage + c * kChunk, &qmap, bar, c * 64, s.h * a.G, (2 * s.pair + m) * a.nodes, s.b);
+            }
+            __syncwarp();
+            ++segs;
+            for (int t = 0; ok && t < nt; ++t) {
+                ok = tile(&vmap, s.t0 + t);
+                if (ok && t + ahead < nt) ok = tile(&kmap, s.t0 + t + ahead);
+            }
+        }
+        // nothing is left in flight when another role has given up
+        if (*(volatile int *)&sh.abort) {
+            for (unsigned i = n > S ? n - S : 0; i < n; ++i)
+                for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.full[i % S]), (i / S) & 1); ++k) {}
+            if (segs > 0)
+                for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full), (segs + 1) & 1); ++k) {}
+        }
+    } else if (warp == 1) {
+        // ---- products ---------------------------------------------------------------------
+        if (lane == 0) {
+            unsigned n = 0, segs = 0, done[2] = {0, 0};
+            uint32_t fixed = 0;   // per stage: parity of the next wait for checked values
+            bool ok = true;
+            while (ok && walk.next(a, s)) {
+                const int jobs = s.jobs(), nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
+                // the position of a tile's keys and values in the order of copies
+                const unsigned n0 = n;
+                auto kpos = [&](int t) { return n0 + (t < ahead ? t : ahead + 2 * (t - ahead) + 1); };
+                auto vpos = [&](int t) { return n0 + (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t); };
+                auto scores = [&](int j) -> bool {
+                    const int g = j & 1, t = s.tile(j) - s.t0;
+                    const unsigned at = kpos(t);
+                    if ((s.act == 1 || g == 0) && !wait(&bars.full[at % S], (at / S) & 1)) return false;
+                    tc::fence_after();
+                    const uint32_t q = base + (s.act == 2 ? g * SM::kStage : 0), k = ring + (at % S) * SM::kStage;
+#pragma unroll
+                    for (int i = 0; i < DC * 4; ++i) {
+                        const uint32_t o = (i >> 2) * kChunk + (i & 3) * 32;
+                        tc::mma_ss(tS[g], tc::operand(q + o, 16), tc::operand(k + o, 16), kIdS, i > 0);
+                    }
+                    tc::commit(tc::smem(&bars.s_full[g]));
+                    if (s.act == 1 || g == 1) tc::commit(tc::smem(&bars.empty[at % S]));
+                    return true;
+                };
+                if (!wait(&bars.q_full, segs & 1)) break;
+                for (int j = 0; ok && j < min(jobs, 2); ++j) ok = scores(j);
+                if (ok && jobs <= 2) tc::commit(tc::smem(&bars.q_empty));
+                for (int j = 0; ok && j < jobs; ++j) {
+                    const int g = j & 1, t = s.tile(j) - s.t0;
+                    const unsigned at = vpos(t), st = at % S;
+                    if (s.act == 1 || g == 0) {
+                        ok = wait(&bars.full[st], (at / S) & 1);
+                        if (ok && s.tail(s.tile(j))) {
+                            ok = wait(&bars.fixed[st], fixed >> st & 1);
+                            fixed ^= 1u << st;
+                        }
+                        if (!ok) break;
+                    }
+                    if (j == 0 && segs > 0 && !(ok = wait(&bars.o_free, (segs + 1) & 1))) break;
+                    if (!(ok = wait(&bars.p_ready[g], done[g] & 1))) break;
+                    tc::fence_after();
+                    const uint32_t v = ring + st * SM::kStage;
+                    const int steps = (s.keys(s.tile(j)) + 15) / 16;
+                    for (int i = 0; i < steps; ++i)
+                        tc::mma_ts(tO[g], tS[g] + i * 8, tc::operand(v + i * 2048, kChunk), kIdO, j >= 2 || i > 0);
+                    tc::commit(tc::smem(&bars.pv_done[g]));
+                    if (s.act == 1 || g == 1) tc::commit(tc::smem(&bars.empty[st]));
+                    ++done[g];
+                    if (j + 2 < jobs) {
+                        ok = scores(j + 2);
+                        if (ok && j + 3 == jobs) tc::commit(tc::smem(&bars.q_empty));
+                    }
+                }
+                n = n0 + 2 * nt;
+                ++segs;
+            }
+            // (none of the products may still run when the CTA ends)
+            tc::commit(tc::smem(&bars.drain));
+            for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.drain), 0); ++k) {}
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ---- values behind the context -----------------------------------------------------
+        unsigned n = 0, segs = 0;
+        int4 join = make_int4(-1, 0, 0, 0);
+        long long at_unit = u0;
+        bool ok = true;
+        while (ok && walk.next(a, s)) {
+            const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
+            if (s.t0 == 0 && s.t1 < s.tiles) join = make_int4(s.b, s.h, s.pair, (int)((at_unit + s.tiles - 1) / per));
+            at_unit += nt;
+            bool first = true;
+            uint32_t *bad = sh.bad[segs % kSegRing];
+            // every tile is waited for and given back in the order of the copies, so that no barrier is
+            // ever two phases ahead of this warp or behind it
+            for (int x = 0; ok && x < 2 * nt; ++x, ++n) {
+                const unsigned st = n % S;
+                if (!(ok = wait_warp(&bars.full[st], (n / S) & 1))) break;
+                const int v = x < min(nt, ahead) ? -1 : x - min(nt, ahead), lag = nt - min(nt, ahead);
+                // values and keys take turns while there are keys left
+                const int t = v < 0 ? -1 : v < 2 * lag ? (v & 1 ? -1 : v >> 1) : v - lag;
+                if (t < 0 || !s.tail(s.t0 + t)) {
+                    if (lane == 0) tc::bar_arrive(tc::smem(&bars.empty[st]));
+                    continue;
+                }
+                if (first && lane < 4) bad[lane] = 0;
+                first = false;
+                __syncwarp();
+                const int at0 = (s.t0 + t) * kTile, keys = s.keys(s.t0 + t), lo = max(0, s.L - at0);
+                char *stage = dyn + SM::kQ + st * SM::kStage;
+                const int rows = ((keys + 15) & ~15) - lo;   // up to the last product's end
+                for (int i = lane; i < rows * DC * 8; i += 32) {
+                    const int r = lo + i / (DC * 8), x = i % (DC * 8);
+                    uint4 *p = reinterpret_cast<uint4 *>(stage + (x >> 3) * kChunk + r * 128 + (x & 7) * 16);
+                    if (r >= keys) {
+                        *p = make_uint4(0, 0, 0, 0);
+                        continue;
+                    }
+                    uint4 w = *p;
+                    uint32_t *u = &w.x;
+                    bool hit = false;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if ((u[e] & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0xffff0000u, hit = true;
+                        if ((u[e] >> 16 & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0x0000ffffu, hit = true;
+                    }
+                    if (hit) {
+                        *p = w;
+                        const int node = at0 + r - s.L;
+                        atomicOr(&bad[node >> 5], 1u << (node & 31));
+                    }
+                }
+                tc::fence_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tc::bar_arrive(tc::smem(&bars.fixed[st]));
+                    tc::bar_arrive(tc::smem(&bars.empty[st]));
+                }
+            }
+            ++segs;
+        }
+        if (lane == 0) a.joins[me] = join;
+    } else if (warp >= 4) {
+        // ---- softmax: a stream each, a row a thread ------------------------------------------
+        const int g = (warp - 4) >> 2, r = threadIdx.x & 127;
+        const uint32_t row_lane = (uint32_t)(warp & 3) << 21;   // (lane of tensor memory in bits 16 and up)
+        const uint32_t mS = tS[g] + row_lane;
+        unsigned segs = 0, merges = 0, jobs_of[2] = {0, 0};   // jobs of both streams so far
+        bool ok = true;
+        while (ok && walk.next(a, s)) {
+            const int jobs = s.jobs();
+            // what this row sees of the nodes
+            const int tile0 = 2 * s.pair + (s.act == 2 ? g : 0), node = tile0 * a.nodes + r / a.G;
+            const bool real = r < a.nodes * a.G && node < s.count;
+            uint32_t v0 = 0, v1 = 0, v2 = 0, v3 = 0;
+            if (real && s.tail(s.t1 - 1)) {
+                for (int j = node; j >= 0; j = parent_of(a, s.b, j)) {
+                    const uint32_t bit = 1u << (j & 31);
+                    const int w = j >> 5;
+                    if (w == 0) v0 |= bit;
+                    else if (w == 1) v1 |= bit;
+                    else if (w == 2) v2 |= bit;
+                    else v3 |= bit;
+                }
+            }
+            float m = neg_inf(), l = 0.f;
+            for (int j = g; j < jobs; j += 2) {
+                if (!(ok = wait_warp(&bars.s_full[g], jobs_of[g] & 1))) break;
+                tc::fence_after();
+                float x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::tmem_load(mS + c * 32, x[c]);
+                tc::tmem_wait_load();
+                if (a.neg)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[c][i] = -x[c][i];
+                const int t = s.tile(j);
+                if (s.tail(t)) {
+                    const int d = t * kTile - s.L;   // node of the tile's first key
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int at = d + 32 * c, w = at >> 5;
+                        auto word = [&](int k) -> uint32_t {
+                            return k < 0 ? ~0u : k == 0 ? v0 : k == 1 ? v1 : k == 2 ? v2 : k == 3 ? v3 : 0u;
+                        };
+                        const uint32_t see = __funnelshift_r(word(w), word(w + 1), at & 31);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) x[c][i] = see >> i & 1 ? x[c][i] : neg_inf();
+                    }
+                }
+                float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[c][i]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sL;
+                const bool move = top > m + kLazy;
+                if (__any_sync(kFull, move)) {
+                    const float to = move ? top : m, keep = move ? ex2(m - to) : 1.f;
+                    m = to;
+                    l *= keep;
+                    if (j >= 2) {   // the output so far
+                        if (!(ok = wait_warp(&bars.pv_done[g], (jobs_of[g] + 1) & 1))) break;
+                        tc::fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < DP / 32; ++c) {
+                            float o[32];
+                            tc::tmem_load(tO[g] + row_lane + c * 32, o);
+                            tc::tmem_wait_load();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) o[i] *= keep;
+                            tc::tmem_store(tO[g] + row_lane + c * 32, o);
+                        }
+                        tc::tmem_wait_store();
+                    }
+                }
+                const float ref = m == neg_inf() ? 0.f : m;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t p[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        const float e0 = ex2(fmaf(x[c][i], a.sL, -ref)), e1 = ex2(fmaf(x[c][i + 1], a.sL, -ref));
+                        sum[i & 2] += e0;
+                        sum[(i & 2) + 1] += e1;
+                        p[i / 2] = Half<T>::pack(e0, e1);
+                    }
+                    tc::tmem_store16(mS + c * 16, p);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tc::tmem_wait_store();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
+                ++jobs_of[g];
+            }
+            if (!ok) break;
+            jobs_of[g ^ 1] += (jobs + (g ^ 1 ? 0 : 1)) / 2;   // the other stream's jobs: ceil for stream 0, floor for 1
+            // ---- the segment's output ---------------------------------------------------------
+            const bool two = s.act == 2, both = !two && jobs > 1;
+            if (both || two || g == 0) {
+                if (!(ok = wait_warp(&bars.pv_done[g], (jobs_of[g] + 1) & 1))) break;
+            }
+            if (!two) {
+                if ((g == 1 || both) && !(ok = wait_warp(&bars.pv_done[g ^ 1], (jobs_of[g ^ 1] + 1) & 1))) break;
+                sh.ml[g][r] = make_float2(m, l);
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.merge));
+                if (!(ok = wait_warp(&bars.merge, merges++ & 1))) break;
+            }
+            tc::fence_after();
+            // one tile: both warpgroups take half of the columns of both streams' outputs
+            float w0 = 1.f, w1 = 0.f;
+            if (!two) {
+                const float2 m0 = sh.ml[0][r], m1 = sh.ml[1][r];
+                m = fmaxf(m0.x, m1.x);
+                const float ref = m == neg_inf() ? 0.f : m;
+                w0 = ex2(m0.x - ref);
+                w1 = both ? ex2(m1.x - ref) : 0.f;
+                l = m0.y * w0 + (both ? m1.y * w1 : 0.f);
+            }
+            const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+            const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
+            w0 *= inv;
+            w1 *= inv;
+            uint32_t bad[4] = {0, 0, 0, 0};
+            if (s.t1 == s.tiles) {
+                const uint32_t *f = sh.bad[segs % kSegRing];
+                bad[0] = f[0] & v0;
+                bad[1] = f[1] & v1;
+                bad[2] = f[2] & v2;
+                bad[3] = f[3] & v3;
+            }
+            const bool spoilt = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
+            const int c0 = two ? 0 : g * (DP / 64), c1 = two ? DP / 32 : c0 + DP / 64;
+            const int hq = s.h * a.G + r % a.G;
+            const long long row = ((long long)s.b * a.N + node) * a.Hq + hq;
+            const long long slot = ((long long)me * 2 + (s.t0 == 0 ? 1 : 0)) * 2 + (two ? g : 0);
+#pragma unroll 1
+            for (int c = c0; c < c1; ++c) {
+                float o[32];
+                tc::tmem_load(tO[two ? g : 0] + row_lane + c * 32, o);
+                tc::tmem_wait_load();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] *= w0;
+                if (both) {
+                    float q[32];
+                    tc::tmem_load(tO[1] + row_lane + c * 32, q);
+                    tc::tmem_wait_load();
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = fmaf(q[i], w1, o[i]);
+                }
+                if (!real) continue;
+                if (spoilt) {
+#pragma unroll 1
+                    for (int j = 0; j < a.N; ++j) {
+                        const uint32_t bits = j < 32 ? bad[0] : j < 64 ? bad[1] : j < 96 ? bad[2] : bad[3];
+                        if (!(bits >> (j & 31) & 1)) continue;
+                        const int key = s.L + j, p = a.table[(long long)s.b * a.M + key / a.page];
+                        if (p < 0 || p >= a.P) continue;
+                        const unsigned short *v = static_cast<const unsigned short *>(a.v) + p * a.vs[0] + key % a.page * a.vs[1] +
+                                                  s.h * a.vs[2] + c * 32;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i < a.D && (v[i] & Half<T>::kExp) == Half<T>::kExp) o[i] += Half<T>::value(v[i]);
+                    }
+                }
+                if (whole) {
+                    uint4 *to = reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * a.D + c * 32);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c * 32 + i * 8 < a.D)
+                            to[i] = make_uint4(Half<T>::pack(o[8 * i], o[8 * i + 1]), Half<T>::pack(o[8 * i + 2], o[8 * i + 3]),
+                                               Half<T>::pack(o[8 * i + 4], o[8 * i + 5]), Half<T>::pack(o[8 * i + 6], o[8 * i + 7]));
+                } else {
+                    float4 *to = reinterpret_cast<float4 *>(a.part_o + (slot * kTile + r) * DP + c * 32);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            if (real && (two || g == 0)) {
+                if (!whole) a.part_ml[slot * kTile + r] = make_float2(m, l);
+                else if (a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (m + log2f(l)) : neg_inf();
+            }
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0) tc::bar_arrive(tc::smem(&bars.o_free));
+            ++segs;
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 1) tc::tmem_free(tmem, 512);
+}
+
+// The pieces of what was cut: CTA x joins what begins in CTA x's part and ends in another's. A warp
+// per row; the pieces' references and sums first, then their outputs.
+constexpr int kJoinRows = 8;
+
+template <typename T, int DC>
+__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int DP = DC * 64, E = DP / 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 join = a.joins[blockIdx.x];
+    if (join.x < 0) return;
+    const int lane = threadIdx.x & 31, rr = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    const int used = a.nodes * a.G, m_tile = rr / used, r = rr - m_tile * used;   // (rows of a tile that are used)
+    const int node = (2 * join.z + m_tile) * a.nodes + r / a.G;
+    int L, count;
+    sequence(a, join.x, L, count);
+    if (m_tile > 1 || node >= count) return;
+    const int first = blockIdx.x, pieces = join.w - first + 1;
+    auto slot = [&](int i) { return (((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + m_tile) * kTile + r; };
+    float m = neg_inf();
+    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, a.part_ml[slot(i)].x);
+    m = warp_max(m);
+    const float ref = m == neg_inf() ? 0.f : m;
+    float l = 0.f, o[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int i0 = 0; i0 < pieces; i0 += 32) {
+        float w = 0.f;
+        if (i0 + lane < pieces) {
+            const float2 ml = a.part_ml[slot(i0 + lane)];
+            w = ex2(ml.x - ref);
+            l += ml.y * w;
+        }
+        const int n = min(32, pieces - i0);
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(kFull, w, i);
+            const float *p = a.part_o + slot(i0 + i) * DP + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(p);
+                o[0] = fmaf(v.x, wi, o[0]);
+                o[1] = fmaf(v.y, wi, o[1]);
+                o[2] = fmaf(v.z, wi, o[2]);
+                o[3] = fmaf(v.w, wi, o[3]);
+            } else {
+                const float2 v = *reinterpret_cast<const float2 *>(p);
+                o[0] = fmaf(v.x, wi, o[0]);
+                o[1] = fmaf(v.y, wi, o[1]);
+            }
+        }
+    }
+    l = warp_sum(l);
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const long long row = ((long long)join.x * a.N + node) * a.Hq + join.y * a.G + r % a.G;
+    if (lane * E < a.D) {   // (D is a multiple of 8)
+        uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * a.D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) to[e] = Half<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
+    }
     if (lane == 0 && a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (m + log2f(l)) : neg_inf();
 }
 
@@ -139,10 +751,90 @@ static int check_attend(const spec_attend_params *p) {
     return SPEC_OK;
 }
 
+// ---- launch --------------------------------------------------------------------------------
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encoder() {
+    static const EncodeFn fn = [] {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<EncodeFn>(f);
+    }();
+    return fn;
+}
+
+// [n3][n2][n1][D] of 16-bit elements, boxes of 64 elements x b1 x b2
+static bool encode(CUtensorMap *map, int bf16, const void *base, int D, const int *n, const int64_t *stride, int b1, int b2) {
+    const EncodeFn fn = encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)n[2], (cuuint64_t)n[1], (cuuint64_t)n[0]};
+    cuuint64_t st[3];
+    for (int i = 0; i < 3; ++i) st[i] = n[2 - i] > 1 ? (cuuint64_t)stride[2 - i] * 2 : (cuuint64_t)(D * 2 + 15) / 16 * 16;
+    const cuuint32_t box[4] = {64, (cuuint32_t)b1, (cuuint32_t)b2, 1}, one[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void *>(base), dims, st, box,
+              one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+static int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+
+constexpr int kMaxCtas = 152;   // one per SM; the workspace's room
+
+static size_t part_floats(int D) { return (size_t)kMaxCtas * 4 * kTile * (D > 64 ? 128 : 64); }
+static size_t workspace_bytes_for(const spec_attend_params *p) {
+    return part_floats(p->D) * 4 + (size_t)kMaxCtas * 4 * kTile * 8 + (size_t)kMaxCtas * 16;
+}
+
+template <typename T, int DC>
+static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, int box, cudaStream_t st) {
+    constexpr size_t smem = AttendSmem<DC>::kTiles + sizeof(AttendShared);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    static std::mutex mu;
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (!done[dev & 63]) {
+            e = cudaFuncSetAttribute(attend_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            done[dev & 63] = true;
+        }
+    }
+    int ctas = sm_count();
+    if (ctas < 1) return cudaErrorUnknown;
+    if (ctas > kMaxCtas) ctas = kMaxCtas;
+    attend_kernel<T, DC><<<ctas, kNT, smem, st>>>(a, maps[0], maps[1], maps[2], box);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int tiles = (a.N + a.nodes - 1) / a.nodes, rows = tiles > 1 ? 2 * a.nodes * a.G : a.N * a.G;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, (rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(32 * kJoinRows);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, join_kernel<T, DC>, a);
+}
+
 }  // namespace sr
 
 extern "C" size_t spec_tree_attention_workspace_size(const spec_attend_params *p) {
-    return sr::check_attend(p) == SPEC_OK ? 16 : 0;
+    return sr::check_attend(p) == SPEC_OK ? sr::workspace_bytes_for(p) : 0;
 }
 
 extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, const void *k, const void *v,
@@ -178,9 +870,8 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
             return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_attention: outputs overlap");
     }
     spec_internal_set_error(SPEC_OK, "");
+    const int G = p->Hq / p->Hkv;
     AttendArgs a{};
-    a.q = q;
-    a.k = k;
     a.v = v;
     a.table = table;
     a.lengths = lengths;
@@ -189,27 +880,36 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
     a.out = out;
     a.lse = lse;
     a.status = status;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(a.part_o + part_floats(p->D));
+    a.joins = reinterpret_cast<int4 *>(a.part_ml + (size_t)kMaxCtas * 4 * kTile);
     a.B = p->B;
     a.N = p->N;
     a.Hq = p->Hq;
     a.Hkv = p->Hkv;
-    a.G = p->Hq / p->Hkv;
+    a.G = G;
     a.D = p->D;
     a.P = p->P;
     a.page = p->page;
     a.M = p->M;
-    a.sL = p->scale * sv::kLog2e;
+    a.fill = counts != nullptr || (int64_t)p->M * p->page < p->N;
+    a.nodes = kTile / G;
+    a.sL = fmaxf(fabsf(p->scale) * sv::kLog2e, FLT_MIN);   // (0 times a masked key's -inf would be NaN)
+    a.neg = p->scale < 0.f;
     a.ps = p->parents_stride;
-    const int n[3][3] = {{p->B, p->N, p->Hq}, {p->P, p->page, p->Hkv}, {p->P, p->page, p->Hkv}};
-    for (int j = 0; j < 3; ++j) {
-        a.qs[j] = n[0][j] > 1 ? p->q_stride[j] : 0;
-        a.ks[j] = n[1][j] > 1 ? p->k_stride[j] : 0;
-        a.vs[j] = n[2][j] > 1 ? p->v_stride[j] : 0;
-    }
+    for (int j = 0; j < 3; ++j) a.vs[j] = p->v_stride[j];
+    const int nq[3] = {p->B, p->N, p->Hq}, nk[3] = {p->P > 0 ? p->P : 1, p->page, p->Hkv}, box = p->page < 64 ? p->page : 64;
+    const int bf16 = p->dtype == SPEC_BF16;
+    const int64_t none[3] = {0, 0, 0};
+    CUtensorMap maps[3];
+    const int empty[3] = {1, 1, 1};
+    if (!encode(&maps[0], bf16, q, p->D, nq, p->q_stride, G, a.nodes) ||
+        !encode(&maps[1], bf16, p->P ? k : q, p->D, p->P ? nk : empty, p->P ? p->k_stride : none, 1, box) ||
+        !encode(&maps[2], bf16, p->P ? v : q, p->D, p->P ? nk : empty, p->P ? p->v_stride : none, 1, box))
+        return spec_internal_set_error(SPEC_ERR_CUDA, "tree_attention: the copies' layout could not be encoded");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const unsigned grid = (unsigned)(((long long)a.B * a.N * a.Hq + 3) / 4);
-    if (p->dtype == SPEC_BF16) attend_simple_kernel<__nv_bfloat16><<<grid, 128, 0, st>>>(a);
-    else attend_simple_kernel<__half><<<grid, 128, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+    cudaError_t e;
+    if (p->D > 64) e = bf16 ? launch_attend<__nv_bfloat16, 2>(a, maps, box, st) : launch_attend<__half, 2>(a, maps, box, st);
+    else e = bf16 ? launch_attend<__nv_bfloat16, 1>(a, maps, box, st) : launch_attend<__half, 1>(a, maps, box, st);
     return e == cudaSuccess ? SPEC_OK : spec_internal_set_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }
