@@ -33,7 +33,7 @@ namespace sr {
 
 constexpr int kTile = 128;             // keys a tile, and rows a tile
 constexpr int kChunk = kTile * 128;    // bytes of 64 elements of a tile's rows
-constexpr int kNT = 384;               // copies, products, values' check, idle; two softmax warpgroups
+constexpr int kNT = 384;               // keys, products, values' check, values; two softmax warpgroups
 constexpr unsigned kSpin = 1u << 20;   // polls of a wait before it gives up
 constexpr int kSegRing = 8;            // segments whose flags of non-finite values are kept
 constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
@@ -44,7 +44,7 @@ struct AttendArgs {
     void *out;
     float *lse;
     int32_t *status;
-    float *part_o;    // [CTA][2][tile][row][D padded]: unnormalised outputs of a sequence's pieces
+    float4 *part_o;   // [CTA][2][tile][D padded / 4][row]: unnormalised outputs of a sequence's pieces
     float2 *part_ml;  // [CTA][2][tile][row]: their reference (log2) and sum
     int4 *joins;      // [CTA]: sequence (-1: none), head, pair of tiles, last CTA of what begins here and ends elsewhere
     int B, N, Hq, Hkv, G, D, P, page, M, fill;
@@ -83,6 +83,12 @@ __device__ __forceinline__ int parent_of(const AttendArgs &a, int b, int n) {
     return -1;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 template <typename T>
 struct Half;
 template <>
@@ -119,6 +125,11 @@ struct Segment {
     __device__ __forceinline__ int tile(int j) const { return t0 + (act == 2 ? j >> 1 : j); }
 };
 
+// (a 64-bit division costs ten times a 32-bit one)
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+    return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
+
 // Every role walks the CTA's segments by itself.
 struct Walk {
     int b;
@@ -135,9 +146,9 @@ struct Walk {
                 continue;
             }
             s.b = b;
-            s.h = (int)(off / head);
+            s.h = (int)quotient(off, head);
             const long long in = off - s.h * head;
-            s.pair = (int)(in / s.tiles);
+            s.pair = (int)quotient(in, s.tiles);
             s.t0 = (int)(in - (long long)s.pair * s.tiles);
             s.left = s.tiles - s.t0;
             s.t1 = s.t0 + (int)min(s.left, left);
@@ -279,190 +290,218 @@ __global__ void __launch_bounds__(kNT, 1)
         return __all_sync(kFull, ok);
     };
 
-    if (warp == 0) {
-        // ---- copies: keys two jobs ahead of the values ---------------------------------
-        unsigned n = 0, segs = 0;
-        bool ok = true;
-        if (lane == 0) {
-            tc::prefetch_map(&qmap);
-            tc::prefetch_map(&kmap);
-            tc::prefetch_map(&vmap);
-        }
-        auto tile = [&](const CUtensorMap *map, int t) {
-            const int st = n % S;
-            if (n >= S && !wait_warp(&bars.empty[st], (n / S + 1) & 1)) return false;
-            const int keys = s.keys(t), boxes = (keys + box - 1) / box, at0 = t * kTile;
-            const uint32_t bar = tc::smem(&bars.full[st]), dst = ring + st * SM::kStage;
-            if (lane == 0) tc::bar_expect(bar, (uint32_t)boxes * box * 128 * DC);
-            __syncwarp();
-            for (int i = lane; i < boxes * DC; i += 32) {
-                const int bx = DC == 2 ? i >> 1 : i, c = DC == 2 ? i & 1 : 0, key = at0 + bx * box;
-                int p = a.table[(long long)s.b * a.M + key / a.page];
-                if (p < 0 || p >= a.P) {
-                    raise_status(a.status, SPEC_ERR_BAD_PAGE);
-                    p = -1;   // (the copy fills zeros)
-                }
-                tc::load_tile(dst + c * kChunk + bx * box * 128, map, bar, c * 64, s.h, key % a.page, p);
-            }
-            ++n;
-            return true;
-        };
-        while (ok && walk.next(a, s)) {
-            const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
-            for (int t = 0; ok && t < min(nt, ahead); ++t) ok = tile(&kmap, s.t0 + t);
-            if (!ok || (segs > 0 && !wait_warp(&bars.q_empty, (segs + 1) & 1))) break;
+    // 168 registers a thread at the launch: 96 for four warps and 200 for eight
+    if (warp < 4) {
+        tc::fewer_registers<96>();
+        if (warp == 0 || warp == 3) {
+            // ---- copies: warp 0 the queries and keys, warp 3 the values ----------------------------
+            // Both fill one ring of stages, in the order in which the products use them:
+            // `ahead` tiles of keys, then values and keys in turn. The products give stages back in
+            // that order, so that a warp's wait for a stage is never two phases ahead.
+            const bool keys = warp == 0;
+            const CUtensorMap *map = keys ? &kmap : &vmap;
+            const int bpt = kTile / box, group = 32 / bpt;   // boxes a tile; tiles whose pages the lanes hold
+            unsigned n0 = 0, segs = 0, last = 0;
+            bool ok = true;
             if (lane == 0) {
-                const uint32_t bar = tc::smem(&bars.q_full);
-                tc::bar_expect(bar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
-                for (int m = 0; m < s.act; ++m)
-                    for (int c = 0; c < DC; ++c)
-                        tc::load_tile(base + m * SM::kStage + c * kChunk, &qmap, bar, c * 64, s.h * a.G, (2 * s.pair + m) * a.nodes, s.b);
+                tc::prefetch_map(&qmap);
+                tc::prefetch_map(map);
             }
-            __syncwarp();
-            ++segs;
-            for (int t = 0; ok && t < nt; ++t) {
-                ok = tile(&vmap, s.t0 + t);
-                if (ok && t + ahead < nt) ok = tile(&kmap, s.t0 + t + ahead);
+            while (ok && walk.next(a, s)) {
+                const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
+                // lane l: the page of box l % bpt of tile l / bpt of the group
+                auto pages = [&](int t) -> int {
+                    const long long key = (long long)(s.t0 + t) * kTile + lane * box;
+                    if (t + lane / bpt >= nt || key >= s.L + s.count) return -1;
+                    const int p = a.table[(long long)s.b * a.M + key / a.page];
+                    if (p >= 0 && p < a.P) return p;
+                    raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                    return -1;   // (the copy fills zeros)
+                };
+                int now = pages(0), next = pages(group);
+                for (int t = 0; ok && t < nt; ++t) {
+                    if (t && t % group == 0) {
+                        now = next;
+                        next = pages(t + group);
+                    }
+                    const unsigned n = n0 + (keys ? (t < ahead ? t : ahead + 2 * (t - ahead) + 1) : (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t));
+                    const int st = n % S;
+                    if (n >= S && !(ok = wait_warp(&bars.empty[st], (n / S + 1) & 1))) break;
+                    const int boxes = (s.keys(s.t0 + t) + box - 1) / box;
+                    const uint32_t bar = tc::smem(&bars.full[st]), dst = ring + st * SM::kStage;
+                    if (lane == 0) tc::bar_expect(bar, (uint32_t)boxes * box * 128 * DC);
+                    __syncwarp();
+                    const int bx = DC == 2 ? lane >> 1 : lane, c = DC == 2 ? lane & 1 : 0;   // (at most 16 boxes)
+                    const int p = __shfl_sync(kFull, now, t % group * bpt + min(bx, bpt - 1));
+                    if (bx < boxes)
+                        tc::load_tile(dst + c * kChunk + bx * box * 128, map, bar, c * 64, s.h, ((s.t0 + t) * kTile + bx * box) % a.page, p);
+                    last = n + 1;
+                    if (keys && t == min(nt, ahead) - 1) {
+                        if (segs > 0 && !(ok = wait_warp(&bars.q_empty, (segs + 1) & 1))) break;
+                        if (lane == 0) {
+                            const uint32_t qbar = tc::smem(&bars.q_full);
+                            tc::bar_expect(qbar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
+                            for (int m = 0; m < s.act; ++m)
+                                for (int x = 0; x < DC; ++x)
+                                    tc::load_tile(base + m * SM::kStage + x * kChunk, &qmap, qbar, x * 64, s.h * a.G, (2 * s.pair + m) * a.nodes, s.b);
+                        }
+                        __syncwarp();
+                        ++segs;
+                    }
+                }
+                n0 += 2 * nt;
             }
-        }
-        // nothing is left in flight when another role has given up
-        if (*(volatile int *)&sh.abort) {
-            for (unsigned i = n > S ? n - S : 0; i < n; ++i)
-                for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.full[i % S]), (i / S) & 1); ++k) {}
-            if (segs > 0)
-                for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full), (segs + 1) & 1); ++k) {}
-        }
-    } else if (warp == 1) {
-        // ---- products ---------------------------------------------------------------------
-        if (lane == 0) {
-            unsigned n = 0, segs = 0, done[2] = {0, 0};
+            // nothing is left in flight when another role has given up
+            if (*(volatile int *)&sh.abort) {
+                for (unsigned i = last > S ? last - S : 0; i < last; ++i)
+                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.full[i % S]), (i / S) & 1); ++k) {}
+                if (segs > 0)
+                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full), (segs + 1) & 1); ++k) {}
+            }
+        } else if (warp == 1) {
+            // ---- products ---------------------------------------------------------------------
+            // The whole warp walks along, so that operands stay in uniform registers; one
+            // thread issues.
+            const bool lead = tc::elect();
+            unsigned n0 = 0, segs = 0, done0 = 0, done1 = 0;
             uint32_t fixed = 0;   // per stage: parity of the next wait for checked values
             bool ok = true;
             while (ok && walk.next(a, s)) {
-                const int jobs = s.jobs(), nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
-                // the position of a tile's keys and values in the order of copies
-                const unsigned n0 = n;
-                auto kpos = [&](int t) { return n0 + (t < ahead ? t : ahead + 2 * (t - ahead) + 1); };
-                auto vpos = [&](int t) { return n0 + (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t); };
+                const int two = s.act == 2, nt = s.t1 - s.t0, ahead = two ? 1 : 2, jobs = two ? 2 * nt : nt;
+                // S of job j: the tile's keys are at this place in the order of copies
                 auto scores = [&](int j) -> bool {
-                    const int g = j & 1, t = s.tile(j) - s.t0;
-                    const unsigned at = kpos(t);
-                    if ((s.act == 1 || g == 0) && !wait(&bars.full[at % S], (at / S) & 1)) return false;
+                    const int g = j & 1, t = two ? j >> 1 : j;
+                    const unsigned at = n0 + (t < ahead ? t : 2 * t - ahead + 1), st = at % S;
+                    if ((!two || g == 0) && !wait_warp(&bars.full[st], (at / S) & 1)) return false;
                     tc::fence_after();
-                    const uint32_t q = base + (s.act == 2 ? g * SM::kStage : 0), k = ring + (at % S) * SM::kStage;
+                    const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g * SM::kStage : 0), 16));
+                    const uint32_t k = tc::uniform(tc::operand_lo(ring + st * SM::kStage, 16));
+                    const uint32_t d = tc::uniform(tS[0] + g * 128);
+                    if (lead) {
 #pragma unroll
-                    for (int i = 0; i < DC * 4; ++i) {
-                        const uint32_t o = (i >> 2) * kChunk + (i & 3) * 32;
-                        tc::mma_ss(tS[g], tc::operand(q + o, 16), tc::operand(k + o, 16), kIdS, i > 0);
+                        for (int i = 0; i < DC * 4; ++i) {
+                            const uint32_t o = ((i >> 2) * kChunk + (i & 3) * 32) >> 4;
+                            tc::mma_ss(d, tc::operand(q + o), tc::operand(k + o), kIdS, i > 0);
+                        }
+                        tc::commit(tc::smem(&bars.s_full[g]));
+                        if (!two || g == 1) tc::commit(tc::smem(&bars.empty[st]));
+                        if (j == jobs - 1) tc::commit(tc::smem(&bars.q_empty));
                     }
-                    tc::commit(tc::smem(&bars.s_full[g]));
-                    if (s.act == 1 || g == 1) tc::commit(tc::smem(&bars.empty[at % S]));
+                    __syncwarp();
                     return true;
                 };
-                if (!wait(&bars.q_full, segs & 1)) break;
-                for (int j = 0; ok && j < min(jobs, 2); ++j) ok = scores(j);
-                if (ok && jobs <= 2) tc::commit(tc::smem(&bars.q_empty));
+                if (!wait_warp(&bars.q_full, segs & 1)) break;
+                ok = scores(0) && (jobs < 2 || scores(1));
                 for (int j = 0; ok && j < jobs; ++j) {
-                    const int g = j & 1, t = s.tile(j) - s.t0;
-                    const unsigned at = vpos(t), st = at % S;
-                    if (s.act == 1 || g == 0) {
-                        ok = wait(&bars.full[st], (at / S) & 1);
-                        if (ok && s.tail(s.tile(j))) {
-                            ok = wait(&bars.fixed[st], fixed >> st & 1);
+                    const int g = j & 1, t = two ? j >> 1 : j;
+                    const unsigned at = n0 + (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t), st = at % S;
+                    if (!two || g == 0) {
+                        ok = wait_warp(&bars.full[st], (at / S) & 1);
+                        if (ok && s.tail(s.t0 + t)) {
+                            ok = wait_warp(&bars.fixed[st], fixed >> st & 1);
                             fixed ^= 1u << st;
                         }
                         if (!ok) break;
                     }
-                    if (j == 0 && segs > 0 && !(ok = wait(&bars.o_free, (segs + 1) & 1))) break;
-                    if (!(ok = wait(&bars.p_ready[g], done[g] & 1))) break;
+                    if (j == 0 && segs > 0 && !(ok = wait_warp(&bars.o_free, (segs + 1) & 1))) break;
+                    if (!(ok = wait_warp(&bars.p_ready[g], (g ? done1 : done0) & 1))) break;
                     tc::fence_after();
-                    const uint32_t v = ring + st * SM::kStage;
-                    const int steps = (s.keys(s.tile(j)) + 15) / 16;
-                    for (int i = 0; i < steps; ++i)
-                        tc::mma_ts(tO[g], tS[g] + i * 8, tc::operand(v + i * 2048, kChunk), kIdO, j >= 2 || i > 0);
-                    tc::commit(tc::smem(&bars.pv_done[g]));
-                    if (s.act == 1 || g == 1) tc::commit(tc::smem(&bars.empty[st]));
-                    ++done[g];
-                    if (j + 2 < jobs) {
-                        ok = scores(j + 2);
-                        if (ok && j + 3 == jobs) tc::commit(tc::smem(&bars.q_empty));
+                    const uint32_t v = tc::uniform(tc::operand_lo(ring + st * SM::kStage, kChunk));
+                    const uint32_t d = tc::uniform(tO[0] + g * DP), p = tc::uniform(tS[0] + g * 128);
+                    const int steps = (s.keys(s.t0 + t) + 15) / 16;
+                    if (lead) {
+                        if (steps == kTile / 16) {
+#pragma unroll
+                            for (int i = 0; i < kTile / 16; ++i) tc::mma_ts(d, p + i * 8, tc::operand(v + i * 128), kIdO, j >= 2 || i > 0);
+                        } else {
+                            for (int i = 0; i < steps; ++i) tc::mma_ts(d, p + i * 8, tc::operand(v + i * 128), kIdO, j >= 2 || i > 0);
+                        }
+                        tc::commit(tc::smem(&bars.pv_done[g]));
+                        if (!two || g == 1) tc::commit(tc::smem(&bars.empty[st]));
                     }
+                    __syncwarp();
+                    if (g) ++done1;
+                    else ++done0;
+                    if (j + 2 < jobs) ok = scores(j + 2);
                 }
-                n = n0 + 2 * nt;
+                n0 += 2 * nt;
                 ++segs;
             }
             // (none of the products may still run when the CTA ends)
-            tc::commit(tc::smem(&bars.drain));
-            for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.drain), 0); ++k) {}
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ---- values behind the context -----------------------------------------------------
-        unsigned n = 0, segs = 0;
-        int4 join = make_int4(-1, 0, 0, 0);
-        long long at_unit = u0;
-        bool ok = true;
-        while (ok && walk.next(a, s)) {
-            const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
-            if (s.t0 == 0 && s.t1 < s.tiles) join = make_int4(s.b, s.h, s.pair, (int)((at_unit + s.tiles - 1) / per));
-            at_unit += nt;
-            bool first = true;
-            uint32_t *bad = sh.bad[segs % kSegRing];
-            // every tile is waited for and given back in the order of the copies, so that no barrier is
-            // ever two phases ahead of this warp or behind it
-            for (int x = 0; ok && x < 2 * nt; ++x, ++n) {
-                const unsigned st = n % S;
-                if (!(ok = wait_warp(&bars.full[st], (n / S) & 1))) break;
-                const int v = x < min(nt, ahead) ? -1 : x - min(nt, ahead), lag = nt - min(nt, ahead);
-                // values and keys take turns while there are keys left
-                const int t = v < 0 ? -1 : v < 2 * lag ? (v & 1 ? -1 : v >> 1) : v - lag;
-                if (t < 0 || !s.tail(s.t0 + t)) {
-                    if (lane == 0) tc::bar_arrive(tc::smem(&bars.empty[st]));
-                    continue;
-                }
-                if (first && lane < 4) bad[lane] = 0;
-                first = false;
-                __syncwarp();
-                const int at0 = (s.t0 + t) * kTile, keys = s.keys(s.t0 + t), lo = max(0, s.L - at0);
-                char *stage = dyn + SM::kQ + st * SM::kStage;
-                const int rows = ((keys + 15) & ~15) - lo;   // up to the last product's end
-                for (int i = lane; i < rows * DC * 8; i += 32) {
-                    const int r = lo + i / (DC * 8), x = i % (DC * 8);
-                    uint4 *p = reinterpret_cast<uint4 *>(stage + (x >> 3) * kChunk + r * 128 + (x & 7) * 16);
-                    if (r >= keys) {
-                        *p = make_uint4(0, 0, 0, 0);
+            if (lead) {
+                tc::commit(tc::smem(&bars.drain));
+                for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.drain), 0); ++k) {}
+            }
+            __syncwarp();
+        } else {
+            // ---- values behind the context -----------------------------------------------------
+            unsigned n = 0, segs = 0;
+            int4 join = make_int4(-1, 0, 0, 0);
+            long long at_unit = u0;
+            bool ok = true;
+            while (ok && walk.next(a, s)) {
+                const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
+                if (s.t0 == 0 && s.t1 < s.tiles) join = make_int4(s.b, s.h, s.pair, (int)((at_unit + s.tiles - 1) / per));
+                at_unit += nt;
+                bool first = true;
+                uint32_t *bad = sh.bad[segs % kSegRing];
+                // every tile is waited for and given back in the order of the copies, so that no barrier is
+                // ever two phases ahead of this warp or behind it
+                for (int x = 0; ok && x < 2 * nt; ++x, ++n) {
+                    const unsigned st = n % S;
+                    if (!(ok = wait_warp(&bars.full[st], (n / S) & 1))) break;
+                    const int v = x < min(nt, ahead) ? -1 : x - min(nt, ahead), lag = nt - min(nt, ahead);
+                    // values and keys take turns while there are keys left
+                    const int t = v < 0 ? -1 : v < 2 * lag ? (v & 1 ? -1 : v >> 1) : v - lag;
+                    if (t < 0 || !s.tail(s.t0 + t)) {
+                        if (lane == 0) tc::bar_arrive(tc::smem(&bars.empty[st]));
                         continue;
                     }
-                    uint4 w = *p;
-                    uint32_t *u = &w.x;
-                    bool hit = false;
+                    if (first && lane < 4) bad[lane] = 0;
+                    first = false;
+                    __syncwarp();
+                    const int at0 = (s.t0 + t) * kTile, keys = s.keys(s.t0 + t), lo = max(0, s.L - at0);
+                    char *stage = dyn + SM::kQ + st * SM::kStage;
+                    const int rows = ((keys + 15) & ~15) - lo;   // up to the last product's end
+                    for (int i = lane; i < rows * DC * 8; i += 32) {
+                        const int r = lo + i / (DC * 8), x = i % (DC * 8);
+                        uint4 *p = reinterpret_cast<uint4 *>(stage + (x >> 3) * kChunk + r * 128 + (x & 7) * 16);
+                        if (r >= keys) {
+                            *p = make_uint4(0, 0, 0, 0);
+                            continue;
+                        }
+                        uint4 w = *p;
+                        uint32_t *u = &w.x;
+                        bool hit = false;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if ((u[e] & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0xffff0000u, hit = true;
-                        if ((u[e] >> 16 & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0x0000ffffu, hit = true;
+                        for (int e = 0; e < 4; ++e) {
+                            if ((u[e] & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0xffff0000u, hit = true;
+                            if ((u[e] >> 16 & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0x0000ffffu, hit = true;
+                        }
+                        if (hit) {
+                            *p = w;
+                            const int node = at0 + r - s.L;
+                            atomicOr(&bad[node >> 5], 1u << (node & 31));
+                        }
                     }
-                    if (hit) {
-                        *p = w;
-                        const int node = at0 + r - s.L;
-                        atomicOr(&bad[node >> 5], 1u << (node & 31));
+                    tc::fence_async();
+                    __syncwarp();
+                    if (lane == 0) {
+                        tc::bar_arrive(tc::smem(&bars.fixed[st]));
+                        tc::bar_arrive(tc::smem(&bars.empty[st]));
                     }
                 }
-                tc::fence_async();
-                __syncwarp();
-                if (lane == 0) {
-                    tc::bar_arrive(tc::smem(&bars.fixed[st]));
-                    tc::bar_arrive(tc::smem(&bars.empty[st]));
-                }
+                ++segs;
             }
-            ++segs;
+            if (lane == 0) a.joins[me] = join;
         }
-        if (lane == 0) a.joins[me] = join;
-    } else if (warp >= 4) {
+    } else {
+        tc::more_registers<200>();
         // ---- softmax: a stream each, a row a thread ------------------------------------------
         const int g = (warp - 4) >> 2, r = threadIdx.x & 127;
         const uint32_t row_lane = (uint32_t)(warp & 3) << 21;   // (lane of tensor memory in bits 16 and up)
         const uint32_t mS = tS[g] + row_lane;
-        unsigned segs = 0, merges = 0, jobs_of[2] = {0, 0};   // jobs of both streams so far
+        unsigned segs = 0, merges = 0, own = 0, other = 0;   // jobs of this stream and the other so far
         bool ok = true;
         while (ok && walk.next(a, s)) {
             const int jobs = s.jobs();
@@ -482,7 +521,7 @@ __global__ void __launch_bounds__(kNT, 1)
             }
             float m = neg_inf(), l = 0.f;
             for (int j = g; j < jobs; j += 2) {
-                if (!(ok = wait_warp(&bars.s_full[g], jobs_of[g] & 1))) break;
+                if (!(ok = wait_warp(&bars.s_full[g], own & 1))) break;
                 tc::fence_after();
                 float x[4][32];
 #pragma unroll
@@ -511,7 +550,7 @@ __global__ void __launch_bounds__(kNT, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], x[c][i]);
+                    for (int i = 0; i < 32; i += 2) mx[c] = max3(mx[c], x[c][i], x[c][i + 1]);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sL;
                 const bool move = top > m + kLazy;
                 if (__any_sync(kFull, move)) {
@@ -519,7 +558,7 @@ __global__ void __launch_bounds__(kNT, 1)
                     m = to;
                     l *= keep;
                     if (j >= 2) {   // the output so far
-                        if (!(ok = wait_warp(&bars.pv_done[g], (jobs_of[g] + 1) & 1))) break;
+                        if (!(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
                         tc::fence_after();
 #pragma unroll 1
                         for (int c = 0; c < DP / 32; ++c) {
@@ -534,35 +573,37 @@ __global__ void __launch_bounds__(kNT, 1)
                     }
                 }
                 const float ref = m == neg_inf() ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 scale = make_float2(a.sL, a.sL), minus = make_float2(-ref, -ref);
+                float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        const float e0 = ex2(fmaf(x[c][i], a.sL, -ref)), e1 = ex2(fmaf(x[c][i + 1], a.sL, -ref));
-                        sum[i & 2] += e0;
-                        sum[(i & 2) + 1] += e1;
-                        p[i / 2] = Half<T>::pack(e0, e1);
+                        float2 e = __ffma2_rn(make_float2(x[c][i], x[c][i + 1]), scale, minus);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        sum[c & 1] = __fadd2_rn(sum[c & 1], e);
+                        p[i / 2] = Half<T>::pack(e.x, e.y);
                     }
                     tc::tmem_store16(mS + c * 16, p);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tc::tmem_wait_store();
                 tc::fence_before();
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
-                ++jobs_of[g];
+                ++own;
             }
             if (!ok) break;
-            jobs_of[g ^ 1] += (jobs + (g ^ 1 ? 0 : 1)) / 2;   // the other stream's jobs: ceil for stream 0, floor for 1
+            other += (jobs + g) / 2;   // (stream 0 has the odd one)
             // ---- the segment's output ---------------------------------------------------------
             const bool two = s.act == 2, both = !two && jobs > 1;
             if (both || two || g == 0) {
-                if (!(ok = wait_warp(&bars.pv_done[g], (jobs_of[g] + 1) & 1))) break;
+                if (!(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
             }
             if (!two) {
-                if ((g == 1 || both) && !(ok = wait_warp(&bars.pv_done[g ^ 1], (jobs_of[g ^ 1] + 1) & 1))) break;
+                if ((g == 1 || both) && !(ok = wait_warp(&bars.pv_done[g ^ 1], (other + 1) & 1))) break;
                 sh.ml[g][r] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem(&bars.merge));
@@ -633,9 +674,9 @@ __global__ void __launch_bounds__(kNT, 1)
                             to[i] = make_uint4(Half<T>::pack(o[8 * i], o[8 * i + 1]), Half<T>::pack(o[8 * i + 2], o[8 * i + 3]),
                                                Half<T>::pack(o[8 * i + 4], o[8 * i + 5]), Half<T>::pack(o[8 * i + 6], o[8 * i + 7]));
                 } else {
-                    float4 *to = reinterpret_cast<float4 *>(a.part_o + (slot * kTile + r) * DP + c * 32);
+                    float4 *to = a.part_o + (slot * (DP / 4) + c * 8) * kTile + r;   // (a warp's rows side by side)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) to[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int i = 0; i < 8; ++i) to[i * kTile] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                 }
             }
             if (real && (two || g == 0)) {
@@ -653,65 +694,48 @@ __global__ void __launch_bounds__(kNT, 1)
     if (warp == 1) tc::tmem_free(tmem, 512);
 }
 
-// The pieces of what was cut: CTA x joins what begins in CTA x's part and ends in another's. A warp
-// per row; the pieces' references and sums first, then their outputs.
+// The pieces of what was cut: CTA x joins what begins in CTA x's part and ends in another's. A
+// thread per row and four columns, eight rows side by side; the pieces' references
+// first, then their outputs.
 constexpr int kJoinRows = 8;
 
 template <typename T, int DC>
-__global__ void __launch_bounds__(32 * kJoinRows) join_kernel(const __grid_constant__ AttendArgs a) {
-    constexpr int DP = DC * 64, E = DP / 32;
+__global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_constant__ AttendArgs a) {
+    constexpr int DP = DC * 64;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 join = a.joins[blockIdx.x];
     if (join.x < 0) return;
-    const int lane = threadIdx.x & 31, rr = blockIdx.y * kJoinRows + (threadIdx.x >> 5);
+    const int rr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
     const int used = a.nodes * a.G, m_tile = rr / used, r = rr - m_tile * used;   // (rows of a tile that are used)
     const int node = (2 * join.z + m_tile) * a.nodes + r / a.G;
     int L, count;
     sequence(a, join.x, L, count);
     if (m_tile > 1 || node >= count) return;
     const int first = blockIdx.x, pieces = join.w - first + 1;
-    auto slot = [&](int i) { return (((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + m_tile) * kTile + r; };
+    auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + m_tile; };
     float m = neg_inf();
-    for (int i = lane; i < pieces; i += 32) m = fmaxf(m, a.part_ml[slot(i)].x);
-    m = warp_max(m);
-    const float ref = m == neg_inf() ? 0.f : m;
-    float l = 0.f, o[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int i0 = 0; i0 < pieces; i0 += 32) {
-        float w = 0.f;
-        if (i0 + lane < pieces) {
-            const float2 ml = a.part_ml[slot(i0 + lane)];
-            w = ex2(ml.x - ref);
-            l += ml.y * w;
-        }
-        const int n = min(32, pieces - i0);
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(kFull, w, i);
-            const float *p = a.part_o + slot(i0 + i) * DP + lane * E;
-            if constexpr (E == 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(p);
-                o[0] = fmaf(v.x, wi, o[0]);
-                o[1] = fmaf(v.y, wi, o[1]);
-                o[2] = fmaf(v.z, wi, o[2]);
-                o[3] = fmaf(v.w, wi, o[3]);
-            } else {
-                const float2 v = *reinterpret_cast<const float2 *>(p);
-                o[0] = fmaf(v.x, wi, o[0]);
-                o[1] = fmaf(v.y, wi, o[1]);
-            }
-        }
+    for (int i = 0; i < pieces; ++i) m = fmaxf(m, a.part_ml[slot(i) * kTile + r].x);
+    const float ref = m == neg_inf() ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = 0; i < pieces; ++i) {
+        const float2 ml = a.part_ml[slot(i) * kTile + r];
+        const float4 v = a.part_o[(slot(i) * (DP / 4) + c4) * kTile + r];
+        const float w = ex2(ml.x - ref);
+        l = fmaf(ml.y, w, l);
+        o.x = fmaf(v.x, w, o.x);
+        o.y = fmaf(v.y, w, o.y);
+        o.z = fmaf(v.z, w, o.z);
+        o.w = fmaf(v.w, w, o.w);
     }
-    l = warp_sum(l);
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const long long row = ((long long)join.x * a.N + node) * a.Hq + join.y * a.G + r % a.G;
-    if (lane * E < a.D) {   // (D is a multiple of 8)
-        uint32_t *to = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * a.D + lane * E);
-#pragma unroll
-        for (int e = 0; e < E / 2; ++e) to[e] = Half<T>::pack(o[2 * e] * inv, o[2 * e + 1] * inv);
-    }
-    if (lane == 0 && a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (m + log2f(l)) : neg_inf();
+    if (c4 * 4 < a.D)
+        *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * a.D + c4 * 4) =
+            make_uint2(Half<T>::pack(o.x * inv, o.y * inv), Half<T>::pack(o.z * inv, o.w * inv));
+    if (c4 == 0 && a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (m + log2f(l)) : neg_inf();
 }
 
 static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
@@ -821,7 +845,7 @@ static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, i
     const int tiles = (a.N + a.nodes - 1) / a.nodes, rows = tiles > 1 ? 2 * a.nodes * a.G : a.N * a.G;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas, (rows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(32 * kJoinRows);
+    cfg.blockDim = dim3(DC * 16 * kJoinRows);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -880,8 +904,8 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
     a.out = out;
     a.lse = lse;
     a.status = status;
-    a.part_o = static_cast<float *>(workspace);
-    a.part_ml = reinterpret_cast<float2 *>(a.part_o + part_floats(p->D));
+    a.part_o = static_cast<float4 *>(workspace);
+    a.part_ml = reinterpret_cast<float2 *>(static_cast<float *>(workspace) + part_floats(p->D));
     a.joins = reinterpret_cast<int4 *>(a.part_ml + (size_t)kMaxCtas * 4 * kTile);
     a.B = p->B;
     a.N = p->N;

@@ -34,6 +34,25 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 
+// one thread of a warp that runs together
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "elect.sync _|p, 0xffffffff;\n"
+        "selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok));
+    return ok != 0;
+}
+// a value that all lanes hold, as the compiler cannot know
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// a warpgroup's share of the registers that the CTA was launched with
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---- fences ------------------------------------------------------------------------
 
 __device__ __forceinline__ void fence_barrier_init() {
@@ -102,9 +121,10 @@ __device__ __forceinline__ void tmem_wait_store() { asm volatile("tcgen05.wait::
 // rows, as a tensor copy with a 128-byte box lays it out. K-major (rows are M or N,
 // 64 elements of K each): lead is not used. MN-major (rows are K, 64 elements of N each): lead is the
 // distance of the next 64 elements of N.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead) {
-    return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)((lead & 0x3ffff) >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 |
-           2ull << 61;
+// The low word holds the address (steps along K add to it) and the lead.
+__device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lead) { return (addr & 0x3ffff) >> 4 | (lead >> 4) << 16; }
+__device__ __forceinline__ uint64_t operand(uint32_t lo) {
+    return (uint64_t)((1024 >> 4) | 1u << 14 | 2u << 29) << 32 | lo;
 }
 // fp32 accumulators, fp16 (0) or bf16 (1) inputs, M = 128, B K-major or MN-major
 __device__ __forceinline__ constexpr uint32_t shape(int bf16, int n, bool b_mn) {
