@@ -35,7 +35,7 @@ constexpr int kTile = 128;             // keys a tile, and rows a tile
 constexpr int kChunk = kTile * 128;    // bytes of 64 elements of a tile's rows
 constexpr int kNT = 384;               // keys, products, values' check, values; two softmax warpgroups
 constexpr unsigned kSpin = 1u << 20;   // polls of a wait before it gives up
-constexpr int kSegRing = 8;            // segments whose flags of non-finite values are kept
+constexpr int kSegRing = 6;            // segments whose flags of non-finite values are kept
 constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
 
 struct AttendArgs {
@@ -114,47 +114,42 @@ struct Half<__half> {
     __device__ static __forceinline__ float value(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
 };
 
-// One piece of a CTA's work: tiles [t0, t1) of `tiles` of (b, h, pair).
-struct Segment {
-    int b, h, pair, t0, t1, tiles, L, count, act;
-    long long left;   // units of the pair from t0 on
-    __device__ __forceinline__ int jobs() const { return act == 2 ? 2 * (t1 - t0) : t1 - t0; }
-    __device__ __forceinline__ int keys(int t) const { return min(kTile, L + count - t * kTile); }
-    __device__ __forceinline__ bool tail(int t) const { return (t + 1) * kTile > L; }
-    // the tile and the stream of a job
-    __device__ __forceinline__ int tile(int j) const { return t0 + (act == 2 ? j >> 1 : j); }
-};
-
 // (a 64-bit division costs ten times a 32-bit one)
 __device__ __forceinline__ long long quotient(long long x, long long y) {
     return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// Every role walks the CTA's segments by itself.
-struct Walk {
-    int b;
-    long long off, left;
-    __device__ __forceinline__ bool next(const AttendArgs &a, Segment &s) {
+// One piece of a CTA's work, tiles [t0, t1) of `tiles` of (b, h, pair), and what is left behind
+// it. Every warp walks the CTA's segments by itself; its place stands in shared memory,
+// which leaves registers to what the warp does.
+struct Segment {
+    int b, h, pair, t0, t1, tiles, L, count;
+    uint8_t act, begun;     // row tiles with nodes; whether next() has given the first one
+    long long off, left;    // units of sequence b behind this piece, and of the CTA's part
+    __device__ __forceinline__ int keys(int t) const { return min(kTile, L + count - t * kTile); }
+    __device__ __forceinline__ bool next(const AttendArgs &a) {
+        if (!begun) {
+            begun = 1;
+            return t1 > t0;
+        }
         while (left > 0) {
-            sequence(a, b, s.L, s.count);
-            const int pairs = (s.count + 2 * a.nodes - 1) / (2 * a.nodes);
-            s.tiles = (s.L + s.count + kTile - 1) / kTile;
-            const long long head = (long long)pairs * s.tiles, all = head * a.Hkv;
+            sequence(a, b, L, count);
+            const int pairs = (count + 2 * a.nodes - 1) / (2 * a.nodes);
+            tiles = (L + count + kTile - 1) / kTile;
+            const long long head = (long long)pairs * tiles, all = head * a.Hkv;
             if (off >= all) {
                 off -= all;
                 ++b;
                 continue;
             }
-            s.b = b;
-            s.h = (int)quotient(off, head);
-            const long long in = off - s.h * head;
-            s.pair = (int)quotient(in, s.tiles);
-            s.t0 = (int)(in - (long long)s.pair * s.tiles);
-            s.left = s.tiles - s.t0;
-            s.t1 = s.t0 + (int)min(s.left, left);
-            s.act = s.count - s.pair * 2 * a.nodes > a.nodes ? 2 : 1;
-            off += s.t1 - s.t0;
-            left -= s.t1 - s.t0;
+            h = (int)quotient(off, head);
+            const long long in = off - h * head;
+            pair = (int)quotient(in, tiles);
+            t0 = (int)(in - (long long)pair * tiles);
+            t1 = t0 + (int)min((long long)(tiles - t0), left);
+            act = count - pair * 2 * a.nodes > a.nodes ? 2 : 1;
+            off += t1 - t0;
+            left -= t1 - t0;
             return true;
         }
         return false;
@@ -169,17 +164,19 @@ struct AttendSmem {
     static constexpr int kTiles = kQ + kStages * kStage;
 };
 
-struct AttendBars {
-    uint64_t full[10], empty[10], fixed[10], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, o_free, merge, drain;
-};
-
 // behind the tiles in shared memory
+template <int S>
 struct AttendShared {
-    AttendBars bars;
-    float2 ml[2][kTile];
-    long long sum[kNT / 32], off;
+    struct {
+        uint64_t full[S], empty[S], fixed[S], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, o_free, merge, drain;
+    } bars;
+    union {
+        float2 ml[2][kTile];
+        long long sum[kNT / 32];
+    };
+    Segment seg[kNT / 32];
     uint32_t tmem, bad[kSegRing][4];
-    int abort, b0;
+    int abort;
 };
 
 template <typename T, int DC>
@@ -189,10 +186,39 @@ __global__ void __launch_bounds__(kNT, 1)
     using SM = AttendSmem<DC>;
     constexpr int S = SM::kStages, DP = DC * 64;
     extern __shared__ __align__(1024) char dyn[];   // (the kernel has no other shared memory, so that this holds)
-    AttendShared &sh = *reinterpret_cast<AttendShared *>(dyn + SM::kTiles);
-    AttendBars &bars = sh.bars;
+    AttendShared<S> &sh = *reinterpret_cast<AttendShared<S> *>(dyn + SM::kTiles);
+    auto &bars = sh.bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t base = tc::smem(dyn), ring = base + SM::kQ;
+    if (threadIdx.x == 0) {
+        tc::prefetch_map(&kmap);
+        tc::prefetch_map(&qmap);
+        tc::prefetch_map(&vmap);
+    }
+
+    if (threadIdx.x == 0) {
+        sh.abort = 0;
+        for (int w = 0; w < kNT / 32; ++w) sh.seg[w].t0 = sh.seg[w].t1 = sh.seg[w].begun = 0;
+        for (int i = 0; i < S; ++i) {
+            tc::bar_init(tc::smem(&bars.full[i]), 1);
+            tc::bar_init(tc::smem(&bars.empty[i]), 2);   // the products and the values' check
+            tc::bar_init(tc::smem(&bars.fixed[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(tc::smem(&bars.s_full[i]), 1);
+            tc::bar_init(tc::smem(&bars.p_ready[i]), 4);
+            tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
+        }
+        tc::bar_init(tc::smem(&bars.q_full), 1);
+        tc::bar_init(tc::smem(&bars.q_empty), 1);
+        tc::bar_init(tc::smem(&bars.o_free), 8);
+        tc::bar_init(tc::smem(&bars.merge), 8);
+        tc::bar_init(tc::smem(&bars.drain), 1);
+        tc::fence_barrier_init();
+    }
+    if (warp == 1) tc::tmem_alloc(tc::smem(&sh.tmem), 512);
+    // (so far nothing that an earlier kernel of the stream may write has been read)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- which part of the line is this CTA's ----------------------------------------
     const int G = gridDim.x, me = blockIdx.x;
@@ -212,28 +238,6 @@ __global__ void __launch_bounds__(kNT, 1)
         if (lane >= o) upto += v;
     }
     if (lane == 31) sh.sum[warp] = upto;
-    if (threadIdx.x == 0) {
-        sh.abort = 0;
-        sh.b0 = a.B;
-        sh.off = 0;
-        for (int i = 0; i < S; ++i) {
-            tc::bar_init(tc::smem(&bars.full[i]), 1);
-            tc::bar_init(tc::smem(&bars.empty[i]), 2);   // the products and the values' check
-            tc::bar_init(tc::smem(&bars.fixed[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            tc::bar_init(tc::smem(&bars.s_full[i]), 1);
-            tc::bar_init(tc::smem(&bars.p_ready[i]), 4);
-            tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
-        }
-        tc::bar_init(tc::smem(&bars.q_full), 1);
-        tc::bar_init(tc::smem(&bars.q_empty), 1);
-        tc::bar_init(tc::smem(&bars.o_free), 8);
-        tc::bar_init(tc::smem(&bars.merge), 8);
-        tc::bar_init(tc::smem(&bars.drain), 1);
-        tc::fence_barrier_init();
-    }
-    if (warp == 1) tc::tmem_alloc(tc::smem(&sh.tmem), 512);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -248,8 +252,14 @@ __global__ void __launch_bounds__(kNT, 1)
         for (int b = b_lo; b < b_hi; ++b) {
             const long long n = units(b);
             if (u0 < at + n) {
-                sh.b0 = b;
-                sh.off = u0 - at;
+                Segment first;
+                first.begun = 1;
+                first.b = b;
+                first.off = u0 - at;
+                first.left = u1 - u0;
+                first.next(a);
+                first.begun = 0;
+                for (int w = 0; w < kNT / 32; ++w) sh.seg[w] = first;
                 break;
             }
             at += n;
@@ -268,8 +278,15 @@ __global__ void __launch_bounds__(kNT, 1)
         }
     }
     __syncthreads();
-    Walk walk{sh.b0, sh.off, u1 - u0};
-    Segment s;
+    Segment &s = sh.seg[warp];
+    auto next_segment = [&]() -> bool {
+        bool more = false;
+        __syncwarp();
+        if (lane == 0) more = s.next(a);
+        more = __shfl_sync(kFull, more, 0);   // (the other lanes see the segment from here on)
+        __syncwarp();
+        return more;
+    };
     const uint32_t tmem = sh.tmem;
     const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + DP};
     constexpr uint32_t kIdS = tc::shape(Half<T>::kBf16, kTile, false), kIdO = tc::shape(Half<T>::kBf16, DP, true);
@@ -300,41 +317,41 @@ __global__ void __launch_bounds__(kNT, 1)
             // that order, so that a warp's wait for a stage is never two phases ahead.
             const bool keys = warp == 0;
             const CUtensorMap *map = keys ? &kmap : &vmap;
-            const int bpt = kTile / box, group = 32 / bpt;   // boxes a tile; tiles whose pages the lanes hold
+            const int bpt = kTile / box, group = 32 / bpt;   // boxes a tile; tiles whose pages the lanes hold (powers of two)
+            const int page_bits = 31 - __clz(a.page);
             unsigned n0 = 0, segs = 0, last = 0;
             bool ok = true;
-            if (lane == 0) {
-                tc::prefetch_map(&qmap);
-                tc::prefetch_map(map);
-            }
-            while (ok && walk.next(a, s)) {
-                const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
+            while (ok && next_segment()) {
+                const int t0 = s.t0, nt = s.t1 - t0, ahead = s.act == 2 ? 1 : 2, head = s.h, end = s.L + s.count;
+                const int32_t *row = a.table + (long long)s.b * a.M;
                 // lane l: the page of box l % bpt of tile l / bpt of the group
                 auto pages = [&](int t) -> int {
-                    const long long key = (long long)(s.t0 + t) * kTile + lane * box;
-                    if (t + lane / bpt >= nt || key >= s.L + s.count) return -1;
-                    const int p = a.table[(long long)s.b * a.M + key / a.page];
-                    if (p >= 0 && p < a.P) return p;
-                    raise_status(a.status, SPEC_ERR_BAD_PAGE);
-                    return -1;   // (the copy fills zeros)
+                    const long long key = (long long)(t0 + t) * kTile + lane * box;
+                    if (t + lane / bpt >= nt || key >= end) return -1;
+                    return row[key >> page_bits];   // (looked at when it is used)
                 };
                 int now = pages(0), next = pages(group);
                 for (int t = 0; ok && t < nt; ++t) {
-                    if (t && t % group == 0) {
+                    if (t && (t & (group - 1)) == 0) {
                         now = next;
                         next = pages(t + group);
                     }
                     const unsigned n = n0 + (keys ? (t < ahead ? t : ahead + 2 * (t - ahead) + 1) : (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t));
                     const int st = n % S;
                     if (n >= S && !(ok = wait_warp(&bars.empty[st], (n / S + 1) & 1))) break;
-                    const int boxes = (s.keys(s.t0 + t) + box - 1) / box;
+                    const int boxes = (min(kTile, end - (t0 + t) * kTile) + box - 1) / box;
                     const uint32_t bar = tc::smem(&bars.full[st]), dst = ring + st * SM::kStage;
                     if (lane == 0) tc::bar_expect(bar, (uint32_t)boxes * box * 128 * DC);
                     __syncwarp();
                     const int bx = DC == 2 ? lane >> 1 : lane, c = DC == 2 ? lane & 1 : 0;   // (at most 16 boxes)
-                    const int p = __shfl_sync(kFull, now, t % group * bpt + min(bx, bpt - 1));
-                    if (bx < boxes)
-                        tc::load_tile(dst + c * kChunk + bx * box * 128, map, bar, c * 64, s.h, ((s.t0 + t) * kTile + bx * box) % a.page, p);
+                    int p = __shfl_sync(kFull, now, (t & (group - 1)) * bpt + min(bx, bpt - 1));
+                    if (bx < boxes) {
+                        if (p < 0 || p >= a.P) {
+                            raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                            p = -1;   // (the copy fills zeros)
+                        }
+                        tc::load_tile(dst + c * kChunk + bx * box * 128, map, bar, c * 64, head, ((t0 + t) * kTile + bx * box) & (a.page - 1), p);
+                    }
                     last = n + 1;
                     if (keys && t == min(nt, ahead) - 1) {
                         if (segs > 0 && !(ok = wait_warp(&bars.q_empty, (segs + 1) & 1))) break;
@@ -366,49 +383,63 @@ __global__ void __launch_bounds__(kNT, 1)
             unsigned n0 = 0, segs = 0, done0 = 0, done1 = 0;
             uint32_t fixed = 0;   // per stage: parity of the next wait for checked values
             bool ok = true;
-            while (ok && walk.next(a, s)) {
+            while (ok && next_segment()) {
                 const int two = s.act == 2, nt = s.t1 - s.t0, ahead = two ? 1 : 2, jobs = two ? 2 * nt : nt;
-                // S of job j: the tile's keys are at this place in the order of copies
-                auto scores = [&](int j) -> bool {
-                    const int g = j & 1, t = two ? j >> 1 : j;
-                    const unsigned at = n0 + (t < ahead ? t : 2 * t - ahead + 1), st = at % S;
-                    if ((!two || g == 0) && !wait_warp(&bars.full[st], (at / S) & 1)) return false;
-                    tc::fence_after();
-                    const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g * SM::kStage : 0), 16));
-                    const uint32_t k = tc::uniform(tc::operand_lo(ring + st * SM::kStage, 16));
-                    const uint32_t d = tc::uniform(tS[0] + g * 128);
-                    if (lead) {
-#pragma unroll
-                        for (int i = 0; i < DC * 4; ++i) {
-                            const uint32_t o = ((i >> 2) * kChunk + (i & 3) * 32) >> 4;
-                            tc::mma_ss(d, tc::operand(q + o), tc::operand(k + o), kIdS, i > 0);
-                        }
-                        tc::commit(tc::smem(&bars.s_full[g]));
-                        if (!two || g == 1) tc::commit(tc::smem(&bars.empty[st]));
-                        if (j == jobs - 1) tc::commit(tc::smem(&bars.q_empty));
-                    }
-                    __syncwarp();
-                    return true;
+                const int tails = max(0, s.L / kTile - s.t0);                   // tiles from here on hold nodes' keys
+                const int end_steps = (s.keys(s.t1 - 1) + 15) / 16;             // products of the last tile
+                // the places of a job's keys and values in the order of copies
+                auto kplace = [&](int j) -> unsigned {
+                    const int t = two ? j >> 1 : j;
+                    return n0 + (t < ahead ? t : 2 * t - ahead + 1);
                 };
+                auto keys_there = [&](int j) -> bool {
+                    const unsigned at = kplace(j);
+                    return (two && (j & 1)) || wait_warp(&bars.full[at % S], (at / S) & 1);
+                };
+                // S of job j
+                auto scores = [&](int j, uint32_t q, uint32_t k, uint32_t d) {
+                    const int g = j & 1;
+#pragma unroll
+                    for (int i = 0; i < DC * 4; ++i) {
+                        const uint32_t o = ((i >> 2) * kChunk + (i & 3) * 32) >> 4;
+                        tc::mma_ss(d, tc::operand(q + o), tc::operand(k + o), kIdS, i > 0);
+                    }
+                    tc::commit(tc::smem(&bars.s_full[g]));
+                    if (!two || g == 1) tc::commit(tc::smem(&bars.empty[kplace(j) % S]));
+                    if (j == jobs - 1) tc::commit(tc::smem(&bars.q_empty));
+                };
+                const uint32_t q0 = tc::operand_lo(base, 16), q1 = two ? q0 + (SM::kStage >> 4) : q0;
                 if (!wait_warp(&bars.q_full, segs & 1)) break;
-                ok = scores(0) && (jobs < 2 || scores(1));
+                for (int j = 0; ok && j < min(jobs, 2); ++j) {
+                    if (!(ok = keys_there(j))) break;
+                    const uint32_t q = tc::uniform(j ? q1 : q0), k = tc::uniform(tc::operand_lo(ring + kplace(j) % S * SM::kStage, 16));
+                    const uint32_t d = tc::uniform(tS[0] + (j & 1) * 128);
+                    tc::fence_after();
+                    if (lead) scores(j, q, k, d);
+                    __syncwarp();
+                }
+                // Job j's P V, then job j + 2's Q K^T into the same columns: all that they wait for but P
+                // is waited for before P, so that the tensor cores get both without a pause.
                 for (int j = 0; ok && j < jobs; ++j) {
                     const int g = j & 1, t = two ? j >> 1 : j;
                     const unsigned at = n0 + (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t), st = at % S;
+                    const bool more = j + 2 < jobs;
                     if (!two || g == 0) {
                         ok = wait_warp(&bars.full[st], (at / S) & 1);
-                        if (ok && s.tail(s.t0 + t)) {
+                        if (ok && t >= tails) {
                             ok = wait_warp(&bars.fixed[st], fixed >> st & 1);
                             fixed ^= 1u << st;
                         }
                         if (!ok) break;
                     }
+                    if (more && !(ok = keys_there(j + 2))) break;
                     if (j == 0 && segs > 0 && !(ok = wait_warp(&bars.o_free, (segs + 1) & 1))) break;
-                    if (!(ok = wait_warp(&bars.p_ready[g], (g ? done1 : done0) & 1))) break;
-                    tc::fence_after();
                     const uint32_t v = tc::uniform(tc::operand_lo(ring + st * SM::kStage, kChunk));
                     const uint32_t d = tc::uniform(tO[0] + g * DP), p = tc::uniform(tS[0] + g * 128);
-                    const int steps = (s.keys(s.t0 + t) + 15) / 16;
+                    const uint32_t q = tc::uniform(g ? q1 : q0), k = tc::uniform(tc::operand_lo(ring + kplace(j + 2) % S * SM::kStage, 16));
+                    const int steps = t == nt - 1 ? end_steps : kTile / 16;
+                    if (!(ok = wait_warp(&bars.p_ready[g], (g ? done1 : done0) & 1))) break;
+                    tc::fence_after();
                     if (lead) {
                         if (steps == kTile / 16) {
 #pragma unroll
@@ -418,11 +449,11 @@ __global__ void __launch_bounds__(kNT, 1)
                         }
                         tc::commit(tc::smem(&bars.pv_done[g]));
                         if (!two || g == 1) tc::commit(tc::smem(&bars.empty[st]));
+                        if (more) scores(j + 2, q, k, p);
                     }
                     __syncwarp();
                     if (g) ++done1;
                     else ++done0;
-                    if (j + 2 < jobs) ok = scores(j + 2);
                 }
                 n0 += 2 * nt;
                 ++segs;
@@ -439,7 +470,7 @@ __global__ void __launch_bounds__(kNT, 1)
             int4 join = make_int4(-1, 0, 0, 0);
             long long at_unit = u0;
             bool ok = true;
-            while (ok && walk.next(a, s)) {
+            while (ok && next_segment()) {
                 const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
                 if (s.t0 == 0 && s.t1 < s.tiles) join = make_int4(s.b, s.h, s.pair, (int)((at_unit + s.tiles - 1) / per));
                 at_unit += nt;
@@ -453,7 +484,7 @@ __global__ void __launch_bounds__(kNT, 1)
                     const int v = x < min(nt, ahead) ? -1 : x - min(nt, ahead), lag = nt - min(nt, ahead);
                     // values and keys take turns while there are keys left
                     const int t = v < 0 ? -1 : v < 2 * lag ? (v & 1 ? -1 : v >> 1) : v - lag;
-                    if (t < 0 || !s.tail(s.t0 + t)) {
+                    if (t < 0 || s.t0 + t < s.L / kTile) {
                         if (lane == 0) tc::bar_arrive(tc::smem(&bars.empty[st]));
                         continue;
                     }
@@ -503,13 +534,13 @@ __global__ void __launch_bounds__(kNT, 1)
         const uint32_t mS = tS[g] + row_lane;
         unsigned segs = 0, merges = 0, own = 0, other = 0;   // jobs of this stream and the other so far
         bool ok = true;
-        while (ok && walk.next(a, s)) {
-            const int jobs = s.jobs();
+        while (ok && next_segment()) {
+            const int first = s.t0, step = s.act == 2, tails = s.L / kTile, jobs = (s.t1 - first) << step;
             // what this row sees of the nodes
             const int tile0 = 2 * s.pair + (s.act == 2 ? g : 0), node = tile0 * a.nodes + r / a.G;
             const bool real = r < a.nodes * a.G && node < s.count;
             uint32_t v0 = 0, v1 = 0, v2 = 0, v3 = 0;
-            if (real && s.tail(s.t1 - 1)) {
+            if (real && s.t1 > tails) {
                 for (int j = node; j >= 0; j = parent_of(a, s.b, j)) {
                     const uint32_t bit = 1u << (j & 31);
                     const int w = j >> 5;
@@ -519,9 +550,15 @@ __global__ void __launch_bounds__(kNT, 1)
                     else v3 |= bit;
                 }
             }
+            const bool idle = !__any_sync(kFull, real);   // a warp without rows: what it leaves in P stays in its rows
             float m = neg_inf(), l = 0.f;
             for (int j = g; j < jobs; j += 2) {
                 if (!(ok = wait_warp(&bars.s_full[g], own & 1))) break;
+                if (idle) {
+                    if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
+                    ++own;
+                    continue;
+                }
                 tc::fence_after();
                 float x[4][32];
 #pragma unroll
@@ -532,8 +569,8 @@ __global__ void __launch_bounds__(kNT, 1)
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
                         for (int i = 0; i < 32; ++i) x[c][i] = -x[c][i];
-                const int t = s.tile(j);
-                if (s.tail(t)) {
+                const int t = first + (step ? j >> 1 : j);
+                if (t >= tails) {
                     const int d = t * kTile - s.L;   // node of the tile's first key
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -638,7 +675,7 @@ __global__ void __launch_bounds__(kNT, 1)
             const long long row = ((long long)s.b * a.N + node) * a.Hq + hq;
             const long long slot = ((long long)me * 2 + (s.t0 == 0 ? 1 : 0)) * 2 + (two ? g : 0);
 #pragma unroll 1
-            for (int c = c0; c < c1; ++c) {
+            for (int c = idle ? c1 : c0; c < c1; ++c) {
                 float o[32];
                 tc::tmem_load(tO[two ? g : 0] + row_lane + c * 32, o);
                 tc::tmem_wait_load();
@@ -713,22 +750,41 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
     if (m_tile > 1 || node >= count) return;
     const int first = blockIdx.x, pieces = join.w - first + 1;
     auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + m_tile; };
-    float m = neg_inf();
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) m = fmaxf(m, a.part_ml[slot(i) * kTile + r].x);
-    const float ref = m == neg_inf() ? 0.f : m;
-    float l = 0.f;
+    float m = neg_inf(), l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = 0; i < pieces; ++i) {
-        const float2 ml = a.part_ml[slot(i) * kTile + r];
-        const float4 v = a.part_o[(slot(i) * (DP / 4) + c4) * kTile + r];
-        const float w = ex2(ml.x - ref);
-        l = fmaf(ml.y, w, l);
-        o.x = fmaf(v.x, w, o.x);
-        o.y = fmaf(v.y, w, o.y);
-        o.z = fmaf(v.z, w, o.z);
-        o.w = fmaf(v.w, w, o.w);
+    constexpr int U = 16;   // pieces whose loads are in flight together
+    for (int i0 = 0; i0 < pieces; i0 += U) {
+        float2 ml[U];
+        float4 v[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (i0 + i < pieces) {
+                ml[i] = a.part_ml[slot(i0 + i) * kTile + r];
+                v[i] = a.part_o[(slot(i0 + i) * (DP / 4) + c4) * kTile + r];
+            }
+        }
+        float to = m;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (i0 + i < pieces) to = fmaxf(to, ml[i].x);
+        const float ref = to == neg_inf() ? 0.f : to, keep = ex2(m - ref);
+        m = to;
+        l *= keep;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (i0 + i < pieces) {
+                const float w = ex2(ml[i].x - ref);
+                l = fmaf(ml[i].y, w, l);
+                o.x = fmaf(v[i].x, w, o.x);
+                o.y = fmaf(v[i].y, w, o.y);
+                o.z = fmaf(v[i].z, w, o.z);
+                o.w = fmaf(v[i].w, w, o.w);
+            }
+        }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const long long row = ((long long)join.x * a.N + node) * a.Hq + join.y * a.G + r % a.G;
@@ -821,7 +877,7 @@ static size_t workspace_bytes_for(const spec_attend_params *p) {
 
 template <typename T, int DC>
 static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, int box, cudaStream_t st) {
-    constexpr size_t smem = AttendSmem<DC>::kTiles + sizeof(AttendShared);
+    constexpr size_t smem = AttendSmem<DC>::kTiles + sizeof(AttendShared<AttendSmem<DC>::kStages>);
     static_assert(smem <= 227 * 1024, "shared memory");
     static std::mutex mu;
     static bool done[64];
@@ -839,19 +895,22 @@ static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, i
     int ctas = sm_count();
     if (ctas < 1) return cudaErrorUnknown;
     if (ctas > kMaxCtas) ctas = kMaxCtas;
-    attend_kernel<T, DC><<<ctas, kNT, smem, st>>>(a, maps[0], maps[1], maps[2], box);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    const int tiles = (a.N + a.nodes - 1) / a.nodes, rows = tiles > 1 ? 2 * a.nodes * a.G : a.N * a.G;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ctas, (rows + kJoinRows - 1) / kJoinRows);
-    cfg.blockDim = dim3(DC * 16 * kJoinRows);
-    cfg.stream = st;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas);
+    cfg.blockDim = dim3(kNT);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DC>, a, maps[0], maps[1], maps[2], box);
+    if (e != cudaSuccess) return e;
+    const int tiles = (a.N + a.nodes - 1) / a.nodes, rows = tiles > 1 ? 2 * a.nodes * a.G : a.N * a.G;
+    cfg.gridDim = dim3(ctas, (rows + kJoinRows - 1) / kJoinRows);
+    cfg.blockDim = dim3(DC * 16 * kJoinRows);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<T, DC>, a);
 }
 
