@@ -291,20 +291,17 @@ __global__ void __launch_bounds__(kNT, 1)
     const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + DP};
     constexpr uint32_t kIdS = tc::shape(Half<T>::kBf16, kTile, false), kIdO = tc::shape(Half<T>::kBf16, DP, true);
 
-    // A wait that gives up: the CTA's other waits then do, too.
-    auto wait = [&](const uint64_t *bar, uint32_t parity) -> bool {
+    // A wait that gives up: the CTA's other waits then do, too. (The lanes vote, so that the
+    // loop does not diverge.)
+    auto wait_warp = [&](const uint64_t *bar, uint32_t parity) -> bool {
         const uint32_t addr = tc::smem(bar);
         for (unsigned i = 0; i < kSpin; ++i) {
-            if (tc::bar_try(addr, parity)) return true;
-            if (*(volatile int *)&sh.abort) return false;
+            if (__all_sync(kFull, tc::bar_try(addr, parity))) return true;
+            if (__any_sync(kFull, *(volatile int *)&sh.abort)) return false;
         }
         *(volatile int *)&sh.abort = 1;
         raise_status(a.status, SPEC_ERR_TIMEOUT);
         return false;
-    };
-    auto wait_warp = [&](const uint64_t *bar, uint32_t parity) -> bool {
-        const bool ok = wait(bar, parity);
-        return __all_sync(kFull, ok);
     };
 
     // 168 registers a thread at the launch: 96 for four warps and 200 for eight
