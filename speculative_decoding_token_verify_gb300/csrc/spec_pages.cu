@@ -9,6 +9,7 @@
 // warps, and the cluster's earlier CTAs. Reference counts change by integer
 // atomics, whose order cannot be seen.
 #include <climits>
+#include <mutex>
 
 #include "spec_rows.cuh"
 
@@ -16,7 +17,8 @@ namespace sr {
 
 constexpr int NTP = 1024;
 constexpr int NWP = NTP / 32;
-constexpr int kMaxPagesCluster = 8;
+constexpr int kMaxPagesCluster = 16;
+constexpr int U = 8;   // groups of 32 entries whose loads are in flight together
 
 struct PagesArgs {
     const int32_t *table, *refs, *lengths, *parent;
@@ -27,8 +29,8 @@ struct PagesArgs {
 };
 
 struct PagesShared {
-    int warp[NWP];            // a count per warp
-    int cta[2][16];           // and per CTA of the cluster, for two counts
+    int warp[2][NWP];         // two counts per warp
+    int cta[2][16];           // and per CTA of the cluster
 };
 
 __device__ __forceinline__ void cluster_sync_all(int C) {
@@ -40,33 +42,44 @@ __device__ __forceinline__ void cluster_sync_all(int C) {
     }
 }
 
-// From every warp's count: how many come before this warp in the cluster, and in
-// all. Ends with a cluster barrier, before which the caller's writes also count.
-__device__ __forceinline__ void ranks(PagesShared &sh, int slot, int mine, int C, int rank, int &before, int &total) {
+// From every warp's counts, in the K slots from `slot` on: how many come before this warp in
+// the cluster, and in all. Ends with a cluster barrier, before which the caller's writes
+// also count.
+template <int K>
+__device__ __forceinline__ void ranks(PagesShared &sh, int slot, const int (&mine)[K], int C, int rank, int (&before)[K], int (&total)[K]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (lane == 0) sh.warp[warp] = mine;
+    if (lane == 0)
+        for (int k = 0; k < K; ++k) sh.warp[slot + k][warp] = mine[k];
     __syncthreads();
-    if (threadIdx.x < C) {
+    if (threadIdx.x < C * K) {
+        const int k = threadIdx.x / C, to = threadIdx.x - k * C;
         int sum = 0;
-        for (int w = 0; w < NWP; ++w) sum += sh.warp[w];
-        if (C > 1) peer_store_u32(peer(&sh.cta[slot][rank], threadIdx.x), (uint32_t)sum);
-        else sh.cta[slot][0] = sum;
+        for (int w = 0; w < NWP; ++w) sum += sh.warp[slot + k][w];
+        if (C > 1) peer_store_u32(peer(&sh.cta[slot + k][rank], to), (uint32_t)sum);
+        else sh.cta[slot + k][0] = sum;
     }
-    before = 0;
-    for (int w = 0; w < warp; ++w) before += sh.warp[w];
+    for (int k = 0; k < K; ++k) {
+        before[k] = 0;
+        for (int w = 0; w < warp; ++w) before[k] += sh.warp[slot + k][w];
+    }
     cluster_sync_all(C);
-    total = 0;
-    for (int c = 0; c < C; ++c) {
-        if (c < rank) before += sh.cta[slot][c];
-        total += sh.cta[slot][c];
+    for (int k = 0; k < K; ++k) {
+        total[k] = 0;
+        for (int c = 0; c < C; ++c) {
+            if (c < rank) before[k] += sh.cta[slot + k][c];
+            total[k] += sh.cta[slot + k][c];
+        }
     }
 }
 
-// A warp's stretch of n entries, in whole groups of 32.
+// A warp's stretch of n entries, in whole groups of 32 (of at least U, so that few entries
+// are not spread thin).
 struct Stretch {
     long long lo, hi;
     __device__ __forceinline__ Stretch(long long n, int warp, int warps) {
-        const long long groups = (n + 31) / 32, per = (groups + warps - 1) / warps;
+        const long long groups = (n + 31) / 32;
+        long long per = (groups + warps - 1) / warps;
+        if (per < U && per > 1) per = min((long long)U, groups);
         lo = min(n, warp * per * 32);
         hi = min(n, (warp + 1) * per * 32);
     }
@@ -76,34 +89,53 @@ __device__ __forceinline__ int lanes_below(unsigned ballot) {
     return __popc(ballot & ((1u << (threadIdx.x & 31)) - 1));
 }
 
-// list[k] = the k-th lowest free page, for k < wanted; the number of free pages
-__device__ __forceinline__ int free_pages(const PagesArgs &a, PagesShared &sh, int wanted, int C, int rank, int gw) {
-    const int lane = threadIdx.x & 31;
-    const Stretch s(a.P, gw, C * NWP);
-    int count = 0, before, total;
-    for (long long i = s.lo + lane; i < s.hi + lane; i += 32)
-        count += __popc(__ballot_sync(kFull, i < s.hi && __ldcg(a.out_refs + i) == 0));
-    ranks(sh, 1, count, C, rank, before, total);
-    for (long long i = s.lo + lane; i < s.hi + lane && before < wanted; i += 32) {
-        const bool free = i < s.hi && __ldcg(a.out_refs + i) == 0;
-        const unsigned all = __ballot_sync(kFull, free);
-        const int k = before + lanes_below(all);
-        if (free && k < wanted) a.list[k] = (int)i;
-        before += __popc(all);
+// U entries of a warp's stretch of pages from i on: whether each is free. (A page that a row
+// has claimed is kept by it where nothing else names it.)
+template <bool kClaims>
+__device__ __forceinline__ void free_of(const PagesArgs &a, long long i, long long hi, bool (&free)[U]) {
+    int refs[U], claim[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        refs[u] = i + 32 * u < hi ? __ldcg(a.out_refs + i + 32 * u) : -1;
+        if (kClaims) claim[u] = i + 32 * u < hi ? __ldcg(a.claim + i + 32 * u) : 0;
     }
-    cluster_sync_all(C);
-    return total;
+#pragma unroll
+    for (int u = 0; u < U; ++u) free[u] = refs[u] == 0 && (!kClaims || claim[u] == INT_MAX);
+}
+template <bool kClaims>
+__device__ __forceinline__ int count_free(const PagesArgs &a, const Stretch &s) {
+    int count = 0;
+    for (long long i = s.lo + (threadIdx.x & 31); i < s.hi + (threadIdx.x & 31); i += 32 * U) {
+        bool free[U];
+        free_of<kClaims>(a, i, s.hi, free);
+#pragma unroll
+        for (int u = 0; u < U; ++u) count += __popc(__ballot_sync(kFull, free[u]));
+    }
+    return count;
+}
+// list[k] = the k-th lowest free page, for k < wanted; `before` free ones lie in front of the stretch
+template <bool kClaims>
+__device__ __forceinline__ void list_free(const PagesArgs &a, const Stretch &s, int before, int wanted) {
+    for (long long i = s.lo + (threadIdx.x & 31); i < s.hi + (threadIdx.x & 31) && before < wanted; i += 32 * U) {
+        bool free[U];
+        free_of<kClaims>(a, i, s.hi, free);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const unsigned all = __ballot_sync(kFull, free[u]);
+            const int k = before + lanes_below(all);
+            if (free[u] && k < wanted) a.list[k] = (int)i + 32 * u;
+            before += __popc(all);
+        }
+    }
 }
 
-__device__ __forceinline__ int pages_for(const PagesArgs &a, int length) {
-    const long long most = (long long)a.M * a.page;
-    if (length < 0 || length > most) {
-        raise_status(a.status, SPEC_ERR_BAD_LENGTH);
-        length = length < 0 ? 0 : (int)most;
-    }
-    return (int)(((long long)length + a.page - 1) / a.page);
+// a length within [0, M page] (M page < 2^31)
+__device__ __forceinline__ int fit(const PagesArgs &a, int length) {
+    const int most = a.M * a.page;
+    if (length >= 0 && length <= most) return length;
+    raise_status(a.status, SPEC_ERR_BAD_LENGTH);
+    return length < 0 ? 0 : most;
 }
-
 // entry i of a table as (row, place), moved on by 32 without a division most of the time
 struct Place {
     int r, m;
@@ -122,59 +154,80 @@ struct Place {
 __global__ void __launch_bounds__(NTP, 1) resize_kernel(PagesArgs a, int C) {
     __shared__ PagesShared sh;
     const int rank = C > 1 ? blockIdx.x : 0, lane = threadIdx.x & 31, gw = rank * NWP + (threadIdx.x >> 5);
-    if (a.out_refs != a.refs)
-        for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) a.out_refs[i] = a.refs[i];
+    if (a.out_refs != a.refs) {
+#pragma unroll 8
+        for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) a.out_refs[i] = __ldg(a.refs + i);
+    }
     cluster_sync_all(C);   // (from here on every CTA of the cluster has shared memory to write to)
     const Stretch s((long long)a.B * a.W * a.M, gw, C * NWP);
-    int wants = 0, before, wanted;
+    const int most = a.M * a.page;
+    int wants = 0;
     {
         Place at(s.lo + lane, a.M);
-        int row = -1, need = 0;
-        for (long long i = s.lo + lane; i < s.hi + lane; i += 32, at.next(a.M)) {
-            bool want = false;
-            if (i < s.hi) {
-                if (at.r != row) need = pages_for(a, a.lengths[row = at.r]);
-                const int e = a.table[i];
-                const bool has = e >= 0 && e < a.P;
-                if (!has && e != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
-                want = !has && at.m < need;
-                if (has && at.m >= need) atomicAdd(a.out_refs + e, -1);
+        for (long long i = s.lo + lane; i < s.hi + lane; i += 32 * U) {
+            int e[U], len[U], m[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u, at.next(a.M)) {
+                m[u] = at.m;
+                e[u] = i + 32 * u < s.hi ? a.table[i + 32 * u] : -1;
+                len[u] = i + 32 * u < s.hi ? a.lengths[at.r] : 0;
             }
-            wants += __popc(__ballot_sync(kFull, want));
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool has = e[u] >= 0 && e[u] < a.P, in = m[u] * a.page < len[u];   // in: m < ceil(len / page)
+                if (!has && e[u] != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                if (len[u] < 0 || len[u] > most) raise_status(a.status, SPEC_ERR_BAD_LENGTH);
+                if (has && !in) atomicAdd(a.out_refs + e[u], -1);
+                wants += __popc(__ballot_sync(kFull, !has && in));
+            }
         }
     }
-    ranks(sh, 0, wants, C, rank, before, wanted);
-    int nfree = 0;
-    if (wanted > 0) nfree = free_pages(a, sh, wanted, C, rank, gw);
+    int ahead[1], all_wants[1];
+    ranks<1>(sh, 0, {wants}, C, rank, ahead, all_wants);
+    const int wanted = all_wants[0];
+    int before = ahead[0], nfree = 0;
+    if (wanted > 0) {   // (the same for the whole cluster)
+        const Stretch pages(a.P, gw, C * NWP);
+        int all_free[1];
+        ranks<1>(sh, 1, {count_free<false>(a, pages)}, C, rank, ahead, all_free);
+        nfree = all_free[0];
+        list_free<false>(a, pages, ahead[0], wanted);
+        cluster_sync_all(C);
+    }
     if (nfree < wanted && rank == 0 && threadIdx.x == 0) raise_status(a.status, SPEC_ERR_NO_PAGES);
     {
         Place at(s.lo + lane, a.M);
-        int row = -1, need = 0;
-        for (long long i = s.lo + lane; i < s.hi + lane; i += 32, at.next(a.M)) {
-            int e = -1;
-            bool want = false;
-            if (i < s.hi) {
-                if (at.r != row) need = pages_for(a, a.lengths[row = at.r]);
-                e = a.table[i];
-                const bool has = e >= 0 && e < a.P;
-                want = !has && at.m < need;
-                if (!has || at.m >= need) e = -1;
+        for (long long i = s.lo + lane; i < s.hi + lane; i += 32 * U) {
+            int e[U], len[U], m[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u, at.next(a.M)) {
+                m[u] = at.m;
+                e[u] = i + 32 * u < s.hi ? a.table[i + 32 * u] : -1;
+                len[u] = i + 32 * u < s.hi ? a.lengths[at.r] : 0;
             }
-            const unsigned all = __ballot_sync(kFull, want);
-            const int k = before + lanes_below(all);
-            if (want && k < nfree) {
-                e = __ldcg(a.list + k);
-                a.out_refs[e] = 1;
+            int k[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const bool has = e[u] >= 0 && e[u] < a.P, in = m[u] * a.page < len[u], want = !has && in;
+                if (!has || !in) e[u] = -1;
+                const unsigned all = __ballot_sync(kFull, want);
+                k[u] = want ? before + lanes_below(all) : INT_MAX;
+                before += __popc(all);
             }
-            before += __popc(all);
-            if (i < s.hi) a.out_table[i] = e;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (k[u] < nfree) e[u] = __ldcg(a.list + k[u]);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (k[u] < nfree) a.out_refs[e[u]] = 1;
+                if (i + 32 * u < s.hi) a.out_table[i + 32 * u] = e[u];
+            }
         }
     }
 }
 
 // What new row (b, n) continues: its old row's index (-1: none) and length.
-__device__ __forceinline__ int source_row(const PagesArgs &a, int r, int &length) {
-    const int b = r / a.N, n = r - b * a.N;
+__device__ __forceinline__ int source_row(const PagesArgs &a, int r, int b, int n, int &length) {
     int w = a.parent[r];
     if (w < -1 || w >= a.W) {
         raise_status(a.status, SPEC_ERR_BAD_PARENT);
@@ -184,12 +237,7 @@ __device__ __forceinline__ int source_row(const PagesArgs &a, int r, int &length
     length = 0;
     if (w < 0) return -1;
     const int src = b * a.W + w;
-    length = a.lengths[src];
-    const long long most = (long long)a.M * a.page;
-    if (length < 0 || length > most) {
-        raise_status(a.status, SPEC_ERR_BAD_LENGTH);
-        length = length < 0 ? 0 : (int)most;
-    }
+    length = fit(a, a.lengths[src]);
     return src;
 }
 
@@ -204,39 +252,54 @@ __device__ __forceinline__ int entry(const PagesArgs &a, int row, int m) {
 __global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
     __shared__ PagesShared sh;
     const int rank = C > 1 ? blockIdx.x : 0, lane = threadIdx.x & 31, gw = rank * NWP + (threadIdx.x >> 5);
-    for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) {
-        if (a.out_refs != a.refs) a.out_refs[i] = a.refs[i];
-        a.claim[i] = INT_MAX;
+    for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) a.claim[i] = INT_MAX;
+    if (a.out_refs != a.refs) {
+#pragma unroll 8
+        for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) a.out_refs[i] = __ldg(a.refs + i);
     }
     cluster_sync_all(C);
     // full pages: the old row's entries lose a reference, the new row's gain one
     {
         const Stretch s((long long)a.B * a.N * a.M, gw, C * NWP);
         Place at(s.lo + lane, a.M);
-        int row = -1, src = -1, length = 0, full = 0, own = -1;
-        for (long long i = s.lo + lane; i < s.hi; i += 32, at.next(a.M)) {
-            if (at.r != row) {
-                row = at.r;
-                src = source_row(a, row, length);
-                full = length / a.page;
-                const int b = row / a.N, n = row - b * a.N;
-                own = n < a.W ? b * a.W + n : -1;
+        for (long long i = s.lo + lane; i < s.hi; i += 32 * U) {
+            int e[U], old[U], row[U];
+            bool last[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u, at.next(a.M)) {
+                e[u] = old[u] = -1;
+                row[u] = at.r;
+                last[u] = false;
+                if (i + 32 * u < s.hi) {
+                    const int b = at.r / a.N, n = at.r - b * a.N;
+                    int length;
+                    const int src = source_row(a, at.r, b, n, length), from = at.m * a.page;
+                    if (from < length) {   // (src >= 0 then)
+                        e[u] = a.table[(long long)src * a.M + at.m];
+                        last[u] = length - from < a.page;
+                        if (e[u] < 0 || e[u] >= a.P) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                    }
+                    if (n < a.W) old[u] = a.table[(long long)(b * a.W + n) * a.M + at.m];
+                }
             }
-            int e = -1;
-            if (src >= 0 && (at.m < full || (at.m == full && length % a.page))) {
-                e = entry(a, src, at.m);
-                if (e < 0) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (i + 32 * u >= s.hi) continue;
+                if (e[u] < 0 || e[u] >= a.P) e[u] = -1;
+                if (old[u] < 0 || old[u] >= a.P) {
+                    if (old[u] != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                    old[u] = -1;
+                }
+                if (last[u]) {
+                    if (e[u] >= 0) atomicMin(a.claim + e[u], row[u]);
+                    e[u] = -1;   // (decided below)
+                }
+                if (old[u] != e[u]) {
+                    if (old[u] >= 0) atomicAdd(a.out_refs + old[u], -1);
+                    if (e[u] >= 0) atomicAdd(a.out_refs + e[u], 1);
+                }
+                a.out_table[i + 32 * u] = e[u];
             }
-            if (at.m == full && e >= 0) {
-                atomicMin(a.claim + e, row);
-                e = -1;   // decided below
-            }
-            const int old = own >= 0 ? entry(a, own, at.m) : -1;
-            if (old != e) {
-                if (old >= 0) atomicAdd(a.out_refs + old, -1);
-                if (e >= 0) atomicAdd(a.out_refs + e, 1);
-            }
-            a.out_table[i] = e;
         }
     }
     if (a.N < a.W) {   // old rows without a new one in their place
@@ -250,13 +313,14 @@ __global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
     }
     cluster_sync_all(C);
     // pages that are not full: kept by the first row that wants them, or copied
-    const Stretch s((long long)a.B * a.N, gw, C * NWP);
-    int wants = 0, before, wanted;
+    const Stretch s((long long)a.B * a.N, gw, C * NWP), pages(a.P, gw, C * NWP);
+    int wants = 0;
     for (long long r = s.lo + lane; r < s.hi + lane; r += 32) {
         bool want = false;
         if (r < s.hi) {
             int length;
-            const int src = source_row(a, (int)r, length), full = length / a.page, part = length % a.page;
+            const int b = (int)r / a.N, src = source_row(a, (int)r, b, (int)r - b * a.N, length);
+            const int full = length / a.page, part = length - full * a.page;
             const int last = src >= 0 && part ? entry(a, src, full) : -1;
             if (last >= 0) {
                 want = __ldcg(a.claim + last) != (int)r || __ldcg(a.out_refs + last) != 0;
@@ -274,24 +338,28 @@ __global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
         }
         wants += __popc(__ballot_sync(kFull, want));
     }
-    ranks(sh, 0, wants, C, rank, before, wanted);
-    if (wanted == 0) return;   // (nothing of the cluster's shared memory is read any more)
-    const int nfree = free_pages(a, sh, wanted, C, rank, gw);
+    // free pages are counted beside it: those that rows keep are claimed
+    int ahead[2], all[2];
+    ranks<2>(sh, 0, {wants, count_free<true>(a, pages)}, C, rank, ahead, all);
+    int before = ahead[0];
+    const int wanted = all[0], nfree = all[1];
+    if (wanted == 0) return;   // (the same for the whole cluster)
+    list_free<true>(a, pages, ahead[1], wanted);
+    cluster_sync_all(C);
     if (nfree < wanted && rank == 0 && threadIdx.x == 0) raise_status(a.status, SPEC_ERR_NO_PAGES);
     for (long long r = s.lo + lane; r < s.hi + lane; r += 32) {
         int32_t *c = a.copies + r * 4;
         const bool want = r < s.hi && c[0] >= 0;   // (written by this thread)
-        const unsigned all = __ballot_sync(kFull, want);
-        const int k = before + lanes_below(all);
+        const unsigned ballot = __ballot_sync(kFull, want);
+        const int k = before + lanes_below(ballot);
         if (want && k < nfree) {
             const int e = __ldcg(a.list + k);
-            int length;
-            source_row(a, (int)r, length);
+            const int length = a.out_lengths[r];   // (written by this thread, as c)
             c[1] = e;
             a.out_refs[e] = 1;
             a.out_table[r * a.M + length / a.page] = e;
         }
-        before += __popc(all);
+        before += __popc(ballot);
     }
 }
 
@@ -311,6 +379,7 @@ constexpr int NTC = 256;
 // copies[y]: the first slots of a page, CP vectors a thread
 template <typename Vec, int CP>
 __global__ void __launch_bounds__(NTC) copy_kernel(CacheArgs a, int count) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched while the stream's last kernel, the fork, ends)
     for (int c = blockIdx.y; c < count; c += gridDim.y) {
         const int src = a.copies[c * 4LL], dst = a.copies[c * 4LL + 1], slots = min(a.copies[c * 4LL + 2], a.page);
         if (src < 0 || src >= a.P || dst < 0 || dst >= a.P || slots <= 0) continue;
@@ -488,6 +557,22 @@ static int pages_cluster(long long ints) {
     return c;
 }
 
+static cudaError_t launch_pages(void (*kernel)(PagesArgs, int), bool *allowed, const PagesArgs &a, int C, cudaStream_t stream) {
+    if (C > 8) {   // (clusters of more than 8 CTAs have to be allowed, once for each device)
+        static std::mutex mu;
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lk(mu);
+        if (!allowed[dev & 63]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (e != cudaSuccess) return e;
+            allowed[dev & 63] = true;
+        }
+    }
+    return launch_cluster(kernel, C, NTP, C, 0, stream, a, C);
+}
+
 static int check_cache(const spec_cache_params *p, const void *cache) {
     if (!p) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "params is NULL");
     if (p->O < 0 || p->P < 0 || p->H < 0 || p->page < 1)
@@ -546,8 +631,16 @@ static cudaError_t launch_copy(CacheArgs &a, int count, cudaStream_t st) {
     const long long gx = (n + NTC * CP - 1) / (NTC * CP);
     const dim3 grid((unsigned)(gx < 1024 ? gx : 1024), (unsigned)(count < 65535 ? count : 65535),
                     (unsigned)(oh < 65535 ? oh : 65535));
-    copy_kernel<Vec, CP><<<grid, NTC, 0, st>>>(a, count);
-    return cudaGetLastError();
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(NTC);
+    cfg.stream = st;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, copy_kernel<Vec, CP>, a, count);
 }
 
 template <typename Vec>
@@ -598,7 +691,8 @@ extern "C" int spec_pages_resize(const spec_pages_params *p, const int32_t *tabl
     a.P = p->P;
     a.page = p->page;
     const int C = pages_cluster(entries + p->P);
-    return done(launch_cluster(resize_kernel, C, NTP, C, 0, static_cast<cudaStream_t>(stream), a, C));
+    static bool allowed[64];
+    return done(launch_pages(resize_kernel, allowed, a, C, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int spec_pages_fork(const spec_pages_params *p, const int32_t *table, const int32_t *refs,
@@ -646,7 +740,8 @@ extern "C" int spec_pages_fork(const spec_pages_params *p, const int32_t *table,
     a.P = p->P;
     a.page = p->page;
     const int C = pages_cluster((rows + out_rows) * p->M + p->P);
-    return done(launch_cluster(fork_kernel, C, NTP, C, 0, static_cast<cudaStream_t>(stream), a, C));
+    static bool allowed[64];
+    return done(launch_pages(fork_kernel, allowed, a, C, static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int spec_pages_copy(const spec_cache_params *p, void *cache, const int32_t *copies, int32_t count,
