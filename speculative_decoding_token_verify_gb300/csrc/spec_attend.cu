@@ -33,9 +33,10 @@ namespace sr {
 
 constexpr int kTile = 128;             // keys a tile, and rows a tile
 constexpr int kChunk = kTile * 128;    // bytes of 64 elements of a tile's rows
-constexpr int kNT = 384;               // keys, products, values' check, values; two softmax warpgroups
+constexpr int kNT = 512;               // warps 0-3 and 12-15 copies and products, 4-7 and 8-11 the streams' softmax
+constexpr int kWarpK = 0, kWarpV = 3, kWarpGo = 2, kWarpMma0 = 1, kWarpMma1 = 14;   // (spread over the four schedulers)
 constexpr unsigned kSpin = 1u << 20;   // polls of a wait before it gives up
-constexpr int kSegRing = 6;            // segments whose flags of non-finite values are kept
+constexpr int kSegRing = 4;            // segments whose flags of non-finite values are kept
 constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
 
 struct AttendArgs {
@@ -46,7 +47,7 @@ struct AttendArgs {
     int32_t *status;
     float4 *part_o;   // [CTA][2][tile][D padded / 4][row]: unnormalised outputs of a sequence's pieces
     float2 *part_ml;  // [CTA][2][tile][row]: their reference (log2) and sum
-    int4 *joins;      // [CTA]: sequence (-1: none), head, pair of tiles, last CTA of what begins here and ends elsewhere
+    int4 *joins;      // [CTA], what begins here and ends elsewhere: sequence (-1: none), head + pair of tiles 2^16, rows, last CTA
     int B, N, Hq, Hkv, G, D, P, page, M, fill;
     int nodes;        // a tile
     float sL;         // |scale| log2 e
@@ -124,14 +125,10 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 // which leaves registers to what the warp does.
 struct Segment {
     int b, h, pair, t0, t1, tiles, L, count;
-    uint8_t act, begun;     // row tiles with nodes; whether next() has given the first one
+    int act;                // row tiles with nodes
     long long off, left;    // units of sequence b behind this piece, and of the CTA's part
     __device__ __forceinline__ int keys(int t) const { return min(kTile, L + count - t * kTile); }
     __device__ __forceinline__ bool next(const AttendArgs &a) {
-        if (!begun) {
-            begun = 1;
-            return t1 > t0;
-        }
         while (left > 0) {
             sequence(a, b, L, count);
             const int pairs = (count + 2 * a.nodes - 1) / (2 * a.nodes);
@@ -156,27 +153,25 @@ struct Segment {
     }
 };
 
+// behind the tiles in shared memory
+template <int SK, int SV>
+struct AttendShared {
+    struct {
+        uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV], s_full[2], p_half[2], p_rest[2], pv_done[2], q_full, q_empty, start, o_free, merge, drain;
+    } bars;
+    float2 ml[2][kTile];
+    Segment seg[13];   // of warps 0-11 and 14
+    uint32_t tmem, bad[kSegRing][4];
+    int abort;
+};
+
 template <int DC>
 struct AttendSmem {
     static constexpr int kStage = DC * kChunk;
-    static constexpr int kStages = DC == 2 ? 5 : 10;
+    static constexpr int kKeys = DC == 2 ? 3 : 5, kValues = DC == 2 ? 2 : 5;   // stages of the rings (keys run ahead)
+    using Shared = AttendShared<kKeys, kValues>;
     static constexpr int kQ = 2 * kStage;
-    static constexpr int kTiles = kQ + kStages * kStage;
-};
-
-// behind the tiles in shared memory
-template <int S>
-struct AttendShared {
-    struct {
-        uint64_t full[S], empty[S], fixed[S], s_full[2], p_ready[2], pv_done[2], q_full, q_empty, o_free, merge, drain;
-    } bars;
-    union {
-        float2 ml[2][kTile];
-        long long sum[kNT / 32];
-    };
-    Segment seg[kNT / 32];
-    uint32_t tmem, bad[kSegRing][4];
-    int abort;
+    static constexpr int kTiles = kQ + (kKeys + kValues) * kStage;
 };
 
 template <typename T, int DC>
@@ -184,87 +179,46 @@ __global__ void __launch_bounds__(kNT, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int box) {
     using SM = AttendSmem<DC>;
-    constexpr int S = SM::kStages, DP = DC * 64;
+    constexpr int SK = SM::kKeys, SV = SM::kValues, DP = DC * 64;
     extern __shared__ __align__(1024) char dyn[];   // (the kernel has no other shared memory, so that this holds)
-    AttendShared<S> &sh = *reinterpret_cast<AttendShared<S> *>(dyn + SM::kTiles);
+    typename SM::Shared &sh = *reinterpret_cast<typename SM::Shared *>(dyn + SM::kTiles);
     auto &bars = sh.bars;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t base = tc::smem(dyn), ring = base + SM::kQ;
+    const uint32_t base = tc::smem(dyn), kring = base + SM::kQ, vring = kring + SK * SM::kStage;
     if (threadIdx.x == 0) {
+        sh.abort = 0;
+        for (int i = 0; i < SK; ++i) {
+            tc::bar_init(tc::smem(&bars.k_full[i]), 1);
+            tc::bar_init(tc::smem(&bars.k_empty[i]), 2);   // the streams' products
+        }
+        for (int i = 0; i < SV; ++i) {
+            tc::bar_init(tc::smem(&bars.v_full[i]), 1);
+            tc::bar_init(tc::smem(&bars.v_empty[i]), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            tc::bar_init(tc::smem(&bars.s_full[i]), 1);
+            tc::bar_init(tc::smem(&bars.p_half[i]), 5);   // four warps, and the copies that the job needs
+            tc::bar_init(tc::smem(&bars.p_rest[i]), 4);
+            tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
+        }
+        tc::bar_init(tc::smem(&bars.q_full), 1);
+        tc::bar_init(tc::smem(&bars.q_empty), 2);
+        tc::bar_init(tc::smem(&bars.start), 1);
+        tc::bar_init(tc::smem(&bars.o_free), 10);          // the softmax's warps and, to keep them in step, the products'
+        tc::bar_init(tc::smem(&bars.merge), 8);
+        tc::bar_init(tc::smem(&bars.drain), 2);
+        tc::fence_barrier_init();
         tc::prefetch_map(&kmap);
         tc::prefetch_map(&qmap);
         tc::prefetch_map(&vmap);
     }
-
-    if (threadIdx.x == 0) {
-        sh.abort = 0;
-        for (int w = 0; w < kNT / 32; ++w) sh.seg[w].t0 = sh.seg[w].t1 = sh.seg[w].begun = 0;
-        for (int i = 0; i < S; ++i) {
-            tc::bar_init(tc::smem(&bars.full[i]), 1);
-            tc::bar_init(tc::smem(&bars.empty[i]), 2);   // the products and the values' check
-            tc::bar_init(tc::smem(&bars.fixed[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            tc::bar_init(tc::smem(&bars.s_full[i]), 1);
-            tc::bar_init(tc::smem(&bars.p_ready[i]), 4);
-            tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
-        }
-        tc::bar_init(tc::smem(&bars.q_full), 1);
-        tc::bar_init(tc::smem(&bars.q_empty), 1);
-        tc::bar_init(tc::smem(&bars.o_free), 8);
-        tc::bar_init(tc::smem(&bars.merge), 8);
-        tc::bar_init(tc::smem(&bars.drain), 1);
-        tc::fence_barrier_init();
-    }
-    if (warp == 1) tc::tmem_alloc(tc::smem(&sh.tmem), 512);
+    if (warp == kWarpMma0) tc::tmem_alloc(tc::smem(&sh.tmem), 512);
     // (so far nothing that an earlier kernel of the stream may write has been read)
     asm volatile("griddepcontrol.wait;" ::: "memory");
-
-    // ---- which part of the line is this CTA's ----------------------------------------
-    const int G = gridDim.x, me = blockIdx.x;
-    const int per_thread = (a.B + kNT - 1) / kNT;
-    const int b_lo = min(a.B, (int)threadIdx.x * per_thread), b_hi = min(a.B, b_lo + per_thread);
-    auto units = [&](int b) -> long long {
-        int L, count;
-        sequence(a, b, L, count);
-        return (long long)a.Hkv * ((count + 2 * a.nodes - 1) / (2 * a.nodes)) * ((L + count + kTile - 1) / kTile);
-    };
-    long long mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += units(b);
-    long long upto = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-        const long long v = __shfl_up_sync(kFull, upto, o);
-        if (lane >= o) upto += v;
-    }
-    if (lane == 31) sh.sum[warp] = upto;
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    long long total = 0;
-    for (int w = 0; w < kNT / 32; ++w) {
-        if (w < warp) upto += sh.sum[w];
-        total += sh.sum[w];
-    }
-    const long long per = (total + G - 1) / G, u0 = min(total, me * per), u1 = min(total, u0 + per);
-    if (u0 < u1 && u0 >= upto - mine && u0 < upto) {   // the thread whose sequences hold u0
-        long long at = upto - mine;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const long long n = units(b);
-            if (u0 < at + n) {
-                Segment first;
-                first.begun = 1;
-                first.b = b;
-                first.off = u0 - at;
-                first.left = u1 - u0;
-                first.next(a);
-                first.begun = 0;
-                for (int w = 0; w < kNT / 32; ++w) sh.seg[w] = first;
-                break;
-            }
-            at += n;
-        }
-    }
+    const int G = gridDim.x, me = blockIdx.x;
     if (a.fill) {   // rows of nodes that do not exist
         const long long rows = (long long)a.B * a.N * a.Hq;
         for (long long r = (long long)me * kNT + threadIdx.x; r < rows; r += (long long)G * kNT) {
@@ -277,8 +231,47 @@ __global__ void __launch_bounds__(kNT, 1)
             if (a.lse) a.lse[r] = neg_inf();
         }
     }
-    __syncthreads();
-    Segment &s = sh.seg[warp];
+
+    // ---- which part of the line is this CTA's: every warp finds it by itself --------------------
+    const bool works = warp < 12 || warp == kWarpMma1;
+    Segment &s = sh.seg[min(warp, 12)];
+    long long per = 1, u0 = 0;
+    if (works) {
+        auto units = [&](int b) -> long long {
+            if (b >= a.B) return 0;
+            int L, count;
+            sequence(a, b, L, count);
+            const int pairs = (count + 2 * a.nodes - 1) / (2 * a.nodes), tiles = (L + count + kTile - 1) / kTile;
+            return (long long)(a.Hkv * pairs) * tiles;
+        };
+        long long total = 0;
+#pragma unroll 4
+        for (int b = lane; b < a.B; b += 32) total += units(b);
+        for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(kFull, total, o);
+        per = quotient(total + G - 1, G);
+        u0 = min(total, me * per);
+        const long long u1 = min(total, u0 + per);
+        long long at = 0;
+        if (lane == 0) s.left = 0;
+        for (int b0 = 0; u0 < u1 && b0 < a.B; b0 += 32) {
+            const long long n = units(b0 + lane);
+            long long upto = n;
+            for (int o = 1; o < 32; o *= 2) {
+                const long long v = __shfl_up_sync(kFull, upto, o);
+                if (lane >= o) upto += v;
+            }
+            const unsigned past = __ballot_sync(kFull, u0 < at + upto);
+            if (past) {
+                if (lane == __ffs(past) - 1) {
+                    s.b = b0 + lane;
+                    s.off = u0 - (at + upto - n);
+                    s.left = u1 - u0;
+                }
+                break;
+            }
+            at += __shfl_sync(kFull, upto, 31);
+        }
+    }
     auto next_segment = [&]() -> bool {
         bool more = false;
         __syncwarp();
@@ -304,19 +297,20 @@ __global__ void __launch_bounds__(kNT, 1)
         return false;
     };
 
-    // 168 registers a thread at the launch: 96 for four warps and 200 for eight
-    if (warp < 4) {
-        tc::fewer_registers<96>();
-        if (warp == 0 || warp == 3) {
-            // ---- copies: warp 0 the queries and keys, warp 3 the values ----------------------------
-            // Both fill one ring of stages, in the order in which the products use them:
-            // `ahead` tiles of keys, then values and keys in turn. The products give stages back in
-            // that order, so that a warp's wait for a stage is never two phases ahead.
-            const bool keys = warp == 0;
+    // 128 registers a thread at the launch: 64 for eight warps and 192 for the eight of the softmax
+    if (warp < 4 || warp >= 12) {
+        tc::fewer_registers<64>();
+        if (warp == kWarpK || warp == kWarpV) {
+            // ---- copies: queries and keys, and values ------------------------------------------------
+            // A ring of stages each, so that every ring is filled and waited for in one order.
+            const bool keys = warp == kWarpK;
             const CUtensorMap *map = keys ? &kmap : &vmap;
+            uint64_t *const full = keys ? bars.k_full : bars.v_full, *const empty = keys ? bars.k_empty : bars.v_empty;
+            const unsigned S = keys ? SK : SV;
+            const uint32_t ring = keys ? kring : vring;
             const int bpt = kTile / box, group = 32 / bpt;   // boxes a tile; tiles whose pages the lanes hold (powers of two)
             const int page_bits = 31 - __clz(a.page);
-            unsigned n0 = 0, segs = 0, last = 0;
+            unsigned n = 0, segs = 0;
             bool ok = true;
             while (ok && next_segment()) {
                 const int t0 = s.t0, nt = s.t1 - t0, ahead = s.act == 2 ? 1 : 2, head = s.h, end = s.L + s.count;
@@ -327,17 +321,31 @@ __global__ void __launch_bounds__(kNT, 1)
                     if (t + lane / bpt >= nt || key >= end) return -1;
                     return row[key >> page_bits];   // (looked at when it is used)
                 };
+                auto queries = [&]() -> bool {
+                    if (segs > 0 && !wait_warp(&bars.q_empty, (segs + 1) & 1)) return false;
+                    if (lane == 0) {
+                        const uint32_t bar = tc::smem(&bars.q_full);
+                        tc::bar_expect(bar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
+                        for (int m = 0; m < s.act; ++m)
+                            for (int x = 0; x < DC; ++x)
+                                tc::load_tile(base + m * SM::kStage + x * kChunk, &qmap, bar, x * 64, head * a.G, (2 * s.pair + m) * a.nodes, s.b);
+                    }
+                    __syncwarp();
+                    ++segs;
+                    return true;
+                };
                 int now = pages(0), next = pages(group);
-                for (int t = 0; ok && t < nt; ++t) {
+                const bool first = segs == 0;   // (later ones: the first keys need not wait for the queries' place)
+                if (keys && first) queries();
+                for (int t = 0; ok && t < nt; ++t, ++n) {
                     if (t && (t & (group - 1)) == 0) {
                         now = next;
                         next = pages(t + group);
                     }
-                    const unsigned n = n0 + (keys ? (t < ahead ? t : ahead + 2 * (t - ahead) + 1) : (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t));
-                    const int st = n % S;
-                    if (n >= S && !(ok = wait_warp(&bars.empty[st], (n / S + 1) & 1))) break;
+                    const unsigned st = n % S;
+                    if (n >= S && !(ok = wait_warp(&empty[st], (n / S + 1) & 1))) break;
                     const int boxes = (min(kTile, end - (t0 + t) * kTile) + box - 1) / box;
-                    const uint32_t bar = tc::smem(&bars.full[st]), dst = ring + st * SM::kStage;
+                    const uint32_t bar = tc::smem(&full[st]), dst = ring + st * SM::kStage;
                     if (lane == 0) tc::bar_expect(bar, (uint32_t)boxes * box * 128 * DC);
                     __syncwarp();
                     const int bx = DC == 2 ? lane >> 1 : lane, c = DC == 2 ? lane & 1 : 0;   // (at most 16 boxes)
@@ -349,111 +357,162 @@ __global__ void __launch_bounds__(kNT, 1)
                         }
                         tc::load_tile(dst + c * kChunk + bx * box * 128, map, bar, c * 64, head, ((t0 + t) * kTile + bx * box) & (a.page - 1), p);
                     }
-                    last = n + 1;
-                    if (keys && t == min(nt, ahead) - 1) {
-                        if (segs > 0 && !(ok = wait_warp(&bars.q_empty, (segs + 1) & 1))) break;
-                        if (lane == 0) {
-                            const uint32_t qbar = tc::smem(&bars.q_full);
-                            tc::bar_expect(qbar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
-                            for (int m = 0; m < s.act; ++m)
-                                for (int x = 0; x < DC; ++x)
-                                    tc::load_tile(base + m * SM::kStage + x * kChunk, &qmap, qbar, x * 64, s.h * a.G, (2 * s.pair + m) * a.nodes, s.b);
-                        }
-                        __syncwarp();
-                        ++segs;
-                    }
+                    if (keys && !first && t == min(nt, ahead) - 1) ok = queries();
                 }
-                n0 += 2 * nt;
             }
             // nothing is left in flight when another role has given up
             if (*(volatile int *)&sh.abort) {
-                for (unsigned i = last > S ? last - S : 0; i < last; ++i)
-                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.full[i % S]), (i / S) & 1); ++k) {}
+                for (unsigned i = n > S ? n - S : 0; i < n; ++i)
+                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&full[i % S]), (i / S) & 1); ++k) {}
                 if (segs > 0)
                     for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full), (segs + 1) & 1); ++k) {}
             }
-        } else if (warp == 1) {
-            // ---- products ---------------------------------------------------------------------
-            // The whole warp walks along, so that operands stay in uniform registers; one
-            // thread issues.
+        } else if (warp == kWarpGo) {
+            // ---- what a job needs: its copies are there, and its values can be multiplied --------------
+            // This warp alone waits for the copies, in their order, and passes a job on when its
+            // values and the keys of the stream's next job are there. (A job before on its
+            // stream has passed first, so that no barrier gets ahead of its waiters.)
+            unsigned kn = 0, vn = 0, segs = 0, sent0 = 0, sent1 = 0;
+            int4 join = make_int4(-1, 0, 0, 0);
+            long long at_unit = u0;
+            bool ok = true;
+            auto keys_there = [&]() -> bool {
+                const unsigned at = kn++;
+                return wait_warp(&bars.k_full[at % SK], (at / SK) & 1);
+            };
+            auto pass = [&](int g) -> bool {
+                const unsigned sent = g ? sent1 : sent0;
+                if (sent > 0 && !wait_warp(&bars.p_half[g], (sent + 1) & 1)) return false;
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_half[g]));
+                if (g) ++sent1;
+                else ++sent0;
+                return true;
+            };
+            while (ok && next_segment()) {
+                const int nt = s.t1 - s.t0, two = s.act == 2, ahead = two ? 1 : 2, tails = s.L / kTile - s.t0;
+                if (s.t0 == 0 && s.t1 < s.tiles)
+                    join = make_int4(s.b, s.h | s.pair << 16, (s.count - 2 * s.pair * a.nodes) * a.G, (int)quotient(at_unit + s.tiles - 1, per));
+                at_unit += nt;
+                uint32_t *bad = sh.bad[segs % kSegRing];
+                if (lane < 4) bad[lane] = 0;
+                ok = wait_warp(&bars.q_full, segs & 1);
+                for (int t = 0; ok && t < min(nt, ahead); ++t) ok = keys_there();
+                if (!ok) break;
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.start));
+                for (int t = 0; t < nt; ++t) {
+                    const unsigned st = vn % SV;
+                    if (!(ok = wait_warp(&bars.v_full[st], (vn / SV) & 1))) break;
+                    ++vn;
+                    if (t >= tails) {
+                        const int at0 = (s.t0 + t) * kTile, keys = s.keys(s.t0 + t), lo = max(0, s.L - at0);
+                        char *stage = dyn + SM::kQ + (SK + st) * SM::kStage;
+                        const int rows = ((keys + 15) & ~15) - lo;   // up to the last product's end
+                        for (int i = lane; i < rows * DC * 8; i += 32) {
+                            const int r = lo + i / (DC * 8), x = i % (DC * 8);
+                            uint4 *p = reinterpret_cast<uint4 *>(stage + (x >> 3) * kChunk + r * 128 + (x & 7) * 16);
+                            if (r >= keys) {
+                                *p = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            uint4 w = *p;
+                            uint32_t *u = &w.x;
+                            bool hit = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if ((u[e] & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0xffff0000u, hit = true;
+                                if ((u[e] >> 16 & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0x0000ffffu, hit = true;
+                            }
+                            if (hit) {
+                                *p = w;
+                                const int node = at0 + r - s.L;
+                                atomicOr(&bad[node >> 5], 1u << (node & 31));
+                            }
+                        }
+                        tc::fence_async();
+                        __syncwarp();
+                    }
+                    if (t + ahead < nt && !(ok = keys_there())) break;
+                    if (!(ok = pass(two ? 0 : t & 1))) break;
+                    if (two && !(ok = pass(1))) break;
+                }
+                ++segs;
+            }
+            if (lane == 0) a.joins[me] = join;
+        } else if (warp == kWarpMma0 || warp == kWarpMma1) {
+            // ---- products, a warp per stream -------------------------------------------------------
+            // (With one warp the tensor cores paused while it prepared the other stream's job.) The
+            // whole warp walks along, so that operands stay in uniform registers; one thread issues.
             const bool lead = tc::elect();
-            unsigned n0 = 0, segs = 0, done0 = 0, done1 = 0;
-            uint32_t fixed = 0;   // per stage: parity of the next wait for checked values
+            const int g = warp == kWarpMma1;
+            const uint32_t S_ = tc::uniform(tS[0] + g * 128), O_ = tc::uniform(tO[0] + g * DP);
+            uint64_t *const half = &bars.p_half[g], *const rest = &bars.p_rest[g];
+            unsigned n0 = 0, segs = 0, done = 0;
             bool ok = true;
             while (ok && next_segment()) {
-                const int two = s.act == 2, nt = s.t1 - s.t0, ahead = two ? 1 : 2, jobs = two ? 2 * nt : nt;
-                const int tails = max(0, s.L / kTile - s.t0);                   // tiles from here on hold nodes' keys
-                const int end_steps = (s.keys(s.t1 - 1) + 15) / 16;             // products of the last tile
-                // the places of a job's keys and values in the order of copies
-                auto kplace = [&](int j) -> unsigned {
-                    const int t = two ? j >> 1 : j;
-                    return n0 + (t < ahead ? t : 2 * t - ahead + 1);
-                };
-                auto keys_there = [&](int j) -> bool {
-                    const unsigned at = kplace(j);
-                    return (two && (j & 1)) || wait_warp(&bars.full[at % S], (at / S) & 1);
-                };
-                // S of job j
-                auto scores = [&](int j, uint32_t q, uint32_t k, uint32_t d) {
-                    const int g = j & 1;
+                const int two = s.act == 2, nt = s.t1 - s.t0, step = two ? 1 : 2;
+                const int end_steps = (s.keys(s.t1 - 1) + 15) / 16;   // products of the last tile
+                const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g * SM::kStage : 0), 16));
+                // S of tile t
+                auto scores = [&](int t) {
+                    const unsigned st = (n0 + t) % SK;
+                    const uint32_t k = tc::uniform(tc::operand_lo(kring + st * SM::kStage, 16));
+                    if (lead) {
 #pragma unroll
-                    for (int i = 0; i < DC * 4; ++i) {
-                        const uint32_t o = ((i >> 2) * kChunk + (i & 3) * 32) >> 4;
-                        tc::mma_ss(d, tc::operand(q + o), tc::operand(k + o), kIdS, i > 0);
-                    }
-                    tc::commit(tc::smem(&bars.s_full[g]));
-                    if (!two || g == 1) tc::commit(tc::smem(&bars.empty[kplace(j) % S]));
-                    if (j == jobs - 1) tc::commit(tc::smem(&bars.q_empty));
-                };
-                const uint32_t q0 = tc::operand_lo(base, 16), q1 = two ? q0 + (SM::kStage >> 4) : q0;
-                if (!wait_warp(&bars.q_full, segs & 1)) break;
-                for (int j = 0; ok && j < min(jobs, 2); ++j) {
-                    if (!(ok = keys_there(j))) break;
-                    const uint32_t q = tc::uniform(j ? q1 : q0), k = tc::uniform(tc::operand_lo(ring + kplace(j) % S * SM::kStage, 16));
-                    const uint32_t d = tc::uniform(tS[0] + (j & 1) * 128);
-                    tc::fence_after();
-                    if (lead) scores(j, q, k, d);
-                    __syncwarp();
-                }
-                // Job j's P V, then job j + 2's Q K^T into the same columns: all that they wait for but P
-                // is waited for before P, so that the tensor cores get both without a pause.
-                for (int j = 0; ok && j < jobs; ++j) {
-                    const int g = j & 1, t = two ? j >> 1 : j;
-                    const unsigned at = n0 + (t < nt - ahead ? min(nt, ahead) + 2 * t : nt + t), st = at % S;
-                    const bool more = j + 2 < jobs;
-                    if (!two || g == 0) {
-                        ok = wait_warp(&bars.full[st], (at / S) & 1);
-                        if (ok && t >= tails) {
-                            ok = wait_warp(&bars.fixed[st], fixed >> st & 1);
-                            fixed ^= 1u << st;
+                        for (int i = 0; i < DC * 4; ++i) {
+                            const uint32_t o = ((i >> 2) * kChunk + (i & 3) * 32) >> 4;
+                            tc::mma_ss(S_, tc::operand(q + o), tc::operand(k + o), kIdS, i > 0);
                         }
-                        if (!ok) break;
+                        tc::commit(tc::smem(&bars.s_full[g]));
+                        tc::commit(tc::smem(&bars.k_empty[st]));
+                        if (!two) tc::commit(tc::smem(&bars.k_empty[st]));   // (for the other stream)
                     }
-                    if (more && !(ok = keys_there(j + 2))) break;
-                    if (j == 0 && segs > 0 && !(ok = wait_warp(&bars.o_free, (segs + 1) & 1))) break;
-                    const uint32_t v = tc::uniform(tc::operand_lo(ring + st * SM::kStage, kChunk));
-                    const uint32_t d = tc::uniform(tO[0] + g * DP), p = tc::uniform(tS[0] + g * 128);
-                    const uint32_t q = tc::uniform(g ? q1 : q0), k = tc::uniform(tc::operand_lo(ring + kplace(j + 2) % S * SM::kStage, 16));
+                    __syncwarp();
+                };
+                const int first = two ? 0 : g;
+                if (!(ok = wait_warp(&bars.start, segs & 1))) break;
+                tc::fence_after();
+                if (first < nt) scores(first);
+                if (lead && first + step >= nt) tc::commit(tc::smem(&bars.q_empty));
+                if (segs > 0 && !(ok = wait_warp(&bars.o_free, (segs + 1) & 1))) break;
+                for (int t = first; t < nt; t += step) {
+                    const unsigned st = (n0 + t) % SV;
+                    const uint32_t v = tc::uniform(tc::operand_lo(vring + st * SM::kStage, kChunk));
                     const int steps = t == nt - 1 ? end_steps : kTile / 16;
-                    if (!(ok = wait_warp(&bars.p_ready[g], (g ? done1 : done0) & 1))) break;
+                    if (!(ok = wait_warp(half, done & 1))) break;
                     tc::fence_after();
                     if (lead) {
-                        if (steps == kTile / 16) {
+                        if (steps >= 4) {
 #pragma unroll
-                            for (int i = 0; i < kTile / 16; ++i) tc::mma_ts(d, p + i * 8, tc::operand(v + i * 128), kIdO, j >= 2 || i > 0);
+                            for (int i = 0; i < 4; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, t > first || i > 0);
                         } else {
-                            for (int i = 0; i < steps; ++i) tc::mma_ts(d, p + i * 8, tc::operand(v + i * 128), kIdO, j >= 2 || i > 0);
+                            for (int i = 0; i < steps; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, t > first || i > 0);
                         }
-                        tc::commit(tc::smem(&bars.pv_done[g]));
-                        if (!two || g == 1) tc::commit(tc::smem(&bars.empty[st]));
-                        if (more) scores(j + 2, q, k, p);
                     }
                     __syncwarp();
-                    if (g) ++done1;
-                    else ++done0;
+                    if (!(ok = wait_warp(rest, done & 1))) break;
+                    tc::fence_after();
+                    if (lead) {
+                        if (steps == 8) {
+#pragma unroll
+                            for (int i = 4; i < 8; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, true);
+                        } else {
+                            for (int i = 4; i < steps; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, true);
+                        }
+                        tc::commit(tc::smem(&bars.pv_done[g]));
+                        tc::commit(tc::smem(&bars.v_empty[st]));
+                        if (!two) tc::commit(tc::smem(&bars.v_empty[st]));
+                    }
+                    __syncwarp();
+                    ++done;
+                    if (t + step < nt) {
+                        scores(t + step);
+                        if (lead && t + 2 * step >= nt) tc::commit(tc::smem(&bars.q_empty));
+                    }
                 }
-                n0 += 2 * nt;
+                n0 += nt;
                 ++segs;
+                if (lead) tc::bar_arrive(tc::smem(&bars.o_free));
+                __syncwarp();
             }
             // (none of the products may still run when the CTA ends)
             if (lead) {
@@ -461,75 +520,14 @@ __global__ void __launch_bounds__(kNT, 1)
                 for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.drain), 0); ++k) {}
             }
             __syncwarp();
-        } else {
-            // ---- values behind the context -----------------------------------------------------
-            unsigned n = 0, segs = 0;
-            int4 join = make_int4(-1, 0, 0, 0);
-            long long at_unit = u0;
-            bool ok = true;
-            while (ok && next_segment()) {
-                const int nt = s.t1 - s.t0, ahead = s.act == 2 ? 1 : 2;
-                if (s.t0 == 0 && s.t1 < s.tiles) join = make_int4(s.b, s.h, s.pair, (int)((at_unit + s.tiles - 1) / per));
-                at_unit += nt;
-                bool first = true;
-                uint32_t *bad = sh.bad[segs % kSegRing];
-                // every tile is waited for and given back in the order of the copies, so that no barrier is
-                // ever two phases ahead of this warp or behind it
-                for (int x = 0; ok && x < 2 * nt; ++x, ++n) {
-                    const unsigned st = n % S;
-                    if (!(ok = wait_warp(&bars.full[st], (n / S) & 1))) break;
-                    const int v = x < min(nt, ahead) ? -1 : x - min(nt, ahead), lag = nt - min(nt, ahead);
-                    // values and keys take turns while there are keys left
-                    const int t = v < 0 ? -1 : v < 2 * lag ? (v & 1 ? -1 : v >> 1) : v - lag;
-                    if (t < 0 || s.t0 + t < s.L / kTile) {
-                        if (lane == 0) tc::bar_arrive(tc::smem(&bars.empty[st]));
-                        continue;
-                    }
-                    if (first && lane < 4) bad[lane] = 0;
-                    first = false;
-                    __syncwarp();
-                    const int at0 = (s.t0 + t) * kTile, keys = s.keys(s.t0 + t), lo = max(0, s.L - at0);
-                    char *stage = dyn + SM::kQ + st * SM::kStage;
-                    const int rows = ((keys + 15) & ~15) - lo;   // up to the last product's end
-                    for (int i = lane; i < rows * DC * 8; i += 32) {
-                        const int r = lo + i / (DC * 8), x = i % (DC * 8);
-                        uint4 *p = reinterpret_cast<uint4 *>(stage + (x >> 3) * kChunk + r * 128 + (x & 7) * 16);
-                        if (r >= keys) {
-                            *p = make_uint4(0, 0, 0, 0);
-                            continue;
-                        }
-                        uint4 w = *p;
-                        uint32_t *u = &w.x;
-                        bool hit = false;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((u[e] & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0xffff0000u, hit = true;
-                            if ((u[e] >> 16 & Half<T>::kExp) == Half<T>::kExp) u[e] &= 0x0000ffffu, hit = true;
-                        }
-                        if (hit) {
-                            *p = w;
-                            const int node = at0 + r - s.L;
-                            atomicOr(&bad[node >> 5], 1u << (node & 31));
-                        }
-                    }
-                    tc::fence_async();
-                    __syncwarp();
-                    if (lane == 0) {
-                        tc::bar_arrive(tc::smem(&bars.fixed[st]));
-                        tc::bar_arrive(tc::smem(&bars.empty[st]));
-                    }
-                }
-                ++segs;
-            }
-            if (lane == 0) a.joins[me] = join;
         }
     } else {
-        tc::more_registers<200>();
+        tc::more_registers<192>();
         // ---- softmax: a stream each, a row a thread ------------------------------------------
         const int g = (warp - 4) >> 2, r = threadIdx.x & 127;
         const uint32_t row_lane = (uint32_t)(warp & 3) << 21;   // (lane of tensor memory in bits 16 and up)
         const uint32_t mS = tS[g] + row_lane;
-        unsigned segs = 0, merges = 0, own = 0, other = 0;   // jobs of this stream and the other so far
+        unsigned segs = 0, merges = 0, own = 0;   // (own: jobs of this stream so far)
         bool ok = true;
         while (ok && next_segment()) {
             const int first = s.t0, step = s.act == 2, tails = s.L / kTile, jobs = (s.t1 - first) << step;
@@ -552,7 +550,10 @@ __global__ void __launch_bounds__(kNT, 1)
             for (int j = g; j < jobs; j += 2) {
                 if (!(ok = wait_warp(&bars.s_full[g], own & 1))) break;
                 if (idle) {
-                    if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
+                    if (lane == 0) {
+                        tc::bar_arrive(tc::smem(&bars.p_half[g]));
+                        tc::bar_arrive(tc::smem(&bars.p_rest[g]));
+                    }
                     ++own;
                     continue;
                 }
@@ -621,24 +622,23 @@ __global__ void __launch_bounds__(kNT, 1)
                         p[i / 2] = Half<T>::pack(e.x, e.y);
                     }
                     tc::tmem_store16(mS + c * 16, p);
+                    if (c & 1) {   // half of the keys: their products can begin
+                        tc::tmem_wait_store();
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::bar_arrive(tc::smem(c == 1 ? &bars.p_half[g] : &bars.p_rest[g]));
+                    }
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-                tc::tmem_wait_store();
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
                 ++own;
             }
             if (!ok) break;
-            other += (jobs + g) / 2;   // (stream 0 has the odd one)
             // ---- the segment's output ---------------------------------------------------------
             const bool two = s.act == 2, both = !two && jobs > 1;
-            if (both || two || g == 0) {
-                if (!(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
-            }
+            const bool mine = both || two || g == 0;   // (a stream may have had no job)
+            if (mine && !(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
             if (!two) {
-                if ((g == 1 || both) && !(ok = wait_warp(&bars.pv_done[g ^ 1], (other + 1) & 1))) break;
-                sh.ml[g][r] = make_float2(m, l);
+                if (mine) sh.ml[g][r] = make_float2(m, l);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem(&bars.merge));
                 if (!(ok = wait_warp(&bars.merge, merges++ & 1))) break;
@@ -648,10 +648,10 @@ __global__ void __launch_bounds__(kNT, 1)
             float w0 = 1.f, w1 = 0.f;
             if (!two) {
                 const float2 m0 = sh.ml[0][r], m1 = sh.ml[1][r];
-                m = fmaxf(m0.x, m1.x);
+                m = both ? fmaxf(m0.x, m1.x) : m0.x;
                 const float ref = m == neg_inf() ? 0.f : m;
                 w0 = ex2(m0.x - ref);
-                w1 = both ? ex2(m1.x - ref) : 0.f;
+                w1 = both ? ex2(m1.x - ref) : 0.f;   // (ml[1] is not written for a stream without jobs)
                 l = m0.y * w0 + (both ? m1.y * w1 : 0.f);
             }
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(kNT, 1)
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 1) tc::tmem_free(tmem, 512);
+    if (warp == kWarpMma0) tc::tmem_free(tmem, 512);
 }
 
 // The pieces of what was cut: CTA x joins what begins in CTA x's part and ends in another's. A
@@ -741,10 +741,8 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
     if (join.x < 0) return;
     const int rr = blockIdx.y * kJoinRows + threadIdx.x % kJoinRows, c4 = threadIdx.x / kJoinRows;
     const int used = a.nodes * a.G, m_tile = rr / used, r = rr - m_tile * used;   // (rows of a tile that are used)
-    const int node = (2 * join.z + m_tile) * a.nodes + r / a.G;
-    int L, count;
-    sequence(a, join.x, L, count);
-    if (m_tile > 1 || node >= count) return;
+    const int h = join.y & 0xffff, node = (2 * (join.y >> 16) + m_tile) * a.nodes + r / a.G;
+    if (m_tile > 1 || rr >= join.z) return;
     const int first = blockIdx.x, pieces = join.w - first + 1;
     auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + m_tile; };
     float m = neg_inf(), l = 0.f;
@@ -784,7 +782,7 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
         }
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
-    const long long row = ((long long)join.x * a.N + node) * a.Hq + join.y * a.G + r % a.G;
+    const long long row = ((long long)join.x * a.N + node) * a.Hq + h * a.G + r % a.G;
     if (c4 * 4 < a.D)
         *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * a.D + c4 * 4) =
             make_uint2(Half<T>::pack(o.x * inv, o.y * inv), Half<T>::pack(o.z * inv, o.w * inv));
@@ -874,7 +872,7 @@ static size_t workspace_bytes_for(const spec_attend_params *p) {
 
 template <typename T, int DC>
 static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, int box, cudaStream_t st) {
-    constexpr size_t smem = AttendSmem<DC>::kTiles + sizeof(AttendShared<AttendSmem<DC>::kStages>);
+    constexpr size_t smem = AttendSmem<DC>::kTiles + sizeof(typename AttendSmem<DC>::Shared);
     static_assert(smem <= 227 * 1024, "shared memory");
     static std::mutex mu;
     static bool done[64];
