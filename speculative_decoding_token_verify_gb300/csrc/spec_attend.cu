@@ -115,6 +115,11 @@ struct Half<__half> {
     __device__ static __forceinline__ float value(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
 };
 
+// pairs of row tiles that `count` nodes fill
+__device__ __forceinline__ int pairs_of(const AttendArgs &a, int count) {
+    return a.N <= 2 * a.nodes ? count > 0 : (count + 2 * a.nodes - 1) / (2 * a.nodes);
+}
+
 // (a 64-bit division costs ten times a 32-bit one)
 __device__ __forceinline__ long long quotient(long long x, long long y) {
     return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
@@ -125,29 +130,39 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
 // which leaves registers to what the warp does.
 struct Segment {
     int b, h, pair, t0, t1, tiles, L, count;
-    int act;                // row tiles with nodes
-    long long off, left;    // units of sequence b behind this piece, and of the CTA's part
+    int act, begun;         // row tiles with nodes; 1: next() is to give this piece itself
+    int off, left;          // units of sequence b behind this piece, and of the CTA's part (below 2^31, the host checks)
     __device__ __forceinline__ int keys(int t) const { return min(kTile, L + count - t * kTile); }
+    // the piece that begins at unit `off` of sequence b, of L tokens and `count` nodes
+    __device__ __forceinline__ bool begin(const AttendArgs &a) {
+        const int pairs = pairs_of(a, count);
+        tiles = (L + count + kTile - 1) / kTile;
+        const int head = pairs * tiles;
+        if (off >= head * a.Hkv) return false;
+        h = (int)((unsigned)off / (unsigned)head);
+        const int in = off - h * head;
+        pair = pairs > 1 ? in / tiles : 0;
+        t0 = in - pair * tiles;
+        t1 = t0 + min(tiles - t0, left);
+        act = count - pair * 2 * a.nodes > a.nodes ? 2 : 1;
+        off += t1 - t0;
+        left -= t1 - t0;
+        return true;
+    }
     __device__ __forceinline__ bool next(const AttendArgs &a) {
-        while (left > 0) {
-            sequence(a, b, L, count);
-            const int pairs = (count + 2 * a.nodes - 1) / (2 * a.nodes);
-            tiles = (L + count + kTile - 1) / kTile;
-            const long long head = (long long)pairs * tiles, all = head * a.Hkv;
-            if (off >= all) {
-                off -= all;
-                ++b;
-                continue;
-            }
-            h = (int)quotient(off, head);
-            const long long in = off - h * head;
-            pair = (int)quotient(in, tiles);
-            t0 = (int)(in - (long long)pair * tiles);
-            t1 = t0 + (int)min((long long)(tiles - t0), left);
-            act = count - pair * 2 * a.nodes > a.nodes ? 2 : 1;
-            off += t1 - t0;
-            left -= t1 - t0;
+        if (begun) {
+            begun = 0;
             return true;
+        }
+        Segment s = *this;
+        while (s.left > 0) {
+            if (s.begin(a)) {
+                *this = s;
+                return true;
+            }
+            s.off -= s.tiles * pairs_of(a, s.count) * a.Hkv;
+            ++s.b;
+            sequence(a, s.b, s.L, s.count);
         }
         return false;
     }
@@ -157,7 +172,7 @@ struct Segment {
 template <int SK, int SV>
 struct AttendShared {
     struct {
-        uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV], s_full[2], p_half[2], p_rest[2], pv_done[2], q_full, q_empty, start, o_free, merge, drain;
+        uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV], s_full[2], p_half[2], p_rest[2], pv_done[2], turn[2], q_full[2], q_empty[2], start[2], o_free, merge, drain;
     } bars;
     float2 ml[2][kTile];
     Segment seg[13];   // of warps 0-11 and 14
@@ -200,10 +215,11 @@ __global__ void __launch_bounds__(kNT, 1)
             tc::bar_init(tc::smem(&bars.p_half[i]), 5);   // four warps, and the copies that the job needs
             tc::bar_init(tc::smem(&bars.p_rest[i]), 4);
             tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
+            tc::bar_init(tc::smem(&bars.turn[i]), 1);
+            tc::bar_init(tc::smem(&bars.q_full[i]), 1);
+            tc::bar_init(tc::smem(&bars.q_empty[i]), 2);
+            tc::bar_init(tc::smem(&bars.start[i]), 1);
         }
-        tc::bar_init(tc::smem(&bars.q_full), 1);
-        tc::bar_init(tc::smem(&bars.q_empty), 2);
-        tc::bar_init(tc::smem(&bars.start), 1);
         tc::bar_init(tc::smem(&bars.o_free), 10);          // the softmax's warps and, to keep them in step, the products'
         tc::bar_init(tc::smem(&bars.merge), 8);
         tc::bar_init(tc::smem(&bars.drain), 2);
@@ -237,39 +253,46 @@ __global__ void __launch_bounds__(kNT, 1)
     Segment &s = sh.seg[min(warp, 12)];
     long long per = 1, u0 = 0;
     if (works) {
-        auto units = [&](int b) -> long long {
-            if (b >= a.B) return 0;
-            int L, count;
+        // lane l: the units of sequences [l, l + 1) run
+        const int run = (a.B + 31) >> 5, b_lo = min(a.B, lane * run), b_hi = min(a.B, b_lo + run);
+        auto units = [&](int b, int &L, int &count) -> long long {
             sequence(a, b, L, count);
-            const int pairs = (count + 2 * a.nodes - 1) / (2 * a.nodes), tiles = (L + count + kTile - 1) / kTile;
-            return (long long)(a.Hkv * pairs) * tiles;
+            return (long long)(a.Hkv * pairs_of(a, count)) * ((L + count + kTile - 1) / kTile);
         };
-        long long total = 0;
-#pragma unroll 4
-        for (int b = lane; b < a.B; b += 32) total += units(b);
-        for (int o = 16; o > 0; o /= 2) total += __shfl_xor_sync(kFull, total, o);
+        long long mine = 0;
+        int L, count;
+#pragma unroll 8
+        for (int b = b_lo; b < b_hi; ++b) mine += units(b, L, count);
+        long long upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o *= 2) {
+            const long long v = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += v;
+        }
+        const long long total = __shfl_sync(kFull, upto, 31);
         per = quotient(total + G - 1, G);
         u0 = min(total, me * per);
         const long long u1 = min(total, u0 + per);
-        long long at = 0;
-        if (lane == 0) s.left = 0;
-        for (int b0 = 0; u0 < u1 && b0 < a.B; b0 += 32) {
-            const long long n = units(b0 + lane);
-            long long upto = n;
-            for (int o = 1; o < 32; o *= 2) {
-                const long long v = __shfl_up_sync(kFull, upto, o);
-                if (lane >= o) upto += v;
-            }
-            const unsigned past = __ballot_sync(kFull, u0 < at + upto);
-            if (past) {
-                if (lane == __ffs(past) - 1) {
-                    s.b = b0 + lane;
-                    s.off = u0 - (at + upto - n);
-                    s.left = u1 - u0;
+        if (lane == 0) s.left = s.begun = 0;
+        __syncwarp();
+        if (u0 < u1 && u0 >= upto - mine && u0 < upto) {
+            long long at = upto - mine;
+            for (int b = b_lo; b < b_hi; ++b) {
+                const long long n = units(b, L, count);
+                if (u0 < at + n) {
+                    Segment first;
+                    first.b = b;
+                    first.L = L;
+                    first.count = count;
+                    first.off = (int)(u0 - at);
+                    first.left = (int)(u1 - u0);
+                    first.begin(a);
+                    first.begun = 1;
+                    s = first;
+                    break;
                 }
-                break;
+                at += n;
             }
-            at += __shfl_sync(kFull, upto, 31);
         }
     }
     auto next_segment = [&]() -> bool {
@@ -297,6 +320,9 @@ __global__ void __launch_bounds__(kNT, 1)
         return false;
     };
 
+    // where one tile holds all nodes' rows, the queries' room for two holds the next segment's, too
+    const bool twin = a.N <= a.nodes;
+
     // 128 registers a thread at the launch: 64 for eight warps and 192 for the eight of the softmax
     if (warp < 4 || warp >= 12) {
         tc::fewer_registers<64>();
@@ -322,21 +348,22 @@ __global__ void __launch_bounds__(kNT, 1)
                     return row[key >> page_bits];   // (looked at when it is used)
                 };
                 auto queries = [&]() -> bool {
-                    if (segs > 0 && !wait_warp(&bars.q_empty, (segs + 1) & 1)) return false;
+                    const unsigned slot = twin ? segs & 1 : 0, use = twin ? segs >> 1 : segs;
+                    if (use > 0 && !wait_warp(&bars.q_empty[slot], (use + 1) & 1)) return false;
                     if (lane == 0) {
-                        const uint32_t bar = tc::smem(&bars.q_full);
+                        const uint32_t bar = tc::smem(&bars.q_full[slot]);
                         tc::bar_expect(bar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
                         for (int m = 0; m < s.act; ++m)
                             for (int x = 0; x < DC; ++x)
-                                tc::load_tile(base + m * SM::kStage + x * kChunk, &qmap, bar, x * 64, head * a.G, (2 * s.pair + m) * a.nodes, s.b);
+                                tc::load_tile(base + (slot + m) * SM::kStage + x * kChunk, &qmap, bar, x * 64, head * a.G, (2 * s.pair + m) * a.nodes, s.b);
                     }
                     __syncwarp();
                     ++segs;
                     return true;
                 };
                 int now = pages(0), next = pages(group);
-                const bool first = segs == 0;   // (later ones: the first keys need not wait for the queries' place)
-                if (keys && first) queries();
+                const bool first = twin || segs == 0;   // (else the first keys need not wait for the queries' place)
+                if (keys && first && !(ok = queries())) break;
                 for (int t = 0; ok && t < nt; ++t, ++n) {
                     if (t && (t & (group - 1)) == 0) {
                         now = next;
@@ -364,8 +391,8 @@ __global__ void __launch_bounds__(kNT, 1)
             if (*(volatile int *)&sh.abort) {
                 for (unsigned i = n > S ? n - S : 0; i < n; ++i)
                     for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&full[i % S]), (i / S) & 1); ++k) {}
-                if (segs > 0)
-                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full), (segs + 1) & 1); ++k) {}
+                for (unsigned i = segs > 1 ? segs - 2 : 0; keys && i < segs; ++i)
+                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full[twin ? i & 1 : 0]), (twin ? i >> 1 : i) & 1); ++k) {}
             }
         } else if (warp == kWarpGo) {
             // ---- what a job needs: its copies are there, and its values can be multiplied --------------
@@ -395,10 +422,11 @@ __global__ void __launch_bounds__(kNT, 1)
                 at_unit += nt;
                 uint32_t *bad = sh.bad[segs % kSegRing];
                 if (lane < 4) bad[lane] = 0;
-                ok = wait_warp(&bars.q_full, segs & 1);
+                const unsigned slot = twin ? segs & 1 : 0;
+                ok = wait_warp(&bars.q_full[slot], (twin ? segs >> 1 : segs) & 1);
                 for (int t = 0; ok && t < min(nt, ahead); ++t) ok = keys_there();
                 if (!ok) break;
-                if (lane == 0) tc::bar_arrive(tc::smem(&bars.start));
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.start[slot]));
                 for (int t = 0; t < nt; ++t) {
                     const unsigned st = vn % SV;
                     if (!(ok = wait_warp(&bars.v_full[st], (vn / SV) & 1))) break;
@@ -440,18 +468,28 @@ __global__ void __launch_bounds__(kNT, 1)
             if (lane == 0) a.joins[me] = join;
         } else if (warp == kWarpMma0 || warp == kWarpMma1) {
             // ---- products, a warp per stream -------------------------------------------------------
-            // (With one warp the tensor cores paused while it prepared the other stream's job.) The
+            // (With one warp the tensor cores paused while it prepared the other stream's job.) They take
+            // turns, so that one stream's products run while the other exponentiates. The
             // whole warp walks along, so that operands stay in uniform registers; one thread issues.
             const bool lead = tc::elect();
             const int g = warp == kWarpMma1;
             const uint32_t S_ = tc::uniform(tS[0] + g * 128), O_ = tc::uniform(tO[0] + g * DP);
             uint64_t *const half = &bars.p_half[g], *const rest = &bars.p_rest[g];
-            unsigned n0 = 0, segs = 0, done = 0;
+            unsigned n0 = 0, segs = 0, done = 0, turns = 0;
+            auto my_turn = [&]() -> bool {   // (stream 0 begins)
+                const unsigned i = turns++;
+                return g ? wait_warp(&bars.turn[1], i & 1) : i == 0 || wait_warp(&bars.turn[0], (i + 1) & 1);
+            };
+            auto pass_on = [&]() {
+                if (lead) tc::bar_arrive(tc::smem(&bars.turn[g ^ 1]));
+                __syncwarp();
+            };
             bool ok = true;
             while (ok && next_segment()) {
                 const int two = s.act == 2, nt = s.t1 - s.t0, step = two ? 1 : 2;
                 const int end_steps = (s.keys(s.t1 - 1) + 15) / 16;   // products of the last tile
-                const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g * SM::kStage : 0), 16));
+                const int slot = twin ? segs & 1 : 0;
+                const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g : slot) * SM::kStage, 16));
                 // S of tile t
                 auto scores = [&](int t) {
                     const unsigned st = (n0 + t) % SK;
@@ -469,16 +507,16 @@ __global__ void __launch_bounds__(kNT, 1)
                     __syncwarp();
                 };
                 const int first = two ? 0 : g;
-                if (!(ok = wait_warp(&bars.start, segs & 1))) break;
+                if (!(ok = wait_warp(&bars.start[slot], (twin ? segs >> 1 : segs) & 1))) break;
                 tc::fence_after();
                 if (first < nt) scores(first);
-                if (lead && first + step >= nt) tc::commit(tc::smem(&bars.q_empty));
+                if (lead && first + step >= nt) tc::commit(tc::smem(&bars.q_empty[slot]));
                 if (segs > 0 && !(ok = wait_warp(&bars.o_free, (segs + 1) & 1))) break;
                 for (int t = first; t < nt; t += step) {
                     const unsigned st = (n0 + t) % SV;
                     const uint32_t v = tc::uniform(tc::operand_lo(vring + st * SM::kStage, kChunk));
                     const int steps = t == nt - 1 ? end_steps : kTile / 16;
-                    if (!(ok = wait_warp(half, done & 1))) break;
+                    if (!(ok = wait_warp(half, done & 1)) || !(ok = my_turn())) break;
                     tc::fence_after();
                     if (lead) {
                         if (steps >= 4) {
@@ -506,8 +544,13 @@ __global__ void __launch_bounds__(kNT, 1)
                     ++done;
                     if (t + step < nt) {
                         scores(t + step);
-                        if (lead && t + 2 * step >= nt) tc::commit(tc::smem(&bars.q_empty));
+                        if (lead && t + 2 * step >= nt) tc::commit(tc::smem(&bars.q_empty[slot]));
                     }
+                    pass_on();
+                }
+                if (ok && g && !two && (nt & 1)) {   // (stream 0 has one job more)
+                    if (!(ok = my_turn())) break;
+                    pass_on();
                 }
                 n0 += nt;
                 ++segs;
@@ -823,6 +866,11 @@ static int check_attend(const spec_attend_params *p) {
             if (n[i][j] > 1 && (s[i][j] <= 0 || s[i][j] % 8 || s[i][j] >= (1LL << 38) || s[i][j] > (INT64_MAX >> 4) / n[i][j]))
                 return spec_internal_set_error(SPEC_ERR_INVALID_ARG,
                                                "tree_attention: strides must be multiples of 8 elements, above 0 and below 2^38");
+    // units of work: of a sequence, and of one CTA of at least 64
+    const int64_t nodes = kTile / (p->Hq / p->Hkv), pairs = (p->N + 2 * nodes - 1) / (2 * nodes);
+    const int64_t units = ((int64_t)p->M * p->page + kTile - 1) / kTile * pairs * p->Hkv;
+    if (units > INT32_MAX || units * p->B > (1LL << 36))
+        return spec_internal_set_error(SPEC_ERR_UNSUPPORTED, "tree_attention: rows too long or too many");
     return SPEC_OK;
 }
 
