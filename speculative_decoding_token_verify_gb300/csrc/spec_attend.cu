@@ -49,7 +49,7 @@ struct AttendArgs {
     float2 *part_ml;  // [CTA][2][tile][row]: their reference (log2) and sum
     int4 *joins;      // [CTA], what begins here and ends elsewhere: sequence (-1: none), head + pair of tiles 2^16, rows, last CTA
     int B, N, Hq, Hkv, G, D, P, page, M, fill;
-    int nodes;        // a tile
+    int nodes, q_rows;   // a tile, and the rows that a copy of queries brings
     float sL;         // |scale| log2 e
     int neg;          // scale < 0
     long long vs[3], ps;
@@ -180,20 +180,24 @@ struct AttendShared {
     int abort;
 };
 
-template <int DC>
+// FEW: at most 64 rows a sequence and key head (one tile). Their queries take a quarter of the
+// room of two tiles of 128 (the products read what lies behind them, for rows that nobody uses), which
+// leaves another stage to the rings.
+template <int DC, bool FEW>
 struct AttendSmem {
     static constexpr int kStage = DC * kChunk;
-    static constexpr int kKeys = DC == 2 ? 3 : 5, kValues = DC == 2 ? 2 : 5;   // stages of the rings (keys run ahead)
+    static constexpr int kQChunk = FEW ? kChunk / 2 : kChunk;   // 64 elements of the rows of a tile
+    static constexpr int kQ = 2 * DC * kQChunk;
+    static constexpr int kKeys = DC == 2 ? 3 : FEW ? 6 : 5, kValues = DC == 2 ? FEW ? 3 : 2 : FEW ? 6 : 5;   // stages of the rings
     using Shared = AttendShared<kKeys, kValues>;
-    static constexpr int kQ = 2 * kStage;
     static constexpr int kTiles = kQ + (kKeys + kValues) * kStage;
 };
 
-template <typename T, int DC>
+template <typename T, int DC, bool FEW>
 __global__ void __launch_bounds__(kNT, 1)
     attend_kernel(const __grid_constant__ AttendArgs a, const __grid_constant__ CUtensorMap qmap,
                   const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, int box) {
-    using SM = AttendSmem<DC>;
+    using SM = AttendSmem<DC, FEW>;
     constexpr int SK = SM::kKeys, SV = SM::kValues, DP = DC * 64;
     extern __shared__ __align__(1024) char dyn[];   // (the kernel has no other shared memory, so that this holds)
     typename SM::Shared &sh = *reinterpret_cast<typename SM::Shared *>(dyn + SM::kTiles);
@@ -321,7 +325,7 @@ __global__ void __launch_bounds__(kNT, 1)
     };
 
     // where one tile holds all nodes' rows, the queries' room for two holds the next segment's, too
-    const bool twin = a.N <= a.nodes;
+    const bool twin = FEW || a.N <= a.nodes;
 
     // 128 registers a thread at the launch: 64 for eight warps and 192 for the eight of the softmax
     if (warp < 4 || warp >= 12) {
@@ -352,10 +356,10 @@ __global__ void __launch_bounds__(kNT, 1)
                     if (use > 0 && !wait_warp(&bars.q_empty[slot], (use + 1) & 1)) return false;
                     if (lane == 0) {
                         const uint32_t bar = tc::smem(&bars.q_full[slot]);
-                        tc::bar_expect(bar, (uint32_t)a.nodes * a.G * 128 * DC * s.act);
+                        tc::bar_expect(bar, (uint32_t)a.q_rows * 128 * DC * s.act);
                         for (int m = 0; m < s.act; ++m)
                             for (int x = 0; x < DC; ++x)
-                                tc::load_tile(base + (slot + m) * SM::kStage + x * kChunk, &qmap, bar, x * 64, head * a.G, (2 * s.pair + m) * a.nodes, s.b);
+                                tc::load_tile(base + ((slot + m) * DC + x) * SM::kQChunk, &qmap, bar, x * 64, head * a.G, (2 * s.pair + m) * a.nodes, s.b);
                     }
                     __syncwarp();
                     ++segs;
@@ -489,7 +493,7 @@ __global__ void __launch_bounds__(kNT, 1)
                 const int two = s.act == 2, nt = s.t1 - s.t0, step = two ? 1 : 2;
                 const int end_steps = (s.keys(s.t1 - 1) + 15) / 16;   // products of the last tile
                 const int slot = twin ? segs & 1 : 0;
-                const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g : slot) * SM::kStage, 16));
+                const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g : slot) * DC * SM::kQChunk, 16));
                 // S of tile t
                 auto scores = [&](int t) {
                     const unsigned st = (n0 + t) % SK;
@@ -497,8 +501,9 @@ __global__ void __launch_bounds__(kNT, 1)
                     if (lead) {
 #pragma unroll
                         for (int i = 0; i < DC * 4; ++i) {
-                            const uint32_t o = ((i >> 2) * kChunk + (i & 3) * 32) >> 4;
-                            tc::mma_ss(S_, tc::operand(q + o), tc::operand(k + o), kIdS, i > 0);
+                            const uint32_t x = (i & 3) * 32;
+                            tc::mma_ss(S_, tc::operand(q + (((i >> 2) * SM::kQChunk + x) >> 4)), tc::operand(k + (((i >> 2) * kChunk + x) >> 4)),
+                                       kIdS, i > 0);
                         }
                         tc::commit(tc::smem(&bars.s_full[g]));
                         tc::commit(tc::smem(&bars.k_empty[st]));
@@ -876,6 +881,7 @@ static int check_attend(const spec_attend_params *p) {
 
 // ---- launch --------------------------------------------------------------------------------
 
+
 typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -918,9 +924,9 @@ static size_t workspace_bytes_for(const spec_attend_params *p) {
     return part_floats(p->D) * 4 + (size_t)kMaxCtas * 4 * kTile * 8 + (size_t)kMaxCtas * 16;
 }
 
-template <typename T, int DC>
+template <typename T, int DC, bool FEW>
 static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, int box, cudaStream_t st) {
-    constexpr size_t smem = AttendSmem<DC>::kTiles + sizeof(typename AttendSmem<DC>::Shared);
+    constexpr size_t smem = AttendSmem<DC, FEW>::kTiles + sizeof(typename AttendSmem<DC, FEW>::Shared);
     static_assert(smem <= 227 * 1024, "shared memory");
     static std::mutex mu;
     static bool done[64];
@@ -930,7 +936,7 @@ static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, i
     {
         std::lock_guard<std::mutex> lk(mu);
         if (!done[dev & 63]) {
-            e = cudaFuncSetAttribute(attend_kernel<T, DC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            e = cudaFuncSetAttribute(attend_kernel<T, DC, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
             done[dev & 63] = true;
         }
@@ -948,13 +954,20 @@ static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, i
     cfg.stream = st;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DC>, a, maps[0], maps[1], maps[2], box);
+    e = cudaLaunchKernelEx(&cfg, attend_kernel<T, DC, FEW>, a, maps[0], maps[1], maps[2], box);
     if (e != cudaSuccess) return e;
     const int tiles = (a.N + a.nodes - 1) / a.nodes, rows = tiles > 1 ? 2 * a.nodes * a.G : a.N * a.G;
     cfg.gridDim = dim3(ctas, (rows + kJoinRows - 1) / kJoinRows);
     cfg.blockDim = dim3(DC * 16 * kJoinRows);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, join_kernel<T, DC>, a);
+}
+
+template <typename T>
+static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, int box, cudaStream_t st) {
+    const bool few = a.N * a.G <= 64;
+    if (a.D > 64) return few ? launch_attend<T, 2, true>(a, maps, box, st) : launch_attend<T, 2, false>(a, maps, box, st);
+    return few ? launch_attend<T, 1, true>(a, maps, box, st) : launch_attend<T, 1, false>(a, maps, box, st);
 }
 
 }  // namespace sr
@@ -1020,6 +1033,8 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
     a.M = p->M;
     a.fill = counts != nullptr || (int64_t)p->M * p->page < p->N;
     a.nodes = kTile / G;
+    const int q_nodes = p->N < a.nodes ? p->N : a.nodes;
+    a.q_rows = q_nodes * G;
     a.sL = fmaxf(fabsf(p->scale) * sv::kLog2e, FLT_MIN);   // (0 times a masked key's -inf would be NaN)
     a.neg = p->scale < 0.f;
     a.ps = p->parents_stride;
@@ -1029,13 +1044,12 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
     const int64_t none[3] = {0, 0, 0};
     CUtensorMap maps[3];
     const int empty[3] = {1, 1, 1};
-    if (!encode(&maps[0], bf16, q, p->D, nq, p->q_stride, G, a.nodes) ||
+    if (!encode(&maps[0], bf16, q, p->D, nq, p->q_stride, G, q_nodes) ||
         !encode(&maps[1], bf16, p->P ? k : q, p->D, p->P ? nk : empty, p->P ? p->k_stride : none, 1, box) ||
         !encode(&maps[2], bf16, p->P ? v : q, p->D, p->P ? nk : empty, p->P ? p->v_stride : none, 1, box))
         return spec_internal_set_error(SPEC_ERR_CUDA, "tree_attention: the copies' layout could not be encoded");
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (p->D > 64) e = bf16 ? launch_attend<__nv_bfloat16, 2>(a, maps, box, st) : launch_attend<__half, 2>(a, maps, box, st);
-    else e = bf16 ? launch_attend<__nv_bfloat16, 1>(a, maps, box, st) : launch_attend<__half, 1>(a, maps, box, st);
+    e = bf16 ? launch_attend<__nv_bfloat16>(a, maps, box, st) : launch_attend<__half>(a, maps, box, st);
     return e == cudaSuccess ? SPEC_OK : spec_internal_set_error(SPEC_ERR_CUDA, cudaGetErrorString(e));
 }
