@@ -172,7 +172,7 @@ struct Segment {
 template <int SK, int SV>
 struct AttendShared {
     struct {
-        uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV], s_full[2], p_half[2], p_rest[2], pv_done[2], turn[2], q_full[2], q_empty[2], start[2], o_free, merge, drain;
+        uint64_t k_full[SK], k_empty[SK], v_full[SV], v_empty[SV], s_full[2], p_ready[2], pv_done[2], turn[2], q_full[2], q_empty[2], start[2], o_free, merge, drain;
     } bars;
     float2 ml[2][kTile];
     Segment seg[13];   // of warps 0-11 and 14
@@ -216,8 +216,7 @@ __global__ void __launch_bounds__(kNT, 1)
         }
         for (int i = 0; i < 2; ++i) {
             tc::bar_init(tc::smem(&bars.s_full[i]), 1);
-            tc::bar_init(tc::smem(&bars.p_half[i]), 5);   // four warps, and the copies that the job needs
-            tc::bar_init(tc::smem(&bars.p_rest[i]), 4);
+            tc::bar_init(tc::smem(&bars.p_ready[i]), 5);   // four warps, and the copies that the job needs
             tc::bar_init(tc::smem(&bars.pv_done[i]), 1);
             tc::bar_init(tc::smem(&bars.turn[i]), 1);
             tc::bar_init(tc::smem(&bars.q_full[i]), 1);
@@ -413,8 +412,8 @@ __global__ void __launch_bounds__(kNT, 1)
             };
             auto pass = [&](int g) -> bool {
                 const unsigned sent = g ? sent1 : sent0;
-                if (sent > 0 && !wait_warp(&bars.p_half[g], (sent + 1) & 1)) return false;
-                if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_half[g]));
+                if (sent > 0 && !wait_warp(&bars.p_ready[g], (sent + 1) & 1)) return false;
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
                 if (g) ++sent1;
                 else ++sent0;
                 return true;
@@ -478,7 +477,6 @@ __global__ void __launch_bounds__(kNT, 1)
             const bool lead = tc::elect();
             const int g = warp == kWarpMma1;
             const uint32_t S_ = tc::uniform(tS[0] + g * 128), O_ = tc::uniform(tO[0] + g * DP);
-            uint64_t *const half = &bars.p_half[g], *const rest = &bars.p_rest[g];
             unsigned n0 = 0, segs = 0, done = 0, turns = 0;
             auto my_turn = [&]() -> bool {   // (stream 0 begins)
                 const unsigned i = turns++;
@@ -521,25 +519,14 @@ __global__ void __launch_bounds__(kNT, 1)
                     const unsigned st = (n0 + t) % SV;
                     const uint32_t v = tc::uniform(tc::operand_lo(vring + st * SM::kStage, kChunk));
                     const int steps = t == nt - 1 ? end_steps : kTile / 16;
-                    if (!(ok = wait_warp(half, done & 1)) || !(ok = my_turn())) break;
+                    if (!(ok = wait_warp(&bars.p_ready[g], done & 1)) || !(ok = my_turn())) break;
                     tc::fence_after();
                     if (lead) {
-                        if (steps >= 4) {
+                        if (steps == kTile / 16) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, t > first || i > 0);
+                            for (int i = 0; i < kTile / 16; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, t > first || i > 0);
                         } else {
                             for (int i = 0; i < steps; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, t > first || i > 0);
-                        }
-                    }
-                    __syncwarp();
-                    if (!(ok = wait_warp(rest, done & 1))) break;
-                    tc::fence_after();
-                    if (lead) {
-                        if (steps == 8) {
-#pragma unroll
-                            for (int i = 4; i < 8; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, true);
-                        } else {
-                            for (int i = 4; i < steps; ++i) tc::mma_ts(O_, S_ + i * 8, tc::operand(v + i * 128), kIdO, true);
                         }
                         tc::commit(tc::smem(&bars.pv_done[g]));
                         tc::commit(tc::smem(&bars.v_empty[st]));
@@ -598,10 +585,7 @@ __global__ void __launch_bounds__(kNT, 1)
             for (int j = g; j < jobs; j += 2) {
                 if (!(ok = wait_warp(&bars.s_full[g], own & 1))) break;
                 if (idle) {
-                    if (lane == 0) {
-                        tc::bar_arrive(tc::smem(&bars.p_half[g]));
-                        tc::bar_arrive(tc::smem(&bars.p_rest[g]));
-                    }
+                    if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
                     ++own;
                     continue;
                 }
@@ -670,13 +654,11 @@ __global__ void __launch_bounds__(kNT, 1)
                         p[i / 2] = Half<T>::pack(e.x, e.y);
                     }
                     tc::tmem_store16(mS + c * 16, p);
-                    if (c & 1) {   // half of the keys: their products can begin
-                        tc::tmem_wait_store();
-                        tc::fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::bar_arrive(tc::smem(c == 1 ? &bars.p_half[g] : &bars.p_rest[g]));
-                    }
                 }
+                tc::tmem_wait_store();
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::bar_arrive(tc::smem(&bars.p_ready[g]));
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 ++own;
             }
