@@ -635,7 +635,8 @@ int spec_tree_attention(const spec_attend_params *params, const void *q, const v
  * choices at them (the accepted drafts and one token more), both [B][N] filled
  * up with -1; accepted_len[b] counts the drafts (nodes but node 0). tokens and
  * outputs contiguous int32; choice with strides in elements. counts NULL: N; a
- * sequence of count 0 has accepted_len 0 and nothing but -1. parents as for
+ * sequence of count 0 has accepted_len 0 and nothing but -1. Outputs must not overlap
+ * inputs or one another. parents as for
  * spec_tree_attention (NULL: a chain); nodes with parent -1 other than node 0
  * are never reached. N in [1, SPEC_MAX_NODES].
  */

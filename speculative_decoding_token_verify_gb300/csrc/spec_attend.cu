@@ -619,7 +619,7 @@ __global__ void __launch_bounds__(kNT, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) mx[c] = max3(mx[c], x[c][i], x[c][i + 1]);
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sL;
-                const bool move = top > m + kLazy;
+                const bool move = real && top > m + kLazy;   // (rows that nobody uses may hold anything)
                 if (__any_sync(kFull, move)) {
                     const float to = move ? top : m, keep = move ? ex2(m - to) : 1.f;
                     m = to;

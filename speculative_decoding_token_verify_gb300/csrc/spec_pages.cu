@@ -573,7 +573,7 @@ static cudaError_t launch_pages(void (*kernel)(PagesArgs, int), bool *allowed, c
     return launch_cluster(kernel, C, NTP, C, 0, stream, a, C);
 }
 
-static int check_cache(const spec_cache_params *p, const void *cache) {
+static int check_cache(const spec_cache_params *p) {
     if (!p) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "params is NULL");
     if (p->O < 0 || p->P < 0 || p->H < 0 || p->page < 1)
         return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: O, P and H must be >= 0, page >= 1");
@@ -585,6 +585,7 @@ static int check_cache(const spec_cache_params *p, const void *cache) {
     for (int i = 0; i < 3; ++i)
         if (p->stride[i] < 0 || (n[i] > 1 && p->stride[i] > (INT64_MAX >> 4) / n[i]))
             return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: strides must be >= 0 and not too large");
+    if (p->O == 0 || p->P == 0 || p->H == 0) return SPEC_OK;
     const int64_t bytes = (int64_t)p->page * p->unit_bytes;
     // segments, pages and outer entries that do not overlap: ordered by stride, each
     // axis steps over the whole extent of the smaller ones
@@ -603,7 +604,6 @@ static int check_cache(const spec_cache_params *p, const void *cache) {
         if (p->stride[k] < extent) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "cache: pages overlap");
         extent += (n[k] - 1) * p->stride[k];
     }
-    (void)cache;
     return SPEC_OK;
 }
 
@@ -747,7 +747,7 @@ extern "C" int spec_pages_fork(const spec_pages_params *p, const int32_t *table,
 extern "C" int spec_pages_copy(const spec_cache_params *p, void *cache, const int32_t *copies, int32_t count,
                                void *stream) {
     using namespace sr;
-    const int rc = check_cache(p, cache);
+    const int rc = check_cache(p);
     if (rc != SPEC_OK) return rc;
     if (count < 0) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_copy: count must be >= 0");
     if (count == 0 || p->O == 0 || p->H == 0 || p->P == 0) return spec_internal_set_error(SPEC_OK, "");
@@ -769,7 +769,7 @@ extern "C" int spec_pages_compact(const spec_cache_params *p, void *cache, int32
                                   const int32_t *table, const int32_t *lengths, const int32_t *path,
                                   int32_t *out_lengths, int32_t *status, void *stream) {
     using namespace sr;
-    const int rc = check_cache(p, cache);
+    const int rc = check_cache(p);
     if (rc != SPEC_OK) return rc;
     if (B < 0 || M < 0) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "pages_compact: B and M must be >= 0");
     if (B > SPEC_MAX_B || N < 1 || N > SPEC_MAX_NODES || (int64_t)M * p->page > INT32_MAX - SPEC_MAX_NODES)
@@ -816,6 +816,22 @@ extern "C" int spec_tree_accept(int32_t B, int32_t N, const int32_t *tokens, con
     if (B == 0) return spec_internal_set_error(SPEC_OK, "");
     if (!tokens || !choice || !accepted_len || !out_tokens || !path)
         return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: an argument is NULL");
+    {
+        const int64_t rows = (int64_t)B * N * 4;
+        const void *in[4] = {tokens, parents, choice, counts};
+        const int64_t in_bytes[4] = {rows, parents ? ((B - 1) * parents_stride + N) * 4 : 0,
+                                     ((B - 1) * choice_batch_stride + (N - 1) * choice_node_stride + 1) * 4, counts ? B * 4LL : 0};
+        const void *out[3] = {accepted_len, out_tokens, path};
+        const int64_t out_bytes[3] = {B * 4LL, rows, rows};
+        for (int i = 0; i < 3; ++i) {
+            for (int j = 0; j < 4; ++j)
+                if (overlap(out[i], out_bytes[i], in[j], in_bytes[j]))
+                    return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: an output overlaps an input");
+            for (int j = 0; j < i; ++j)
+                if (overlap(out[i], out_bytes[i], out[j], out_bytes[j]))
+                    return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "tree_accept: outputs overlap");
+        }
+    }
     spec_internal_set_error(SPEC_OK, "");
     const AcceptArgs a{tokens, parents, choice, counts, accepted_len, out_tokens, path, status,
                        parents_stride, choice_batch_stride, choice_node_stride, B, N};

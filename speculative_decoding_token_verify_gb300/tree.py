@@ -210,6 +210,11 @@ def _caches(cache, page_dim, slot_dim, P=None):
             raise ValueError("the caches must be on one device")
         found.append((t, _cache_params(t, page_dim, slot_dim, P, page)))
         P, page = found[0][1].P, found[0][1].page
+    if len(found) > 1:
+        if len({t.data_ptr() for t, p in found if p.O}) < sum(p.O > 0 for _, p in found):
+            raise ValueError("the caches must not overlap")
+        for _, p in found:   # all are looked at before any is written
+            _check(_native.lib().spec_pages_copy(ctypes.byref(p), None, None, 0, None))
     return found, dev, P, page
 
 
@@ -222,8 +227,8 @@ def pages_compact(cache: Cache, table: torch.Tensor, lengths: torch.Tensor, path
     """The kept nodes of a tree moved to the end of the context, in place
     (spec_pages_compact). ``cache`` is a tensor of any dtype with the pool's
     pages along ``page_dim`` and their slots along ``slot_dim`` (None: the next
-    axis), or a sequence of such tensors (layers, keys, values) that share the
-    table; ``table`` [B,M], ``lengths`` [B], ``path`` [B,N] as tree_accept
+    axis), or a sequence of such tensors (layers, keys, values), none over
+    another, that share the table; ``table`` [B,M], ``lengths`` [B], ``path`` [B,N] as tree_accept
     returns it. Returns the new lengths [B] int32; ``out`` to write them into must not
     overlap ``lengths``."""
     found, dev, P, page = _caches(cache, page_dim, slot_dim)

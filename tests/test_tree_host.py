@@ -157,14 +157,26 @@ def test_cache_arguments_refused(L):
 
 
 def test_accept_arguments_refused(L):
-    def call(B=2, N=4, tokens=FAKE, parents=0, ps=0, choice=FAKE, cb=4, cn=1, acc=FAKE, out=FAKE, path=FAKE):
+    def call(B=2, N=4, tokens=FAKE, parents=0, ps=0, choice=FAKE + FAR, cb=4, cn=1, acc=FAKE + 2 * FAR, out=FAKE + 3 * FAR, path=FAKE + 4 * FAR):
         return L.spec_tree_accept(B, N, P(tokens), P(parents), ps, P(choice), cb, cn, None, P(acc), P(out), P(path), None, None)
 
     for kw, code in ((dict(B=-1), 1), (dict(N=0), 2), (dict(N=129), 2), (dict(B=(1 << 24) + 1), 2), (dict(parents=FAKE, ps=3), 1), (dict(ps=-1, parents=FAKE), 1),
                      (dict(cb=-1), 1), (dict(cn=-1), 1), (dict(cb=1 << 62), 1), (dict(cn=1 << 62), 1), (dict(tokens=0), 1), (dict(choice=0), 1),
-                     (dict(acc=0), 1), (dict(out=0), 1), (dict(path=0), 1)):
+                     (dict(acc=0), 1), (dict(out=0), 1), (dict(path=0), 1), (dict(out=FAKE + 4), 1), (dict(path=FAKE + FAR), 1),
+                     (dict(acc=FAKE + FAR + 28), 1), (dict(path=FAKE + 3 * FAR + 28), 1), (dict(parents=FAKE + 4 * FAR + 4, ps=4), 1)):
         assert call(**kw) == code, kw
     assert call(B=0, tokens=0) == 0
+
+
+def test_overlapping_caches_refused(monkeypatch):
+    monkeypatch.setattr(tree, "_on_gpu", lambda t, name: t.device)
+    t, i = torch.zeros((4, 16, 8)), torch.zeros((2, 4), dtype=torch.int32)
+    for bad in ([t, t], [t, t[:, :8]], [t, torch.zeros((3, 16, 8))]):
+        with pytest.raises(ValueError):
+            tree._caches(bad, 0, None)
+    with pytest.raises(sv.SpecError):
+        tree._caches([t, torch.zeros((1, 16, 8)).expand(4, 16, 8)], 0, None)      # pages over one another
+    assert len(tree._caches([t, torch.zeros((4, 16, 3)), torch.zeros((4, 16, 0))], 0, None)[0]) == 3
 
 
 # ---- the binding ----------------------------------------------------------------------------
