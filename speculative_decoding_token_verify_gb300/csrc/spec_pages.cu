@@ -18,7 +18,7 @@ namespace sr {
 constexpr int NTP = 1024;
 constexpr int NWP = NTP / 32;
 constexpr int kMaxPagesCluster = 16;
-constexpr int U = 8;   // groups of 32 entries whose loads are in flight together
+constexpr int U = 4;   // groups of 32 entries whose loads are in flight together (8, 16: more code, and slower)
 
 struct PagesArgs {
     const int32_t *table, *refs, *lengths, *parent;
@@ -48,84 +48,106 @@ __device__ __forceinline__ void cluster_sync_all(int C) {
 template <int K>
 __device__ __forceinline__ void ranks(PagesShared &sh, int slot, const int (&mine)[K], int C, int rank, int (&before)[K], int (&total)[K]) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    static_assert(NWP == 32, "a lane per warp");
     if (lane == 0)
         for (int k = 0; k < K; ++k) sh.warp[slot + k][warp] = mine[k];
     __syncthreads();
-    if (threadIdx.x < C * K) {
-        const int k = threadIdx.x / C, to = threadIdx.x - k * C;
-        int sum = 0;
-        for (int w = 0; w < NWP; ++w) sum += sh.warp[slot + k][w];
-        if (C > 1) peer_store_u32(peer(&sh.cta[slot + k][rank], to), (uint32_t)sum);
-        else sh.cta[slot + k][0] = sum;
-    }
     for (int k = 0; k < K; ++k) {
-        before[k] = 0;
-        for (int w = 0; w < warp; ++w) before[k] += sh.warp[slot + k][w];
+        const int n = sh.warp[slot + k][lane];
+        before[k] = __reduce_add_sync(kFull, lane < warp ? n : 0);
+        if (warp == 0) {
+            const int sum = __reduce_add_sync(kFull, n);
+            if (C == 1) sh.cta[slot + k][0] = sum;
+            else if (lane < C) peer_store_u32(peer(&sh.cta[slot + k][rank], lane), (uint32_t)sum);
+        }
     }
     cluster_sync_all(C);
     for (int k = 0; k < K; ++k) {
-        total[k] = 0;
-        for (int c = 0; c < C; ++c) {
-            if (c < rank) before[k] += sh.cta[slot + k][c];
-            total[k] += sh.cta[slot + k][c];
-        }
+        const int n = lane < C ? sh.cta[slot + k][lane] : 0;
+        before[k] += __reduce_add_sync(kFull, lane < rank ? n : 0);
+        total[k] = __reduce_add_sync(kFull, n);
     }
 }
 
-// A warp's stretch of n entries, in whole groups of 32 (of at least U, so that few entries
+// A warp's stretch of n entries, in whole groups of 32 V (of at least U, so that few entries
 // are not spread thin).
 struct Stretch {
     long long lo, hi;
-    __device__ __forceinline__ Stretch(long long n, int warp, int warps) {
-        const long long groups = (n + 31) / 32;
+    __device__ __forceinline__ Stretch(long long n, int warp, int warps, int V = 1) {
+        const long long size = 32 * V, groups = (n + size - 1) / size;
         long long per = (groups + warps - 1) / warps;
         if (per < U && per > 1) per = min((long long)U, groups);
-        lo = min(n, warp * per * 32);
-        hi = min(n, (warp + 1) * per * 32);
+        lo = min(n, warp * per * size);
+        hi = min(n, (warp + 1) * per * size);
     }
 };
+
+// V entries from i on, those past hi as `none`
+template <int V>
+__device__ __forceinline__ void load_entries(const int32_t *p, long long i, long long hi, int none, int (&e)[V]) {
+    if (V == 4 && i + 3 < hi) {
+        const int4 v = __ldcg(reinterpret_cast<const int4 *>(p + i));
+        e[0] = v.x, e[V / 3] = v.y, e[V / 2] = v.z, e[V - 1] = v.w;
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < V; ++k) e[k] = i + k < hi ? __ldcg(p + i + k) : none;
+}
 
 __device__ __forceinline__ int lanes_below(unsigned ballot) {
     return __popc(ballot & ((1u << (threadIdx.x & 31)) - 1));
 }
 
-// U entries of a warp's stretch of pages from i on: whether each is free. (A page that a row
-// has claimed is kept by it where nothing else names it.)
-template <bool kClaims>
-__device__ __forceinline__ void free_of(const PagesArgs &a, long long i, long long hi, bool (&free)[U]) {
-    int refs[U], claim[U];
+// Whether V pages from i on are free. (A page that a row has claimed is kept by it where nothing
+// else names it.)
+template <int V, bool kClaims>
+__device__ __forceinline__ unsigned free_of(const PagesArgs &a, long long i, long long hi) {
+    int refs[V], claim[V];
+    load_entries<V>(a.out_refs, i, hi, -1, refs);
+    if (kClaims) load_entries<V>(a.claim, i, hi, 0, claim);
+    unsigned free = 0;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-        refs[u] = i + 32 * u < hi ? __ldcg(a.out_refs + i + 32 * u) : -1;
-        if (kClaims) claim[u] = i + 32 * u < hi ? __ldcg(a.claim + i + 32 * u) : 0;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) free[u] = refs[u] == 0 && (!kClaims || claim[u] == INT_MAX);
+    for (int k = 0; k < V; ++k) free |= (unsigned)(refs[k] == 0 && (!kClaims || claim[k] == INT_MAX)) << k;
+    return free;
 }
-template <bool kClaims>
+template <int V, bool kClaims>
 __device__ __forceinline__ int count_free(const PagesArgs &a, const Stretch &s) {
     int count = 0;
-    for (long long i = s.lo + (threadIdx.x & 31); i < s.hi + (threadIdx.x & 31); i += 32 * U) {
-        bool free[U];
-        free_of<kClaims>(a, i, s.hi, free);
-#pragma unroll
-        for (int u = 0; u < U; ++u) count += __popc(__ballot_sync(kFull, free[u]));
+#pragma unroll 4
+    for (long long i = s.lo + (threadIdx.x & 31) * V; i < s.hi; i += 32 * V) count += __popc(free_of<V, kClaims>(a, i, s.hi));
+    return __reduce_add_sync(kFull, count);
+}
+// how many of the lower lanes' bits are set, and of all lanes'
+template <int V>
+__device__ __forceinline__ int bits_below(unsigned bits, int &all) {
+    if (V == 1) {
+        const unsigned ballot = __ballot_sync(kFull, bits);
+        all = __popc(ballot);
+        return lanes_below(ballot);
     }
-    return count;
+    int upto = __popc(bits);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int v = __shfl_up_sync(kFull, upto, o);
+        if ((threadIdx.x & 31) >= o) upto += v;
+    }
+    all = __shfl_sync(kFull, upto, 31);
+    return upto - __popc(bits);
 }
 // list[k] = the k-th lowest free page, for k < wanted; `before` free ones lie in front of the stretch
-template <bool kClaims>
+template <int V, bool kClaims>
 __device__ __forceinline__ void list_free(const PagesArgs &a, const Stretch &s, int before, int wanted) {
-    for (long long i = s.lo + (threadIdx.x & 31); i < s.hi + (threadIdx.x & 31) && before < wanted; i += 32 * U) {
-        bool free[U];
-        free_of<kClaims>(a, i, s.hi, free);
+    const int off = (threadIdx.x & 31) * V;
+    for (long long i = s.lo + off; i < s.hi + off && before < wanted; i += 32 * V) {
+        const unsigned free = free_of<V, kClaims>(a, i, s.hi);
+        int all, k = before + bits_below<V>(free, all);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const unsigned all = __ballot_sync(kFull, free[u]);
-            const int k = before + lanes_below(all);
-            if (free[u] && k < wanted) a.list[k] = (int)i + 32 * u;
-            before += __popc(all);
-        }
+        for (int v = 0; v < V; ++v)
+            if (free >> v & 1) {
+                if (k < wanted) a.list[k] = (int)i + v;
+                ++k;
+            }
+        before += all;
     }
 }
 
@@ -140,8 +162,8 @@ __device__ __forceinline__ int fit(const PagesArgs &a, int length) {
 struct Place {
     int r, m;
     __device__ __forceinline__ Place(long long i, int M) : r((int)(i / max(M, 1))), m((int)(i - (long long)r * M)) {}
-    __device__ __forceinline__ void next(int M) {
-        m += 32;
+    __device__ __forceinline__ void next(int M, int by = 32) {
+        m += by;
         if (m >= M) {
             const int q = m / M;
             r += q;
@@ -150,77 +172,107 @@ struct Place {
     }
 };
 
-// Rows of exactly the pages that their lengths ask for.
+// Rows of exactly the pages that their lengths ask for. V = 4: a lane takes four entries
+// together, of one row (M is a multiple of 4); a 512 x 1024 table then takes 18 us in place of 26.
+template <int V>
 __global__ void __launch_bounds__(NTP, 1) resize_kernel(PagesArgs a, int C) {
     __shared__ PagesShared sh;
     const int rank = C > 1 ? blockIdx.x : 0, lane = threadIdx.x & 31, gw = rank * NWP + (threadIdx.x >> 5);
+    const Stretch pages(a.P, gw, C * NWP, V), s((long long)a.B * a.W * a.M, gw, C * NWP, V);
     if (a.out_refs != a.refs) {
-#pragma unroll 8
-        for (int i = rank * NTP + threadIdx.x; i < a.P; i += C * NTP) a.out_refs[i] = __ldg(a.refs + i);
+#pragma unroll 4
+        for (long long i = pages.lo + lane * V; i < pages.hi; i += 32 * V) {
+            int refs[V];
+            load_entries<V>(a.refs, i, pages.hi, 0, refs);
+            if (V == 4 && i + 3 < pages.hi) {
+                *reinterpret_cast<int4 *>(a.out_refs + i) = make_int4(refs[0], refs[V / 3], refs[V / 2], refs[V - 1]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < V; ++k)
+                    if (i + k < pages.hi) a.out_refs[i + k] = refs[k];
+            }
+        }
     }
     cluster_sync_all(C);   // (from here on every CTA of the cluster has shared memory to write to)
-    const Stretch s((long long)a.B * a.W * a.M, gw, C * NWP);
     const int most = a.M * a.page;
-    int wants = 0;
+    int wants = 0, bad = 0;
     {
-        Place at(s.lo + lane, a.M);
-        for (long long i = s.lo + lane; i < s.hi + lane; i += 32 * U) {
-            int e[U], len[U], m[U];
+        Place at(s.lo + lane * V, a.M);
+        for (long long i = s.lo + lane * V; i < s.hi; i += 32 * V * U) {
+            int e[U][V], len[U], from[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u, at.next(a.M)) {
-                m[u] = at.m;
-                e[u] = i + 32 * u < s.hi ? a.table[i + 32 * u] : -1;
-                len[u] = i + 32 * u < s.hi ? a.lengths[at.r] : 0;
+            for (int u = 0; u < U; ++u, at.next(a.M, 32 * V)) {
+                from[u] = at.m * a.page;
+                load_entries<V>(a.table, i + 32 * V * u, s.hi, -1, e[u]);
+                len[u] = i + 32 * V * u < s.hi ? a.lengths[at.r] : 0;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const bool has = e[u] >= 0 && e[u] < a.P, in = m[u] * a.page < len[u];   // in: m < ceil(len / page)
-                if (!has && e[u] != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
-                if (len[u] < 0 || len[u] > most) raise_status(a.status, SPEC_ERR_BAD_LENGTH);
-                if (has && !in) atomicAdd(a.out_refs + e[u], -1);
-                wants += __popc(__ballot_sync(kFull, !has && in));
+                if ((unsigned)len[u] > (unsigned)most) bad = SPEC_ERR_BAD_LENGTH;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const bool has = (unsigned)e[u][k] < (unsigned)a.P, in = from[u] + k * a.page < len[u];   // in: m < ceil(len / page)
+                    if (!has && e[u][k] != -1) bad = max(bad, SPEC_ERR_BAD_PAGE);
+                    if (has && !in) atomicAdd(a.out_refs + e[u][k], -1);
+                    wants += !has && in;
+                }
             }
         }
+        if (bad) raise_status(a.status, bad);
+        wants = __reduce_add_sync(kFull, wants);
     }
     int ahead[1], all_wants[1];
     ranks<1>(sh, 0, {wants}, C, rank, ahead, all_wants);
     const int wanted = all_wants[0];
     int before = ahead[0], nfree = 0;
     if (wanted > 0) {   // (the same for the whole cluster)
-        const Stretch pages(a.P, gw, C * NWP);
         int all_free[1];
-        ranks<1>(sh, 1, {count_free<false>(a, pages)}, C, rank, ahead, all_free);
+        ranks<1>(sh, 1, {count_free<V, false>(a, pages)}, C, rank, ahead, all_free);
         nfree = all_free[0];
-        list_free<false>(a, pages, ahead[0], wanted);
+        list_free<V, false>(a, pages, ahead[0], wanted);
         cluster_sync_all(C);
     }
     if (nfree < wanted && rank == 0 && threadIdx.x == 0) raise_status(a.status, SPEC_ERR_NO_PAGES);
     {
-        Place at(s.lo + lane, a.M);
-        for (long long i = s.lo + lane; i < s.hi + lane; i += 32 * U) {
-            int e[U], len[U], m[U];
+        Place at(s.lo + lane * V, a.M);
+        for (long long i = s.lo + lane * V; i < s.hi + lane * V; i += 32 * V * U) {
+            int e[U][V], len[U], from[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u, at.next(a.M)) {
-                m[u] = at.m;
-                e[u] = i + 32 * u < s.hi ? a.table[i + 32 * u] : -1;
-                len[u] = i + 32 * u < s.hi ? a.lengths[at.r] : 0;
-            }
-            int k[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const bool has = e[u] >= 0 && e[u] < a.P, in = m[u] * a.page < len[u], want = !has && in;
-                if (!has || !in) e[u] = -1;
-                const unsigned all = __ballot_sync(kFull, want);
-                k[u] = want ? before + lanes_below(all) : INT_MAX;
-                before += __popc(all);
+            for (int u = 0; u < U; ++u, at.next(a.M, 32 * V)) {
+                from[u] = at.m * a.page;
+                load_entries<V>(a.table, i + 32 * V * u, s.hi, -1, e[u]);
+                len[u] = i + 32 * V * u < s.hi ? a.lengths[at.r] : 0;
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (k[u] < nfree) e[u] = __ldcg(a.list + k[u]);
-#pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (k[u] < nfree) a.out_refs[e[u]] = 1;
-                if (i + 32 * u < s.hi) a.out_table[i + 32 * u] = e[u];
+                const long long at_i = i + 32 * V * u;
+                unsigned want = 0;
+#pragma unroll
+                for (int k = 0; k < V; ++k) {
+                    const bool has = (unsigned)e[u][k] < (unsigned)a.P, in = from[u] + k * a.page < len[u] && at_i + k < s.hi;
+                    if (!has || !in) e[u][k] = -1;
+                    want |= (unsigned)(!has && in) << k;
+                }
+                if (__any_sync(kFull, want)) {   // (few groups want any)
+                    int all, rank_of = before + bits_below<V>(want, all);
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (want >> k & 1) {
+                            if (rank_of < nfree) {
+                                e[u][k] = __ldcg(a.list + rank_of);
+                                a.out_refs[e[u][k]] = 1;
+                            }
+                            ++rank_of;
+                        }
+                    before += all;
+                }
+                if (V == 4 && at_i + 3 < s.hi) {
+                    *reinterpret_cast<int4 *>(a.out_table + at_i) = make_int4(e[u][0], e[u][V / 3], e[u][V / 2], e[u][V - 1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        if (at_i + k < s.hi) a.out_table[at_i + k] = e[u][k];
+                }
             }
         }
     }
@@ -262,36 +314,44 @@ __global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
     {
         const Stretch s((long long)a.B * a.N * a.M, gw, C * NWP);
         Place at(s.lo + lane, a.M);
+        int row = -1, length = 0, bad = 0;
+        const int32_t *src = nullptr, *own = nullptr;   // the old rows' tables
         for (long long i = s.lo + lane; i < s.hi; i += 32 * U) {
-            int e[U], old[U], row[U];
-            bool last[U];
+            int e[U], old[U], of[U];
+            unsigned in = 0, last = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u, at.next(a.M)) {
                 e[u] = old[u] = -1;
-                row[u] = at.r;
-                last[u] = false;
                 if (i + 32 * u < s.hi) {
-                    const int b = at.r / a.N, n = at.r - b * a.N;
-                    int length;
-                    const int src = source_row(a, at.r, b, n, length), from = at.m * a.page;
-                    if (from < length) {   // (src >= 0 then)
-                        e[u] = a.table[(long long)src * a.M + at.m];
-                        last[u] = length - from < a.page;
-                        if (e[u] < 0 || e[u] >= a.P) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                    if (at.r != row) {
+                        row = at.r;
+                        const int b = row / a.N, n = row - b * a.N;
+                        src = a.table + (long long)source_row(a, row, b, n, length) * a.M;   // (not read where length is 0)
+                        own = n < a.W ? a.table + (long long)(b * a.W + n) * a.M : nullptr;
                     }
-                    if (n < a.W) old[u] = a.table[(long long)(b * a.W + n) * a.M + at.m];
+                    const int left = length - at.m * a.page;   // tokens from this entry on
+                    if (left > 0) {
+                        e[u] = src[at.m];
+                        in |= 1u << u;
+                        last |= (unsigned)(left < a.page) << u;
+                    }
+                    if (own) old[u] = own[at.m];
                 }
+                of[u] = row;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (i + 32 * u >= s.hi) continue;
-                if (e[u] < 0 || e[u] >= a.P) e[u] = -1;
-                if (old[u] < 0 || old[u] >= a.P) {
-                    if (old[u] != -1) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                if ((unsigned)e[u] >= (unsigned)a.P) {
+                    if (in >> u & 1) bad = SPEC_ERR_BAD_PAGE;
+                    e[u] = -1;
+                }
+                if ((unsigned)old[u] >= (unsigned)a.P) {
+                    if (old[u] != -1) bad = SPEC_ERR_BAD_PAGE;
                     old[u] = -1;
                 }
-                if (last[u]) {
-                    if (e[u] >= 0) atomicMin(a.claim + e[u], row[u]);
+                if (last >> u & 1) {
+                    if (e[u] >= 0) atomicMin(a.claim + e[u], of[u]);
                     e[u] = -1;   // (decided below)
                 }
                 if (old[u] != e[u]) {
@@ -301,6 +361,7 @@ __global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
                 a.out_table[i + 32 * u] = e[u];
             }
         }
+        if (bad) raise_status(a.status, bad);
     }
     if (a.N < a.W) {   // old rows without a new one in their place
         const int gone = a.W - a.N;
@@ -340,11 +401,11 @@ __global__ void __launch_bounds__(NTP, 1) fork_kernel(PagesArgs a, int C) {
     }
     // free pages are counted beside it: those that rows keep are claimed
     int ahead[2], all[2];
-    ranks<2>(sh, 0, {wants, count_free<true>(a, pages)}, C, rank, ahead, all);
+    ranks<2>(sh, 0, {wants, count_free<1, true>(a, pages)}, C, rank, ahead, all);
     int before = ahead[0];
     const int wanted = all[0], nfree = all[1];
     if (wanted == 0) return;   // (the same for the whole cluster)
-    list_free<true>(a, pages, ahead[1], wanted);
+    list_free<1, true>(a, pages, ahead[1], wanted);
     cluster_sync_all(C);
     if (nfree < wanted && rank == 0 && threadIdx.x == 0) raise_status(a.status, SPEC_ERR_NO_PAGES);
     for (long long r = s.lo + lane; r < s.hi + lane; r += 32) {
@@ -691,8 +752,12 @@ extern "C" int spec_pages_resize(const spec_pages_params *p, const int32_t *tabl
     a.P = p->P;
     a.page = p->page;
     const int C = pages_cluster(entries + p->P);
-    static bool allowed[64];
-    return done(launch_pages(resize_kernel, allowed, a, C, static_cast<cudaStream_t>(stream)));
+    const uintptr_t all = reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(refs) | reinterpret_cast<uintptr_t>(out_table) |
+                          reinterpret_cast<uintptr_t>(out_refs) | reinterpret_cast<uintptr_t>(workspace);
+    static bool allowed[64], allowed4[64];
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (all % 16 == 0 && p->M % 4 == 0) return done(launch_pages(resize_kernel<4>, allowed4, a, C, st));
+    return done(launch_pages(resize_kernel<1>, allowed, a, C, st));
 }
 
 extern "C" int spec_pages_fork(const spec_pages_params *p, const int32_t *table, const int32_t *refs,
