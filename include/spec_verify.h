@@ -50,7 +50,7 @@
  *    slice, token) against the buffer it addresses before the access, and
  *    on a failed check skip the access and raise SPEC_ERR_INDEX in the
  *    status word. They are for testing; the default build has no checks.
- *    (The row operators at the end have the same code in both builds.)
+ *    (The row and tree operators at the end have the same code in both builds.)
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H
@@ -727,7 +727,9 @@ int spec_get_device_status(const void *workspace, int32_t *status_out);
  * 2^20, well under a second) before it raises SPEC_ERR_TIMEOUT in the status
  * word and leaves that work undone. 0 makes every such wait give up at once,
  * so that a test can see the timeout path without a hang: the outputs of
- * the draw are then unspecified. The setting applies to launches enqueued
+ * the draw are then unspecified. The waits of spec_tree_attention's warps for one
+ * another have the same limit (a call that gave up raises SPEC_ERR_TIMEOUT in its status, its
+ * outputs are unspecified). The setting applies to launches enqueued
  * after the call, from any thread; returns the previous setting.
  */
 uint32_t spec_debug_set_wait_limit(uint32_t polls);

@@ -29,13 +29,15 @@
 #include "spec_rows.cuh"
 #include "spec_tc.cuh"
 
+extern "C" unsigned spec_internal_wait_limit(void);   // (spec_verify.cu)
+
 namespace sr {
 
 constexpr int kTile = 128;             // keys a tile, and rows a tile
 constexpr int kChunk = kTile * 128;    // bytes of 64 elements of a tile's rows
 constexpr int kNT = 512;               // warps 0-3 and 12-15 copies and products, 4-7 and 8-11 the streams' softmax
 constexpr int kWarpK = 0, kWarpV = 3, kWarpGo = 2, kWarpMma0 = 1, kWarpMma1 = 14;   // (spread over the four schedulers)
-constexpr unsigned kSpin = 1u << 20;   // polls of a wait before it gives up
+constexpr unsigned kDrain = 1u << 20;  // polls for what is in flight at the end
 constexpr int kSegRing = 4;            // segments whose flags of non-finite values are kept
 constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
 
@@ -51,6 +53,7 @@ struct AttendArgs {
     int B, N, Hq, Hkv, G, D, P, page, M, fill;
     int nodes, q_rows;   // a tile, and the rows that a copy of queries brings
     float sL;         // |scale| log2 e
+    unsigned spin;    // polls of a wait before it gives up
     int neg;          // scale < 0
     long long vs[3], ps;
 };
@@ -314,7 +317,7 @@ __global__ void __launch_bounds__(kNT, 1)
     // loop does not diverge.)
     auto wait_warp = [&](const uint64_t *bar, uint32_t parity) -> bool {
         const uint32_t addr = tc::smem(bar);
-        for (unsigned i = 0; i < kSpin; ++i) {
+        for (unsigned i = 0; i < a.spin; ++i) {
             if (__all_sync(kFull, tc::bar_try(addr, parity))) return true;
             if (__any_sync(kFull, *(volatile int *)&sh.abort)) return false;
         }
@@ -390,13 +393,11 @@ __global__ void __launch_bounds__(kNT, 1)
                     if (keys && !first && t == min(nt, ahead) - 1) ok = queries();
                 }
             }
-            // nothing is left in flight when another role has given up
-            if (*(volatile int *)&sh.abort) {
-                for (unsigned i = n > S ? n - S : 0; i < n; ++i)
-                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&full[i % S]), (i / S) & 1); ++k) {}
-                for (unsigned i = segs > 1 ? segs - 2 : 0; keys && i < segs; ++i)
-                    for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.q_full[twin ? i & 1 : 0]), (twin ? i >> 1 : i) & 1); ++k) {}
-            }
+            // no copy may still be in flight when the CTA ends, whether or not another role has given up
+            for (unsigned i = n > S ? n - S : 0; i < n; ++i)
+                for (unsigned k = 0; k < kDrain && !tc::bar_try(tc::smem(&full[i % S]), (i / S) & 1); ++k) {}
+            for (unsigned i = segs > (twin ? 1 : 0) ? segs - (twin ? 2 : 1) : 0; keys && i < segs; ++i)
+                for (unsigned k = 0; k < kDrain && !tc::bar_try(tc::smem(&bars.q_full[twin ? i & 1 : 0]), (twin ? i >> 1 : i) & 1); ++k) {}
         } else if (warp == kWarpGo) {
             // ---- what a job needs: its copies are there, and its values can be multiplied --------------
             // This warp alone waits for the copies, in their order, and passes a job on when its
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kNT, 1)
             // (none of the products may still run when the CTA ends)
             if (lead) {
                 tc::commit(tc::smem(&bars.drain));
-                for (unsigned k = 0; k < kSpin && !tc::bar_try(tc::smem(&bars.drain), 0); ++k) {}
+                for (unsigned k = 0; k < kDrain && !tc::bar_try(tc::smem(&bars.drain), 0); ++k) {}
             }
             __syncwarp();
         }
@@ -1019,6 +1020,7 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
     a.q_rows = q_nodes * G;
     a.sL = fmaxf(fabsf(p->scale) * sv::kLog2e, FLT_MIN);   // (0 times a masked key's -inf would be NaN)
     a.neg = p->scale < 0.f;
+    a.spin = spec_internal_wait_limit();
     a.ps = p->parents_stride;
     for (int j = 0; j < 3; ++j) a.vs[j] = p->v_stride[j];
     const int nq[3] = {p->B, p->N, p->Hq}, nk[3] = {p->P > 0 ? p->P : 1, p->page, p->Hkv}, box = p->page < 64 ? p->page : 64;

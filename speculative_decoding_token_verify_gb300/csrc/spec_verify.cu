@@ -1858,6 +1858,9 @@ int spec_get_device_status(const void *workspace, int32_t *status_out) {
 
 uint32_t spec_debug_set_wait_limit(uint32_t polls) { return g_wait_limit.exchange(polls); }
 
+// the limit, for the other kernels that wait
+__attribute__((visibility("hidden"))) unsigned spec_internal_wait_limit(void) { return g_wait_limit.load(); }
+
 // Allocation-free variant of spec_verify: the workspace is the library's
 // static scratch array instead of caller memory. The host-side name of that
 // array is not a device address, so its address is looked up once per device

@@ -299,6 +299,26 @@ def test_repeated_under_load():
     assert all(torch.equal(o["out"], want["out"]) and torch.equal(o["lse"], want["lse"]) for o in outs)
 
 
+def test_waits_give_up():
+    """With no polls allowed every wait gives up: a code, and nothing left behind."""
+    sv = _sv()
+    from speculative_decoding_token_verify_gb300 import _native
+    for N, lengths in ((1, [5]), (9, [900, 30, 0]), (64, [2000, 100])):
+        c = _case(23, BF16, N, 8, 2, 64, 16, lengths)
+        want, st = _run(sv, c), _i32([0])
+        torch.cuda.synchronize()
+        old = _native.lib().spec_debug_set_wait_limit(0)
+        try:
+            _run(sv, c, status=st)
+            torch.cuda.synchronize()
+        finally:
+            _native.lib().spec_debug_set_wait_limit(old)
+        assert int(st) == 4
+        st.zero_()
+        got = _run(sv, c, status=st)
+        assert int(st) == 0 and torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
 def test_empty():
     sv = _sv()
     c = _case(12, BF16, 3, 4, 2, 64, 16, [5])
