@@ -173,7 +173,9 @@ struct Place {
 };
 
 // Rows of exactly the pages that their lengths ask for. V = 4: a lane takes four entries
-// together, of one row (M is a multiple of 4); a 512 x 1024 table then takes 18 us in place of 26.
+// together, of one row (M is a multiple of 4). A 512 x 1024 table over 315,000 pages takes 23 us
+// (one by one 26), ten times its bytes: seven phases that each wait for memory and for the
+// cluster. Tables that one CTA handles take their entries one by one (4 x 64: 6.2 us, by fours 7.2).
 template <int V>
 __global__ void __launch_bounds__(NTP, 1) resize_kernel(PagesArgs a, int C) {
     __shared__ PagesShared sh;
@@ -611,15 +613,13 @@ static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
     return na > 0 && nb > 0 && x < y + nb && y < x + na;
 }
 
-// Small tables are one CTA's work (cluster barriers cost more than they share out).
-static int pages_cluster(long long ints) {
-    int c = 1;
-    while (c < kMaxPagesCluster && ints > 8192LL * c) c *= 2;
-    return c;
-}
+// Small tables are one CTA's work, whose barriers cost less; all others the largest cluster's. In a
+// graph, one CTA against 16: 8.6 and 10.6 us for rows of 16 x 64 entries, 14.7 and 12.6 for 64 x 128, 58 and
+// 16.7 for 256 x 512 (2, 4 and 8 CTAs lie between; 8 are as fast as 16 up to there, and 16 faster beyond).
+static int pages_cluster(long long ints) { return ints > 4096 ? kMaxPagesCluster : 1; }
 
 static cudaError_t launch_pages(void (*kernel)(PagesArgs, int), bool *allowed, const PagesArgs &a, int C, cudaStream_t stream) {
-    if (C > 8) {   // (clusters of more than 8 CTAs have to be allowed, once for each device)
+    if (C > 1) {   // (clusters of more than 8 CTAs have to be allowed, once for each device)
         static std::mutex mu;
         int dev = 0;
         cudaError_t e = cudaGetDevice(&dev);
@@ -756,7 +756,7 @@ extern "C" int spec_pages_resize(const spec_pages_params *p, const int32_t *tabl
                           reinterpret_cast<uintptr_t>(out_refs) | reinterpret_cast<uintptr_t>(workspace);
     static bool allowed[64], allowed4[64];
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (all % 16 == 0 && p->M % 4 == 0) return done(launch_pages(resize_kernel<4>, allowed4, a, C, st));
+    if (C > 1 && all % 16 == 0 && p->M % 4 == 0) return done(launch_pages(resize_kernel<4>, allowed4, a, C, st));
     return done(launch_pages(resize_kernel<1>, allowed, a, C, st));
 }
 
