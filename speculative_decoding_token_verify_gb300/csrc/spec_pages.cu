@@ -466,11 +466,13 @@ __global__ void __launch_bounds__(NTC) copy_kernel(CacheArgs a, int count) {
 
 // The kept nodes of row b = blockIdx.y. A thread owns one vector of a unit and
 // makes its moves in order, eight loads ahead of their stores: a source path[j]
-// lies behind every place i <= j that was written before it is read.
+// lies behind every place i <= j that was written before it is read. 64 rows of 33 nodes,
+// 64 KB a node, 67 MB in all: 14.6 us in a graph, 4.6 TB/s; about 4 us of it are the launch and the
+// chain of lengths, path and table (16 loads ahead leave one CTA an SM: 28 us; 4, 6 and 12: 14.7 to 15.4).
 template <typename Vec>
 __global__ void __launch_bounds__(NTC) compact_kernel(CacheArgs a) {
     __shared__ long long s_src[SPEC_MAX_NODES], s_dst[SPEC_MAX_NODES];
-    __shared__ int s_kept;
+    __shared__ int s_kept, s_moves[SPEC_MAX_NODES / 32];
     constexpr int U = 8;
     const bool lead = blockIdx.x == 0;
     for (int b = blockIdx.y; b < a.B; b += gridDim.y) {
@@ -488,10 +490,10 @@ __global__ void __launch_bounds__(NTC) compact_kernel(CacheArgs a) {
         }
         __syncthreads();
         const int kept = s_kept;
-        if (threadIdx.x < kept) {
-            const int i = threadIdx.x, p = path[i];
-            const int from = L + p, to = L + i;
-            long long so = -1, dof = 0;
+        long long so = -1, dof = 0;
+        unsigned moves = 0;
+        if (threadIdx.x < SPEC_MAX_NODES) {
+            const int i = threadIdx.x, p = i < kept ? path[i] : i, from = L + p, to = L + i;
             if (p != i) {
                 const int mf = from / a.page, mt = to / a.page;
                 const int pf = mf < a.M ? a.table[(long long)b * a.M + mf] : -1;
@@ -503,8 +505,17 @@ __global__ void __launch_bounds__(NTC) compact_kernel(CacheArgs a) {
                     raise_status(a.status, SPEC_ERR_BAD_PAGE);
                 }
             }
-            s_src[i] = so;
-            s_dst[i] = dof;
+            moves = __ballot_sync(kFull, so >= 0);
+            if ((threadIdx.x & 31) == 0) s_moves[threadIdx.x >> 5] = __popc(moves);
+        }
+        __syncthreads();
+        int total = 0;
+        for (int w = 0; w < SPEC_MAX_NODES / 32; ++w) {
+            if (so >= 0 && w == (int)(threadIdx.x >> 5)) {
+                s_src[total + lanes_below(moves)] = so;
+                s_dst[total + lanes_below(moves)] = dof;
+            }
+            total += s_moves[w];
         }
         if (lead && threadIdx.x == 0) {
             a.out_lengths[b] = L + kept;
@@ -516,14 +527,14 @@ __global__ void __launch_bounds__(NTC) compact_kernel(CacheArgs a) {
         for (long long x = (long long)blockIdx.x * NTC + threadIdx.x; x < columns; x += (long long)gridDim.x * NTC) {
             const long long oh = x / a.vecs, o = oh / a.H;
             char *base = a.cache + o * a.ss[0] + (oh - o * a.H) * a.ss[2] + (x - oh * a.vecs) * (long long)sizeof(Vec);
-            for (int i = 0; i < kept; i += U) {
+            for (int i = 0; i < total; i += U) {
                 Vec v[U];
 #pragma unroll
                 for (int k = 0; k < U; ++k)
-                    if (i + k < kept && s_src[i + k] >= 0) v[k] = *reinterpret_cast<const Vec *>(base + s_src[i + k]);
+                    if (i + k < total) v[k] = *reinterpret_cast<const Vec *>(base + s_src[i + k]);
 #pragma unroll
                 for (int k = 0; k < U; ++k)
-                    if (i + k < kept && s_src[i + k] >= 0) *reinterpret_cast<Vec *>(base + s_dst[i + k]) = v[k];
+                    if (i + k < total) *reinterpret_cast<Vec *>(base + s_dst[i + k]) = v[k];
             }
         }
     }
