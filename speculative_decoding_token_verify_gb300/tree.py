@@ -18,6 +18,7 @@ free), ``lengths`` int32 are tokens. One decoding step::
 from __future__ import annotations
 
 import ctypes
+import math
 from typing import Optional, Sequence, Union
 
 import torch
@@ -32,6 +33,7 @@ F16 = 2
 _TYPES = {torch.bfloat16: BF16, torch.float16: F16}
 _F32, _I32 = torch.float32, torch.int32
 _MOST = (1 << 31) - 1
+_I3 = ctypes.c_int64 * 3
 
 
 def _need(t, name, shape, device, dtype=_I32):
@@ -64,9 +66,8 @@ def _new(out, name, shape, device, dtype=_I32):
 
 
 def _small(what, *sizes):
-    for n in sizes:
-        if n > _MOST:   # before the C ABI's 32-bit fields
-            raise SpecError(SPEC_ERR_UNSUPPORTED, f"{what}: a size is outside the supported range")
+    if max(sizes) > _MOST:   # before the C ABI's 32-bit fields
+        raise SpecError(SPEC_ERR_UNSUPPORTED, f"{what}: a size is outside the supported range")
 
 
 def _parents(parents, B, N, device):
@@ -91,21 +92,22 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: tor
     slots lengths[b] + n. ``parents`` [B,N] or [N] int32 (None: a chain),
     ``counts`` [B] int32 or None (N). ``scale`` None is D ** -0.5. Returns ``out``
     [B,N,Hq,D] and ``lse`` [B,N,Hq] float32. No part of an autograd graph."""
-    dev = _on_gpu(q, "q")
-    dt = _TYPES.get(q.dtype)
+    dev, dtype = _on_gpu(q, "q"), q.dtype
+    dt = _TYPES.get(dtype)
     if dt is None:
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    qshape, kshape = q.shape, k.shape
+    if len(qshape) != 4 or len(kshape) != 4 or v.shape != kshape:
         raise ValueError("q must be [B, N, Hq, D], k and v [P, page, Hkv, D]")
-    if k.dtype != q.dtype or v.dtype != q.dtype or k.device != dev or v.device != dev:
+    if k.dtype != dtype or v.dtype != dtype or k.device != dev or v.device != dev:
         raise ValueError("q, k and v must have one dtype and device")
-    B, N, Hq, D = q.shape
-    P, page, Hkv, Dk = k.shape
+    B, N, Hq, D = qshape
+    P, page, Hkv, Dk = kshape
     if Dk != D:
         raise ValueError("q, k and v must have the same head size")
-    for t, name in ((q, "q"), (k, "k"), (v, "v")):
-        if t.stride(3) != 1 and D > 1:
-            raise ValueError(f"{name}: the head's elements must be contiguous")
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    if (qs[3] != 1 or ks[3] != 1 or vs[3] != 1) and D > 1:
+        raise ValueError("q, k and v: the head's elements must be contiguous")
     if table.dim() != 2:
         raise ValueError("table must be [B, M]")
     M = table.shape[1]
@@ -114,16 +116,13 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: tor
     _maybe(counts, "counts", (B,), dev)
     ps = _parents(parents, B, N, dev)
     _status(status, dev)
-    _small("tree_attention", *q.shape, *k.shape, M)
-    p = _native.AttendParams(B, N, Hq, Hkv, D, dt, P, page, M, D ** -0.5 if scale is None else scale)
-    p.q_stride[:] = q.stride()[:3]
-    p.k_stride[:] = k.stride()[:3]
-    p.v_stride[:] = v.stride()[:3]
-    p.parents_stride = ps
+    _small("tree_attention", B, N, Hq, P, page, Hkv, D, M)
+    p = _native.AttendParams(B, N, Hq, Hkv, D, dt, P, page, M, D ** -0.5 if scale is None else scale, _I3(*qs[:3]),
+                             _I3(*ks[:3]), _I3(*vs[:3]), ps)
 
     def body(s):
         L = _native.lib()
-        o = _new(out, "out", q.shape, dev, q.dtype)
+        o = _new(out, "out", qshape, dev, dtype)
         lse = _new(out, "lse", (B, N, Hq), dev, _F32)
         size = L.spec_tree_attention_workspace_size(ctypes.byref(p))
         ws = torch.empty(size, dtype=torch.uint8, device=dev)
@@ -183,6 +182,10 @@ def _cache_params(t, page_dim, slot_dim, P, page):
         raise ValueError("caches and refs must have the same pages")
     if 0 in shape[sd + 1:]:   # nothing to move
         return _native.CacheParams(0, shape[pd], 0, shape[sd], es)
+    if t.is_contiguous():   # (strides from the shape: those of axes of one entry say nothing)
+        O, H, unit = math.prod(shape[:pd]), math.prod(shape[pd + 1:sd]), math.prod(shape[sd + 1:])
+        seg = shape[sd] * unit
+        return _params((O, shape[pd] * H * seg if O > 1 else 0), (H, seg if H > 1 else 0), shape[pd], H * seg, shape[sd], unit, es)
     unit = 1
     for c, k in zip(reversed(shape[sd + 1:]), reversed(stride[sd + 1:])):
         if c != 1 and k != unit:
@@ -193,10 +196,12 @@ def _cache_params(t, page_dim, slot_dim, P, page):
     outer, seg = _merged(shape[:pd], stride[:pd]), _merged(shape[pd + 1:sd], stride[pd + 1:sd])
     if outer is None or seg is None:
         raise ValueError("cache: the axes before the pages, and those between page and slot, must each be evenly spaced")
-    _small("cache", outer[0], seg[0], shape[pd], shape[sd], unit * es)
-    p = _native.CacheParams(outer[0], shape[pd], seg[0], shape[sd], unit * es)
-    p.stride[:] = [outer[1] * es, stride[pd] * es, seg[1] * es]
-    return p
+    return _params(outer, seg, shape[pd], stride[pd], shape[sd], unit, es)
+
+
+def _params(outer, seg, pages, page_stride, slots, unit, es):
+    _small("cache", outer[0], seg[0], pages, slots, unit * es)
+    return _native.CacheParams(outer[0], pages, seg[0], slots, unit * es, _I3(outer[1] * es, page_stride * es, seg[1] * es))
 
 
 def _caches(cache, page_dim, slot_dim, P=None):

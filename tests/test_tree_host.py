@@ -203,6 +203,8 @@ def test_cache_layouts():
     assert of(t, 1, 3) == [3, 2, 10, 16, 64, [20480, 10240, 1024]]
     assert of(t[:, 0], 1) == [3, 10, 1, 16, 64, [20480, 1024, 0]]
     assert of(t[:, :, 2:5], 2, pool=3)[:2] == [6, 3]
+    odd = t[:, :, :1].as_strided((3, 2, 1, 16, 4, 8), (1024, 512, 7, 32, 8, 1))    # an axis of one entry with any stride
+    assert odd.is_contiguous() and of(odd, 2)[:5] == [6, 1, 1, 16, 64] and of(odd, 2)[5][0] == 1024
     assert of(t[..., :0], 2)[0] == 0 and of(t[..., :0], 2)[4] == 2
     for bad in (lambda: of(t[..., :4], 2), lambda: of(t[:, :, :, ::2], 2), lambda: of(t, 5), lambda: of(t, 2, 2), lambda: of(t, 2, 1),
                 lambda: of(t, 2, pool=9), lambda: of(t, 2, page=8), lambda: of(t[:, :, :, :, :3], 2), lambda: of(t.transpose(0, 1)[:, :2], 2)):
