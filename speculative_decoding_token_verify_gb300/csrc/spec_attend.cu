@@ -15,6 +15,12 @@
 // part's ends may lie inside a sequence. Those pieces go to the workspace unnormalised, and a
 // second kernel joins them.
 //
+// Measured (in a graph; bf16, 8 key heads of 128): 64 sequences of up to 8192 tokens, 9 nodes
+// of 32 heads, 1.37 GB: 224 us, 6.1 TB/s, 0.90 of a copy's rate; one token for 256 sequences of up
+// to 4096: 417 us, 6.5 TB/s. 8 sequences of up to 32768, 64 nodes of 64 heads, 0.37 TFLOP: 300 us, 1.23
+// PFLOP/s; there a job's products take 1440 of the 1800 cycles between two streams' turns (scores
+// read both operands from shared memory, at its full rate). One token over 2048: 12 us.
+//
 // What a row must not see. Keys behind the context are masked by a bit per node. A
 // probability of 0 does not stop a NaN value, so a warp of its own looks at the values behind the
 // context before they are multiplied: slots that no node owns become 0, and of the nodes' own values the NaN and infinities
@@ -183,7 +189,8 @@ struct AttendShared {
     int abort;
 };
 
-// FEW: at most 64 rows a sequence and key head (one tile). Their queries take a quarter of the
+// FEW: at most 64 rows a sequence and key head (one tile): 64 x 9 nodes of 36 rows take 227 us, 236
+// without it, and 256 x 1 436 and 453. Their queries take a quarter of the
 // room of two tiles of 128 (the products read what lies behind them, for rows that nobody uses), which
 // leaves another stage to the rings.
 template <int DC, bool FEW>

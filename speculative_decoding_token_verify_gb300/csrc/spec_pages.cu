@@ -7,7 +7,8 @@
 // cluster barrier between the phases. Each warp owns a contiguous stretch of entries (and later of pages),
 // so that a rank is a sum of ballots: over the warp's own stretch, the CTA's earlier
 // warps, and the cluster's earlier CTAs. Reference counts change by integer
-// atomics, whose order cannot be seen.
+// atomics, whose order cannot be seen. What bounds them is the chain of phases: 5.4 us for 4 rows of
+// 64 entries, 23 for 512 of 1024; 256 beams of 257 entries forked 13 us with the copies (in a graph).
 #include <climits>
 #include <mutex>
 
@@ -439,7 +440,7 @@ struct CacheArgs {
 
 constexpr int NTC = 256;
 
-// copies[y]: the first slots of a page, CP vectors a thread
+// copies[y]: the first slots of a page, CP vectors a thread (4: 16 KB of a page in one CTA's loads)
 template <typename Vec, int CP>
 __global__ void __launch_bounds__(NTC) copy_kernel(CacheArgs a, int count) {
     asm volatile("griddepcontrol.wait;" ::: "memory");   // (launched while the stream's last kernel, the fork, ends)
@@ -553,7 +554,7 @@ constexpr int kPerLane = SPEC_MAX_NODES / 32;
 constexpr int NTA = 128;
 
 // A warp per sequence; lane l holds nodes l, l + 32, ..: a step of the walk is a
-// comparison and a ballot for each.
+// comparison and a ballot for each. 256 trees of 128 nodes 3.1 us in a graph, one of 9 2.1: a launch.
 __global__ void __launch_bounds__(NTA) accept_kernel(AcceptArgs a) {
     __shared__ int32_t s_choice[NTA / 32][SPEC_MAX_NODES];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
