@@ -712,6 +712,7 @@ __global__ void __launch_bounds__(kNT, 1)
 #pragma unroll 1
             for (int c = idle ? c1 : c0; c < c1; ++c) {
                 float o[32];
+                __syncwarp();
                 tc::tmem_load(tO[two ? g : 0] + row_lane + c * 32, o);
                 tc::tmem_wait_load();
 #pragma unroll
