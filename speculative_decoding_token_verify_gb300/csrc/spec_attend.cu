@@ -602,6 +602,8 @@ __global__ void __launch_bounds__(kNT, 1)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) tc::tmem_load(mS + c * 32, x[c]);
                 tc::tmem_wait_load();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tc::loaded(x[c]);
                 if (a.neg)
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
@@ -640,6 +642,7 @@ __global__ void __launch_bounds__(kNT, 1)
                             float o[32];
                             tc::tmem_load(tO[g] + row_lane + c * 32, o);
                             tc::tmem_wait_load();
+                            tc::loaded(o);
 #pragma unroll
                             for (int i = 0; i < 32; ++i) o[i] *= keep;
                             tc::tmem_store(tO[g] + row_lane + c * 32, o);
@@ -715,12 +718,14 @@ __global__ void __launch_bounds__(kNT, 1)
                 __syncwarp();
                 tc::tmem_load(tO[two ? g : 0] + row_lane + c * 32, o);
                 tc::tmem_wait_load();
+                tc::loaded(o);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) o[i] *= w0;
                 if (both) {
                     float q[32];
                     tc::tmem_load(tO[1] + row_lane + c * 32, q);
                     tc::tmem_wait_load();
+                    tc::loaded(q);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = fmaf(q[i], w1, o[i]);
                 }

@@ -363,6 +363,44 @@ def test_streams_and_graphs():
                 v.zero_()
 
 
+def test_on_a_stream_of_its_own():
+    """Every call with stream=, beside work on the current stream; outputs written there."""
+    sv = _sv()
+    s = torch.cuda.Stream()
+    tokens, choice = _i32([[5, 1, 2, 3]] * 3), _i32([[1, 2, 9, 9]] * 3)
+    table, refs, lengths = _i32([[0, 1], [2, -1], [3, -1]]), _i32([1, 1, 1, 1, 0, 0]), _i32([20, 9, 3])
+    cache = torch.arange(96, device=DEV, dtype=torch.int32).view(6, 16, 1)
+    want = [sv.tree_accept(tokens, None, choice), sv.pages_resize(table, refs, lengths, 16)]
+    kept = cache.clone()
+    path = want[0]["path"]
+    new = sv.pages_compact(kept, table, lengths, path)
+    s.wait_stream(torch.cuda.current_stream())
+    got = [sv.tree_accept(tokens, None, choice, stream=s), sv.pages_resize(table, refs, lengths, 16, stream=s)]
+    other = sv.pages_compact(cache, table, lengths, got[0]["path"], stream=s)
+    s.synchronize()
+    for a, b in zip(got, want):
+        assert all(torch.equal(a[k], b[k]) for k in b)
+    assert torch.equal(other, new) and torch.equal(cache, kept)
+    with pytest.raises(ValueError):
+        sv.tree_accept(tokens.cpu(), None, choice)
+
+
+def test_writes_are_seen_by_autograd():
+    sv = _sv()
+    cache = torch.zeros((4, 16, 2), device=DEV)
+    w = torch.ones((4, 16, 2), device=DEV, requires_grad=True)
+    y = (w * cache).sum()
+    sv.pages_compact(cache, _i32([[0, 1]]), _i32([4]), _i32([[1, 2]]))
+    with pytest.raises(RuntimeError):
+        y.backward()                        # the cache that it kept was written
+    table, refs = _i32([[0, -1]]), _i32([1, 0, 0, 0])
+    v = table._version, refs._version
+    sv.pages_resize(table, refs, _i32([20]), 16)
+    assert (table._version, refs._version) == v
+    sv.pages_resize(table, refs, _i32([20]), 16, out={"table": table, "refs": refs})
+    assert table._version > v[0] and refs._version > v[1]
+
+
 # ---- together -------------------------------------------------------------------------------
 
 

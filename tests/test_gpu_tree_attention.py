@@ -359,6 +359,27 @@ def test_bad_device_values():
     status(lambda t: t["table"].__setitem__((0, 2), -(1 << 31)), 10)
 
 
+def test_out_and_autograd():
+    """Outputs into the caller's tensors, whose versions move; queries that want a gradient."""
+    sv = _sv()
+    c = _case(24, BF16, 5, 8, 2, 64, 16, [40])
+    want = _run(sv, c)
+    o = {"out": torch.empty((1, 5, 8, 64), dtype=BF16, device=DEV), "lse": torch.empty((1, 5, 8), device=DEV)}
+    v = o["out"]._version, o["lse"]._version
+    q = c["q"].to(DEV).requires_grad_(True)
+    r = sv.tree_attention(q, c["k"].to(DEV), c["v"].to(DEV), c["table"].to(DEV), _i32(c["lengths"]), _i32(c["parents"]), out=o)
+    assert r["out"] is o["out"] and r["lse"] is o["lse"] and not r["out"].requires_grad
+    assert o["out"]._version > v[0] and o["lse"]._version > v[1]
+    assert torch.equal(r["out"], want["out"]) and torch.equal(r["lse"], want["lse"])
+    with pytest.raises(ValueError):
+        sv.tree_attention(q, c["k"].to(DEV), c["v"].to(DEV), c["table"].to(DEV), _i32(c["lengths"]), out={"out": o["out"][:, :4]})
+    with pytest.raises(TypeError):
+        sv.tree_attention(q.float(), c["k"].to(DEV), c["v"].to(DEV), c["table"].to(DEV), _i32(c["lengths"]))
+    with pytest.raises(sv.SpecError):
+        sv.tree_attention(q.expand(3, 5, 8, 64), c["k"].to(DEV), c["v"].to(DEV), c["table"].expand(3, -1).contiguous().to(DEV),
+                          _i32(c["lengths"] * 3))         # a stride of 0
+
+
 def test_streams_and_graphs():
     sv = _sv()
     c, d = _case(14, BF16, 9, 8, 2, 64, 16, [3000, 40]), _case(15, BF16, 9, 8, 2, 64, 16, [64, 2500])
