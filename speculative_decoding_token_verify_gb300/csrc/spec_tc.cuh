@@ -132,7 +132,7 @@ __device__ __forceinline__ uint32_t operand_lo(uint32_t addr, uint32_t lead) { r
 __device__ __forceinline__ uint64_t operand(uint32_t lo) {
     return (uint64_t)((1024 >> 4) | 1u << 14 | 2u << 29) << 32 | lo;
 }
-// fp32 accumulators, fp16 (0) or bf16 (1) inputs, M = 128, B K-major or MN-major
+// fp32 accumulators, fp16 (0) or bf16 (1) inputs, M = 128, N a multiple of 16, B K-major or MN-major
 __device__ __forceinline__ constexpr uint32_t shape(int bf16, int n, bool b_mn) {
     return 1u << 4 | (uint32_t)bf16 << 7 | (uint32_t)bf16 << 10 | (b_mn ? 1u << 16 : 0u) | (uint32_t)(n >> 3) << 17 | (128u >> 4) << 24;
 }
