@@ -570,13 +570,14 @@ __global__ void __launch_bounds__(kNT, 1)
         const int g = (warp - 4) >> 2, r = threadIdx.x & 127;
         const uint32_t row_lane = (uint32_t)(warp & 3) << 21;   // (lane of tensor memory in bits 16 and up)
         const uint32_t mS = tS[g] + row_lane;
+        const int row_node = r / a.G, row_head = r - row_node * a.G;   // within a tile and a key head's group
         unsigned segs = 0, merges = 0, own = 0;   // (own: jobs of this stream so far)
         bool ok = true;
-        while (ok && next_segment()) {
+        for (bool more = next_segment(); ok && more;) {
             const int first = s.t0, step = s.act == 2, tails = s.L / kTile, jobs = (s.t1 - first) << step;
             // what this row sees of the nodes
-            const int tile0 = 2 * s.pair + (s.act == 2 ? g : 0), node = tile0 * a.nodes + r / a.G;
-            const bool real = r < a.nodes * a.G && node < s.count;
+            const int tile0 = 2 * s.pair + (s.act == 2 ? g : 0), node = tile0 * a.nodes + row_node;
+            const bool real = row_node < a.nodes && node < s.count;
             uint32_t v0 = 0, v1 = 0, v2 = 0, v3 = 0;
             if (real && s.t1 > tails) {
                 for (int j = node; j >= 0; j = parent_of(a, s.b, j)) {
@@ -677,6 +678,14 @@ __global__ void __launch_bounds__(kNT, 1)
             // ---- the segment's output ---------------------------------------------------------
             const bool two = s.act == 2, both = !two && jobs > 1;
             const bool mine = both || two || g == 0;   // (a stream may have had no job)
+            // while the last products run: where the output goes, and the next segment
+            const bool whole = s.t0 == 0 && s.t1 == s.tiles, ends = s.t1 == s.tiles;
+            const long long row = ((long long)s.b * a.N + node) * a.Hq + s.h * a.G + row_head;
+            const long long slot = ((long long)me * 2 + (s.t0 == 0 ? 1 : 0)) * 2 + (two ? g : 0);
+            const int b = s.b, h = s.h, L = s.L;
+            __syncwarp();
+            more = false;
+            if (lane == 0) more = s.next(a);
             if (mine && !(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
             if (!two) {
                 if (mine) sh.ml[g][r] = make_float2(m, l);
@@ -695,12 +704,11 @@ __global__ void __launch_bounds__(kNT, 1)
                 w1 = both ? ex2(m1.x - ref) : 0.f;   // (ml[1] is not written for a stream without jobs)
                 l = m0.y * w0 + (both ? m1.y * w1 : 0.f);
             }
-            const bool whole = s.t0 == 0 && s.t1 == s.tiles;
             const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
             w0 *= inv;
             w1 *= inv;
             uint32_t bad[4] = {0, 0, 0, 0};
-            if (s.t1 == s.tiles) {
+            if (ends) {
                 const uint32_t *f = sh.bad[segs % kSegRing];
                 bad[0] = f[0] & v0;
                 bad[1] = f[1] & v1;
@@ -709,9 +717,6 @@ __global__ void __launch_bounds__(kNT, 1)
             }
             const bool spoilt = (bad[0] | bad[1] | bad[2] | bad[3]) != 0;
             const int c0 = two ? 0 : g * (DP / 64), c1 = two ? DP / 32 : c0 + DP / 64;
-            const int hq = s.h * a.G + r % a.G;
-            const long long row = ((long long)s.b * a.N + node) * a.Hq + hq;
-            const long long slot = ((long long)me * 2 + (s.t0 == 0 ? 1 : 0)) * 2 + (two ? g : 0);
 #pragma unroll 1
             for (int c = idle ? c1 : c0; c < c1; ++c) {
                 float o[32];
@@ -735,10 +740,10 @@ __global__ void __launch_bounds__(kNT, 1)
                     for (int j = 0; j < a.N; ++j) {
                         const uint32_t bits = j < 32 ? bad[0] : j < 64 ? bad[1] : j < 96 ? bad[2] : bad[3];
                         if (!(bits >> (j & 31) & 1)) continue;
-                        const int key = s.L + j, p = a.table[(long long)s.b * a.M + key / a.page];
+                        const int key = L + j, p = a.table[(long long)b * a.M + key / a.page];
                         if (p < 0 || p >= a.P) continue;
                         const unsigned short *v = static_cast<const unsigned short *>(a.v) + p * a.vs[0] + key % a.page * a.vs[1] +
-                                                  s.h * a.vs[2] + c * 32;
+                                                  h * a.vs[2] + c * 32;
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (c * 32 + i < a.D && (v[i] & Half<T>::kExp) == Half<T>::kExp) o[i] += Half<T>::value(v[i]);
@@ -764,6 +769,7 @@ __global__ void __launch_bounds__(kNT, 1)
             tc::fence_before();
             __syncwarp();
             if (lane == 0) tc::bar_arrive(tc::smem(&bars.o_free));
+            more = __shfl_sync(kFull, more, 0);
             ++segs;
         }
     }
