@@ -479,8 +479,10 @@ __global__ void __launch_bounds__(kNT, 1)
             if (lane == 0) a.joins[me] = join;
         } else if (warp == kWarpMma0 || warp == kWarpMma1) {
             // ---- products, a warp per stream -------------------------------------------------------
-            // (With one warp the tensor cores paused while it prepared the other stream's job.) They take
-            // turns, so that one stream's products run while the other exponentiates. The
+            // (With one warp the tensor cores paused while it prepared the other stream's job.) Two tiles' streams take
+            // turns, so that one's products run while the other exponentiates (8 x 64 nodes of 32k: 302 us,
+            // without 313); streams of one tile are faster without (32 x 1 with heads of 64: 25.4 us, with
+            // turns 26.8; 44 x 3 with heads of 40: 45.0 and 47.7). The
             // whole warp walks along, so that operands stay in uniform registers; one thread issues.
             const bool lead = tc::elect();
             const int g = warp == kWarpMma1;
@@ -490,13 +492,13 @@ __global__ void __launch_bounds__(kNT, 1)
                 const unsigned i = turns++;
                 return g ? wait_warp(&bars.turn[1], i & 1) : i == 0 || wait_warp(&bars.turn[0], (i + 1) & 1);
             };
-            auto pass_on = [&]() {
+            auto pass_on = [&]() {   // (both have as many jobs)
                 if (lead) tc::bar_arrive(tc::smem(&bars.turn[g ^ 1]));
                 __syncwarp();
             };
             bool ok = true;
             while (ok && next_segment()) {
-                const int two = s.act == 2, nt = s.t1 - s.t0, step = two ? 1 : 2;
+                const int two = !FEW && s.act == 2, nt = s.t1 - s.t0, step = two ? 1 : 2;
                 const int end_steps = (s.keys(s.t1 - 1) + 15) / 16;   // products of the last tile
                 const int slot = twin ? segs & 1 : 0;
                 const uint32_t q = tc::uniform(tc::operand_lo(base + (two ? g : slot) * DC * SM::kQChunk, 16));
@@ -527,7 +529,7 @@ __global__ void __launch_bounds__(kNT, 1)
                     const unsigned st = (n0 + t) % SV;
                     const uint32_t v = tc::uniform(tc::operand_lo(vring + st * SM::kStage, kChunk));
                     const int steps = t == nt - 1 ? end_steps : kTile / 16;
-                    if (!(ok = wait_warp(&bars.p_ready[g], done & 1)) || !(ok = my_turn())) break;
+                    if (!(ok = wait_warp(&bars.p_ready[g], done & 1)) || (two && !(ok = my_turn()))) break;
                     tc::fence_after();
                     if (lead) {
                         if (steps == kTile / 16) {
@@ -546,11 +548,7 @@ __global__ void __launch_bounds__(kNT, 1)
                         scores(t + step);
                         if (lead && t + 2 * step >= nt) tc::commit(tc::smem(&bars.q_empty[slot]));
                     }
-                    pass_on();
-                }
-                if (ok && g && !two && (nt & 1)) {   // (stream 0 has one job more)
-                    if (!(ok = my_turn())) break;
-                    pass_on();
+                    if (two) pass_on();
                 }
                 n0 += nt;
                 ++segs;
