@@ -913,12 +913,6 @@ static bool encode(CUtensorMap *map, int bf16, const void *base, int D, const in
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-static int sm_count() {
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
-    return n;
-}
-
 constexpr int kMaxCtas = 152;   // one per SM; the workspace's room
 
 static size_t part_floats(int D) { return (size_t)kMaxCtas * 4 * kTile * (D > 64 ? 128 : 64); }
@@ -930,22 +924,24 @@ template <typename T, int DC, bool FEW>
 static cudaError_t launch_attend(const AttendArgs &a, const CUtensorMap *maps, int box, cudaStream_t st) {
     constexpr size_t smem = AttendSmem<DC, FEW>::kTiles + sizeof(typename AttendSmem<DC, FEW>::Shared);
     static_assert(smem <= 227 * 1024, "shared memory");
+    // once for each device: the shared memory allowed, and the number of SMs
     static std::mutex mu;
-    static bool done[64];
-    int dev = 0;
+    static int sms[64];
+    int dev = 0, ctas = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     {
         std::lock_guard<std::mutex> lk(mu);
-        if (!done[dev & 63]) {
-            e = cudaFuncSetAttribute(attend_kernel<T, DC, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (sms[dev & 63] == 0) {
+            int n = 0;
+            e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(attend_kernel<T, DC, FEW>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
             if (e != cudaSuccess) return e;
-            done[dev & 63] = true;
+            sms[dev & 63] = n < kMaxCtas ? n : kMaxCtas;
         }
+        ctas = sms[dev & 63];
     }
-    int ctas = sm_count();
-    if (ctas < 1) return cudaErrorUnknown;
-    if (ctas > kMaxCtas) ctas = kMaxCtas;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

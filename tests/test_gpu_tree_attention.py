@@ -274,6 +274,20 @@ def test_ragged_batches(N, Hq, Hkv, B, most):
     _check(c, {x: y[keep] for x, y in got.items()}, 0.125)
 
 
+def test_shared_and_repeated_pages():
+    """Sequences over one prompt, a page twice in a row, keys and values in one tensor."""
+    sv = _sv()
+    c = _case(25, BF16, 6, 8, 2, 64, 16, [150, 160, 90], poison=False)
+    t = c["table"]
+    t[1, :9], t[2, :5] = t[0, :9], t[0, :5]          # full pages of the first sequence
+    t[2, 3] = t[2, 1]
+    _check(c, _run(sv, c), 0.125)
+    same = {**c, "v": c["k"]}
+    k = c["k"].to(DEV)
+    got = sv.tree_attention(c["q"].to(DEV), k, k, t.to(DEV), _i32(c["lengths"]), _i32(c["parents"]))
+    _check(same, got, 0.125)
+
+
 def test_one_large_page():
     sv = _sv()
     c = _case(21, BF16, 5, 8, 2, 64, 1 << 20, [3000, 129], poison=False, spare=0)
