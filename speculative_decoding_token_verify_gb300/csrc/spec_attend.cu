@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kNT, 1)
             const bool two = s.act == 2, both = !two && jobs > 1;
             const bool mine = both || two || g == 0;   // (a stream may have had no job)
             // while the last products run: where the output goes, and the next segment
-            const bool whole = s.t0 == 0 && s.t1 == s.tiles, ends = s.t1 == s.tiles;
+            const bool whole = s.t0 == 0 && s.t1 == s.tiles, holds_nodes = s.t1 > tails;
             const long long row = ((long long)s.b * a.N + node) * a.Hq + s.h * a.G + row_head;
             const long long slot = ((long long)me * 2 + (s.t0 == 0 ? 1 : 0)) * 2 + (two ? g : 0);
             const int b = s.b, h = s.h, L = s.L;
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kNT, 1)
             w0 *= inv;
             w1 *= inv;
             uint32_t bad[4] = {0, 0, 0, 0};
-            if (ends) {
+            if (holds_nodes) {   // (a node's value is in one piece, and its flag in that piece's alone)
                 const uint32_t *f = sh.bad[segs % kSegRing];
                 bad[0] = f[0] & v0;
                 bad[1] = f[1] & v1;
@@ -781,6 +781,10 @@ __global__ void __launch_bounds__(kNT, 1)
 // first, then their outputs.
 constexpr int kJoinRows = 8;
 
+// the weight of x: an infinity stays one (a weight below fp32's range is not 0, and a sequence
+// that is not cut keeps its nodes' infinities, too)
+__device__ __forceinline__ float weight_of(float x, float w) { return fabsf(x) == INFINITY ? 1.f : w; }
+
 template <typename T, int DC>
 __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_constant__ AttendArgs a) {
     constexpr int DP = DC * 64;
@@ -813,19 +817,19 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
         const float ref = to == neg_inf() ? 0.f : to, keep = ex2(m - ref);
         m = to;
         l *= keep;
-        o.x *= keep;
-        o.y *= keep;
-        o.z *= keep;
-        o.w *= keep;
+        o.x *= weight_of(o.x, keep);
+        o.y *= weight_of(o.y, keep);
+        o.z *= weight_of(o.z, keep);
+        o.w *= weight_of(o.w, keep);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (i0 + i < pieces) {
                 const float w = ex2(ml[i].x - ref);
                 l = fmaf(ml[i].y, w, l);
-                o.x = fmaf(v[i].x, w, o.x);
-                o.y = fmaf(v[i].y, w, o.y);
-                o.z = fmaf(v[i].z, w, o.z);
-                o.w = fmaf(v[i].w, w, o.w);
+                o.x = fmaf(v[i].x, weight_of(v[i].x, w), o.x);
+                o.y = fmaf(v[i].y, weight_of(v[i].y, w), o.y);
+                o.z = fmaf(v[i].z, weight_of(v[i].z, w), o.z);
+                o.w = fmaf(v[i].w, weight_of(v[i].w, w), o.w);
             }
         }
     }
