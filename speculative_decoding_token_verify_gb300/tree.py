@@ -204,8 +204,9 @@ def _params(outer, seg, pages, page_stride, slots, unit, es):
     return _native.CacheParams(outer[0], pages, seg[0], slots, unit * es, _I3(outer[1] * es, page_stride * es, seg[1] * es))
 
 
-def _caches(cache, page_dim, slot_dim, P=None):
-    """[(tensor, layout)] of one cache or several that share a table."""
+def _caches(cache, page_dim, slot_dim, P=None, ahead=False):
+    """[(tensor, layout)] of one cache or several that share a table. ``ahead``: something
+    else is written before the first of them."""
     tensors = [cache] if isinstance(cache, torch.Tensor) else list(cache)
     if not tensors:
         raise ValueError("no cache given")
@@ -218,7 +219,8 @@ def _caches(cache, page_dim, slot_dim, P=None):
     if len(found) > 1:
         if len({t.data_ptr() for t, p in found if p.O}) < sum(p.O > 0 for _, p in found):
             raise ValueError("the caches must not overlap")
-        for _, p in found:   # all are looked at before any is written
+    if ahead or len(found) > 1:
+        for _, p in found:   # all are looked at before anything is written
             _check(_native.lib().spec_pages_copy(ctypes.byref(p), None, None, 0, None))
     return found, dev, P, page
 
@@ -305,7 +307,7 @@ def pages_fork(cache: Cache, table: torch.Tensor, refs: torch.Tensor, lengths: t
     hold tensors for them, of which only ``refs`` may be the given one."""
     if refs.dim() != 1 or table.dim() != 3 or parent.dim() != 2:
         raise ValueError("table must be [B, W, M], refs [P] and parent [B, N]")
-    found, dev, P, page = _caches(cache, page_dim, slot_dim, refs.shape[0])
+    found, dev, P, page = _caches(cache, page_dim, slot_dim, refs.shape[0], ahead=True)
     (B, W, M), N = table.shape, parent.shape[1]
     _need(table, "table", (B, W, M), dev)
     _need(refs, "refs", (P,), dev)

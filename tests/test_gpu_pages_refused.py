@@ -1,0 +1,45 @@
+"""Calls on caches that are refused leave everything as it was."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def _sv():
+    import speculative_decoding_token_verify_gb300 as sv
+    sv.build()
+    return sv
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device=DEV)
+
+
+@pytest.mark.parametrize("several", [False, True])
+@pytest.mark.parametrize("kind", ["pages over one another", "outer entries over one another", "outer axis too long"])
+def test_fork_refused_before_it_writes(kind, several):
+    """One cache or two whose pages the copy cannot move: tables, counts and lengths stay."""
+    sv = _sv()
+    if kind == "pages over one another":
+        cache, pd = torch.zeros((1, 16, 4), device=DEV).expand(6, 16, 4), 0
+    elif kind == "outer entries over one another":
+        cache, pd = torch.zeros((1, 6, 16, 4), device=DEV).expand(3, 6, 16, 4), 1
+    else:
+        cache, pd = torch.zeros((65536, 6, 16, 1), dtype=torch.uint8, device=DEV), 1
+    table, refs, lengths, parent = _i32([[[0, 1], [2, 3]]]), _i32([1, 1, 1, 1, 0, 0]), _i32([[20, 20]]), _i32([[1, 1]])
+    out = {"table": torch.full((1, 2, 2), 77, dtype=torch.int32, device=DEV), "refs": refs,
+           "lengths": torch.full((1, 2), 77, dtype=torch.int32, device=DEV)}
+    versions = [t._version for t in out.values()]
+    caches = [torch.zeros_like(cache, memory_format=torch.contiguous_format), cache] if several else cache
+    if several and kind == "outer axis too long":
+        caches[0] = torch.zeros((6, 6, 16, 1), dtype=torch.uint8, device=DEV)
+    with pytest.raises(sv.SpecError):
+        sv.pages_fork(caches, table, refs, lengths, parent, page_dim=pd, out=out)
+    assert refs.tolist() == [1, 1, 1, 1, 0, 0] and (out["table"] == 77).all() and (out["lengths"] == 77).all()
+    assert [t._version for t in out.values()] == versions
+    # the same call on a cache that it takes
+    good = torch.zeros((6, 16, 4), device=DEV)
+    r = sv.pages_fork(good, table, refs, lengths, parent, out=out)
+    assert r["refs"] is refs and int(refs.sum()) == 4 and r["lengths"].tolist() == [[20, 20]]
