@@ -602,7 +602,8 @@ int spec_beam_reorder(const spec_reorder_params *params, const void *src, void *
  * sequence needs is outside [0, P), SPEC_ERR_BAD_PAGE is raised and that
  * sequence's outputs are unspecified.
  * Precision: scores and sums in fp32; the probabilities are rounded to the
- * inputs' type before they multiply the values (relative error 2^-9 each in bf16).
+ * inputs' type before they multiply the values (relative error 2^-8 each in bf16,
+ * 2^-11 in fp16, and there no less than 2^-32 of the row's largest).
  * q, k and v: strides in elements, multiples of 8 and > 0 (where the axis has more
  * than one entry), 16-byte aligned, D contiguous. out [B][N][Hq][D] in the inputs' type, lse
  * [B][N][Hq] f32 or NULL, contiguous; out must not overlap an input.

@@ -99,12 +99,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// Probabilities are rounded to the inputs' type before they multiply the values, which is what the
+// tensor cores take (in fp32 they would have to be split in two, and the product done twice); the sum
+// takes them unrounded. A row's reference lies kUp below its maximum (in log2): in fp16 what is
+// smaller than 2^-14 loses bits and below 2^-25 everything, so that a long context behind one large
+// score would vanish (32767 keys 17 nats below it: their part of the output 44% off, at 18 nats gone; with
+// 2^7 times the probabilities 0.1% and 0.9% off). bf16 has fp32's exponents.
 template <typename T>
 struct Half;
 template <>
 struct Half<__nv_bfloat16> {
     static constexpr int kBf16 = 1;
     static constexpr uint32_t kExp = 0x7f80;
+    static constexpr float kUp = 0.f;
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -116,6 +123,7 @@ template <>
 struct Half<__half> {
     static constexpr int kBf16 = 0;
     static constexpr uint32_t kExp = 0x7c00;
+    static constexpr float kUp = 7.f;   // (with kLazy: probabilities reach 2^15, and fp16 65504)
     __device__ static __forceinline__ uint32_t pack(float lo, float hi) {
         uint32_t r;
         asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -627,7 +635,7 @@ __global__ void __launch_bounds__(kNT, 1)
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) mx[c] = max3(mx[c], x[c][i], x[c][i + 1]);
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.sL;
+                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.sL, -Half<T>::kUp);
                 const bool move = real && top > m + kLazy;   // (rows that nobody uses may hold anything)
                 if (__any_sync(kFull, move)) {
                     const float to = move ? top : m, keep = move ? ex2(m - to) : 1.f;
