@@ -596,7 +596,7 @@ int spec_beam_reorder(const spec_reorder_params *params, const void *src, void *
  * (parents[n] = n - 1); N = 1: an ordinary decoding step.
  * Keys and values that a row does not see do not reach it, NaN and infinities
  * among them (slots never written, other branches). What it sees may make it NaN,
- * and so do scores beyond fp32's range.
+ * and so do scores and products q . k beyond 2^127.
  * parents outside [-1, n) count as -1 (SPEC_ERR_BAD_PARENT). counts are clamped to
  * [0, N], lengths to [0, M page - counts[b]] (SPEC_ERR_BAD_LENGTH). Where a page that a
  * sequence needs is outside [0, P), SPEC_ERR_BAD_PAGE is raised and that

@@ -46,6 +46,7 @@ constexpr int kWarpK = 0, kWarpV = 3, kWarpGo = 2, kWarpMma0 = 1, kWarpMma1 = 14
 constexpr unsigned kDrain = 1u << 20;  // polls for what is in flight at the end
 constexpr int kSegRing = 4;            // segments whose flags of non-finite values are kept
 constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
+constexpr float kFarRef = 4096.f;         // (log2) references from which their rounding counts
 
 struct AttendArgs {
     const void *v;
@@ -54,11 +55,12 @@ struct AttendArgs {
     float *lse;
     int32_t *status;
     float4 *part_o;   // [CTA][2][tile][D padded / 4][row]: unnormalised outputs of a sequence's pieces
-    float2 *part_ml;  // [CTA][2][tile][row]: their reference (log2) and sum
+    float2 *part_ml;  // [CTA][2][tile][row]: their reference score and sum
     int4 *joins;      // [CTA], what begins here and ends elsewhere: sequence (-1: none), head + pair of tiles 2^16, rows, last CTA
     int B, N, Hq, Hkv, G, D, P, page, M, fill;
     int nodes, q_rows;   // a tile, and the rows that a copy of queries brings
     float sL;         // |scale| log2 e
+    float lazy;       // kLazy as a difference of scores
     unsigned spin;    // polls of a wait before it gives up
     int neg;          // scale < 0
     long long vs[3], ps;
@@ -131,6 +133,34 @@ struct Half<__half> {
     }
     __device__ static __forceinline__ float value(uint32_t h) { return __half2float(__ushort_as_half((unsigned short)h)); }
 };
+
+// A row's sums stand against a reference score mr that its maximum once was. In log2 that is m = mr sL - kUp,
+// rounded, and where all use the same m its rounding cancels. But it is half a step of m, which
+// beside scores of 2^30 is more than a probability's range: from kFarRef on probabilities and weights are
+// taken from differences of scores. Such tiles are read a second time (8 x 64 nodes of 32k 364 us
+// in place of 297, 64 x 9 231 and 229 in eager calls); all others take the same time.
+template <typename T>
+__device__ __forceinline__ float log2_of(const AttendArgs &a, float mr) {   // (rounded here, whatever it is added to)
+    return Half<T>::kUp == 0.f ? __fmul_rn(mr, a.sL) : __fmaf_rn(mr, a.sL, -Half<T>::kUp);
+}
+struct Reference {
+    float base, minus;   // a score's exponent is (score - base) sL + minus
+    bool far;
+};
+template <typename T>
+__device__ __forceinline__ Reference reference(const AttendArgs &a, float mr) {
+    const float at = mr == neg_inf() ? 0.f : mr, m = log2_of<T>(a, at);   // (-inf: nothing seen)
+    Reference r;
+    r.far = fabsf(m) > kFarRef && at < INFINITY;
+    r.base = r.far ? at : 0.f;
+    r.minus = r.far ? Half<T>::kUp : -m;
+    return r;
+}
+// the weight of sums against `from` among those against r, which is no smaller
+template <typename T>
+__device__ __forceinline__ float weight(const AttendArgs &a, float from, const Reference &r) {
+    return ex2(__fadd_rn(log2_of<T>(a, from - r.base), r.minus));
+}
 
 // pairs of row tiles that `count` nodes fill
 __device__ __forceinline__ int pairs_of(const AttendArgs &a, int count) {
@@ -596,7 +626,9 @@ __global__ void __launch_bounds__(kNT, 1)
                 }
             }
             const bool idle = !__any_sync(kFull, real);   // a warp without rows: what it leaves in P stays in its rows
-            float m = neg_inf(), l = 0.f;
+            // lim: a maximum that is not at or below it is looked at (NaN: each, the reference is far;
+            // infinity: none, rows that nobody uses may hold anything). minus: what is added to x sL
+            float mr = neg_inf(), l = 0.f, lim = real ? neg_inf() : INFINITY, minus = 0.f;
             for (int j = g; j < jobs; j += 2) {
                 if (!(ok = wait_warp(&bars.s_full[g], own & 1))) break;
                 if (idle) {
@@ -605,43 +637,61 @@ __global__ void __launch_bounds__(kNT, 1)
                     continue;
                 }
                 tc::fence_after();
+                const int t = first + (step ? j >> 1 : j);
                 float x[4][32];
+                // once, and where a reference is far once more, less the reference
+                float base = -0.f;
+                for (int again = 0;; again = 1) {
+                    asm volatile("" : "+r"(again));   // (one copy of this code)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tc::tmem_load(mS + c * 32, x[c]);
-                tc::tmem_wait_load();
+                    for (int c = 0; c < 4; ++c) tc::tmem_load(mS + c * 32, x[c]);
+                    tc::tmem_wait_load();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) tc::loaded(x[c]);
-                if (a.neg)
+                    for (int c = 0; c < 4; ++c) tc::loaded(x[c]);
+                    if (a.neg | again) {
+                        const float sign = a.neg ? -1.f : 1.f;
+                        const float2 sign2 = make_float2(sign, sign), base2 = make_float2(base, base);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+#pragma unroll
+                            for (int i = 0; i < 32; i += 2) {
+                                const float2 d = __ffma2_rn(make_float2(x[c][i], x[c][i + 1]), sign2, base2);
+                                x[c][i] = d.x;
+                                x[c][i + 1] = d.y;
+                            }
+                    }
+                    if (t >= tails) {
+                        const int d = t * kTile - s.L;   // node of the tile's first key
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            const int at = d + 32 * c, w = at >> 5;
+                            auto word = [&](int k) -> uint32_t {
+                                return k < 0 ? ~0u : k == 0 ? v0 : k == 1 ? v1 : k == 2 ? v2 : k == 3 ? v3 : 0u;
+                            };
+                            const uint32_t see = __funnelshift_r(word(w), word(w + 1), at & 31);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) x[c][i] = see >> i & 1 ? x[c][i] : neg_inf();
+                        }
+                    }
+                    if (again) break;
+                    float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
                     for (int c = 0; c < 4; ++c)
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[c][i] = -x[c][i];
-                const int t = first + (step ? j >> 1 : j);
-                if (t >= tails) {
-                    const int d = t * kTile - s.L;   // node of the tile's first key
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int at = d + 32 * c, w = at >> 5;
-                        auto word = [&](int k) -> uint32_t {
-                            return k < 0 ? ~0u : k == 0 ? v0 : k == 1 ? v1 : k == 2 ? v2 : k == 3 ? v3 : 0u;
-                        };
-                        const uint32_t see = __funnelshift_r(word(w), word(w + 1), at & 31);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) x[c][i] = see >> i & 1 ? x[c][i] : neg_inf();
+                        for (int i = 0; i < 32; i += 2) mx[c] = max3(mx[c], x[c][i], x[c][i + 1]);
+                    const float high = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    const bool look = !(high <= lim);
+                    if (!__any_sync(kFull, look)) break;
+                    const bool move = look && high > mr;
+                    const Reference to = reference<T>(a, move ? high : mr);
+                    const float keep = move ? weight<T>(a, mr, to) : 1.f;
+                    if (move) {
+                        mr = high;
+                        lim = to.far ? NAN : mr + a.lazy;
                     }
-                }
-                float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) mx[c] = max3(mx[c], x[c][i], x[c][i + 1]);
-                const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), a.sL, -Half<T>::kUp);
-                const bool move = real && top > m + kLazy;   // (rows that nobody uses may hold anything)
-                if (__any_sync(kFull, move)) {
-                    const float to = move ? top : m, keep = move ? ex2(m - to) : 1.f;
-                    m = to;
                     l *= keep;
-                    if (j >= 2) {   // the output so far
+                    minus = to.minus;
+                    if (j >= 2 && __any_sync(kFull, move)) {   // the output so far
                         if (!(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
                         tc::fence_after();
 #pragma unroll 1
@@ -656,16 +706,19 @@ __global__ void __launch_bounds__(kNT, 1)
                         }
                         tc::tmem_wait_store();
                     }
+                    if (!__any_sync(kFull, to.far)) break;
+                    base = mr == neg_inf() ? -0.f : -mr;   // (all of the warp's rows, then)
+                    minus = Half<T>::kUp;
                 }
-                const float ref = m == neg_inf() ? 0.f : m;
-                const float2 scale = make_float2(a.sL, a.sL), minus = make_float2(-ref, -ref);
+                if (!ok) break;
+                const float2 scale = make_float2(a.sL, a.sL), minus2 = make_float2(minus, minus);
                 float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     uint32_t p[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
-                        float2 e = __ffma2_rn(make_float2(x[c][i], x[c][i + 1]), scale, minus);
+                        float2 e = __ffma2_rn(make_float2(x[c][i], x[c][i + 1]), scale, minus2);
                         e.x = ex2(e.x);
                         e.y = ex2(e.y);
                         sum[c & 1] = __fadd2_rn(sum[c & 1], e);
@@ -694,7 +747,7 @@ __global__ void __launch_bounds__(kNT, 1)
             if (lane == 0) more = s.next(a);
             if (mine && !(ok = wait_warp(&bars.pv_done[g], (own + 1) & 1))) break;
             if (!two) {
-                if (mine) sh.ml[g][r] = make_float2(m, l);
+                if (mine) sh.ml[g][r] = make_float2(mr, l);
                 __syncwarp();
                 if (lane == 0) tc::bar_arrive(tc::smem(&bars.merge));
                 if (!(ok = wait_warp(&bars.merge, merges++ & 1))) break;
@@ -704,10 +757,10 @@ __global__ void __launch_bounds__(kNT, 1)
             float w0 = 1.f, w1 = 0.f;
             if (!two) {
                 const float2 m0 = sh.ml[0][r], m1 = sh.ml[1][r];
-                m = both ? fmaxf(m0.x, m1.x) : m0.x;
-                const float ref = m == neg_inf() ? 0.f : m;
-                w0 = ex2(m0.x - ref);
-                w1 = both ? ex2(m1.x - ref) : 0.f;   // (ml[1] is not written for a stream without jobs)
+                mr = both ? fmaxf(m0.x, m1.x) : m0.x;
+                const Reference to = reference<T>(a, mr);
+                w0 = weight<T>(a, m0.x, to);
+                w1 = both ? weight<T>(a, m1.x, to) : 0.f;   // (ml[1] is not written for a stream without jobs)
                 l = m0.y * w0 + (both ? m1.y * w1 : 0.f);
             }
             const float inv = whole ? (l != 0.f ? 1.f / l : 0.f) : 1.f;
@@ -769,8 +822,8 @@ __global__ void __launch_bounds__(kNT, 1)
                 }
             }
             if (real && (two || g == 0)) {
-                if (!whole) a.part_ml[slot * kTile + r] = make_float2(m, l);
-                else if (a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (m + log2f(l)) : neg_inf();
+                if (!whole) a.part_ml[slot * kTile + r] = make_float2(mr, l);
+                else if (a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (log2_of<T>(a, mr) + log2f(l)) : neg_inf();
             }
             tc::fence_before();
             __syncwarp();
@@ -789,9 +842,9 @@ __global__ void __launch_bounds__(kNT, 1)
 // first, then their outputs.
 constexpr int kJoinRows = 8;
 
-// the weight of x: an infinity stays one (a weight below fp32's range is not 0, and a sequence
-// that is not cut keeps its nodes' infinities, too)
-__device__ __forceinline__ float weight_of(float x, float w) { return fabsf(x) == INFINITY ? 1.f : w; }
+// A piece's part of a sum that came out NaN: an infinity stays one (a weight below fp32's
+// range is not 0, and a sequence that is not cut keeps its nodes' infinities, too)
+__device__ __forceinline__ float part(float x, float w) { return fabsf(x) == INFINITY ? x : x * w; }
 
 template <typename T, int DC>
 __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_constant__ AttendArgs a) {
@@ -805,7 +858,7 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
     if (m_tile > 1 || rr >= join.z) return;
     const int first = blockIdx.x, pieces = join.w - first + 1;
     auto slot = [&](int i) { return ((long long)(first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + m_tile; };
-    float m = neg_inf(), l = 0.f;
+    float mr = neg_inf(), l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 16;   // pieces whose loads are in flight together
     for (int i0 = 0; i0 < pieces; i0 += U) {
@@ -818,35 +871,53 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
                 v[i] = a.part_o[(slot(i0 + i) * (DP / 4) + c4) * kTile + r];
             }
         }
-        float to = m;
+        float to = mr;
 #pragma unroll
         for (int i = 0; i < U; ++i)
             if (i0 + i < pieces) to = fmaxf(to, ml[i].x);
-        const float ref = to == neg_inf() ? 0.f : to, keep = ex2(m - ref);
-        m = to;
+        const Reference ref = reference<T>(a, to);
+        const float keep = weight<T>(a, mr, ref);
+        mr = to;
         l *= keep;
-        o.x *= weight_of(o.x, keep);
-        o.y *= weight_of(o.y, keep);
-        o.z *= weight_of(o.z, keep);
-        o.w *= weight_of(o.w, keep);
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (i0 + i < pieces) {
-                const float w = ex2(ml[i].x - ref);
+                const float w = weight<T>(a, ml[i].x, ref);
                 l = fmaf(ml[i].y, w, l);
-                o.x = fmaf(v[i].x, weight_of(v[i].x, w), o.x);
-                o.y = fmaf(v[i].y, weight_of(v[i].y, w), o.y);
-                o.z = fmaf(v[i].z, weight_of(v[i].z, w), o.z);
-                o.w = fmaf(v[i].w, weight_of(v[i].w, w), o.w);
+                o.x = fmaf(v[i].x, w, o.x);
+                o.y = fmaf(v[i].y, w, o.y);
+                o.z = fmaf(v[i].z, w, o.z);
+                o.w = fmaf(v[i].w, w, o.w);
             }
         }
+    }
+    if (isnan((o.x + o.y) + (o.z + o.w))) {
+        const Reference ref = reference<T>(a, mr);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+        for (int i = 0; i < pieces; ++i) {
+            const float w = weight<T>(a, a.part_ml[slot(i) * kTile + r].x, ref);
+            const float4 v = a.part_o[(slot(i) * (DP / 4) + c4) * kTile + r];
+            sum.x += part(v.x, w);
+            sum.y += part(v.y, w);
+            sum.z += part(v.z, w);
+            sum.w += part(v.w, w);
+        }
+        if (isnan(o.x)) o.x = sum.x;
+        if (isnan(o.y)) o.y = sum.y;
+        if (isnan(o.z)) o.z = sum.z;
+        if (isnan(o.w)) o.w = sum.w;
     }
     const float inv = l != 0.f ? 1.f / l : 0.f;
     const long long row = ((long long)join.x * a.N + node) * a.Hq + h * a.G + r % a.G;
     if (c4 * 4 < a.D)
         *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * a.D + c4 * 4) =
             make_uint2(Half<T>::pack(o.x * inv, o.y * inv), Half<T>::pack(o.z * inv, o.w * inv));
-    if (c4 == 0 && a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (m + log2f(l)) : neg_inf();
+    if (c4 == 0 && a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (log2_of<T>(a, mr) + log2f(l)) : neg_inf();
 }
 
 static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
@@ -1046,6 +1117,7 @@ extern "C" int spec_tree_attention(const spec_attend_params *p, const void *q, c
     const int q_nodes = p->N < a.nodes ? p->N : a.nodes;
     a.q_rows = q_nodes * G;
     a.sL = fmaxf(fabsf(p->scale) * sv::kLog2e, FLT_MIN);   // (0 times a masked key's -inf would be NaN)
+    a.lazy = kLazy / a.sL;   // (infinite for scales next to 0: no score reaches it)
     a.neg = p->scale < 0.f;
     a.spin = spec_internal_wait_limit();
     a.ps = p->parents_stride;
