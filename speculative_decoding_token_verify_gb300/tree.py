@@ -204,6 +204,77 @@ def _params(outer, seg, pages, page_stride, slots, unit, es):
     return _native.CacheParams(outer[0], pages, seg[0], slots, unit * es, _I3(outer[1] * es, page_stride * es, seg[1] * es))
 
 
+_STEPS = 10000   # of a search for common bytes, before it is given up (caches with one layout take less than 100)
+
+
+def _layout(t, p):
+    """(first byte, extent, [(stride, entries)] from the widest on, bytes of a segment) of a cache."""
+    axes = [(s, n) for s, n in zip(p.stride, (p.O, p.P, p.H)) if n > 1]
+    axes.sort(reverse=True)
+    seg = p.page * p.unit_bytes
+    return t.data_ptr(), seg + sum(s * (n - 1) for s, n in axes), axes, seg
+
+
+def _meet(a, b):
+    """Whether two caches have a byte in common."""
+    steps = {}
+    for s, n in a[2]:
+        steps[s] = [1 - n, 0]
+    for s, n in b[2]:
+        lo, hi = steps.get(s, (0, 0))
+        steps[s] = [lo, hi + n - 1]
+    axes = sorted(steps.items(), reverse=True)
+    left = _STEPS
+
+    def search(k, off):   # off: b's segment less a's, with the axes from k on still free
+        nonlocal left
+        left -= 1
+        if left < 0:
+            return True   # (not shown to be apart)
+        if k == len(axes):
+            return -b[3] < off < a[3]
+        s, (lo, hi) = axes[k]
+        least = off + sum(x * r[0] for x, r in axes[k + 1:])
+        most = off + sum(x * r[1] for x, r in axes[k + 1:])
+        first, last = max(lo, -((b[3] - 1 + most) // s)), min(hi, (a[3] - 1 - least) // s)
+        return any(search(k + 1, off + d * s) for d in range(first, last + 1))
+
+    return search(0, b[0] - a[0])
+
+
+def _blocks(tensors):
+    """Whether they are contiguous and one behind the other, as a cache per layer mostly is."""
+    if not all(t.is_contiguous() for t in tensors):
+        return False
+    at = sorted((t.data_ptr(), t.nbytes) for t in tensors)
+    return all(p + n <= q for (p, n), (q, _) in zip(at, at[1:]))
+
+
+def _apart(layouts):
+    """Whether no two caches have a byte in common; views of one buffer may lie between one another."""
+    group, end = [], 0
+    for x in sorted(layouts, key=lambda x: x[0]) + [(math.inf,)]:
+        if x[0] < end:
+            group.append(x)
+            end = max(end, x[0] + x[1])
+            continue
+        if len(group) > 1 and not _between(group) and any(_meet(a, b) for i, a in enumerate(group) for b in group[:i]):
+            return False
+        if len(x) > 1:
+            group, end = [x], x[0] + x[1]
+    return True
+
+
+def _between(group):
+    """Whether one entry of the widest axis, which all have, holds the others' entries beside it."""
+    widest = {x[2][0][0] if x[2] else 0 for x in group}
+    s = widest.pop()
+    if widest or s == 0:
+        return False
+    at = sorted((x[0] % s, x[1] - s * (x[2][0][1] - 1)) for x in group)
+    return all(r + size <= nxt for (r, size), nxt in zip(at, [r for r, _ in at[1:]] + [at[0][0] + s]))
+
+
 def _caches(cache, page_dim, slot_dim, P=None, ahead=False):
     """[(tensor, layout)] of one cache or several that share a table. ``ahead``: something
     else is written before the first of them."""
@@ -216,12 +287,11 @@ def _caches(cache, page_dim, slot_dim, P=None, ahead=False):
             raise ValueError("the caches must be on one device")
         found.append((t, _cache_params(t, page_dim, slot_dim, P, page)))
         P, page = found[0][1].P, found[0][1].page
-    if len(found) > 1:
-        if len({t.data_ptr() for t, p in found if p.O}) < sum(p.O > 0 for _, p in found):
-            raise ValueError("the caches must not overlap")
     if ahead or len(found) > 1:
         for _, p in found:   # all are looked at before anything is written
             _check(_native.lib().spec_pages_copy(ctypes.byref(p), None, None, 0, None))
+    if len(found) > 1 and not _blocks(tensors) and not _apart([_layout(t, p) for t, p in found if p.O and p.P and p.H]):
+        raise ValueError("the caches must not overlap")
     return found, dev, P, page
 
 

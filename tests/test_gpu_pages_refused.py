@@ -43,3 +43,32 @@ def test_fork_refused_before_it_writes(kind, several):
     good = torch.zeros((6, 16, 4), device=DEV)
     r = sv.pages_fork(good, table, refs, lengths, parent, out=out)
     assert r["refs"] is refs and int(refs.sum()) == 4 and r["lengths"].tolist() == [[20, 20]]
+
+
+@pytest.mark.parametrize("call", ["compact", "fork"])
+def test_caches_over_one_another(call):
+    """Caches that share some layers, from different first bytes on, and views between one another."""
+    sv = _sv()
+    layers = torch.randn((4, 2, 6, 16, 2, 8), device=DEV)          # [layer, keys and values, page, slot, head, D]
+    kept = layers.clone()
+    table, refs, lengths = _i32([[[0, 1], [2, 3]]]), _i32([1, 1, 1, 1, 0, 0]), _i32([[20, 20]])
+
+    def run(caches, page_dim):
+        if call == "compact":
+            return sv.pages_compact(caches, table[0], lengths[0], _i32([[1, 3, -1, -1], [0, 2, 3, -1]]), page_dim=page_dim)
+        return sv.pages_fork(caches, table, refs, lengths, _i32([[1, 1]]), page_dim=page_dim)
+
+    for caches, pd in (([layers[0:2], layers[1:3]], 2), ([layers[:, 0], layers[2:, 0]], 1), ([layers, layers[3:]], 2)):
+        with pytest.raises(ValueError, match="overlap"):
+            run(caches, pd)
+        assert torch.equal(layers, kept)
+    one = layers.clone()
+    run(one, 2)
+    assert not torch.equal(one, layers)
+    for caches, pd in (([layers[:, 0], layers[:, 1]], 1), ([layers[3:], layers[:3]], 2), ([layers[i, j] for j in (1, 0) for i in range(4)], 0)):
+        layers.copy_(kept)
+        run(caches, pd)
+        assert torch.equal(layers, one)
+    mixed = kept.permute(2, 0, 1, 3, 4, 5).contiguous()             # pages first, the layers between one another
+    run([mixed[:, i, j] for i in range(4) for j in range(2)], 0)
+    assert torch.equal(mixed, one.permute(2, 0, 1, 3, 4, 5))
