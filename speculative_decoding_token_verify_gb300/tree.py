@@ -66,7 +66,7 @@ def _new(out, name, shape, device, dtype=_I32):
 
 
 def _small(what, *sizes):
-    if max(sizes) > _MOST:   # before the C ABI's 32-bit fields
+    if max(sizes) > _MOST or min(sizes) < -_MOST:   # before the C ABI's 32-bit fields
         raise SpecError(SPEC_ERR_UNSUPPORTED, f"{what}: a size is outside the supported range")
 
 
@@ -117,7 +117,7 @@ def tree_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: tor
     ps = _parents(parents, B, N, dev)
     _status(status, dev)
     _small("tree_attention", B, N, Hq, P, page, Hkv, D, M)
-    p = _native.AttendParams(B, N, Hq, Hkv, D, dt, P, page, M, D ** -0.5 if scale is None else scale, _I3(*qs[:3]),
+    p = _native.AttendParams(B, N, Hq, Hkv, D, dt, P, page, M, max(D, 1) ** -0.5 if scale is None else scale, _I3(*qs[:3]),
                              _I3(*ks[:3]), _I3(*vs[:3]), ps)
 
     def body(s):
