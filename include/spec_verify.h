@@ -661,8 +661,8 @@ typedef struct {
  * outer entries and segments, in place. path [B][N] int32, ends at its first -1;
  * it must ascend (path[i] >= i follows): an entry that does not, or is outside
  * [0, N), ends it and raises SPEC_ERR_BAD_PATH. out_lengths[b] = lengths[b] + entries kept;
- * out_lengths must not overlap lengths. A move whose page is missing is left out
- * (SPEC_ERR_BAD_PAGE); lengths outside [0, M page] move nothing and stay
+ * out_lengths must not overlap lengths. A move whose page is missing is left out, and
+ * counts all the same (SPEC_ERR_BAD_PAGE, also for kept nodes that stay in their place); lengths outside [0, M page] move nothing and stay
  * (SPEC_ERR_BAD_LENGTH). Rows must not share pages behind lengths. Several caches
  * with one table take one call each. N in [1, SPEC_MAX_NODES].
  */

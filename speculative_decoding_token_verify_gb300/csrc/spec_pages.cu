@@ -495,15 +495,15 @@ __global__ void __launch_bounds__(NTC) compact_kernel(CacheArgs a) {
         unsigned moves = 0;
         if (threadIdx.x < SPEC_MAX_NODES) {
             const int i = threadIdx.x, p = i < kept ? path[i] : i, from = L + p, to = L + i;
-            if (p != i) {
+            if (p != i || (lead && i < kept)) {   // (nodes that keep their place need a page, too)
                 const int mf = from / a.page, mt = to / a.page;
                 const int pf = mf < a.M ? a.table[(long long)b * a.M + mf] : -1;
                 const int pt = mt < a.M ? a.table[(long long)b * a.M + mt] : -1;
-                if (pf >= 0 && pf < a.P && pt >= 0 && pt < a.P) {
+                if (pf < 0 || pf >= a.P || pt < 0 || pt >= a.P) {
+                    if (lead) raise_status(a.status, SPEC_ERR_BAD_PAGE);
+                } else if (p != i) {
                     so = pf * a.ss[1] + (from - mf * a.page) * a.unit;
                     dof = pt * a.ss[1] + (to - mt * a.page) * a.unit;
-                } else if (lead) {
-                    raise_status(a.status, SPEC_ERR_BAD_PAGE);
                 }
             }
             moves = __ballot_sync(kFull, so >= 0);

@@ -72,3 +72,21 @@ def test_caches_over_one_another(call):
     mixed = kept.permute(2, 0, 1, 3, 4, 5).contiguous()             # pages first, the layers between one another
     run([mixed[:, i, j] for i in range(4) for j in range(2)], 0)
     assert torch.equal(mixed, one.permute(2, 0, 1, 3, 4, 5))
+
+
+@pytest.mark.parametrize("path,length,table,code", [
+    ([0, 1, 2, 3], 15, [0, -1], 10), ([0, 1, 2, 3], 15, [0, 9], 10), ([0, 1, 2, 3], 30, [0, 1], 10), ([0, 1, -1, -1], 30, [0, 1], 0),
+    ([0, 1, 3, -1], 13, [0, 1], 0), ([0, 1, 3, -1], 15, [0, -1], 10), ([0, -1, -1, -1], 15, [0, -1], 0), ([-1, -1, -1, -1], 32, [0, 1], 0),
+    ([0, -1, -1, -1], 32, [0, 1], 10), ([0, 1, 2, 3], 16, [-1, 1], 0)])
+def test_compact_without_a_page(path, length, table, code):
+    """Kept nodes without a page, moved or not: the status tells, the lengths count them."""
+    sv = _sv()
+    cache = torch.arange(48, device=DEV).to(torch.int32).view(3, 16, 1)
+    want, kept = cache.clone(), sum(p >= 0 for p in path)
+    for i in range(kept):
+        a, z = length + path[i], length + i
+        if a // 16 < 2 and 0 <= table[a // 16] < 3 and 0 <= table[z // 16] < 3:
+            want[table[z // 16], z % 16] = cache[table[a // 16], a % 16]
+    st = _i32([0])
+    r = sv.pages_compact(cache, _i32([table]), _i32([length]), _i32([path]), status=st)
+    assert int(st) == code and r.tolist() == [length + kept] and torch.equal(cache, want)
