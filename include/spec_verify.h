@@ -596,7 +596,8 @@ int spec_beam_reorder(const spec_reorder_params *params, const void *src, void *
  * (parents[n] = n - 1); N = 1: an ordinary decoding step.
  * Keys and values that a row does not see do not reach it, NaN and infinities
  * among them (slots never written, other branches). What it sees may make it NaN,
- * and so do scores and products q . k beyond 2^127.
+ * and so do scores and products q . k beyond 2^127; values beyond 2^119 over the number of
+ * keys may become infinite (the sum is divided at its end, its weights reach 2^8).
  * parents outside [-1, n) count as -1 (SPEC_ERR_BAD_PARENT). counts are clamped to
  * [0, N], lengths to [0, M page - counts[b]] (SPEC_ERR_BAD_LENGTH). Where a page that a
  * sequence needs is outside [0, P), SPEC_ERR_BAD_PAGE is raised and that

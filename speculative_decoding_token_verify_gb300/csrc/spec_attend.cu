@@ -920,11 +920,6 @@ __global__ void __launch_bounds__(DC * 16 * kJoinRows) join_kernel(const __grid_
     if (c4 == 0 && a.lse) a.lse[row] = l != 0.f ? sv::kLn2 * (log2_of<T>(a, mr) + log2f(l)) : neg_inf();
 }
 
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-
 static int check_attend(const spec_attend_params *p) {
     if (!p) return spec_internal_set_error(SPEC_ERR_INVALID_ARG, "params is NULL");
     if (p->B < 0 || p->N < 0 || p->M < 0 || p->P < 0)

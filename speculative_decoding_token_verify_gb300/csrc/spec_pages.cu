@@ -620,11 +620,6 @@ static int check_pages(const spec_pages_params *p, bool fork) {
     return SPEC_OK;
 }
 
-static bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
-    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
-    return na > 0 && nb > 0 && x < y + nb && y < x + na;
-}
-
 // Small tables are one CTA's work, whose barriers cost less; all others the largest cluster's. In a
 // graph, one CTA against 16: 8.6 and 10.6 us for rows of 16 x 64 entries, 14.7 and 12.6 for 64 x 128, 58 and
 // 16.7 for 256 x 512 (2, 4 and 8 CTAs lie between; 8 are as fast as 16 up to there, and 16 faster beyond).

@@ -432,10 +432,15 @@ cudaError_t launch_cluster(void (*kernel)(P...), unsigned grid, unsigned nt, uns
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// ---- host-side checks shared by the row operators --------------------------------
+// ---- host-side checks shared by the row and tree operators --------------------------------
 
 int check_rows(const spec_rows_params *p, int max_m, int max_k);
 int check_strided(const void *base, int64_t batch_stride, int64_t row_stride, int es, bool out, int B, int K, int V);
+// whether na bytes from a on and nb from b on have one in common
+inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const char *x = static_cast<const char *>(a), *y = static_cast<const char *>(b);
+    return na > 0 && nb > 0 && x < y + nb && y < x + na;
+}
 
 }  // namespace sr
 
