@@ -17,8 +17,8 @@
 //
 // Measured (in a graph; bf16, 8 key heads of 128): 64 sequences of up to 8192 tokens, 9 nodes
 // of 32 heads, 1.37 GB: 224 us, 6.1 TB/s, 0.90 of a copy's rate; one token for 256 sequences of up
-// to 4096: 417 us, 6.5 TB/s. 8 sequences of up to 32768, 64 nodes of 64 heads, 0.37 TFLOP: 300 us, 1.23
-// PFLOP/s; there a job's products take 1440 of the 1800 cycles between two streams' turns (scores
+// to 4096: 416 us, 6.5 TB/s. 8 sequences of up to 32768, 64 nodes of 64 heads, 0.37 TFLOP: 292 to 298 us, 1.25
+// PFLOP/s (319 in runs so long that the power cap holds); there a job's products take 1440 of the 1800 cycles between two streams' turns (scores
 // read both operands from shared memory, at its full rate). One token over 2048: 12 us.
 //
 // What a row must not see. Keys behind the context are masked by a bit per node. A
@@ -227,8 +227,8 @@ struct AttendShared {
     int abort;
 };
 
-// FEW: at most 64 rows a sequence and key head (one tile): 64 x 9 nodes of 36 rows take 227 us, 236
-// without it, and 256 x 1 436 and 453. Their queries take a quarter of the
+// FEW: at most 64 rows a sequence and key head (one tile): 64 x 9 nodes of 36 rows take 224 us, 232
+// without it, 256 x 1 415 and 431, and 32 x 1 with heads of 64 25.7 and 27.0. Their queries take a quarter of the
 // room of two tiles of 128 (the products read what lies behind them, for rows that nobody uses), which
 // leaves another stage to the rings.
 template <int DC, bool FEW>
@@ -518,9 +518,9 @@ __global__ void __launch_bounds__(kNT, 1)
         } else if (warp == kWarpMma0 || warp == kWarpMma1) {
             // ---- products, a warp per stream -------------------------------------------------------
             // (With one warp the tensor cores paused while it prepared the other stream's job.) Two tiles' streams take
-            // turns, so that one's products run while the other exponentiates (8 x 64 nodes of 32k: 302 us,
-            // without 313); streams of one tile are faster without (32 x 1 with heads of 64: 25.4 us, with
-            // turns 26.8; 44 x 3 with heads of 40: 45.0 and 47.7). The
+            // turns, so that one's products run while the other exponentiates (8 x 64 nodes of 32k take 4%
+            // more without); streams of one tile are faster without (32 x 1 with heads of 64 take 5% more with
+            // turns, 44 x 3 with heads of 40 6%). The
             // whole warp walks along, so that operands stay in uniform registers; one thread issues.
             const bool lead = tc::elect();
             const int g = warp == kWarpMma1;

@@ -7,8 +7,9 @@
 // cluster barrier between the phases. Each warp owns a contiguous stretch of entries (and later of pages),
 // so that a rank is a sum of ballots: over the warp's own stretch, the CTA's earlier
 // warps, and the cluster's earlier CTAs. Reference counts change by integer
-// atomics, whose order cannot be seen. What bounds them is the chain of phases: 5.4 us for 4 rows of
-// 64 entries, 23 for 512 of 1024; 256 beams of 257 entries forked 13 us with the copies (in a graph).
+// atomics, whose order cannot be seen. What bounds them is the chain of five phases with four barriers
+// between: 5.5 us for 4 rows of 64 entries, 23 for 512 of 1024; 256 beams of 257 entries forked 13 us with the
+// copies (in a graph).
 #include <climits>
 #include <mutex>
 
@@ -175,8 +176,9 @@ struct Place {
 
 // Rows of exactly the pages that their lengths ask for. V = 4: a lane takes four entries
 // together, of one row (M is a multiple of 4). A 512 x 1024 table over 315,000 pages takes 23 us
-// (one by one 26), ten times its bytes: seven phases that each wait for memory and for the
-// cluster. Tables that one CTA handles take their entries one by one (4 x 64: 6.2 us, by fours 7.2).
+// (one by one 26), twenty times its bytes: 16 SMs, which read the table twice and the counts three times, and
+// wait for memory and for the cluster between the phases. Tables that one CTA handles take their entries
+// one by one (4 x 64: by fours 1 us more).
 template <int V>
 __global__ void __launch_bounds__(NTP, 1) resize_kernel(PagesArgs a, int C) {
     __shared__ PagesShared sh;
