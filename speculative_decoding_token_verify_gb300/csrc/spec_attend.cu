@@ -46,7 +46,7 @@ constexpr int kWarpK = 0, kWarpV = 3, kWarpGo = 2, kWarpMma0 = 1, kWarpMma1 = 14
 constexpr unsigned kDrain = 1u << 20;  // polls for what is in flight at the end
 constexpr int kSegRing = 4;            // segments whose flags of non-finite values are kept
 constexpr float kLazy = 8.f;           // a row's reference moves when its maximum is 2^8 above it
-constexpr float kFarRef = 4096.f;         // (log2) references from which their rounding counts
+constexpr float kFarRef = 4096.f;      // (log2) references from which their rounding counts
 
 struct AttendArgs {
     const void *v;
@@ -138,7 +138,7 @@ struct Half<__half> {
 // rounded, and where all use the same m its rounding cancels. But it is half a step of m, which
 // beside scores of 2^30 is more than a probability's range: from kFarRef on probabilities and weights are
 // taken from differences of scores. Such tiles are read a second time (8 x 64 nodes of 32k 364 us
-// in place of 297, 64 x 9 231 and 229 in eager calls); all others take the same time.
+// in place of 297, 64 x 9 231 and 229 in eager calls); all others take the same time within 1%.
 template <typename T>
 __device__ __forceinline__ float log2_of(const AttendArgs &a, float mr) {   // (rounded here, whatever it is added to)
     return Half<T>::kUp == 0.f ? __fmul_rn(mr, a.sL) : __fmaf_rn(mr, a.sL, -Half<T>::kUp);
